@@ -189,6 +189,25 @@ CB_API cb_status_t cb_moe_forward(cb_moe_t *h, const void *x, void *out, void *s
 CB_API cb_status_t cb_moe_forward_f32out(cb_moe_t *h, const void *x, float *out, void *stream);
 
 /*
+ * The layer for a few tokens, 0 <= n_tokens <= CB_MOE_MAX_FEW, whatever
+ * n_tokens the handle was made for: the decode step of a handle that also
+ * runs prompts, on the same weights.  x bf16 [n_tokens][d] -> out bf16 (or
+ * fp32) [n_tokens][d], device pointers as for cb_moe_forward.  The same
+ * formulas in the same precision (bf16 H, fp32 sums, another order of them),
+ * every weight format and router mode.  One kernel launch (two with the hash
+ * router), which reads the weights of the chosen experts once.  The routing
+ * of cb_moe_routing and the stage times stay those of the last full forward.
+ * Asynchronous on `stream`, ordered after the handle's other forwards as
+ * cb_moe_forward is; it can be captured into a graph.  Errors:
+ * CB_ERR_INVALID_ARG (NULL (x and out may be NULL for no tokens), n_tokens <
+ * 0, x overlapping out), CB_ERR_UNSUPPORTED (n_tokens > CB_MOE_MAX_FEW), CB_ERR_ALIGNMENT,
+ * CB_ERR_CUDA.
+ */
+#define CB_MOE_MAX_FEW 16
+CB_API cb_status_t cb_moe_forward_few(cb_moe_t *h, const void *x, int32_t n_tokens, void *out, void *stream);
+CB_API cb_status_t cb_moe_forward_few_f32out(cb_moe_t *h, const void *x, int32_t n_tokens, float *out, void *stream);
+
+/*
  * Same pass from host memory: x_host (bf16 [T][d]) in, out_host (bf16 [T][d])
  * back.  The input copy, the layer and the output copy run on three streams
  * of the handle, through two handle-owned device staging slots that

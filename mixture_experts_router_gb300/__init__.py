@@ -29,9 +29,10 @@ STAGE_NAMES = ("router", "dispatch", "gateup_gemm", "down_gemm", "combine")
 ABI_SYMBOLS = ("cb_moe_init", "cb_moe_forward", "cb_moe_forward_f32out", "cb_moe_forward_host",
                "cb_moe_routing", "cb_moe_stage_times", "cb_moe_last_error", "cb_moe_device_bytes",
                "cb_moe_free", "cb_status_string", "cb_moe_dispatch_noalloc", "cb_moe_kernels_per_forward",
-               "cb_moe_set_stage_timing", "cb_moe_check_guards")
+               "cb_moe_set_stage_timing", "cb_moe_check_guards", "cb_moe_forward_few", "cb_moe_forward_few_f32out")
 
 
+CB_MOE_MAX_FEW = 16
 CB_ROUTER_SOFTMAX_TOPK, CB_ROUTER_RAW_LOGITS, CB_ROUTER_HASH = 0, 1, 2
 CB_MAX_HASH_DIMS = 8
 ROUTER_MODES = {"softmax": CB_ROUTER_SOFTMAX_TOPK, "raw": CB_ROUTER_RAW_LOGITS, "hash": CB_ROUTER_HASH}
@@ -81,6 +82,8 @@ def load_library(path: str = LIB_PATH):
     lib.cb_moe_forward.argtypes = [vp, vp, vp, vp]
     lib.cb_moe_forward_f32out.argtypes = [vp, vp, vp, vp]
     lib.cb_moe_forward_host.argtypes = [vp, vp, vp, vp]
+    lib.cb_moe_forward_few.argtypes = [vp, vp, ctypes.c_int32, vp, vp]
+    lib.cb_moe_forward_few_f32out.argtypes = [vp, vp, ctypes.c_int32, vp, vp]
     lib.cb_moe_routing.argtypes = [vp, ctypes.POINTER(cb_routing_view_t)]
     lib.cb_moe_stage_times.argtypes = [vp, ctypes.POINTER(ctypes.c_float), ctypes.c_int32]
     lib.cb_moe_last_error.argtypes = [vp]
@@ -94,7 +97,8 @@ def load_library(path: str = LIB_PATH):
     lib.cb_moe_dispatch_noalloc.restype = i32
     for name in ("cb_moe_init", "cb_moe_forward", "cb_moe_forward_f32out", "cb_moe_forward_host",
                  "cb_moe_routing", "cb_moe_stage_times", "cb_moe_last_error", "cb_moe_device_bytes",
-                 "cb_moe_free", "cb_moe_kernels_per_forward", "cb_moe_set_stage_timing", "cb_moe_check_guards"):
+                 "cb_moe_free", "cb_moe_kernels_per_forward", "cb_moe_set_stage_timing", "cb_moe_check_guards",
+                 "cb_moe_forward_few", "cb_moe_forward_few_f32out"):
         getattr(lib, name).restype = i32
     lib.cb_status_string.argtypes = [i32]
     lib.cb_status_string.restype = ctypes.c_char_p
@@ -120,6 +124,14 @@ def cb_moe_forward(handle, x_ptr: int, out_ptr: int, stream: int = 0) -> int:
 
 def cb_moe_forward_f32out(handle, x_ptr: int, out_ptr: int, stream: int = 0) -> int:
     return load_library().cb_moe_forward_f32out(handle, x_ptr, out_ptr, stream)
+
+
+def cb_moe_forward_few(handle, x_ptr: int, n_tokens: int, out_ptr: int, stream: int = 0) -> int:
+    return load_library().cb_moe_forward_few(handle, x_ptr, n_tokens, out_ptr, stream)
+
+
+def cb_moe_forward_few_f32out(handle, x_ptr: int, n_tokens: int, out_ptr: int, stream: int = 0) -> int:
+    return load_library().cb_moe_forward_few_f32out(handle, x_ptr, n_tokens, out_ptr, stream)
 
 
 def cb_moe_forward_host(handle, x_host_ptr: int, out_host_ptr: int, stream: int = 0) -> int:
@@ -243,6 +255,22 @@ class MoELayer:
         st = fn(self.handle, x.data_ptr(), out.data_ptr(), s)
         if st != CB_OK:
             raise CbMoeError(st, "cb_moe_forward")
+        return out
+
+    def forward_few(self, x, out, stream=None, f32out=False):
+        """The layer for x.shape[0] <= CB_MOE_MAX_FEW tokens, whatever T the handle was made for.
+        x bf16 (or int16 bits) and out bf16 (fp32 with f32out), both contiguous [n][d] on the
+        handle's device."""
+        if x.shape != out.shape or x.dim() != 2 or x.shape[1] != self.cfg.d_model:
+            raise ValueError(f"forward_few: x {tuple(x.shape)}, out {tuple(out.shape)}, d = {self.cfg.d_model}")
+        if not (x.is_contiguous() and out.is_contiguous()) or x.element_size() != 2 or \
+                out.element_size() != (4 if f32out else 2):
+            raise ValueError("forward_few: x is contiguous bf16, out contiguous bf16 (fp32 with f32out)")
+        s = 0 if stream is None else stream.cuda_stream
+        fn = cb_moe_forward_few_f32out if f32out else cb_moe_forward_few
+        st = fn(self.handle, x.data_ptr(), int(x.shape[0]), out.data_ptr(), s)
+        if st != CB_OK:
+            raise CbMoeError(st, "cb_moe_forward_few")
         return out
 
     def forward_host(self, x_host, out_host, stream=None):

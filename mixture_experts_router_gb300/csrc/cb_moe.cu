@@ -65,6 +65,7 @@ struct cb_moe {
   bool timing_events;      // the events exist (CB_FLAG_STAGE_TIMING at init)
   bool router_tc;          // tcgen05 router (else the mma.sync router)
   bool use_graphs;         // replay each forward variant from a captured CUDA graph
+  int32_t gu_block;        // gate/up rows interleaved in blocks of this size
   bool pair_gu, pair_dn;   // bf16 gate/up, down GEMMs on CTA pairs (2-SM MMA)
   int32_t rd_grid;         // > 0: router and dispatch run as one cooperative launch of this many blocks
   int32_t rd_box;          // the tcgen05 form's x box rows (a block's token share)
@@ -82,6 +83,10 @@ struct cb_moe {
   bool gather_a;           // gate/up GEMM gathers its rows from x (no Xp copy)
   bool int8_tm;            // int8 GEMMs convert their weights into tensor memory
   bool use_pdl;            // programmatic dependent launch between the forward's kernels
+  uint16_t* few_h;         // the few-token layer's H, logits and (hash router) experts
+  float* few_logits;
+  int32_t* few_ids;
+  int32_t few_grid;        // blocks of its cooperative launch
   bool fused_combine;      // the CTA-pair down GEMM adds its rows into the token sums
   const void* tm_x_src;    // x pointer tm_x was encoded for
   const void* tm_xg_src;   // x pointer tm_xg was encoded for
@@ -103,7 +108,7 @@ struct Layout {
   int32_t n_guards;
   uint64_t off_wr, off_bias, off_wgu, off_wd, off_sg, off_su, off_sd, off_wh, off_zg, off_zu, off_zd;
   uint64_t off_xp, off_hb, off_y, off_ids, off_w, off_logits, off_rpart, off_chunk, off_counts, off_offsets, off_mtile_off,
-      off_mtile_expert, off_ptile_off, off_ptile_expert, off_tok, off_inv, off_err, off_bar, off_xs, off_os;
+      off_mtile_expert, off_ptile_off, off_ptile_expert, off_tok, off_inv, off_err, off_bar, off_xs, off_os, off_few_h, off_few_logits, off_few_ids;
   uint64_t total;
   int32_t max_mtiles, n_chunks;
 };
@@ -165,6 +170,9 @@ Layout plan(const cb_moe_config_t& c) {
   L.off_bar = take(64);
   L.off_xs = take(2 * T * d * 2);
   L.off_os = take(2 * T * d * 2);
+  L.off_few_h = take(static_cast<uint64_t>(kFewTokens) * k * f * 2);
+  L.off_few_logits = take(static_cast<uint64_t>(kFewTokens) * E * 4);
+  L.off_few_ids = take(2 * kFewTokens * 4);  // and the hash router's weights behind them
   L.total = o;
   return L;
 }
@@ -242,6 +250,23 @@ struct DeviceGuard {
   }
 };
 
+WeightFormat weight_format(const cb_moe_config_t& c) {
+  return c.wdtype == CB_W_INT4 ? kWInt4 : c.wdtype == CB_W_FP8 ? kWFp8 : kWInt8;
+}
+
+HashRouterArgs hash_router_args(const cb_moe_t* h, const void* x, int32_t n, int32_t* ids, float* w) {
+  HashRouterArgs ha{};
+  ha.x = static_cast<const uint16_t*>(x);
+  ha.wh = h->wh;
+  ha.T = n;
+  ha.d = h->cfg.d_model;
+  ha.E = h->cfg.n_experts;
+  ha.hash_dims = h->cfg.hash_dims;
+  ha.ids = ids;
+  ha.w = w;
+  return ha;
+}
+
 cb_status_t enqueue_forward(cb_moe_t* h, const void* x, void* out, bool f32out, cudaStream_t s) {
   const cb_moe_config_t& c = h->cfg;
   if (fault_injected("launch")) return CB_ERR_CUDA;
@@ -282,16 +307,7 @@ cb_status_t enqueue_forward(cb_moe_t* h, const void* x, void* out, bool f32out, 
   }
   ra.raw_weights = c.router_mode == CB_ROUTER_RAW_LOGITS ? 1 : 0;
   if (c.router_mode == CB_ROUTER_HASH) {
-    HashRouterArgs ha{};
-    ha.x = static_cast<const uint16_t*>(x);
-    ha.wh = h->wh;
-    ha.T = c.n_tokens;
-    ha.d = c.d_model;
-    ha.E = c.n_experts;
-    ha.hash_dims = c.hash_dims;
-    ha.ids = h->ids;
-    ha.w = h->w;
-    if (launch_router_hash(ha, s) != cudaSuccess || !mark(1)) return CB_ERR_CUDA;
+    if (launch_router_hash(hash_router_args(h, x, c.n_tokens, h->ids, h->w), s) != cudaSuccess || !mark(1)) return CB_ERR_CUDA;
   } else if (h->router_tc) {
     if (h->tm_x_src != x) {
       const uint32_t box = h->rd_grid > 0 ? static_cast<uint32_t>(h->rd_box) : 128u;
@@ -349,9 +365,8 @@ cb_status_t enqueue_forward(cb_moe_t* h, const void* x, void* out, bool f32out, 
     return CB_ERR_CUDA;
   }
 
-  const bool int4w = c.wdtype == CB_W_INT4;
   const bool int8w = c.wdtype != CB_W_BF16;  // quantized weights (int8, int4 or fp8)
-  const WeightFormat wf = int4w ? kWInt4 : c.wdtype == CB_W_FP8 ? kWFp8 : kWInt8;
+  const WeightFormat wf = weight_format(c);
   GemmArgs ga{};
   ga.mtile_off = h->mtile_off;
   ga.mtile_expert = h->mtile_expert;
@@ -524,11 +539,12 @@ cb_status_t run_graphed(cb_moe_t* h, int slot, const void* a, const void* b, cud
   return cudaGraphLaunch(g.exec, s) == cudaSuccess ? CB_OK : CB_ERR_CUDA;
 }
 
-cb_status_t check_forward_args(const cb_moe_t* h, const void* x, const void* out, uint64_t out_elem_bytes) {
+cb_status_t check_forward_args(const cb_moe_t* h, const void* x, const void* out, uint64_t n_tokens,
+                               uint64_t out_elem_bytes) {
   if (h == nullptr || x == nullptr || out == nullptr) return CB_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(out)) return CB_ERR_ALIGNMENT;
-  const uint64_t xb = static_cast<uint64_t>(h->cfg.n_tokens) * h->cfg.d_model * 2;
-  const uint64_t ob = static_cast<uint64_t>(h->cfg.n_tokens) * h->cfg.d_model * out_elem_bytes;
+  const uint64_t xb = n_tokens * h->cfg.d_model * 2;
+  const uint64_t ob = n_tokens * h->cfg.d_model * out_elem_bytes;
   const uintptr_t xa = reinterpret_cast<uintptr_t>(x), oa = reinterpret_cast<uintptr_t>(out);
   if (xb > 0 && xa < oa + ob && oa < xa + xb) return CB_ERR_INVALID_ARG;  // overlap
   return CB_OK;
@@ -588,6 +604,60 @@ cb_status_t device_forward(cb_moe_t* h, int slot, const void* x, void* out, cuda
   const cb_status_t st = run_graphed(h, slot, x, out, s, body);
   if (st == CB_OK && !cap && !mark_last_forward(h, s)) return CB_ERR_CUDA;
   return st;
+}
+
+// The few-token layer on the caller's stream: the hash router's kernel where
+// the handle has one, and the one launch that is the rest.
+cb_status_t few_forward(cb_moe_t* h, const void* x, int32_t n, void* out, bool f32out, void* stream) {
+  if (h == nullptr || n < 0) return CB_ERR_INVALID_ARG;
+  if (n > CB_MOE_MAX_FEW) return CB_ERR_UNSUPPORTED;
+  if (n == 0) return CB_OK;
+  const cb_status_t st = check_forward_args(h, x, out, static_cast<uint64_t>(n), f32out ? 4 : 2);
+  if (st != CB_OK) return st;
+  if (h->few_grid <= 0) return CB_ERR_UNSUPPORTED;
+  if (fault_injected("launch")) return CB_ERR_CUDA;
+  DeviceGuard guard(h->cfg.device);
+  if (!guard.ok) return CB_ERR_CUDA;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool cap = capturing(s);
+  if (!cap && !wait_last_forward(h, s)) return CB_ERR_CUDA;
+  const cb_moe_config_t& c = h->cfg;
+  const bool quantised = c.wdtype != CB_W_BF16;
+  FewArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.n = n;
+  a.d = c.d_model;
+  a.f = c.d_ff;
+  a.E = c.n_experts;
+  a.k = c.top_k;
+  a.wr = h->wr;
+  a.bias = h->bias;
+  a.raw_weights = c.router_mode == CB_ROUTER_RAW_LOGITS ? 1 : 0;
+  a.wgu = h->wgu;
+  a.wd = h->wd;
+  a.gu_block = h->gu_block;
+  a.sg = h->sg;
+  a.su = h->su;
+  a.sd = h->sd;
+  a.zg = h->zg;
+  a.zu = h->zu;
+  a.zd = h->zd;
+  a.logits = h->few_logits;
+  a.h = h->few_h;
+  a.out = out;
+  a.out_f32 = f32out ? 1 : 0;
+  a.bar = h->coop_bar + 4;  // words 0 and 1 are the dispatch's
+  a.err = h->err;
+  a.wait_limit_ns = kWaitLimitNs;
+  if (c.router_mode == CB_ROUTER_HASH) {
+    a.ids = h->few_ids;
+    const HashRouterArgs ha =
+        hash_router_args(h, x, n, h->few_ids, reinterpret_cast<float*>(h->few_ids + kFewTokens));
+    if (launch_router_hash(ha, s) != cudaSuccess) return CB_ERR_CUDA;
+  }
+  if (launch_few_tokens(few_format(quantised, weight_format(c)), a, h->few_grid, s) != cudaSuccess) return CB_ERR_CUDA;
+  if (!cap && !mark_last_forward(h, s)) return CB_ERR_CUDA;
+  return CB_OK;
 }
 
 }  // namespace
@@ -669,6 +739,7 @@ cb_status_t cb_moe_init(const cb_moe_config_t* cfg, const cb_moe_weights_t* wts,
   const Layout L = plan(*cfg);
   cb_moe_t* h = new (std::nothrow) cb_moe_t();
   if (h == nullptr) return CB_ERR_OOM;
+  static_assert(kFewTokens == CB_MOE_MAX_FEW, "tokens of the few-token layer");
   static_assert(sizeof(h->guard_off) / sizeof(h->guard_off[0]) == kMaxGuards, "guard table");
   for (int i = 0; i < L.n_guards; ++i) h->guard_off[i] = L.guard_off[i];
   h->n_guards = L.n_guards;
@@ -712,6 +783,9 @@ cb_status_t cb_moe_init(const cb_moe_config_t* cfg, const cb_moe_weights_t* wts,
   h->inv = reinterpret_cast<int32_t*>(b + L.off_inv);
   h->err = reinterpret_cast<int*>(b + L.off_err);
   h->coop_bar = reinterpret_cast<unsigned int*>(b + L.off_bar);
+  h->few_h = reinterpret_cast<uint16_t*>(b + L.off_few_h);
+  h->few_logits = reinterpret_cast<float*>(b + L.off_few_logits);
+  h->few_ids = reinterpret_cast<int32_t*>(b + L.off_few_ids);
   for (int i = 0; i < 2; ++i) {
     h->x_stage[i] = reinterpret_cast<uint16_t*>(b + L.off_xs) + static_cast<uint64_t>(i) * cfg->n_tokens * cfg->d_model;
     h->out_stage[i] = reinterpret_cast<uint16_t*>(b + L.off_os) + static_cast<uint64_t>(i) * cfg->n_tokens * cfg->d_model;
@@ -752,6 +826,7 @@ cb_status_t cb_moe_init(const cb_moe_config_t* cfg, const cb_moe_weights_t* wts,
   }
   const uint64_t brows =
       int8w ? (h->int8_tm ? grouped_gemm_int8_tm_gateup_block() : grouped_gemm_int8_gateup_block()) : 128;
+  h->gu_block = static_cast<int32_t>(brows);
   const uint64_t blk = brows * d * wbits / 8;  // bytes of one block of weight rows
   const uint64_t nblk = E * (f / brows);
   ok = ok && cudaMemcpy2D(h->wgu, 2 * blk, wts->w_gate, blk, blk, nblk, cudaMemcpyDeviceToDevice) == cudaSuccess;
@@ -785,6 +860,9 @@ cb_status_t cb_moe_init(const cb_moe_config_t* cfg, const cb_moe_weights_t* wts,
        grouped_gemm_int8_tm_prepare() == cudaSuccess &&
        router_prepare() == cudaSuccess && router_tc_prepare() == cudaSuccess && dispatch_prepare() == cudaSuccess &&
        route_dispatch_prepare() == cudaSuccess && route_dispatch_tc_prepare() == cudaSuccess;
+  int few_per_sm = 0;
+  ok = ok && few_tokens_prepare(few_format(int8w, weight_format(*cfg)), &few_per_sm) == cudaSuccess;
+  h->few_grid = std::min(few_per_sm, 1) * h->num_sms;
   // router: tcgen05 for wide expert counts, the mma.sync split-K router for
   // E <= 16 (bound by reading x, where more CTAs help); CB_MOE_ROUTER=tc|mma
   // overrides the choice
@@ -947,7 +1025,7 @@ cb_status_t cb_moe_init(const cb_moe_config_t* cfg, const cb_moe_weights_t* wts,
 }
 
 cb_status_t cb_moe_forward(cb_moe_t* h, const void* x, void* out, void* stream) {
-  const cb_status_t st = check_forward_args(h, x, out, 2);
+  const cb_status_t st = check_forward_args(h, x, out, h != nullptr ? h->cfg.n_tokens : 0, 2);
   if (st != CB_OK) return st;
   if (h->cfg.n_tokens == 0) return CB_OK;
   if (fault_injected("launch")) return CB_ERR_CUDA;
@@ -958,7 +1036,7 @@ cb_status_t cb_moe_forward(cb_moe_t* h, const void* x, void* out, void* stream) 
 }
 
 cb_status_t cb_moe_forward_f32out(cb_moe_t* h, const void* x, float* out, void* stream) {
-  const cb_status_t st = check_forward_args(h, x, out, 4);
+  const cb_status_t st = check_forward_args(h, x, out, h != nullptr ? h->cfg.n_tokens : 0, 4);
   if (st != CB_OK) return st;
   if (h->cfg.n_tokens == 0) return CB_OK;
   if (fault_injected("launch")) return CB_ERR_CUDA;
@@ -966,6 +1044,14 @@ cb_status_t cb_moe_forward_f32out(cb_moe_t* h, const void* x, float* out, void* 
   if (!guard.ok) return CB_ERR_CUDA;
   return device_forward(h, 1, x, out, static_cast<cudaStream_t>(stream),
                         [&](cudaStream_t s) { return enqueue_forward(h, x, out, true, s); });
+}
+
+cb_status_t cb_moe_forward_few(cb_moe_t* h, const void* x, int32_t n_tokens, void* out, void* stream) {
+  return few_forward(h, x, n_tokens, out, false, stream);
+}
+
+cb_status_t cb_moe_forward_few_f32out(cb_moe_t* h, const void* x, int32_t n_tokens, float* out, void* stream) {
+  return few_forward(h, x, n_tokens, out, true, stream);
 }
 
 cb_status_t cb_moe_forward_host(cb_moe_t* h, const void* x_host, void* out_host, void* stream) {

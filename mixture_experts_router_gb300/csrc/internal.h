@@ -295,4 +295,31 @@ cudaError_t grouped_gemm_int8_tm_prepare();
 int grouped_gemm_int8_tm_tile_n(GemmKind kind);
 int grouped_gemm_int8_tm_gateup_block();  // gate/up rows interleaved in blocks of this size
 
+// -------------------------------------------------- a few tokens, one launch
+constexpr int kFewTokens = 16;  // at most
+struct FewArgs {
+  const uint16_t* x;     // bf16 [n][d]
+  int32_t n, d, f, E, k;
+  const uint16_t* wr;    // bf16 [E][d]
+  const float* bias;     // [E] or nullptr
+  int32_t raw_weights;   // 1: w = the selected raw logits (no softmax)
+  const int32_t* ids;    // the hash router's [n] experts (k = 1, weights 1), else nullptr: routed here
+  const void* wgu;       // the handle's gate/up rows, interleaved in blocks of gu_block
+  const void* wd;
+  int32_t gu_block;
+  const float *sg, *su, *sd;    // per-channel scales (quantised weights)
+  const uint8_t *zg, *zu, *zd;  // zero points (int4)
+  float* logits;         // scratch [n][E]
+  uint16_t* h;           // scratch bf16 [n k][f]
+  void* out;             // bf16 or fp32 [n][d]
+  int32_t out_f32;
+  unsigned int* bar;     // two grid barriers: 4 words, zero between launches
+  int* err;
+  uint64_t wait_limit_ns;
+};
+int few_format(bool quantised, WeightFormat wf);  // the kernel's name of a weight format
+// one-time function attributes; blocks of the launch that fit one SM at once
+cudaError_t few_tokens_prepare(int format, int* blocks_per_sm);
+cudaError_t launch_few_tokens(int format, const FewArgs& a, int grid, cudaStream_t s);
+
 }  // namespace cbmoe
