@@ -33,6 +33,12 @@ ABI_SYMBOLS = ("cb_moe_init", "cb_moe_forward", "cb_moe_forward_f32out", "cb_moe
 
 
 CB_MOE_MAX_FEW = 16
+# every symbol include/cb_fp4.h declares
+FP4_SYMBOLS = ("cb_fp4_scale_bytes", "cb_fp4_quantize", "cb_fp4_dequantize", "cb_fp4_matmul")
+CB_FP4_MX, CB_FP4_NV = 0, 1
+CB_T_BF16, CB_T_F32 = 0, 1
+FP4_FORMATS = {"mx": CB_FP4_MX, "nv": CB_FP4_NV}
+FP4_BLOCK = {"mx": 32, "nv": 16}
 CB_ROUTER_SOFTMAX_TOPK, CB_ROUTER_RAW_LOGITS, CB_ROUTER_HASH = 0, 1, 2
 CB_MAX_HASH_DIMS = 8
 ROUTER_MODES = {"softmax": CB_ROUTER_SOFTMAX_TOPK, "raw": CB_ROUTER_RAW_LOGITS, "hash": CB_ROUTER_HASH}
@@ -57,6 +63,15 @@ class cb_routing_view_t(ctypes.Structure):
     _fields_ = [("ids", ctypes.c_void_p), ("w", ctypes.c_void_p), ("counts", ctypes.c_void_p),
                 ("offsets", ctypes.c_void_p), ("tok", ctypes.c_void_p), ("inv", ctypes.c_void_p),
                 ("logits", ctypes.c_void_p), ("tile_offsets", ctypes.c_void_p)]
+
+
+class cb_fp4_matmul_t(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("out_type", ctypes.c_int32),
+                ("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("a_codes", ctypes.c_void_p), ("a_scales", ctypes.c_void_p), ("a_tensor_scale", ctypes.c_void_p),
+                ("b_codes", ctypes.c_void_p), ("b_scales", ctypes.c_void_p), ("b_tensor_scale", ctypes.c_void_p),
+                ("n_groups", ctypes.c_int32), ("tile_offsets", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("ld_out", ctypes.c_int64), ("status", ctypes.c_void_p)]
 
 
 class CbMoeError(RuntimeError):
@@ -99,6 +114,13 @@ def load_library(path: str = LIB_PATH):
                  "cb_moe_routing", "cb_moe_stage_times", "cb_moe_last_error", "cb_moe_device_bytes",
                  "cb_moe_free", "cb_moe_kernels_per_forward", "cb_moe_set_stage_timing", "cb_moe_check_guards",
                  "cb_moe_forward_few", "cb_moe_forward_few_f32out"):
+        getattr(lib, name).restype = i32
+    i64 = ctypes.c_int64
+    lib.cb_fp4_scale_bytes.argtypes = [ctypes.c_int32, i64, i64, ctypes.POINTER(ctypes.c_uint64)]
+    lib.cb_fp4_quantize.argtypes = [ctypes.c_int32, vp, ctypes.c_int32, i64, i64, i64, vp, vp, vp, vp]
+    lib.cb_fp4_dequantize.argtypes = [ctypes.c_int32, vp, vp, vp, i64, i64, vp, ctypes.c_int32, i64, vp]
+    lib.cb_fp4_matmul.argtypes = [ctypes.POINTER(cb_fp4_matmul_t), vp]
+    for name in FP4_SYMBOLS:
         getattr(lib, name).restype = i32
     lib.cb_status_string.argtypes = [i32]
     lib.cb_status_string.restype = ctypes.c_char_p
@@ -180,6 +202,27 @@ def cb_moe_dispatch_noalloc(ids_ptr, n_tokens, top_k, n_experts, counts_ptr, off
     """Dispatch of routing ids with no device allocation (static scratch); see cb_moe.h."""
     return load_library().cb_moe_dispatch_noalloc(ids_ptr, n_tokens, top_k, n_experts, counts_ptr, offsets_ptr,
                                                   tok_ptr, inv_ptr, status_ptr, stream)
+
+
+def cb_fp4_scale_bytes(fmt: int, rows: int, cols: int):
+    b = ctypes.c_uint64()
+    st = load_library().cb_fp4_scale_bytes(fmt, rows, cols, ctypes.byref(b))
+    return st, b.value
+
+
+def cb_fp4_quantize(fmt, x_ptr, x_type, rows, cols, ld, tensor_scale_ptr, codes_ptr, scales_ptr, stream: int = 0) -> int:
+    return load_library().cb_fp4_quantize(fmt, x_ptr, x_type, rows, cols, ld, tensor_scale_ptr, codes_ptr, scales_ptr,
+                                          stream)
+
+
+def cb_fp4_dequantize(fmt, codes_ptr, scales_ptr, tensor_scale_ptr, rows, cols, out_ptr, out_type, ld,
+                      stream: int = 0) -> int:
+    return load_library().cb_fp4_dequantize(fmt, codes_ptr, scales_ptr, tensor_scale_ptr, rows, cols, out_ptr, out_type,
+                                            ld, stream)
+
+
+def cb_fp4_matmul(args: cb_fp4_matmul_t, stream: int = 0) -> int:
+    return load_library().cb_fp4_matmul(ctypes.byref(args), stream)
 
 
 # ------------------------------------------------------- torch convenience
@@ -323,3 +366,121 @@ class MoELayer:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------ 4-bit floats with block scales, over torch tensors
+def _check(st, what):
+    if st != CB_OK:
+        raise CbMoeError(st, what)
+
+
+def _fp4_type(dtype):
+    import torch
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"4-bit floats are made from and turned into bfloat16 or float32, not {dtype}")
+    return CB_T_BF16 if dtype == torch.bfloat16 else CB_T_F32
+
+
+def _row_stride(t, what):
+    """Elements between the rows of a 2-D CUDA tensor whose rows are contiguous."""
+    if t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: a 2-D CUDA tensor with contiguous rows is needed")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+class Fp4Matrix:
+    """A matrix of 4-bit floats with block scales, as include/cb_fp4.h lays it out: `codes`
+    uint8 [rows][cols / 2] and `scales` uint8; format "mx" or "nv", the latter with
+    `tensor_scale` (fp32 [1]).  One matrix per expert: codes [E][rows][cols / 2], scales of
+    E arrays, tensor_scale [E]."""
+
+    def __init__(self, format, rows, cols, codes, scales, tensor_scale=None):
+        import torch
+        if format not in FP4_FORMATS:
+            raise ValueError(f"unknown 4-bit format {format!r}: one of {sorted(FP4_FORMATS)}")
+        self.format, self.rows, self.cols = format, int(rows), int(cols)
+        self.groups = int(codes.shape[0]) if codes.dim() == 3 else 1
+        st, need = cb_fp4_scale_bytes(FP4_FORMATS[format], self.rows, self.cols)
+        _check(st, "cb_fp4_scale_bytes")
+        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or \
+                tuple(codes.shape[-2:]) != (self.rows, self.cols // 2) or scales.numel() != need * self.groups or \
+                not (codes.is_contiguous() and scales.is_contiguous()):
+            raise ValueError(f"codes {tuple(codes.shape)} {codes.dtype}, scales {tuple(scales.shape)} {scales.dtype}: "
+                             f"not a contiguous {format} matrix of {self.rows} x {self.cols} ({need} scale bytes)")
+        if (tensor_scale is not None) != (format == "nv") or \
+                (tensor_scale is not None and (tensor_scale.dtype != torch.float32 or tensor_scale.numel() != self.groups
+                                               or not tensor_scale.is_contiguous())):
+            raise ValueError("format nv has one fp32 tensor scale per matrix, format mx none")
+        self.codes, self.scales, self.tensor_scale = codes, scales, tensor_scale
+
+
+def _stream_of(stream, device):
+    """The stream to run on (torch's current one unless given), for use as a context too, so
+    that a result allocated within it belongs to it."""
+    import torch
+    return torch.cuda.current_stream(device) if stream is None else stream
+
+
+def fp4_quantize(x, format, tensor_scale=None, stream=None) -> Fp4Matrix:
+    """x (2-D, bf16 or fp32, contiguous rows with any stride) as an Fp4Matrix; format "nv"
+    takes tensor_scale, an fp32 CUDA tensor of one element, e.g. max|x| / (6 * 448).  Runs on
+    `stream`, or on torch's current stream."""
+    import torch
+    if format not in FP4_FORMATS:
+        raise ValueError(f"unknown 4-bit format {format!r}: one of {sorted(FP4_FORMATS)}")
+    kind, ld = _fp4_type(x.dtype), _row_stride(x, "fp4_quantize")
+    rows, cols = int(x.shape[0]), int(x.shape[1])
+    if tensor_scale is not None and (tensor_scale.dtype != torch.float32 or tensor_scale.numel() != 1):
+        raise ValueError("tensor_scale: one fp32 element")
+    st, nbytes = cb_fp4_scale_bytes(FP4_FORMATS[format], rows, cols)
+    _check(st, "cb_fp4_quantize")
+    s = _stream_of(stream, x.device)
+    with torch.cuda.device(x.device), torch.cuda.stream(s):
+        codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=x.device)
+        scales = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        _check(cb_fp4_quantize(FP4_FORMATS[format], x.data_ptr(), kind, rows, cols, ld, _ptr(tensor_scale),
+                               codes.data_ptr(), scales.data_ptr(), s.cuda_stream), "cb_fp4_quantize")
+    return Fp4Matrix(format, rows, cols, codes, scales, tensor_scale)
+
+
+def fp4_dequantize(m: Fp4Matrix, dtype=None, out=None, stream=None):
+    """The values that m stands for, as bf16 (or `dtype`), or into `out` (2-D, contiguous rows
+    with any stride)."""
+    import torch
+    if m.groups != 1:
+        raise ValueError("fp4_dequantize: one matrix at a time")
+    s = _stream_of(stream, m.codes.device)
+    with torch.cuda.device(m.codes.device), torch.cuda.stream(s):
+        if out is None:
+            out = torch.empty((m.rows, m.cols), dtype=dtype or torch.bfloat16, device=m.codes.device)
+        elif tuple(out.shape) != (m.rows, m.cols) or (dtype is not None and out.dtype != dtype):
+            raise ValueError(f"out {tuple(out.shape)} {out.dtype} for a {m.rows} x {m.cols} matrix")
+        _check(cb_fp4_dequantize(FP4_FORMATS[m.format], m.codes.data_ptr(), m.scales.data_ptr(), _ptr(m.tensor_scale),
+                                 m.rows, m.cols, out.data_ptr(), _fp4_type(out.dtype),
+                                 _row_stride(out, "fp4_dequantize"), s.cuda_stream), "cb_fp4_dequantize")
+    return out
+
+
+def fp4_matmul(a: Fp4Matrix, b: Fp4Matrix, dtype=None, out=None, tile_offsets=None, status=None, stream=None):
+    """a b^T ([a.rows][b.rows], bf16 or `dtype`, or into `out`).  With `tile_offsets` (int32
+    CUDA tensor [b.groups + 1], cb_routing_view_t's) rows 128 tile_offsets[e] .. 128
+    tile_offsets[e + 1] of `a` meet b's e-th matrix; rows past the last are not written.
+    `status`: an int32 CUDA tensor that receives CB_ERR_TIMEOUT if a device-side wait ran out."""
+    import torch
+    if a.format != b.format or a.cols != b.cols or a.groups != 1:
+        raise ValueError(f"fp4_matmul: {a.groups} x [{a.rows} x {a.cols}] {a.format} by [{b.rows} x {b.cols}] {b.format}")
+    for name, t, n in (("tile_offsets", tile_offsets, b.groups + 1), ("status", status, 1)):
+        if t is not None and (t.dtype != torch.int32 or not t.is_cuda or t.numel() != n or not t.is_contiguous()):
+            raise ValueError(f"fp4_matmul: {name} is a contiguous int32 CUDA tensor of {n}")
+    s = _stream_of(stream, a.codes.device)
+    with torch.cuda.device(a.codes.device), torch.cuda.stream(s):
+        if out is None:
+            out = torch.empty((a.rows, b.rows), dtype=dtype or torch.bfloat16, device=a.codes.device)
+        elif tuple(out.shape) != (a.rows, b.rows) or (dtype is not None and out.dtype != dtype):
+            raise ValueError(f"out {tuple(out.shape)} {out.dtype} for a {a.rows} x {b.rows} product")
+        p = cb_fp4_matmul_t(FP4_FORMATS[a.format], _fp4_type(out.dtype), a.rows, b.rows, a.cols, a.codes.data_ptr(),
+                            a.scales.data_ptr(), _ptr(a.tensor_scale), b.codes.data_ptr(), b.scales.data_ptr(),
+                            _ptr(b.tensor_scale), b.groups, _ptr(tile_offsets), out.data_ptr(),
+                            _row_stride(out, "fp4_matmul"), _ptr(status))
+        _check(cb_fp4_matmul(p, s.cuda_stream), "cb_fp4_matmul")
+    return out

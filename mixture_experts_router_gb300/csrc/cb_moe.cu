@@ -222,11 +222,10 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
-// 2-D row-major tensor [outer][inner] with a box of box_outer x box_inner
-// elements, 128-byte swizzled (bf16 operands) or unswizzled (int8 staging).
-bool make_tmap(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t elem_bytes, uint64_t inner,
-               uint64_t outer, uint32_t box_inner, uint32_t box_outer,
-               CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+}  // namespace
+
+bool cbmoe::make_tmap(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t elem_bytes, uint64_t inner,
+                      uint64_t outer, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle) {
   auto enc = tensor_map_encoder();
   if (enc == nullptr) return false;
   cuuint64_t dims[2] = {inner, outer};
@@ -237,6 +236,8 @@ bool make_tmap(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 struct DeviceGuard {
   int prev = -1;

@@ -1,0 +1,401 @@
+// Product of two 4-bit block-scaled matrices: out = g_a g_b (A s_a) (B s_b)^T,
+// one pair, or one B per expert for A's rows in 128-row tiles.
+//
+// The block-scaled tcgen05.mma (kind::mxf4: a power-of-two scale per 32
+// elements; kind::mxf4nvf4: an e4m3 scale per 16) takes K = 64 codes per
+// instruction from shared memory and the scales of both operands from tensor
+// memory, and sums in fp32.  Codes arrive by TMA (128-byte swizzled rows of
+// K = 256), scales as whole 512-byte tiles of 128 rows x 4 blocks, the order
+// in which tcgen05.cp puts them into tensor memory: 4 columns per tile, the
+// same for each quarter of the lanes.  A row's tail past k is zero codes
+// (TMA's fill); scale words past the array are not loaded, and no
+// instruction runs past k.
+//
+// The two operands' roles.  The MMA's M side is 128 rows, its N side BN.
+//  * more than 128 rows of A, or experts: A's rows are the M side, BN rows of
+//    B the N side;
+//  * up to 128 rows of A ("swap"): B's rows (the weights) are the M side and
+//    all of A the N side, BN >= m of 16..128, so the 128-row side is never
+//    padding and a CTA streams its weight rows once.  What bounds these is
+//    the weights' HBM traffic; a cluster of up to 8 CTAs shares a tile along
+//    k and adds its partial sums through distributed shared memory, in rank
+//    order.
+//
+// Per CTA: warp 0 TMA producer, warp 1 tensor memory and MMA issuer, warps
+// 2..5 epilogue.  Stage s of the ring has its own scale columns in tensor
+// memory, so a stage's commit frees both.  All waits are bounded.
+#include <cuda_bf16.h>
+
+#include "fp4.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace cbmoe {
+namespace {
+
+constexpr int BP = 128;            // rows of the M side
+constexpr int BK = 256;            // elements per stage: 128 bytes of codes
+constexpr int ROW_BYTES = BK / 2;
+constexpr int STAGES = 4;
+constexpr int THREADS = 192;
+constexpr int EPI_WARP0 = 2;
+constexpr int P_BYTES = BP * ROW_BYTES;
+
+constexpr int pow2_at_least(int v) {
+  int p = 32;
+  while (p < v) p *= 2;
+  return p;
+}
+
+template <int FMT, int BN>
+struct Cfg {
+  static constexpr int W = BK / (4 * kFp4Block<FMT>);   // scale words per stage: 2 (MX) or 4 (NV)
+  static constexpr int QT = (BN + 127) / 128;           // scale row tiles of the N side
+  static constexpr int Q_BYTES = BN * ROW_BYTES;
+  static constexpr int SF_BYTES = W * kScaleTileBytes;  // of one row tile
+  static constexpr int STAGE = P_BYTES + Q_BYTES + (1 + QT) * SF_BYTES;
+  static constexpr int SF0 = BN < 32 ? 32 : BN;         // first scale column
+  static constexpr int SF_COLS = W * 4 * (1 + QT);      // per stage
+  static constexpr int TMEM = pow2_at_least(SF0 + STAGES * SF_COLS);
+  static constexpr int BYTES = STAGES * STAGE + 1024 + 256;
+  static_assert(STAGE % 1024 == 0 && Q_BYTES % 1024 == 0 && BYTES <= 232448 && TMEM <= 512, "layout");
+  static_assert(STAGES * STAGE >= BN * BP * 4 || BN > 128, "the ring holds the partial sums");
+};
+
+// A tile of the output: M-side rows from p0, N-side rows from q0.
+struct Tile {
+  int p0, q0, e;
+};
+
+template <int BN, bool SWAP>
+struct Tiles {
+  int pt, total;
+  __device__ __forceinline__ explicit Tiles(const Fp4MatmulArgs& a) {
+    const int mt = (a.m + BP - 1) / BP;
+    if constexpr (SWAP) {
+      pt = (a.n + BP - 1) / BP;
+      total = pt;
+    } else {
+      pt = a.tile_offsets != nullptr ? min(max(a.tile_offsets[a.n_groups], 0), mt) : mt;
+      total = pt * ((a.n + BN - 1) / BN);
+    }
+  }
+  // consecutive tiles take the row tiles against one column tile, so that
+  // the CTAs running together read few rows of B
+  __device__ __forceinline__ Tile at(int i, const Fp4MatmulArgs& a) const {
+    Tile t{i % pt * BP, i / pt * BN, 0};
+    if (!SWAP && a.tile_offsets != nullptr) {  // the expert: the last e with tile_offsets[e] <= row tile
+      int lo = 0, hi = a.n_groups - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (__ldg(a.tile_offsets + mid) <= i % pt)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      t.e = lo;
+    }
+    return t;
+  }
+};
+
+template <int FMT, int BN, bool SWAP>
+__global__ void __launch_bounds__(THREADS, 1)
+    fp4_matmul_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
+                      const Fp4MatmulArgs a, const int ksplit, const int vec) {
+  using C = Cfg<FMT, BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 1);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int rank = SWAP ? static_cast<int>(cluster_ctarank()) : 0;
+  const int worker = SWAP ? static_cast<int>(blockIdx.x) / ksplit : static_cast<int>(blockIdx.x);
+  const int workers = SWAP ? static_cast<int>(gridDim.x) / ksplit : static_cast<int>(gridDim.x);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(tfull, 1);
+    mbar_init(tempty, 4);
+    fence_barrier_init();
+    prefetch_tensormap(&tm_p);
+    prefetch_tensormap(&tm_q);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::TMEM);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dep_wait();
+
+  const Tiles<BN, SWAP> tiles(a);
+  const int stages = (a.k + BK - 1) / BK;
+  const int kb0 = SWAP ? rank * stages / ksplit : 0;
+  const int kb1 = SWAP ? (rank + 1) * stages / ksplit : stages;
+  const int words = (a.k / kFp4Block<FMT> + 3) / 4;  // scale tiles per row tile
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint8_t* ps = SWAP ? a.b_scales : a.a_scales;
+      const uint8_t* qs = SWAP ? a.a_scales : a.b_scales;
+      const int64_t q_tiles = ((SWAP ? a.m : a.n) + 127) / 128;
+      int64_t it = 0;
+      bool ok = true;
+      for (int i = worker; ok && i < tiles.total; i += workers) {
+        const Tile t = tiles.at(i, a);
+        const int q_row = t.q0 + (SWAP ? 0 : t.e * a.n);
+        const uint8_t* p_sf = ps + static_cast<int64_t>(t.p0 / 128) * words * kScaleTileBytes;
+        const uint8_t* q_sf = qs + (t.e * q_tiles + t.q0 / 128) * words * kScaleTileBytes;
+        const int nq = min(C::QT, static_cast<int>(q_tiles - t.q0 / 128));
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const int s = static_cast<int>(it % STAGES);
+          if (!mbar_wait(&empty[s], static_cast<uint32_t>(((it / STAGES) & 1) ^ 1), a.wait_limit_ns)) {
+            set_error(a.status, kErrTimeout);
+            ok = false;
+            break;
+          }
+          uint8_t* st = smem + s * C::STAGE;
+          uint8_t* sf = st + P_BYTES + C::Q_BYTES;
+          const int nw = min(C::W, words - kb * C::W);
+          const uint32_t sf_bytes = static_cast<uint32_t>(nw * kScaleTileBytes);
+          mbar_arrive_expect_tx(&full[s], P_BYTES + C::Q_BYTES + (1 + nq) * sf_bytes);
+          tma_load_2d(st, &tm_p, &full[s], kb * ROW_BYTES, t.p0);
+          tma_load_2d(st + P_BYTES, &tm_q, &full[s], kb * ROW_BYTES, q_row);
+          bulk_load(sf, p_sf + static_cast<int64_t>(kb) * C::SF_BYTES, sf_bytes, &full[s]);
+          for (int j = 0; j < nq; ++j)
+            bulk_load(sf + (1 + j) * C::SF_BYTES,
+                      q_sf + (static_cast<int64_t>(j) * words + kb * C::W) * kScaleTileBytes, sf_bytes, &full[s]);
+        }
+      }
+      // no copy may still be in flight into shared memory at exit
+      for (int64_t j = (it > STAGES ? it - STAGES : 0); j < it; ++j)
+        if (!mbar_wait(&full[j % STAGES], static_cast<uint32_t>((j / STAGES) & 1), a.wait_limit_ns))
+          set_error(a.status, kErrTimeout);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int64_t it = 0;
+      uint32_t tphase = 0;
+      bool ok = true;
+      for (int i = worker; ok && i < tiles.total; i += workers, tphase ^= 1u) {
+        if (!mbar_wait(tempty, tphase ^ 1u, a.wait_limit_ns)) {
+          set_error(a.status, kErrTimeout);
+          break;
+        }
+        tc_fence_after();
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const int s = static_cast<int>(it % STAGES);
+          if (!mbar_wait(&full[s], static_cast<uint32_t>((it / STAGES) & 1), a.wait_limit_ns)) {
+            set_error(a.status, kErrTimeout);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = smem_u32(smem + s * C::STAGE);
+          const uint32_t sf = st + P_BYTES + C::Q_BYTES;
+          const uint32_t sfp = tmem + C::SF0 + static_cast<uint32_t>(s) * C::SF_COLS;
+          const uint32_t sfq = sfp + 4 * C::W;
+          const int nw = min(C::W, words - kb * C::W);
+#pragma unroll
+          for (int w = 0; w < C::W; ++w)
+            if (w < nw) {
+              tc_copy_scales(sfp + 4 * w, scale_desc(sf + w * kScaleTileBytes));
+#pragma unroll
+              for (int j = 0; j < C::QT; ++j)
+                tc_copy_scales(sfq + 4 * (w * C::QT + j), scale_desc(sf + (1 + j) * C::SF_BYTES + w * kScaleTileBytes));
+            }
+          const uint64_t pd = sw128_desc(st), qd = sw128_desc(st + P_BYTES);
+          const int steps = min(4, (a.k - kb * BK + 63) / 64);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j < steps) {
+              const uint32_t acc = (kb != kb0 || j != 0) ? 1u : 0u;
+              if constexpr (FMT == kFp4Mx)
+                tc_mma_mx4(tmem, pd + 2 * j, qd + 2 * j, idesc_fp4(BP, BN, true, (j & 1) * 2), sfp + 4 * (j / 2),
+                           sfq + 4 * C::QT * (j / 2), acc);
+              else
+                tc_mma_nv4(tmem, pd + 2 * j, qd + 2 * j, idesc_fp4(BP, BN, false, 0), sfp + 4 * j,
+                           sfq + 4 * C::QT * j, acc);
+            }
+          tc_commit(&empty[s]);
+        }
+        if (!ok) break;
+        tc_commit(tfull);
+      }
+    }
+  } else {
+    const int q = warp & 3;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    uint32_t tphase = 0;
+    for (int i = worker; i < tiles.total; i += workers, tphase ^= 1u) {
+      const Tile t = tiles.at(i, a);
+      if (!mbar_wait(tfull, tphase, a.wait_limit_ns)) {
+        set_error(a.status, kErrTimeout);
+        break;
+      }
+      tc_fence_after();
+      if constexpr (SWAP) {
+        // partial sums into the ring (its loads and MMAs are done): [token][weight row]
+        float* part = reinterpret_cast<float*>(smem);
+#pragma unroll 1
+        for (int c0 = 0; c0 < BN; c0 += 16) {
+          uint32_t v[16];
+          tmem_load16(lanes + c0, v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) part[(c0 + j) * BP + q * 32 + lane] = __uint_as_float(v[j]);
+        }
+      } else {
+        const float alpha = FMT == kFp4Nv ? __ldg(a.a_tensor_scale) * __ldg(a.b_tensor_scale + t.e) : 1.f;
+        const int row = t.p0 + q * 32 + lane;
+#pragma unroll 1
+        for (int c0 = 0; c0 < BN; c0 += 32) {
+          if (t.q0 + c0 >= a.n) break;
+          uint32_t v[32];
+          tmem_load32(lanes + c0, v);
+          const int left = a.n - (t.q0 + c0);
+          const int64_t at = static_cast<int64_t>(row) * a.ld_out + t.q0 + c0;
+          if (row < a.m && a.out_f32) {
+            float* o = static_cast<float*>(a.out) + at;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 f = make_float4(alpha * __uint_as_float(v[4 * j]), alpha * __uint_as_float(v[4 * j + 1]),
+                                           alpha * __uint_as_float(v[4 * j + 2]), alpha * __uint_as_float(v[4 * j + 3]));
+              if (vec && 4 * j + 4 <= left) {
+                reinterpret_cast<float4*>(o)[j] = f;
+              } else {
+                if (4 * j < left) o[4 * j] = f.x;
+                if (4 * j + 1 < left) o[4 * j + 1] = f.y;
+                if (4 * j + 2 < left) o[4 * j + 2] = f.z;
+                if (4 * j + 3 < left) o[4 * j + 3] = f.w;
+              }
+            }
+          } else if (row < a.m) {
+            uint16_t* o = static_cast<uint16_t*>(a.out) + at;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t h[4];
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(alpha * __uint_as_float(v[8 * j + 2 * u]),
+                                                               alpha * __uint_as_float(v[8 * j + 2 * u + 1]));
+                h[u] = *reinterpret_cast<const uint32_t*>(&b);
+              }
+              if (vec && 8 * j + 8 <= left) {
+                reinterpret_cast<uint4*>(o)[j] = make_uint4(h[0], h[1], h[2], h[3]);
+              } else {
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                  if (8 * j + u < left) o[8 * j + u] = static_cast<uint16_t>(h[u / 2] >> (16 * (u & 1)));
+              }
+            }
+          }
+          __syncwarp();  // whole again for the next load
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty);
+      }
+    }
+  }
+
+  if constexpr (SWAP) {
+    __syncwarp();
+    cluster_sync();  // every rank's partial sums are in its shared memory
+    if (warp >= EPI_WARP0) {
+      const int r = (warp - EPI_WARP0) * 32 + lane;  // weight row of the tile
+      const int col = worker * BP + r;
+      const float alpha = FMT == kFp4Nv ? __ldg(a.a_tensor_scale) * __ldg(a.b_tensor_scale) : 1.f;
+      for (int t = rank; t < a.m; t += ksplit) {
+        const uint32_t at = smem_u32(reinterpret_cast<float*>(smem) + t * BP + r);
+        float v = 0.f;
+        for (int j = 0; j < ksplit; ++j) v += ld_shared_cluster_f32(mapa_shared(at, j));
+        if (col < a.n) {
+          const int64_t o = static_cast<int64_t>(t) * a.ld_out + col;
+          if (a.out_f32)
+            static_cast<float*>(a.out)[o] = alpha * v;
+          else
+            static_cast<uint16_t*>(a.out)[o] = __bfloat16_as_ushort(__float2bfloat16_rn(alpha * v));
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // no rank leaves while another reads its sums
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM);
+  }
+}
+
+bool map_codes(CUtensorMap* m, const uint8_t* codes, int64_t rows, int k, int box) {
+  return make_tmap(m, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, static_cast<uint64_t>(k / 2),
+                   static_cast<uint64_t>(rows), ROW_BYTES, static_cast<uint32_t>(box));
+}
+
+template <int FMT, int BN, bool SWAP>
+cudaError_t launch(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s) {
+  using C = Cfg<FMT, BN>;
+  auto kernel = fp4_matmul_kernel<FMT, BN, SWAP>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
+  if (e != cudaSuccess) return e;
+  CUtensorMap tp, tq;
+  const int64_t b_rows = static_cast<int64_t>(a.n) * a.n_groups;
+  if (!map_codes(&tp, SWAP ? a.b_codes : a.a_codes, SWAP ? b_rows : a.m, a.k, BP) ||
+      !map_codes(&tq, SWAP ? a.a_codes : a.b_codes, SWAP ? a.m : b_rows, a.k, BN))
+    return cudaErrorInvalidValue;
+  const int64_t elem = a.out_f32 ? 4 : 2;
+  const int vec = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && a.ld_out * elem % 16 == 0 ? 1 : 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = C::BYTES;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  int ksplit = 1;
+  if (SWAP) {
+    const int tiles = (a.n + BP - 1) / BP, stages = (a.k + BK - 1) / BK;
+    while (ksplit < 8 && 4 * ksplit <= stages && 2 * ksplit * tiles <= 3 * num_sms) ksplit *= 2;
+    cfg.gridDim = dim3(tiles * ksplit, 1, 1);
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ksplit;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  } else {
+    const int64_t tiles = static_cast<int64_t>((a.m + BP - 1) / BP) * ((a.n + BN - 1) / BN);
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles < num_sms ? tiles : num_sms), 1, 1);
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, tp, tq, a, ksplit, vec);
+}
+
+template <int FMT>
+cudaError_t launch_format(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s) {
+  if (a.tile_offsets == nullptr && a.m <= 128) {
+    if (a.m <= 16) return launch<FMT, 16, true>(a, num_sms, s);
+    if (a.m <= 32) return launch<FMT, 32, true>(a, num_sms, s);
+    if (a.m <= 64) return launch<FMT, 64, true>(a, num_sms, s);
+    return launch<FMT, 128, true>(a, num_sms, s);
+  }
+  // 128-column tiles while the 256-column ones would leave SMs without a tile
+  const int64_t wide = static_cast<int64_t>((a.m + BP - 1) / BP) * ((a.n + 255) / 256);
+  return wide < num_sms ? launch<FMT, 128, false>(a, num_sms, s) : launch<FMT, 256, false>(a, num_sms, s);
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_matmul(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s) {
+  return a.format == kFp4Mx ? launch_format<kFp4Mx>(a, num_sms, s) : launch_format<kFp4Nv>(a, num_sms, s);
+}
+
+}  // namespace cbmoe

@@ -322,4 +322,43 @@ int few_format(bool quantised, WeightFormat wf);  // the kernel's name of a weig
 cudaError_t few_tokens_prepare(int format, int* blocks_per_sm);
 cudaError_t launch_few_tokens(int format, const FewArgs& a, int grid, cudaStream_t s);
 
+// ------------------------------------------- 4-bit floats with block scales
+struct Fp4Args {
+  int32_t format;      // kFp4Mx, kFp4Nv (fp4.cuh)
+  int32_t f32;         // x is fp32 (else bf16)
+  void* x;             // [rows][cols], row stride ld elements: read, or written by the way back
+  int64_t rows, cols, ld;
+  const float* tensor_scale;
+  uint8_t* codes;
+  uint8_t* scales;
+};
+int64_t fp4_tiles(int64_t rows, int64_t cols);  // blocks of either launch
+cudaError_t launch_fp4_quantize(const Fp4Args& a, cudaStream_t s);
+cudaError_t launch_fp4_dequantize(const Fp4Args& a, cudaStream_t s);
+
+struct Fp4MatmulArgs {
+  int32_t format;
+  int32_t out_f32;
+  int32_t m, n, k;
+  const uint8_t* a_codes;
+  const uint8_t* a_scales;
+  const float* a_tensor_scale;
+  const uint8_t* b_codes;
+  const uint8_t* b_scales;
+  const float* b_tensor_scale;
+  int32_t n_groups;
+  const int32_t* tile_offsets;
+  void* out;
+  int64_t ld_out;
+  int32_t* status;
+  uint64_t wait_limit_ns;
+};
+cudaError_t launch_fp4_matmul(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s);
+
+// 2-D row-major tensor [outer][inner] with a box of box_outer x box_inner
+// elements, 128-byte swizzled (MMA operands) unless said otherwise.
+bool make_tmap(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t elem_bytes, uint64_t inner,
+               uint64_t outer, uint32_t box_inner, uint32_t box_outer,
+               CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
+
 }  // namespace cbmoe

@@ -352,6 +352,73 @@ __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, 
       : "memory");
 }
 
+// ------------------------------------------- block-scaled 4-bit operands
+// `bytes` consecutive bytes into shared memory (both addresses and the size
+// multiples of 16), signalled as transaction bytes on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// Descriptor of 32 rows of 16 bytes stored one after the other (8-row core
+// matrices 128 bytes apart, no swizzle): a 512-byte scale tile.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(128u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  return d;
+}
+
+// A scale tile from shared memory into 4 tensor-memory columns, row i of its
+// 32 in lane i of each of the four 32-lane quarters.  Runs in order with the
+// tcgen05.mma that this thread issues after it.
+__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Instruction descriptor of the block-scaled e2m1 kinds (K = 64, fp32 D, both
+// operands K-major): A and B format e2m1 (1) in bits 7-9 and 10-11, N >> 3 in
+// bits 17-22, the scales' type in bit 23 (0: e4m3, 1: a power of two),
+// M >> 4 in bits 24-28; sf_id, the byte pair (0 or 2) of each scale word that
+// the instruction takes, in bits 4-5 (B) and 29-30 (A).
+__host__ __device__ constexpr uint32_t idesc_fp4(int M, int N, bool e8m0, uint32_t sf_id) {
+  return (sf_id << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (e8m0 ? 1u << 23 : 0u) |
+         (static_cast<uint32_t>(M >> 4) << 24) | (sf_id << 29);
+}
+
+// D[tmem] (+)= (A s_a) (B s_b)^T over K = 64 e2m1 elements from shared
+// memory: MX, a power-of-two scale per 32 elements; NV, an e4m3 scale per 16.
+__device__ __forceinline__ void tc_mma_mx4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_nv4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
 // Named barrier `id` over `n` threads (whole warps).
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
