@@ -130,7 +130,8 @@ typedef enum { CB_ROUTER_SOFTMAX_TOPK = 0, CB_ROUTER_RAW_LOGITS = 1, CB_ROUTER_H
                                       routing tables keep their previous
                                       values (zeros after init), the output is
                                       garbage and cb_moe_last_error returns
-                                      CB_ERR_TIMEOUT                            */
+                                      CB_ERR_TIMEOUT.  The few-token forward's
+                                      grid barriers likewise                    */
 
 typedef struct {
   int32_t n_tokens;   /* T: tokens in every forward on this handle (>= 0)         */

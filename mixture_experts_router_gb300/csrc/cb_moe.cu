@@ -86,6 +86,7 @@ struct cb_moe {
   uint16_t* few_h;         // the few-token layer's H, logits and (hash router) experts
   float* few_logits;
   int32_t* few_ids;
+  FewMaps few_maps;
   int32_t few_grid;        // blocks of its cooperative launch
   bool fused_combine;      // the CTA-pair down GEMM adds its rows into the token sums
   const void* tm_x_src;    // x pointer tm_x was encoded for
@@ -237,6 +238,16 @@ bool cbmoe::make_tmap(CUtensorMap* m, const void* base, CUtensorMapDataType dt, 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool cbmoe::make_tmap_nd(CUtensorMap* m, const void* base, uint32_t rank, const cuuint64_t* dims,
+                         const cuuint64_t* strides, const cuuint32_t* box) {
+  auto enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 struct DeviceGuard {
@@ -266,6 +277,34 @@ HashRouterArgs hash_router_args(const cb_moe_t* h, const void* x, int32_t n, int
   ha.ids = ids;
   ha.w = w;
   return ha;
+}
+
+// The few-token layer's arguments but for the call's own.
+FewArgs few_args(const cb_moe_t* h) {
+  const cb_moe_config_t& c = h->cfg;
+  FewArgs a{};
+  a.d = c.d_model;
+  a.f = c.d_ff;
+  a.E = c.n_experts;
+  a.k = c.top_k;
+  a.wr = h->wr;
+  a.bias = h->bias;
+  a.raw_weights = c.router_mode == CB_ROUTER_RAW_LOGITS ? 1 : 0;
+  a.wgu = h->wgu;
+  a.wd = h->wd;
+  a.gu_block = h->gu_block;
+  a.sg = h->sg;
+  a.su = h->su;
+  a.sd = h->sd;
+  a.zg = h->zg;
+  a.zu = h->zu;
+  a.zd = h->zd;
+  a.logits = h->few_logits;
+  a.h = h->few_h;
+  a.bar = h->coop_bar + 4;  // words 0 and 1 are the dispatch's
+  a.err = h->err;
+  a.wait_limit_ns = kWaitLimitNs;
+  return a;
 }
 
 cb_status_t enqueue_forward(cb_moe_t* h, const void* x, void* out, bool f32out, cudaStream_t s) {
@@ -623,40 +662,23 @@ cb_status_t few_forward(cb_moe_t* h, const void* x, int32_t n, void* out, bool f
   const bool cap = capturing(s);
   if (!cap && !wait_last_forward(h, s)) return CB_ERR_CUDA;
   const cb_moe_config_t& c = h->cfg;
-  const bool quantised = c.wdtype != CB_W_BF16;
-  FewArgs a{};
+  FewArgs a = few_args(h);
   a.x = static_cast<const uint16_t*>(x);
   a.n = n;
-  a.d = c.d_model;
-  a.f = c.d_ff;
-  a.E = c.n_experts;
-  a.k = c.top_k;
-  a.wr = h->wr;
-  a.bias = h->bias;
-  a.raw_weights = c.router_mode == CB_ROUTER_RAW_LOGITS ? 1 : 0;
-  a.wgu = h->wgu;
-  a.wd = h->wd;
-  a.gu_block = h->gu_block;
-  a.sg = h->sg;
-  a.su = h->su;
-  a.sd = h->sd;
-  a.zg = h->zg;
-  a.zu = h->zu;
-  a.zd = h->zd;
-  a.logits = h->few_logits;
-  a.h = h->few_h;
   a.out = out;
   a.out_f32 = f32out ? 1 : 0;
-  a.bar = h->coop_bar + 4;  // words 0 and 1 are the dispatch's
-  a.err = h->err;
-  a.wait_limit_ns = kWaitLimitNs;
+  const int format = few_format(c.wdtype != CB_W_BF16, weight_format(c));
+  if (c.flags & CB_FLAG_TEST_STALL_DISPATCH) {
+    a.test_stall = 1;
+    a.wait_limit_ns = 1000000ull;  // 1 ms
+  }
   if (c.router_mode == CB_ROUTER_HASH) {
     a.ids = h->few_ids;
     const HashRouterArgs ha =
         hash_router_args(h, x, n, h->few_ids, reinterpret_cast<float*>(h->few_ids + kFewTokens));
     if (launch_router_hash(ha, s) != cudaSuccess) return CB_ERR_CUDA;
   }
-  if (launch_few_tokens(few_format(quantised, weight_format(c)), a, h->few_grid, s) != cudaSuccess) return CB_ERR_CUDA;
+  if (launch_few_tokens(format, h->few_maps, a, h->few_grid, s) != cudaSuccess) return CB_ERR_CUDA;
   if (!cap && !mark_last_forward(h, s)) return CB_ERR_CUDA;
   return CB_OK;
 }
@@ -864,6 +886,7 @@ cb_status_t cb_moe_init(const cb_moe_config_t* cfg, const cb_moe_weights_t* wts,
   int few_per_sm = 0;
   ok = ok && few_tokens_prepare(few_format(int8w, weight_format(*cfg)), &few_per_sm) == cudaSuccess;
   h->few_grid = std::min(few_per_sm, 1) * h->num_sms;
+  ok = ok && few_token_maps(few_format(int8w, weight_format(*cfg)), few_args(h), &h->few_maps);
   // router: tcgen05 for wide expert counts, the mma.sync split-K router for
   // E <= 16 (bound by reading x, where more CTAs help); CB_MOE_ROUTER=tc|mma
   // overrides the choice

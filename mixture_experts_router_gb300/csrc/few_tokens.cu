@@ -11,29 +11,38 @@
 //      -- grid barrier --
 //   4. down and combine   out[t][c] = sum_s w[t][s] (H[t k + s] . Wd[ids[t][s]][c]).
 //
-// What bounds it: the chosen experts' weights, read once from HBM; with at most 16
-// tokens an expert's 128-row tiles of the large kernels would be nearly all
-// padding, so nothing is staged in shared memory: a weight element goes
-// straight from global memory into the register fragment of an
-// mma.sync m16n8k16 (A: 16 weight rows, B: 8 tokens), in the manner of the
-// mma router.  A dot product does not depend on the order of its terms, so a
-// thread's k-slots are consecutive elements and every weight load is 16
-// bytes.  In step 3 the 16 rows are 8 gate rows and the same 8 features' up
-// rows, which puts a feature's g and u into one thread; in step 4 they are
-// 16 output columns.
+// What bounds it: the chosen experts' weights, read once from HBM; with at
+// most 16 tokens an expert's 128-row tiles of the large kernels would be
+// nearly all padding.  So a tile here is at most 32 weight rows (in step 3, 16
+// features' gate and up rows; in step 4, 32 output columns), streamed through
+// a ring of stages of 512 bytes per row, with the same stretch of the chosen
+// tokens' activations beside them.
+//
+//   warp 16     weights, one TMA copy per stage.  The tensor maps split a row
+//               into 128-byte chunks as a dimension of its own, so that one
+//               copy brings 512 bytes of every row of the tile; there is a
+//               map for each height.  A copy costs its SM about 55 ns and then
+//               2.2 ns per 128 bytes, so several small ones per stage would
+//               bound the kernel (a bulk copy per row held it at 2 TB/s).  It
+//               runs ahead across tiles, experts and the second barrier: step
+//               4's weights do not wait for H.
+//   warp 17     tokens, by cp.async into the stage, in the weights' swizzle.
+//   warps 0-15  two sets of 8 that take the stages in turn; a warp owns one
+//               64-byte step of a stage, reads fragments with 16-byte loads,
+//               widens quantised codes to bf16 exactly in registers and issues
+//               mma.sync m16n8k16 (A: weight rows, B: the expert's own tokens,
+//               in their order).  A dot product does not depend on the order
+//               of its terms, so a thread's k-slots are consecutive elements.
 //
 // The balance: the active experts' features (step 3) and the output columns
-// (step 4) are cut into one contiguous share per block, to the row; a share's
-// last tile loads only the rows that it has.  A block's 16 warps split the
-// rows' bytes in turns of 64, so that together they read 1 KB runs of each
-// row.  Each warp keeps kSlots steps (32 bytes a thread each: 128 KB per SM)
-// in flight, across tiles and experts; the first of step 4's are requested
-// before the barrier that ends step 3, since they do not depend on it.
+// (step 4) are cut into one contiguous share per block, in steps of 4 (the
+// rows of the smallest copy).
 //
-// Every sum is fp32 in a fixed order (mma accumulators, then the warps'
-// partial sums in warp order, experts in ascending order), so results do not
-// change from run to run.  H is rounded to bf16 as everywhere in the layer:
-// it is the MMA's operand.
+// Every sum is fp32 in a fixed order (mma accumulators, experts in ascending
+// order, then the 16 warps in order), so results do not change from run to
+// run.  H is rounded to bf16 as everywhere in the layer: it is the MMA's
+// operand.  Rows past the tile's end and columns past the expert's tokens
+// read the last one again, and their sums are dropped.
 #include <cuda_bf16.h>
 
 #include "grid_barrier.cuh"
@@ -46,523 +55,689 @@
 namespace cbmoe {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kSlots = 8;         // steps in flight per warp
-constexpr int kStepBytes = 64;    // bytes of a row per step: 4 threads x 16
+constexpr int kUsers = 512;             // threads that use the ring
+constexpr int kUserWarps = kUsers / 32;
+constexpr int kWeightWarp = kUserWarps;
+constexpr int kTokenWarp = kUserWarps + 1;
+constexpr int kThreads = kUsers + 64;
+constexpr int kRows = 32;               // weight rows of a tile: two m16 fragments
+constexpr int kAlong = 8;               // warps along a row's stretch
+constexpr int kStepBytes = 64;          // of a row per warp and stage: 4 threads x 16
+constexpr int kSeg = kAlong * kStepBytes;  // of a row per stage
+constexpr int kRowLines = kSeg / 128;
+constexpr int kWeightBytes = kRows * kSeg;
+constexpr int kShareStep = kFewRowStep; // shares and tiles are multiples of this many rows
 constexpr int kMaxTokens = kFewTokens;
 constexpr int kMaxExperts = 256;
 constexpr int kMaxK = 16;
+constexpr uint32_t kUserBar = 1;        // named barrier of the ring's users
+constexpr int kSmemLimit = 232448;
 
 // Weight formats of the kernel: the quantised ones as in WeightFormat.
 constexpr int kBf16 = 3;
 template <int WF>
 constexpr int kElems = WF == kBf16 ? 8 : WF == kWInt4 ? 32 : 16;  // elements per 16 bytes
 
-struct Smem {
-  float red[2][kWarps][16][kMaxTokens];  // partial sums: [buffer][warp][row][token]
-  float logit[kMaxTokens * kMaxExperts];
-  float w[kMaxTokens * kMaxK];           // gate weight of each (token, slot)
-  uint32_t mask[kMaxExperts];            // tokens of each expert
-  uint8_t slot[kMaxExperts][kMaxTokens]; // the slot at which a token chose it
-  int16_t act[kMaxExperts];              // active experts, ascending
+template <int NT>
+struct Shared {
+  union {
+    float red[kUserWarps][kRows][NT * 8]; // partial sums: [warp][row][token]
+    float logit[kMaxTokens * kMaxExperts];
+    float part[kUserWarps][kMaxTokens];   // the logits' partial sums
+  };
+  float w[kMaxTokens * kMaxK];            // gate weight of each (token, slot)
+  uint32_t mask[kMaxExperts];             // tokens of each expert
+  uint8_t slot[kMaxExperts][kMaxTokens];  // the slot at which a token chose it
+  uint8_t tok[kMaxExperts][kMaxTokens];   // the tokens of each active expert
+  uint8_t count[kMaxExperts];             // and their number
+  int16_t act[kMaxExperts];               // active experts, ascending
+  int16_t row0[kMaxExperts];              // an active expert's first row of H
   int n_act;
   int warp_act[kMaxExperts / 32];
   int ok;
 };
 
-__device__ __forceinline__ uint4 load_stream(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
+template <int WF, int NT>
+struct Geo {
+  static constexpr int kTokBytes = kSeg / 16 * kElems<WF> * 2;  // a token's stretch in a stage
+  static constexpr int kTokLines = kTokBytes / 128;
+  static constexpr int kStage = kWeightBytes + NT * 8 * kTokBytes;
+  static constexpr int kShared = (static_cast<int>(sizeof(Shared<NT>)) + 256 + 1023) / 1024 * 1024;
+  static constexpr int kFit = (kSmemLimit - kShared - 1024) / kStage;
+  static constexpr int kStages = kFit < 8 ? kFit : 8;
+  static constexpr int kBytes = 1024 + kShared + kStages * kStage;
+  static_assert(kStages >= 3 && 16 * kStages <= 256 && kStage % 1024 == 0, "ring");
+};
 
-// 16 bytes of a weight row -> its elements as bf16 pairs, in memory order.
+// Byte of 16-byte unit `unit` of 128-byte line `line` of a swizzled area.
+__device__ __forceinline__ int swizzled(int line, int unit) { return line * 128 + ((unit ^ (line & 7)) << 4); }
+
+// Elements 8 i .. 8 i + 7 of a thread's 16 bytes of a weight row as four bf16
+// pairs, in memory order.
 template <int WF>
-__device__ __forceinline__ void widen(const uint4& v, uint32_t zz, uint32_t (&o)[kElems<WF> / 2]) {
+__device__ __forceinline__ void widen8(const uint4& v, int i, uint32_t zz, uint32_t (&o)[4]) {
   const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (WF == kBf16) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (WF == kBf16) {
-      o[i] = in[i];
-    } else if constexpr (WF == kWInt4) {
-      uint32_t t[4];
-      int4x8_minus_zero_to_bf16(in[i], zz, t);
+    for (int j = 0; j < 4; ++j) o[j] = in[j];
+  } else if constexpr (WF == kWInt4) {
+    int4x8_minus_zero_to_bf16(in[i], zz, o);
+  } else {
 #pragma unroll
-      for (int m = 0; m < 4; ++m) o[4 * i + m] = t[m];
-    } else if constexpr (WF == kWFp8) {
-      fp8x4_to_bf16x4(in[i], o[2 * i], o[2 * i + 1]);
-    } else {
-      int8x4_to_bf16x4(in[i], o[2 * i], o[2 * i + 1]);
+    for (int j = 0; j < 2; ++j) {
+      if constexpr (WF == kWFp8)
+        fp8x4_to_bf16x4(in[2 * i + j], o[2 * j], o[2 * j + 1]);
+      else
+        int8x4_to_bf16x4(in[2 * i + j], o[2 * j], o[2 * j + 1]);
     }
   }
 }
 
-// acc += the two rows' elements times NT x 8 tokens' elements.  act[n]: this
-// lane's token row (column lane / 4 of n-tile n) at the step's first element,
-// or nullptr (reads as zero).
-template <int WF, int NT>
-__device__ __forceinline__ void step_mma(const uint4& lo, const uint4& hi, uint32_t zlo, uint32_t zhi,
-                                         const uint16_t* const (&act)[NT], float (&acc)[NT][4]) {
-  constexpr int P = kElems<WF> / 2;  // pairs per thread and row
-  uint4 b[NT][P / 4];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < P / 4; ++i)
-      b[n][i] = act[n] != nullptr ? reinterpret_cast<const uint4*>(act[n])[i] : make_uint4(0, 0, 0, 0);
-  uint32_t a0[P], a1[P];
-  widen<WF>(lo, zlo, a0);
-  widen<WF>(hi, zhi, a1);
-#pragma unroll
-  for (int i = 0; i < P / 4; ++i)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      router_detail::mma_bf16(acc[n], a0[4 * i], a1[4 * i], a0[4 * i + 1], a1[4 * i + 1], b[n][i].x, b[n][i].y);
-      router_detail::mma_bf16(acc[n], a0[4 * i + 2], a1[4 * i + 2], a0[4 * i + 3], a1[4 * i + 3], b[n][i].z, b[n][i].w);
+// A stretch of the ring's stages, one after the other.
+template <int STAGES>
+struct RingPos {
+  int stage = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++stage == STAGES) {
+      stage = 0;
+      phase ^= 1u;
     }
-}
+  }
+};
 
-// ------------------------------------------------------------- 1. logits
-__device__ __forceinline__ void few_logits(const FewArgs& p, Smem& s) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  for (int e = blockIdx.x; e < p.E; e += gridDim.x) {
-    float sum[kMaxTokens];
+template <int WF, int NT>
+struct Block {
+  using G = Geo<WF, NT>;
+  const FewArgs& p;
+  const FewMaps& maps;
+  Shared<NT>& s;
+  uint64_t* full;
+  uint64_t* empty;
+  uint8_t* ring;
+  RingPos<G::kStages> pos;  // the producer's, or a user's, place in the ring
+  bool ok = true;           // no wait of this thread has run out
+  int turn = 0;             // set of warps that takes the next stage
+  const int warp, lane;
+
+  __device__ __forceinline__ Block(const FewArgs& p_, const FewMaps& maps_, uint8_t* smem)
+      : p(p_),
+        maps(maps_),
+        s(*reinterpret_cast<Shared<NT>*>(smem)),
+        full(reinterpret_cast<uint64_t*>(smem + G::kShared - 256)),
+        empty(full + G::kStages),
+        ring(smem + G::kShared),
+        warp(threadIdx.x / 32),
+        lane(threadIdx.x % 32) {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < G::kStages; ++i) {
+        mbar_init(&full[i], 1 + 32);  // the weights' announcement, the token warp's lanes
+        mbar_init(&empty[i], kAlong);
+      }
+      fence_barrier_init();
+    }
+  }
+  __device__ __forceinline__ bool user() const { return warp < kUserWarps; }
+
+  // A wait that ran out is recorded once; the thread then runs through without
+  // waiting (the results are garbage), so that no barrier is left short, and
+  // a producer copies nothing more.
+  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
+    if (ok && !mbar_wait(bar, parity, p.wait_limit_ns)) {
+      set_error(p.err, kErrTimeout);
+      ok = false;
+    }
+  }
+
+  // ------------------------------------------------------------- 1. logits
+  __device__ __forceinline__ void logits() {
+    for (int e = blockIdx.x; e < p.E; e += gridDim.x) {
+      if (user()) {
+        float sum[kMaxTokens];
 #pragma unroll
-    for (int t = 0; t < kMaxTokens; ++t) sum[t] = 0.f;
-    for (int c = threadIdx.x * 8; c < p.d; c += kThreads * 8) {
-      const uint4 wv = __ldg(reinterpret_cast<const uint4*>(p.wr + static_cast<int64_t>(e) * p.d + c));
-      const uint32_t wu[4] = {wv.x, wv.y, wv.z, wv.w};
+        for (int t = 0; t < kMaxTokens; ++t) sum[t] = 0.f;
+        for (int c = threadIdx.x * 8; c < p.d; c += kUsers * 8) {
+          const uint4 wv = __ldg(reinterpret_cast<const uint4*>(p.wr + static_cast<int64_t>(e) * p.d + c));
+          const uint32_t wu[4] = {wv.x, wv.y, wv.z, wv.w};
 #pragma unroll
-      for (int t = 0; t < kMaxTokens; ++t) {
-        if (t >= p.n) break;
-        const uint4 xv = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.d + c));
-        const uint32_t xu[4] = {xv.x, xv.y, xv.z, xv.w};
+          for (int t = 0; t < kMaxTokens; ++t) {
+            if (t >= p.n) break;
+            const uint4 xv = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.d + c));
+            const uint32_t xu[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sum[t] = fmaf(__uint_as_float(xu[i] << 16), __uint_as_float(wu[i] << 16), sum[t]);
-          sum[t] = fmaf(__uint_as_float(xu[i] & 0xFFFF0000u), __uint_as_float(wu[i] & 0xFFFF0000u), sum[t]);
+            for (int i = 0; i < 4; ++i) {
+              sum[t] = fmaf(__uint_as_float(xu[i] << 16), __uint_as_float(wu[i] << 16), sum[t]);
+              sum[t] = fmaf(__uint_as_float(xu[i] & 0xFFFF0000u), __uint_as_float(wu[i] & 0xFFFF0000u), sum[t]);
+            }
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < kMaxTokens; ++t) {
+          if (t >= p.n) break;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) sum[t] += __shfl_xor_sync(0xffffffffu, sum[t], o);
+          if (lane == 0) s.part[warp][t] = sum[t];
         }
       }
+      __syncthreads();
+      if (threadIdx.x < p.n) {
+        float v = 0.f;
+        for (int i = 0; i < kUserWarps; ++i) v += s.part[i][threadIdx.x];
+        p.logits[threadIdx.x * p.E + e] = v + (p.bias != nullptr ? p.bias[e] : 0.f);
+      }
+      __syncthreads();
     }
-#pragma unroll
-    for (int t = 0; t < kMaxTokens; ++t) {
-      if (t >= p.n) break;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum[t] += __shfl_xor_sync(0xffffffffu, sum[t], o);
-      if (lane == 0) s.red[0][warp][0][t] = sum[t];
-    }
-    __syncthreads();
-    if (threadIdx.x < p.n) {
-      float v = 0.f;
-      for (int i = 0; i < kWarps; ++i) v += s.red[0][i][0][threadIdx.x];
-      p.logits[threadIdx.x * p.E + e] = v + (p.bias != nullptr ? p.bias[e] : 0.f);
-    }
-    __syncthreads();
   }
-}
 
-// --------------------------------------------------------------- 2. gate
-__device__ __forceinline__ void few_gate(const FewArgs& p, Smem& s) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  for (int e = threadIdx.x; e < kMaxExperts; e += kThreads) s.mask[e] = 0u;
-  if (p.ids == nullptr)
-    for (int i = threadIdx.x; i < p.n * p.E; i += kThreads) s.logit[i] = __ldcg(p.logits + i);
-  __syncthreads();
-  if (p.ids == nullptr) {
-    if (warp < p.n) {
-      int id;
-      float w;
-      const float* ls = s.logit + warp * p.E;
-      if (p.E <= 32)
-        router_detail::warp_gate<1>(ls, p.E, p.k, p.raw_weights, id, w);
-      else if (p.E <= 128)
-        router_detail::warp_gate<4>(ls, p.E, p.k, p.raw_weights, id, w);
-      else
-        router_detail::warp_gate<8>(ls, p.E, p.k, p.raw_weights, id, w);
-      if (lane < p.k) {
-        s.w[warp * p.k + lane] = w;
-        s.slot[id][warp] = static_cast<uint8_t>(lane);
-        atomicOr(&s.mask[id], 1u << warp);
+  // --------------------------------------------------------------- 2. gate
+  __device__ __forceinline__ void gate() {
+    for (int e = threadIdx.x; e < kMaxExperts; e += kThreads) s.mask[e] = 0u;
+    if (p.ids == nullptr)
+      for (int i = threadIdx.x; i < p.n * p.E; i += kThreads) s.logit[i] = __ldcg(p.logits + i);
+    __syncthreads();
+    if (p.ids == nullptr) {
+      if (warp < p.n) {
+        int id;
+        float w;
+        const float* ls = s.logit + warp * p.E;
+        if (p.E <= 32)
+          router_detail::warp_gate<1>(ls, p.E, p.k, p.raw_weights, id, w);
+        else if (p.E <= 128)
+          router_detail::warp_gate<4>(ls, p.E, p.k, p.raw_weights, id, w);
+        else
+          router_detail::warp_gate<8>(ls, p.E, p.k, p.raw_weights, id, w);
+        if (lane < p.k) {
+          s.w[warp * p.k + lane] = w;
+          s.slot[id][warp] = static_cast<uint8_t>(lane);
+          atomicOr(&s.mask[id], 1u << warp);
+        }
+      }
+    } else if (threadIdx.x < p.n) {  // the hash router's experts: one per token, weight 1
+      const int id = p.ids[threadIdx.x];
+      s.w[threadIdx.x] = 1.f;
+      s.slot[id][threadIdx.x] = 0;
+      atomicOr(&s.mask[id], 1u << threadIdx.x);
+    }
+    __syncthreads();
+    const int e = threadIdx.x;
+    const bool on = e < p.E && s.mask[e] != 0u;
+    const uint32_t ballot = __ballot_sync(0xffffffffu, on);
+    if (e < kMaxExperts && lane == 0) s.warp_act[warp] = __popc(ballot);
+    __syncthreads();
+    if (e < kMaxExperts) {
+      int base = 0;
+      for (int i = 0; i < warp; ++i) base += s.warp_act[i];
+      if (on) s.act[base + __popc(ballot & ((1u << lane) - 1u))] = static_cast<int16_t>(e);
+      if (e == kMaxExperts - 1) s.n_act = base + __popc(ballot);
+    }
+    __syncthreads();
+    if (warp == 0) {  // rows of H: an expert's tokens one after the other
+      int base = 0;
+      for (int a0 = 0; a0 < s.n_act; a0 += 32) {
+        const int a = a0 + lane;
+        uint32_t m = a < s.n_act ? s.mask[s.act[a]] : 0u;
+        const int c = __popc(m);
+        int sum = c;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          const int below = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += below;
+        }
+        if (a < s.n_act) {
+          s.row0[a] = static_cast<int16_t>(base + sum - c);
+          s.count[a] = static_cast<uint8_t>(c);
+          for (int i = 0; m != 0u; m &= m - 1u, ++i) s.tok[a][i] = static_cast<uint8_t>(__ffs(m) - 1);
+        }
+        base += __shfl_sync(0xffffffffu, sum, 31);
       }
     }
-  } else if (threadIdx.x < p.n) {  // the hash router's experts: one per token, weight 1
-    const int id = p.ids[threadIdx.x];
-    s.w[threadIdx.x] = 1.f;
-    s.slot[id][threadIdx.x] = 0;
-    atomicOr(&s.mask[id], 1u << threadIdx.x);
+    __syncthreads();
   }
-  __syncthreads();
-  const int e = threadIdx.x;
-  const bool on = e < p.E && s.mask[e] != 0u;
-  const uint32_t ballot = __ballot_sync(0xffffffffu, on);
-  if (e < kMaxExperts && lane == 0) s.warp_act[warp] = __popc(ballot);
-  __syncthreads();
-  if (e < kMaxExperts) {
-    int base = 0;
-    for (int i = 0; i < warp; ++i) base += s.warp_act[i];
-    if (on) s.act[base + __popc(ballot & ((1u << lane) - 1u))] = static_cast<int16_t>(e);
-    if (e == kMaxExperts - 1) s.n_act = base + __popc(ballot);
-  }
-  __syncthreads();
-}
 
-// --------------------------------------------------------- 3. gate and up
-// A share's features are cut into tiles of at most 8 of one expert.  A cursor
-// walks (tile, step); the loads' runs kSlots steps ahead of the sums'.
-struct UpCursor {
-  int j, end;    // first feature of the tile and the share's end, in act index x f + feature
-  int step, steps;
-  int a, feat, rows;  // active expert, feature within it, rows of the tile
-  __device__ __forceinline__ void open(int f) {
-    if (j < end) {
-      a = j / f;
-      feat = j - a * f;
-      rows = min(8, min(end - j, f - feat));
-    } else {
-      rows = 0;
-    }
-  }
-  __device__ __forceinline__ bool next(int f) {  // true: a new tile
-    if (++step < steps) return false;
-    step = 0;
-    j += rows;
-    open(f);
+  // ---------------------------------------------------- the second barrier
+  // The users' arrival (their H is written) and their wait; the token warp
+  // only waits, and the weight warp runs past.
+  __device__ __forceinline__ bool poll(unsigned expected) {
+    const uint64_t start = globaltimer_ns();
+    for (int i = 0; ld_acquire_gpu_u32(p.bar + 2) < expected; ++i)
+      if ((i & 63) == 63 && globaltimer_ns() - start > p.wait_limit_ns) {
+        set_error(p.err, kErrTimeout);
+        return false;
+      }
     return true;
   }
-};
+  __device__ __forceinline__ bool users_meet(unsigned expected) {
+    named_bar_sync(kUserBar, kUsers);
+    if (threadIdx.x == 0) {
+      __threadfence();
+      atomicAdd(p.bar + 2, 1u);
+      s.ok = poll(expected) ? 1 : 0;
+      __threadfence();
+    }
+    named_bar_sync(kUserBar, kUsers);
+    return s.ok != 0;
+  }
 
-template <int WF, int NT>
-__device__ __forceinline__ void few_gateup(const FewArgs& p, Smem& s, int64_t row_bytes) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane >> 2, q = lane & 3;
-  const int64_t total = static_cast<int64_t>(s.n_act) * p.f;
-  const int row_steps = static_cast<int>(row_bytes / kStepBytes);
-  UpCursor ld{};
-  ld.j = static_cast<int>(total * blockIdx.x / gridDim.x);
-  ld.end = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
-  ld.steps = (row_steps + kWarps - 1) / kWarps;
-  ld.open(p.f);
-  UpCursor use = ld;
-  const uint8_t* gate_ptr = nullptr;  // this thread's gate row of the loads' tile, at its warp's first step
-  const uint8_t* up_ptr = nullptr;
-  auto locate = [&]() {
-    gate_ptr = up_ptr = nullptr;
-    if (g < ld.rows) {
-      const int feat = ld.feat + g;
-      const int64_t row = static_cast<int64_t>(s.act[ld.a]) * 2 * p.f + (feat / p.gu_block) * 2 * p.gu_block +
-                          feat % p.gu_block;
-      gate_ptr = static_cast<const uint8_t*>(p.wgu) + row * row_bytes + warp * kStepBytes + q * 16;
-      up_ptr = gate_ptr + p.gu_block * row_bytes;
-    }
-  };
-  locate();
-  uint4 lo[kSlots], hi[kSlots];
-  auto load = [&](uint4& l, uint4& h) {
-    l = h = make_uint4(0, 0, 0, 0);
-    if (gate_ptr != nullptr && ld.step * kWarps + warp < row_steps) {
-      const int64_t at = static_cast<int64_t>(ld.step) * kWarps * kStepBytes;
-      l = load_stream(gate_ptr + at);
-      h = load_stream(up_ptr + at);
-    }
-    if (ld.next(p.f)) locate();
-  };
+  // ------------------------------------------------------------- the ring
+  __device__ __forceinline__ uint8_t* stage() const { return ring + pos.stage * G::kStage; }
+
+  // Weight warp, one thread: wait for the stage, announce its bytes.  False:
+  // nothing may be copied.
+  __device__ __forceinline__ bool open_stage(int rows) {
+    wait(&empty[pos.stage], pos.phase ^ 1u);
+    if (ok) mbar_arrive_expect_tx(&full[pos.stage], static_cast<uint32_t>(rows * kSeg));
+    return ok;
+  }
+
+  // Token warp: the `seg` bytes of weights from byte `at` of a row, as bytes
+  // of the count tokens' rows; row(i) is the i-th one.
+  template <typename F>
+  __device__ __forceinline__ void feed_tokens(int at, int seg, int count, F&& row) {
+    wait(&empty[pos.stage], pos.phase ^ 1u);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return;
+    const int bytes = seg / 16 * kElems<WF> * 2;
+    uint8_t* dst = stage() + kWeightBytes;
+    for (int i = 0; i < count; ++i) {
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(row(i)) + static_cast<int64_t>(at) / 16 * kElems<WF> * 2;
 #pragma unroll
-  for (int i = 0; i < kSlots; ++i) load(lo[i], hi[i]);
+      for (int u = lane; u < G::kTokBytes / 16; u += 32)
+        if (u * 16 < bytes) cp_async_16(dst + swizzled(i * G::kTokLines + u / 8, u % 8), src + u * 16);
+    }
+    cp_async_arrive(&full[pos.stage]);
+    pos.next();
+  }
 
-  float acc[NT][4];
-  const uint16_t* act[NT];
-  uint32_t zlo = 0, zhi = 0;
-  auto begin = [&]() {  // of a tile's sums
+  // Where a user's fragments stand in a stage: rows lo and hi of both m16
+  // halves, and the tokens of its columns.
+  struct Places {
+    int w[4];
+    int tok[NT][kElems<WF> / 8];
+  };
+  __device__ __forceinline__ void place_rows(Places& at, const int (&row)[4]) const {
+    const int q = lane & 3, along = warp % kAlong;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) at.w[i] = swizzled(row[i] * kRowLines + along / 2, along % 2 * 4 + q);
+  }
+  __device__ __forceinline__ void place_tokens(Places& at, int count) const {
+    const int g = lane >> 2, q = lane & 3, along = warp % kAlong;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-      act[n] = nullptr;
-    }
-    if (use.rows == 0) return;
-    const int e = s.act[use.a];
+      const int row = min(n * 8 + g, count - 1);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-      if ((s.mask[e] >> (n * 8 + g)) & 1u)
-        act[n] = p.x + static_cast<int64_t>(n * 8 + g) * p.d + (warp * 4 + q) * kElems<WF>;
-    if constexpr (WF == kWInt4) {
-      const int64_t at = static_cast<int64_t>(e) * p.f + use.feat + min(g, use.rows - 1);
-      zlo = (0x4300u | __ldg(p.zg + at)) * 0x00010001u;
-      zhi = (0x4300u | __ldg(p.zu + at)) * 0x00010001u;
-    }
-  };
-  begin();
-  int buf = 0;
-  while (use.rows > 0) {
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i) {
-      if (use.rows > 0) {
-        const uint16_t* at[NT];
-        const bool in = use.step * kWarps + warp < row_steps;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          at[n] = in && act[n] != nullptr ? act[n] + use.step * kWarps * 4 * kElems<WF> : nullptr;
-        step_mma<WF, NT>(lo[i], hi[i], zlo, zhi, at, acc);
-        load(lo[i], hi[i]);
-        const UpCursor done = use;
-        if (use.next(p.f)) {  // the tile's sums are complete in the 16 warps
-          auto* red = s.red[buf][warp];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            *reinterpret_cast<float2*>(&red[g][n * 8 + 2 * q]) = make_float2(acc[n][0], acc[n][1]);
-            *reinterpret_cast<float2*>(&red[g + 8][n * 8 + 2 * q]) = make_float2(acc[n][2], acc[n][3]);
-          }
-          __syncthreads();
-          const int r = threadIdx.x % 8, t = threadIdx.x / 8;
-          const int e = s.act[done.a];
-          if (t < NT * 8 && r < done.rows && ((s.mask[e] >> t) & 1u)) {
-            float gs = 0.f, us = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-              gs += s.red[buf][w][r][t];
-              us += s.red[buf][w][r + 8][t];
-            }
-            if constexpr (WF != kBf16) {
-              const int64_t at2 = static_cast<int64_t>(e) * p.f + done.feat + r;
-              gs *= __ldg(p.sg + at2);
-              us *= __ldg(p.su + at2);
-            }
-            const __nv_bfloat16 h = __float2bfloat16_rn(silu(gs) * us);
-            p.h[(static_cast<int64_t>(t) * p.k + s.slot[e][t]) * p.f + done.feat + r] = __bfloat16_as_ushort(h);
-          }
-          buf ^= 1;  // the other buffer's readers passed this barrier
-          begin();
-        }
+      for (int i = 0; i < kElems<WF> / 8; ++i) {
+        const int unit = (along * 4 + q) * (kElems<WF> / 8) + i;
+        at.tok[n][i] = kWeightBytes + swizzled(row * G::kTokLines + unit / 8, unit % 8);
       }
     }
   }
-}
 
-// ------------------------------------------------- 4. down and combine
-struct DownCursor {
-  int c, end;  // first output column of the tile, the share's end
-  int a, n_act;
-  int step, steps;
-  __device__ __forceinline__ int rows() const { return min(16, end - c); }
-  // 0: another step; 1: another expert; 2: another tile
-  __device__ __forceinline__ int next() {
-    if (++step < steps) return 0;
-    step = 0;
-    if (++a < n_act) return 1;
-    a = 0;
-    c += 16;
-    return 2;
-  }
-};
-
-template <int WF, int NT>
-struct Down {
-  const FewArgs& p;
-  Smem& s;
-  int64_t row_bytes;
-  int row_steps;
-  DownCursor ld, use;
-  const uint8_t* ptr;  // this thread's row g of the loads' tile and expert; row g + 8 is 8 rows on
-  bool v0, v1;
-  uint4 lo[kSlots], hi[kSlots];
-
-  __device__ __forceinline__ Down(const FewArgs& p_, Smem& s_, int64_t rb) : p(p_), s(s_), row_bytes(rb) {
-    row_steps = static_cast<int>(row_bytes / kStepBytes);
-    ld.c = static_cast<int>(static_cast<int64_t>(p.d) * blockIdx.x / gridDim.x);
-    ld.end = static_cast<int>(static_cast<int64_t>(p.d) * (blockIdx.x + 1) / gridDim.x);
-    ld.a = 0;
-    ld.n_act = s.n_act;
-    ld.step = 0;
-    ld.steps = (row_steps + kWarps - 1) / kWarps;
-    use = ld;
-    locate();
-  }
-  __device__ __forceinline__ void locate() {
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane >> 2, q = lane & 3;
-    v0 = g < ld.rows();
-    v1 = g + 8 < ld.rows();
-    const int64_t row = static_cast<int64_t>(s.act[ld.a]) * p.d + ld.c + g;
-    ptr = static_cast<const uint8_t*>(p.wd) + row * row_bytes + warp * kStepBytes + q * 16;
-  }
-  __device__ __forceinline__ void load(uint4& l, uint4& h) {
-    const int warp = threadIdx.x / 32;
-    l = h = make_uint4(0, 0, 0, 0);
-    if (ld.step * kWarps + warp < row_steps) {
-      const uint8_t* at = ptr + static_cast<int64_t>(ld.step) * kWarps * kStepBytes;
-      if (v0) l = load_stream(at);
-      if (v1) h = load_stream(at + 8 * row_bytes);
-    }
-    if (ld.next() != 0) locate();
-  }
-  __device__ __forceinline__ void prologue() {
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i) load(lo[i], hi[i]);
-  }
-  __device__ __forceinline__ void run() {
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane >> 2, q = lane & 3;
-    float acc[NT][4], tot[NT][4];
-    const uint16_t* act[NT];
-    uint32_t zlo = 0, zhi = 0;
-    auto clear = [&](float (&v)[NT][4]) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) v[n][0] = v[n][1] = v[n][2] = v[n][3] = 0.f;
-    };
-    auto begin = [&]() {  // of an expert's sums
-      clear(acc);
-      const int e = s.act[use.a];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int t = n * 8 + g;
-        act[n] = (s.mask[e] >> t) & 1u
-                     ? p.h + (static_cast<int64_t>(t) * p.k + s.slot[e][t]) * p.f + (warp * 4 + q) * kElems<WF>
-                     : nullptr;
+  // User: the tile's stages in order; the warp's set takes every second one.
+  // acc += its fragments of those, over the first `halves` m16 halves and
+  // n-tiles `tiles`.  True: it took one.
+  __device__ __forceinline__ bool use_stages(int row_bytes, int halves, int tiles, const Places& at,
+                                             const uint32_t (&zz)[4], float (&acc)[2][NT][4]) {
+    bool took = false;
+    for (int b = 0; b < row_bytes; b += kSeg, turn ^= 1) {
+      if (turn != warp / kAlong) {
+        pos.next();
+        continue;
       }
-      if constexpr (WF == kWInt4) {
-        const int64_t at = static_cast<int64_t>(e) * p.d;
-        zlo = (0x4300u | __ldg(p.zd + at + min(use.c + g, p.d - 1))) * 0x00010001u;
-        zhi = (0x4300u | __ldg(p.zd + at + min(use.c + g + 8, p.d - 1))) * 0x00010001u;
-      }
-    };
-    clear(tot);
-    int buf = 0;
-    if (use.rows() > 0) begin();
-    while (use.rows() > 0) {
+      wait(&full[pos.stage], pos.phase);
+      if (warp % kAlong * kStepBytes < row_bytes - b) {
+        took = true;
+        const uint8_t* st = stage();
+        uint4 v[4];
 #pragma unroll
-      for (int i = 0; i < kSlots; ++i) {
-        if (use.rows() > 0) {
-          const uint16_t* at[NT];
-          const bool in = use.step * kWarps + warp < row_steps;
+        for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(st + at.w[i]);
+#pragma unroll
+        for (int i = 0; i < kElems<WF> / 8; ++i) {
+          uint4 t[NT];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            at[n] = in && act[n] != nullptr ? act[n] + use.step * kWarps * 4 * kElems<WF> : nullptr;
-          step_mma<WF, NT>(lo[i], hi[i], zlo, zhi, at, acc);
-          load(lo[i], hi[i]);
-          const DownCursor done = use;
-          const int moved = use.next();
-          if (moved != 0) {  // this warp's part of the expert is complete: weigh it
-            const int e = s.act[done.a];
-            float sc0 = 1.f, sc1 = 1.f;
-            if constexpr (WF != kBf16) {
-              const int64_t row = static_cast<int64_t>(e) * p.d;
-              sc0 = __ldg(p.sd + row + min(done.c + g, p.d - 1));
-              sc1 = __ldg(p.sd + row + min(done.c + g + 8, p.d - 1));
+            if (n == 0 || n < tiles) t[n] = *reinterpret_cast<const uint4*>(st + at.tok[n][i]);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            if (m == 1 && halves < 2) break;
+            uint32_t a0[4], a1[4];
+            widen8<WF>(v[2 * m], i, zz[2 * m], a0);
+            widen8<WF>(v[2 * m + 1], i, zz[2 * m + 1], a1);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              if (n > 0 && n >= tiles) break;
+              router_detail::mma_bf16(acc[m][n], a0[0], a1[0], a0[1], a1[1], t[n].x, t[n].y);
+              router_detail::mma_bf16(acc[m][n], a0[2], a1[2], a0[3], a1[3], t[n].z, t[n].w);
             }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int t = n * 8 + 2 * q + u;
-                if ((s.mask[e] >> t) & 1u) {  // a token that did not choose e takes nothing from it
-                  const float w = s.w[t * p.k + s.slot[e][t]];
-                  tot[n][u] = fmaf(w * sc0, acc[n][u], tot[n][u]);
-                  tot[n][2 + u] = fmaf(w * sc1, acc[n][2 + u], tot[n][2 + u]);
-                }
-              }
-            if (moved == 2) {
-              auto* red = s.red[buf][warp];
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                *reinterpret_cast<float2*>(&red[g][n * 8 + 2 * q]) = make_float2(tot[n][0], tot[n][1]);
-                *reinterpret_cast<float2*>(&red[g + 8][n * 8 + 2 * q]) = make_float2(tot[n][2], tot[n][3]);
-              }
-              clear(tot);
-              __syncthreads();
-              const int r = threadIdx.x % 16, t = threadIdx.x / 16;
-              if (t < p.n && r < done.rows()) {
-                float v = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) v += s.red[buf][w][r][t];
-                const int64_t o = static_cast<int64_t>(t) * p.d + done.c + r;
-                if (p.out_f32)
-                  static_cast<float*>(p.out)[o] = v;
-                else
-                  static_cast<uint16_t*>(p.out)[o] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-              }
-              buf ^= 1;
-            }
-            if (use.rows() > 0) begin();
           }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[pos.stage]);
+      pos.next();
     }
+    return took;
+  }
+  __device__ __forceinline__ void clear(float (&v)[2][NT][4]) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) v[m][n][0] = v[m][n][1] = v[m][n][2] = v[m][n][3] = 0.f;
+  }
+
+  // --------------------------------------------------------- 3. gate and up
+  // Calls f(active expert, first feature, features) for each tile of the
+  // block's share: at most 16 features of one interleave block of one expert.
+  template <typename F>
+  __device__ __forceinline__ void up_tiles(F&& f) {
+    const int64_t total = static_cast<int64_t>(s.n_act) * p.f / kShareStep;
+    int j = static_cast<int>(total * blockIdx.x / gridDim.x) * kShareStep;
+    const int end = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x) * kShareStep;
+    int a = j / p.f, feat = j - a * p.f;
+    while (j < end) {
+      const int rows = min(16, min(end - j, p.gu_block - feat % p.gu_block));
+      f(a, feat, rows);
+      j += rows;
+      feat += rows;
+      if (feat == p.f) {
+        feat = 0;
+        ++a;
+      }
+    }
+  }
+
+  __device__ __forceinline__ void feed_gateup(int row_bytes) {
+    up_tiles([&](int a, int feat, int rows) {
+      const int blk = s.act[a] * (p.f / p.gu_block) + feat / p.gu_block;
+      const CUtensorMap* map = &maps.gate_up[rows / kShareStep - 1];
+      for (int at = 0; at < row_bytes && open_stage(2 * rows); at += kSeg, pos.next())
+        tma_load_5d(stage(), map, &full[pos.stage], 0, at / 128, feat % p.gu_block, 0, blk);
+    });
+  }
+  __device__ __forceinline__ void feed_x(int row_bytes) {
+    up_tiles([&](int a, int, int) {
+      for (int at = 0; at < row_bytes && ok; at += kSeg)
+        feed_tokens(at, min(kSeg, row_bytes - at), s.count[a],
+                    [&](int i) { return p.x + static_cast<int64_t>(s.tok[a][i]) * p.d; });
+    });
+  }
+
+  __device__ __forceinline__ void gateup(int row_bytes) {
+    const int g = lane >> 2, q = lane & 3;
+    up_tiles([&](int a, int feat0, int rows) {
+      const int e = s.act[a], count = s.count[a];
+      const int f0 = min(g, rows - 1), f1 = min(8 + g, rows - 1);  // gate rows; up rows stand `rows` further
+      Places at;
+      place_rows(at, {f0, rows + f0, f1, rows + f1});
+      place_tokens(at, count);
+      uint32_t zz[4] = {0, 0, 0, 0};
+      if constexpr (WF == kWInt4) {
+        const int64_t z = static_cast<int64_t>(e) * p.f + feat0;
+        zz[0] = (0x4300u | __ldg(p.zg + z + f0)) * 0x00010001u;
+        zz[1] = (0x4300u | __ldg(p.zu + z + f0)) * 0x00010001u;
+        zz[2] = (0x4300u | __ldg(p.zg + z + f1)) * 0x00010001u;
+        zz[3] = (0x4300u | __ldg(p.zu + z + f1)) * 0x00010001u;
+      }
+      float acc[2][NT][4];
+      clear(acc);
+      use_stages(row_bytes, rows > 8 ? 2 : 1, count > 8 ? 2 : 1, at, zz, acc);
+      named_bar_sync(kUserBar, kUsers);  // the last tile's sums are read
+      // row 16 m + r of a warp's sums: gate (r < 8) or up of feature 8 m + r % 8
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          *reinterpret_cast<float2*>(&s.red[warp][16 * m + g][n * 8 + 2 * q]) = make_float2(acc[m][n][0], acc[m][n][1]);
+          *reinterpret_cast<float2*>(&s.red[warp][16 * m + 8 + g][n * 8 + 2 * q]) =
+              make_float2(acc[m][n][2], acc[m][n][3]);
+        }
+      named_bar_sync(kUserBar, kUsers);
+      const int r = threadIdx.x % 16, t = threadIdx.x / 16;
+      if (t < count && r < rows) {
+        const int row = (r & 8) * 2 + (r & 7);
+        float gs = 0.f, us = 0.f;
+#pragma unroll
+        for (int w = 0; w < kUserWarps; ++w) {
+          gs += s.red[w][row][t];
+          us += s.red[w][row + 8][t];
+        }
+        if constexpr (WF != kBf16) {
+          const int64_t sc = static_cast<int64_t>(e) * p.f + feat0 + r;
+          gs *= __ldg(p.sg + sc);
+          us *= __ldg(p.su + sc);
+        }
+        const __nv_bfloat16 h = __float2bfloat16_rn(silu(gs) * us);
+        p.h[static_cast<int64_t>(s.row0[a] + t) * p.f + feat0 + r] = __bfloat16_as_ushort(h);
+      }
+    });
+  }
+
+  // ------------------------------------------------- 4. down and combine
+  // Calls f(first column, columns, active expert) over the block's share:
+  // tiles of at most 32 output columns, all active experts for each.
+  template <typename F>
+  __device__ __forceinline__ void down_tiles(F&& f) {
+    const int64_t total = p.d / kShareStep;
+    const int end = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x) * kShareStep;
+    for (int c = static_cast<int>(total * blockIdx.x / gridDim.x) * kShareStep; c < end; c += kRows)
+      for (int a = 0; a < s.n_act; ++a) f(c, min(kRows, end - c), a);
+  }
+
+  __device__ __forceinline__ void feed_down(int row_bytes) {
+    down_tiles([&](int c, int rows, int a) {
+      const CUtensorMap* map = &maps.down[rows / kShareStep - 1];
+      const int row = s.act[a] * p.d + c;
+      for (int at = 0; at < row_bytes && open_stage(rows); at += kSeg, pos.next())
+        tma_load_3d(stage(), map, &full[pos.stage], 0, at / 128, row);
+    });
+  }
+  __device__ __forceinline__ void feed_h(int row_bytes) {
+    down_tiles([&](int, int, int a) {
+      const uint16_t* h = p.h + static_cast<int64_t>(s.row0[a]) * p.f;
+      for (int at = 0; at < row_bytes && ok; at += kSeg)
+        feed_tokens(at, min(kSeg, row_bytes - at), s.count[a], [&](int i) { return h + static_cast<int64_t>(i) * p.f; });
+    });
+  }
+  // After a second barrier that was not met: nobody will use the stages that
+  // the weight warp opened ahead; see their copies land.
+  __device__ __forceinline__ void drop_down(int row_bytes) {
+    int left = G::kStages;
+    down_tiles([&](int, int, int) {
+      for (int at = 0; at < row_bytes && left > 0; at += kSeg, --left, pos.next()) {
+        mbar_arrive(&full[pos.stage]);
+        mbar_wait(&full[pos.stage], pos.phase, p.wait_limit_ns);
+      }
+    });
+  }
+
+  __device__ __forceinline__ void down(int row_bytes) {
+    const int g = lane >> 2, q = lane & 3;
+    auto zero = [&]() {  // the warp's own sums
+      float4* r = reinterpret_cast<float4*>(&s.red[warp][0][0]);
+      for (int i = lane; i < kRows * NT * 8 / 4; i += 32) r[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      __syncwarp();
+    };
+    zero();
+    down_tiles([&](int c, int rows, int a) {
+      const int e = s.act[a], count = s.count[a];
+      int row[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) row[i] = min(8 * i + g, rows - 1);
+      Places at;
+      place_rows(at, row);
+      place_tokens(at, count);
+      const int64_t ch = static_cast<int64_t>(e) * p.d + c;
+      uint32_t zz[4] = {0, 0, 0, 0};
+      float sc[4] = {1.f, 1.f, 1.f, 1.f};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (WF == kWInt4) zz[i] = (0x4300u | __ldg(p.zd + ch + row[i])) * 0x00010001u;
+        if constexpr (WF != kBf16) sc[i] = __ldg(p.sd + ch + row[i]);
+      }
+      float acc[2][NT][4];
+      clear(acc);
+      // the warp's part of the expert, weighed and added to its tokens' sums
+      if (use_stages(row_bytes, rows > 16 ? 2 : 1, count > 8 ? 2 : 1, at, zz, acc)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int i = n * 8 + 2 * q + u;
+            if (i >= count) continue;
+            const int t = s.tok[a][i];
+            const float w = s.w[t * p.k + s.slot[e][t]];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              float& sum = s.red[warp][8 * r + g][t];
+              sum = fmaf(w * sc[r], acc[r / 2][n][(r & 1) * 2 + u], sum);
+            }
+          }
+        __syncwarp();
+      }
+      if (a + 1 < s.n_act) return;
+      named_bar_sync(kUserBar, kUsers);
+      for (int o = threadIdx.x; o < kRows * NT * 8; o += kUsers) {
+        const int r = o % kRows, t = o / kRows;
+        if (t >= p.n || r >= rows) continue;
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kUserWarps; ++w) sum += s.red[w][r][t];
+        const int64_t to = static_cast<int64_t>(t) * p.d + c + r;
+        if (p.out_f32)
+          static_cast<float*>(p.out)[to] = sum;
+        else
+          static_cast<uint16_t*>(p.out)[to] = __bfloat16_as_ushort(__float2bfloat16_rn(sum));
+      }
+      named_bar_sync(kUserBar, kUsers);
+      zero();
+    });
   }
 };
 
 template <int WF, int NT>
-__global__ void __launch_bounds__(kThreads, 1) few_tokens_kernel(const FewArgs p) {
+__global__ void __launch_bounds__(kThreads, 1)
+    few_tokens_kernel(const __grid_constant__ FewMaps maps, const FewArgs p) {
+  using G = Geo<WF, NT>;
   extern __shared__ uint8_t smem_raw[];
-  Smem& s = *reinterpret_cast<Smem*>(smem_raw);
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Block<WF, NT> b(p, maps, smem);
   grid_dep_wait();
-  const unsigned G = gridDim.x;
+  const unsigned blocks = gridDim.x;
+  const unsigned expected = blocks + static_cast<unsigned>(p.test_stall);
   bool ok = true;
   if (p.ids == nullptr) {
-    few_logits(p, s);
-    ok = grid_barrier_wait(p.bar, G, p.wait_limit_ns, p.err, &s.ok);
-    if (threadIdx.x == 0) grid_barrier_depart(p.bar, G);
-  }
-  const int64_t up_bytes = static_cast<int64_t>(p.d) / kElems<WF> * 16;
-  const int64_t down_bytes = static_cast<int64_t>(p.f) / kElems<WF> * 16;
-  if (ok) {
-    few_gate(p, s);
-    few_gateup<WF, NT>(p, s, up_bytes);
-    Down<WF, NT> down(p, s, down_bytes);
-    down.prologue();
-    if (grid_barrier_wait(p.bar + 2, G, p.wait_limit_ns, p.err, &s.ok)) down.run();
+    b.logits();
+    ok = grid_barrier_wait(p.bar, expected, p.wait_limit_ns, p.err, &b.s.ok);
+    if (threadIdx.x == 0) grid_barrier_depart(p.bar, blocks);
   } else {
-    // the other blocks still find this one at the second barrier
-    grid_barrier_wait(p.bar + 2, G, p.wait_limit_ns, p.err, &s.ok);
+    __syncthreads();
   }
-  if (threadIdx.x == 0) grid_barrier_depart(p.bar + 2, G);
+  const int up_bytes = p.d / kElems<WF> * 16, down_bytes = p.f / kElems<WF> * 16;
+  if (ok) b.gate();
+  // (a block that timed out above still meets the others at the second barrier)
+  if (b.warp == kWeightWarp) {
+    if (ok && b.lane == 0) {
+      b.feed_gateup(up_bytes);
+      b.feed_down(down_bytes);
+    }
+  } else if (b.warp == kTokenWarp) {
+    if (ok) {
+      b.feed_x(up_bytes);
+      bool met = true;
+      if (b.lane == 0) {
+        met = b.poll(expected);
+        __threadfence();
+      }
+      if (__all_sync(0xffffffffu, met))
+        b.feed_h(down_bytes);
+      else
+        b.drop_down(down_bytes);
+      cp_async_wait_all();
+    }
+  } else {
+    if (ok) b.gateup(up_bytes);
+    if (b.users_meet(expected) && ok) b.down(down_bytes);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) grid_barrier_depart(p.bar + 2, blocks);
 }
 
-template <typename F>
-cudaError_t for_kernel(int wf, int n, F&& f) {
-  const bool two = n > 8;
-  switch (wf) {
-    case kBf16: return two ? f(few_tokens_kernel<kBf16, 2>) : f(few_tokens_kernel<kBf16, 1>);
-    case kWInt8: return two ? f(few_tokens_kernel<kWInt8, 2>) : f(few_tokens_kernel<kWInt8, 1>);
-    case kWInt4: return two ? f(few_tokens_kernel<kWInt4, 2>) : f(few_tokens_kernel<kWInt4, 1>);
-    case kWFp8: return two ? f(few_tokens_kernel<kWFp8, 2>) : f(few_tokens_kernel<kWFp8, 1>);
-  }
-  return cudaErrorInvalidValue;
+template <int WF, int NT>
+cudaError_t prepare(int* per_sm) {
+  auto kernel = few_tokens_kernel<WF, NT>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<WF, NT>::kBytes);
+  if (e != cudaSuccess) return e;
+  int n = 0;
+  const cudaError_t o = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, Geo<WF, NT>::kBytes);
+  *per_sm = n < *per_sm ? n : *per_sm;
+  return o;
+}
+
+template <int WF, int NT>
+cudaError_t launch(const FewMaps& m, const FewArgs& a, int grid, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Geo<WF, NT>::kBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, few_tokens_kernel<WF, NT>, m, a);
 }
 
 }  // namespace
 
 int few_format(bool quantised, WeightFormat wf) { return quantised ? static_cast<int>(wf) : kBf16; }
 
-cudaError_t few_tokens_prepare(int wf, int* blocks_per_sm) {
-  *blocks_per_sm = 0;
-  for (int n : {1, kMaxTokens}) {
-    const cudaError_t e = for_kernel(wf, n, [&](auto kernel) {
-      cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem));
-      int per_sm = 0;
-      if (r == cudaSuccess) r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, sizeof(Smem));
-      *blocks_per_sm = n == 1 ? per_sm : (per_sm < *blocks_per_sm ? per_sm : *blocks_per_sm);
-      return r;
-    });
-    if (e != cudaSuccess) return e;
+cudaError_t few_tokens_prepare(int format, int* blocks_per_sm) {
+  *blocks_per_sm = 1;
+  auto both = [&](auto one, auto two) {
+    const cudaError_t e = one(blocks_per_sm);
+    return e == cudaSuccess ? two(blocks_per_sm) : e;
+  };
+  switch (format) {
+    case kBf16: return both(prepare<kBf16, 1>, prepare<kBf16, 2>);
+    case kWInt8: return both(prepare<kWInt8, 1>, prepare<kWInt8, 2>);
+    case kWInt4: return both(prepare<kWInt4, 1>, prepare<kWInt4, 2>);
+    case kWFp8: return both(prepare<kWFp8, 1>, prepare<kWFp8, 2>);
   }
-  return cudaSuccess;
+  return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_few_tokens(int wf, const FewArgs& a, int grid, cudaStream_t s) {
+bool few_token_maps(int format, const FewArgs& a, FewMaps* m) {
+  const uint64_t elems = format == kBf16 ? kElems<kBf16> : format == kWInt4 ? kElems<kWInt4> : kElems<kWInt8>;
+  const uint64_t up = a.d / elems * 16, down = a.f / elems * 16, blk = a.gu_block;
+  // rows of bytes as (byte of a 128-byte chunk, chunk, row[, gate or up, interleave block])
+  const cuuint64_t up_dims[5] = {128, up / 128, blk, 2, static_cast<uint64_t>(a.E) * a.f / blk};
+  const cuuint64_t up_strides[4] = {128, up, blk * up, 2 * blk * up};
+  const cuuint64_t down_dims[3] = {128, down / 128, static_cast<uint64_t>(a.E) * a.d};
+  const cuuint64_t down_strides[2] = {128, down};
+  bool ok = true;
+  for (int i = 0; i < kRows / 2 / kShareStep; ++i) {
+    const cuuint32_t box[5] = {128, kRowLines, static_cast<cuuint32_t>((i + 1) * kShareStep), 2, 1};
+    ok = ok && make_tmap_nd(&m->gate_up[i], a.wgu, 5, up_dims, up_strides, box);
+  }
+  for (int i = 0; i < kRows / kShareStep; ++i) {
+    const cuuint32_t box[3] = {128, kRowLines, static_cast<cuuint32_t>((i + 1) * kShareStep)};
+    ok = ok && make_tmap_nd(&m->down[i], a.wd, 3, down_dims, down_strides, box);
+  }
+  return ok;
+}
+
+cudaError_t launch_few_tokens(int format, const FewMaps& m, const FewArgs& a, int grid, cudaStream_t s) {
   if (a.n <= 0) return cudaSuccess;
   if (a.n > kMaxTokens || a.E > kMaxExperts || a.k > kMaxK || grid <= 0) return cudaErrorInvalidValue;
-  return for_kernel(wf, a.n, [&](auto kernel) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = sizeof(Smem);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeCooperative;
-    attr[0].val.cooperative = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
-  });
+  const bool two = a.n > 8;
+  switch (format) {
+    case kBf16: return two ? launch<kBf16, 2>(m, a, grid, s) : launch<kBf16, 1>(m, a, grid, s);
+    case kWInt8: return two ? launch<kWInt8, 2>(m, a, grid, s) : launch<kWInt8, 1>(m, a, grid, s);
+    case kWInt4: return two ? launch<kWInt4, 2>(m, a, grid, s) : launch<kWInt4, 1>(m, a, grid, s);
+    case kWFp8: return two ? launch<kWFp8, 2>(m, a, grid, s) : launch<kWFp8, 1>(m, a, grid, s);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace cbmoe

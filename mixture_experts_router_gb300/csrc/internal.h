@@ -316,11 +316,20 @@ struct FewArgs {
   unsigned int* bar;     // two grid barriers: 4 words, zero between launches
   int* err;
   uint64_t wait_limit_ns;
+  int32_t test_stall;    // test only: the barriers wait for one block more than exist
 };
 int few_format(bool quantised, WeightFormat wf);  // the kernel's name of a weight format
 // one-time function attributes; blocks of the launch that fit one SM at once
 cudaError_t few_tokens_prepare(int format, int* blocks_per_sm);
-cudaError_t launch_few_tokens(int format, const FewArgs& a, int grid, cudaStream_t s);
+// Tensor maps of its weight copies, which a handle keeps: 4, 8, .. 16 features'
+// gate and up rows, and 4, 8, .. 32 columns' rows.
+constexpr int kFewRowStep = 4;
+struct FewMaps {
+  CUtensorMap gate_up[16 / kFewRowStep];
+  CUtensorMap down[32 / kFewRowStep];
+};
+bool few_token_maps(int format, const FewArgs& a, FewMaps* m);
+cudaError_t launch_few_tokens(int format, const FewMaps& m, const FewArgs& a, int grid, cudaStream_t s);
 
 // ------------------------------------------- 4-bit floats with block scales
 struct Fp4Args {
@@ -360,5 +369,8 @@ cudaError_t launch_fp4_matmul(const Fp4MatmulArgs& a, int num_sms, cudaStream_t 
 bool make_tmap(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t elem_bytes, uint64_t inner,
                uint64_t outer, uint32_t box_inner, uint32_t box_outer,
                CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
+// A tensor of bytes of up to 5 dimensions, innermost first, 128-byte swizzled.
+bool make_tmap_nd(CUtensorMap* m, const void* base, uint32_t rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                  const cuuint32_t* box);
 
 }  // namespace cbmoe
