@@ -15,20 +15,20 @@
 // most 16 tokens an expert's 128-row tiles of the large kernels would be
 // nearly all padding.  So a tile here is at most 32 weight rows (in step 3, 16
 // features' gate and up rows; in step 4, 32 output columns), streamed through
-// a ring of stages of 512 bytes per row, with the same stretch of the chosen
+// a ring of stages of 512 (int4: 256) bytes per row, with the same stretch of the chosen
 // tokens' activations beside them.
 //
 //   warp 16     weights, one TMA copy per stage.  The tensor maps split a row
 //               into 128-byte chunks as a dimension of its own, so that one
-//               copy brings 512 bytes of every row of the tile; there is a
+//               copy brings that much of every row of the tile; there is a
 //               map for each height.  A copy costs its SM about 55 ns and then
 //               2.2 ns per 128 bytes, so several small ones per stage would
 //               bound the kernel (a bulk copy per row held it at 2 TB/s).  It
 //               runs ahead across tiles, experts and the second barrier: step
 //               4's weights do not wait for H.
 //   warp 17     tokens, by cp.async into the stage, in the weights' swizzle.
-//   warps 0-15  two sets of 8 that take the stages in turn; a warp owns one
-//               64-byte step of a stage, reads fragments with 16-byte loads,
+//   warps 0-15  two sets of 8 that take the stages in turn; a warp owns an
+//               eighth of a stage's stretch, reads fragments with wide loads,
 //               widens quantised codes to bf16 exactly in registers and issues
 //               mma.sync m16n8k16 (A: weight rows, B: the expert's own tokens,
 //               in their order).  A dot product does not depend on the order
@@ -61,11 +61,8 @@ constexpr int kWeightWarp = kUserWarps;
 constexpr int kTokenWarp = kUserWarps + 1;
 constexpr int kThreads = kUsers + 64;
 constexpr int kRows = 32;               // weight rows of a tile: two m16 fragments
-constexpr int kAlong = 8;               // warps along a row's stretch
-constexpr int kStepBytes = 64;          // of a row per warp and stage: 4 threads x 16
-constexpr int kSeg = kAlong * kStepBytes;  // of a row per stage
-constexpr int kRowLines = kSeg / 128;
-constexpr int kWeightBytes = kRows * kSeg;
+constexpr int kAlong = 8;               // warps along a row's stretch: a set
+constexpr int kSets = kUserWarps / kAlong;
 constexpr int kShareStep = kFewRowStep; // shares and tiles are multiples of this many rows
 constexpr int kMaxTokens = kFewTokens;
 constexpr int kMaxExperts = 256;
@@ -97,16 +94,29 @@ struct Shared {
   int ok;
 };
 
+// Bytes of a row per stage; int4's, with four times as many bytes of tokens
+// beside them, are fewer.
+template <int WF>
+constexpr int kSeg = WF == kWInt4 ? 256 : 512;
+
 template <int WF, int NT>
 struct Geo {
+  static constexpr int kSeg = cbmoe::kSeg<WF>;
+  static constexpr int kRowLines = kSeg / 128;
+  static constexpr int kWeightBytes = kRows * kSeg;
+  static constexpr int kStep = kSeg / kAlong;             // bytes of a row per warp
+  static constexpr int kStepElems = kStep / 64 ? kElems<WF> : kElems<WF> / 2;  // elements per thread and row
   static constexpr int kTokBytes = kSeg / 16 * kElems<WF> * 2;  // a token's stretch in a stage
   static constexpr int kTokLines = kTokBytes / 128;
   static constexpr int kStage = kWeightBytes + NT * 8 * kTokBytes;
   static constexpr int kShared = (static_cast<int>(sizeof(Shared<NT>)) + 256 + 1023) / 1024 * 1024;
   static constexpr int kFit = (kSmemLimit - kShared - 1024) / kStage;
-  static constexpr int kStages = kFit < 8 ? kFit : 8;
+  // A whole number of turns of the sets: a stage always belongs to the same
+  // set, whose waits then see every phase of its barrier (a set that met a
+  // stage only every second time could take one phase for the other).
+  static constexpr int kStages = (kFit < 12 ? kFit : 12) / kSets * kSets;
   static constexpr int kBytes = 1024 + kShared + kStages * kStage;
-  static_assert(kStages >= 3 && 16 * kStages <= 256 && kStage % 1024 == 0, "ring");
+  static_assert(kStages >= 4 && 16 * kStages <= 256 && kStage % 1024 == 0, "ring");
 };
 
 // Byte of 16-byte unit `unit` of 128-byte line `line` of a swizzled area.
@@ -128,7 +138,7 @@ __device__ __forceinline__ void widen8(const uint4& v, int i, uint32_t zz, uint3
       if constexpr (WF == kWFp8)
         fp8x4_to_bf16x4(in[2 * i + j], o[2 * j], o[2 * j + 1]);
       else
-        int8x4_to_bf16x4(in[2 * i + j], o[2 * j], o[2 * j + 1]);
+        int8x4_to_bf16x4_fma(in[2 * i + j], o[2 * j], o[2 * j + 1]);
     }
   }
 }
@@ -149,6 +159,7 @@ struct RingPos {
 template <int WF, int NT>
 struct Block {
   using G = Geo<WF, NT>;
+  static constexpr int kSeg = G::kSeg;
   const FewArgs& p;
   const FewMaps& maps;
   Shared<NT>& s;
@@ -337,7 +348,7 @@ struct Block {
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) return;
     const int bytes = seg / 16 * kElems<WF> * 2;
-    uint8_t* dst = stage() + kWeightBytes;
+    uint8_t* dst = stage() + G::kWeightBytes;
     for (int i = 0; i < count; ++i) {
       const uint8_t* src = reinterpret_cast<const uint8_t*>(row(i)) + static_cast<int64_t>(at) / 16 * kElems<WF> * 2;
 #pragma unroll
@@ -352,12 +363,13 @@ struct Block {
   // halves, and the tokens of its columns.
   struct Places {
     int w[4];
-    int tok[NT][kElems<WF> / 8];
+    int tok[NT][G::kStepElems / 8];
   };
   __device__ __forceinline__ void place_rows(Places& at, const int (&row)[4]) const {
-    const int q = lane & 3, along = warp % kAlong;
+    const int at_row = warp % kAlong * G::kStep + (lane & 3) * (G::kStep / 4);  // byte of the row's stretch
 #pragma unroll
-    for (int i = 0; i < 4; ++i) at.w[i] = swizzled(row[i] * kRowLines + along / 2, along % 2 * 4 + q);
+    for (int i = 0; i < 4; ++i)
+      at.w[i] = swizzled(row[i] * G::kRowLines + at_row / 128, at_row % 128 / 16) + at_row % 16;
   }
   __device__ __forceinline__ void place_tokens(Places& at, int count) const {
     const int g = lane >> 2, q = lane & 3, along = warp % kAlong;
@@ -365,9 +377,9 @@ struct Block {
     for (int n = 0; n < NT; ++n) {
       const int row = min(n * 8 + g, count - 1);
 #pragma unroll
-      for (int i = 0; i < kElems<WF> / 8; ++i) {
-        const int unit = (along * 4 + q) * (kElems<WF> / 8) + i;
-        at.tok[n][i] = kWeightBytes + swizzled(row * G::kTokLines + unit / 8, unit % 8);
+      for (int i = 0; i < G::kStepElems / 8; ++i) {
+        const int unit = (along * 4 + q) * (G::kStepElems / 8) + i;
+        at.tok[n][i] = G::kWeightBytes + swizzled(row * G::kTokLines + unit / 8, unit % 8);
       }
     }
   }
@@ -384,14 +396,21 @@ struct Block {
         continue;
       }
       wait(&full[pos.stage], pos.phase);
-      if (warp % kAlong * kStepBytes < row_bytes - b) {
+      if (warp % kAlong * G::kStep < row_bytes - b) {
         took = true;
         const uint8_t* st = stage();
         uint4 v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(st + at.w[i]);
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (G::kStep == 64) {
+            v[i] = *reinterpret_cast<const uint4*>(st + at.w[i]);
+          } else {
+            const uint2 half = *reinterpret_cast<const uint2*>(st + at.w[i]);
+            v[i] = make_uint4(half.x, half.y, 0u, 0u);
+          }
+        }
 #pragma unroll
-        for (int i = 0; i < kElems<WF> / 8; ++i) {
+        for (int i = 0; i < G::kStepElems / 8; ++i) {
           uint4 t[NT];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
@@ -710,6 +729,7 @@ cudaError_t few_tokens_prepare(int format, int* blocks_per_sm) {
 bool few_token_maps(int format, const FewArgs& a, FewMaps* m) {
   const uint64_t elems = format == kBf16 ? kElems<kBf16> : format == kWInt4 ? kElems<kWInt4> : kElems<kWInt8>;
   const uint64_t up = a.d / elems * 16, down = a.f / elems * 16, blk = a.gu_block;
+  const cuuint32_t lines = (format == kWInt4 ? kSeg<kWInt4> : kSeg<kBf16>) / 128;
   // rows of bytes as (byte of a 128-byte chunk, chunk, row[, gate or up, interleave block])
   const cuuint64_t up_dims[5] = {128, up / 128, blk, 2, static_cast<uint64_t>(a.E) * a.f / blk};
   const cuuint64_t up_strides[4] = {128, up, blk * up, 2 * blk * up};
@@ -717,11 +737,11 @@ bool few_token_maps(int format, const FewArgs& a, FewMaps* m) {
   const cuuint64_t down_strides[2] = {128, down};
   bool ok = true;
   for (int i = 0; i < kRows / 2 / kShareStep; ++i) {
-    const cuuint32_t box[5] = {128, kRowLines, static_cast<cuuint32_t>((i + 1) * kShareStep), 2, 1};
+    const cuuint32_t box[5] = {128, lines, static_cast<cuuint32_t>((i + 1) * kShareStep), 2, 1};
     ok = ok && make_tmap_nd(&m->gate_up[i], a.wgu, 5, up_dims, up_strides, box);
   }
   for (int i = 0; i < kRows / kShareStep; ++i) {
-    const cuuint32_t box[3] = {128, kRowLines, static_cast<cuuint32_t>((i + 1) * kShareStep)};
+    const cuuint32_t box[3] = {128, lines, static_cast<cuuint32_t>((i + 1) * kShareStep)};
     ok = ok && make_tmap_nd(&m->down[i], a.wd, 3, down_dims, down_strides, box);
   }
   return ok;

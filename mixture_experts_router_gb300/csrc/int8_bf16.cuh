@@ -17,6 +17,26 @@ __device__ __forceinline__ void int8x4_to_bf16x4(uint32_t w, uint32_t& lo, uint3
   asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(m23), "r"(s23));
 }
 
+// The same with half the integer instructions (the integer pipe runs at half
+// the rate): v = 0x4300 | (q + 128) is 256 + q for q < 0 and 256 + 2 q
+// otherwise; d = v - 256 is q or 2 q, r = max(0, v / 2 - 128) is 0 or q, and
+// d - r is q.  All are integers below 2^8 in magnitude or even ones below
+// 2^9: exact in bf16.
+__device__ __forceinline__ void int8x4_to_bf16x4_fma(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const uint32_t v[2] = {__byte_perm(u, 0x43434343u, 0x4140), __byte_perm(u, 0x43434343u, 0x4342)};
+  uint32_t o[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t d, r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(v[i]), "r"(0x43804380u));
+    asm("fma.rn.relu.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v[i]), "r"(0x3F003F00u), "r"(0xC300C300u));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(d), "r"(r));
+  }
+  lo = o[0];
+  hi = o[1];
+}
+
 // 16 staged int8 codes (K elements 16c..16c+15 of a weight row) -> the two
 // 16-byte bf16 chunks 2c and 2c+1 of that row in a 128-byte-swizzled K-major
 // tile (row r at r * 128, chunk i at 16 * (i ^ (r & 7))).

@@ -161,6 +161,20 @@ def test_on_a_handle_of_another_size_between_its_forwards(wdtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("wdtype", ["bf16", "int8", "int4", "fp8"])
+@pytest.mark.parametrize("n", [6, 14])
+def test_long_streams_repeat_bit_for_bit(wdtype, n):
+    """Hundreds of stages per block, two n-tiles and one: every run gives the first one's bits."""
+    r = Run(synth.custom_shape("few", n, 2048, 1536, 24, 6, wdtype=wdtype, seed=31))
+    want = check(r)
+    for _ in range(200):
+        out = torch.empty(r.x.shape, dtype=torch.float32, device="cuda")
+        r.m.forward_few(r.x, out, f32out=True)
+        assert np.array_equal(out.double().cpu().numpy(), want)
+    assert r.m.last_error() == cb.CB_OK
+
+
+@pytest.mark.gpu
 def test_repeats_bit_for_bit_and_in_a_graph():
     r = Run(synth.custom_shape("few", 13, 768, 1024, 16, 4, seed=2), T=16)
     want = r.few()
