@@ -34,7 +34,7 @@
 //               in their order).  A dot product does not depend on the order
 //               of its terms, so a thread's k-slots are consecutive elements.
 //
-// The balance: the active experts' features (step 3) and the output columns
+// The balance: the parts' features (step 3) and the output columns
 // (step 4) are cut into one contiguous share per block, in steps of 4 (the
 // rows of the smallest copy).
 //
@@ -67,6 +67,7 @@ constexpr int kShareStep = kFewRowStep; // shares and tiles are multiples of thi
 constexpr int kMaxTokens = kFewTokens;
 constexpr int kMaxExperts = 256;
 constexpr int kMaxK = 16;
+constexpr int kMaxParts = kMaxTokens * kMaxK;
 constexpr uint32_t kUserBar = 1;        // named barrier of the ring's users
 constexpr int kSmemLimit = 232448;
 
@@ -75,22 +76,24 @@ constexpr int kBf16 = 3;
 template <int WF>
 constexpr int kElems = WF == kBf16 ? 8 : WF == kWInt4 ? 32 : 16;  // elements per 16 bytes
 
-template <int NT>
+// NT: n-tiles of 8 tokens per part; MT: 8 or 16, at least the tokens of the call.
+template <int NT, int MT>
 struct Shared {
   union {
-    float red[kUserWarps][kRows][NT * 8]; // partial sums: [warp][row][token]
+    float red[kUserWarps][kRows][MT];     // partial sums: [warp][row][token]
     float logit[kMaxTokens * kMaxExperts];
     float part[kUserWarps][kMaxTokens];   // the logits' partial sums
   };
   float w[kMaxTokens * kMaxK];            // gate weight of each (token, slot)
   uint32_t mask[kMaxExperts];             // tokens of each expert
   uint8_t slot[kMaxExperts][kMaxTokens];  // the slot at which a token chose it
-  uint8_t tok[kMaxExperts][kMaxTokens];   // the tokens of each active expert
-  uint8_t count[kMaxExperts];             // and their number
-  int16_t act[kMaxExperts];               // active experts, ascending
-  int16_t row0[kMaxExperts];              // an active expert's first row of H
+  // parts: an active expert and at most NT x 8 of its tokens (n k at most)
+  int16_t act[kMaxParts];                 // the expert, ascending
+  uint8_t tok[kMaxParts][NT * 8];
+  uint8_t count[kMaxParts];
+  int16_t row0[kMaxParts];                // the part's first row of H
   int n_act;
-  int warp_act[kMaxExperts / 32];
+  int warp_parts[kMaxExperts / 32];
   int ok;
 };
 
@@ -99,7 +102,7 @@ struct Shared {
 template <int WF>
 constexpr int kSeg = WF == kWInt4 ? 256 : 512;
 
-template <int WF, int NT>
+template <int WF, int NT, int MT>
 struct Geo {
   static constexpr int kSeg = cbmoe::kSeg<WF>;
   static constexpr int kRowLines = kSeg / 128;
@@ -109,7 +112,7 @@ struct Geo {
   static constexpr int kTokBytes = kSeg / 16 * kElems<WF> * 2;  // a token's stretch in a stage
   static constexpr int kTokLines = kTokBytes / 128;
   static constexpr int kStage = kWeightBytes + NT * 8 * kTokBytes;
-  static constexpr int kShared = (static_cast<int>(sizeof(Shared<NT>)) + 256 + 1023) / 1024 * 1024;
+  static constexpr int kShared = (static_cast<int>(sizeof(Shared<NT, MT>)) + 256 + 1023) / 1024 * 1024;
   static constexpr int kFit = (kSmemLimit - kShared - 1024) / kStage;
   // A whole number of turns of the sets: a stage always belongs to the same
   // set, whose waits then see every phase of its barrier (a set that met a
@@ -121,6 +124,12 @@ struct Geo {
 
 // Byte of 16-byte unit `unit` of 128-byte line `line` of a swizzled area.
 __device__ __forceinline__ int swizzled(int line, int unit) { return line * 128 + ((unit ^ (line & 7)) << 4); }
+// The same byte of row `row`, rows being LINES (a power of two) lines: `first`
+// is row 0's.
+template <int LINES>
+__device__ __forceinline__ int in_row(int first, int row) {
+  return row * (LINES * 128) + (first ^ (((row * LINES) & 7) << 4));
+}
 
 // Elements 8 i .. 8 i + 7 of a thread's 16 bytes of a weight row as four bf16
 // pairs, in memory order.
@@ -156,13 +165,13 @@ struct RingPos {
   }
 };
 
-template <int WF, int NT>
+template <int WF, int NT, int MT>
 struct Block {
-  using G = Geo<WF, NT>;
+  using G = Geo<WF, NT, MT>;
   static constexpr int kSeg = G::kSeg;
   const FewArgs& p;
   const FewMaps& maps;
-  Shared<NT>& s;
+  Shared<NT, MT>& s;
   uint64_t* full;
   uint64_t* empty;
   uint8_t* ring;
@@ -170,16 +179,26 @@ struct Block {
   bool ok = true;           // no wait of this thread has run out
   int turn = 0;             // set of warps that takes the next stage
   const int warp, lane;
+  int first_w;
+  int first_tok[G::kStepElems / 8];
 
   __device__ __forceinline__ Block(const FewArgs& p_, const FewMaps& maps_, uint8_t* smem)
       : p(p_),
         maps(maps_),
-        s(*reinterpret_cast<Shared<NT>*>(smem)),
+        s(*reinterpret_cast<Shared<NT, MT>*>(smem)),
         full(reinterpret_cast<uint64_t*>(smem + G::kShared - 256)),
         empty(full + G::kStages),
         ring(smem + G::kShared),
         warp(threadIdx.x / 32),
         lane(threadIdx.x % 32) {
+    const int along = warp % kAlong, q = lane & 3;
+    const int byte = along * G::kStep + q * (G::kStep / 4);  // of a row's stretch
+    first_w = swizzled(byte / 128, byte % 128 / 16) + byte % 16;
+#pragma unroll
+    for (int i = 0; i < G::kStepElems / 8; ++i) {
+      const int unit = (along * 4 + q) * (G::kStepElems / 8) + i;
+      first_tok[i] = swizzled(unit / 8, unit % 8);
+    }
     if (threadIdx.x == 0) {
       for (int i = 0; i < G::kStages; ++i) {
         mbar_init(&full[i], 1 + 32);  // the weights' announcement, the token warp's lanes
@@ -270,36 +289,44 @@ struct Block {
       atomicOr(&s.mask[id], 1u << threadIdx.x);
     }
     __syncthreads();
+    // the parts: an expert's tokens in order, NT x 8 at most to a part
     const int e = threadIdx.x;
-    const bool on = e < p.E && s.mask[e] != 0u;
-    const uint32_t ballot = __ballot_sync(0xffffffffu, on);
-    if (e < kMaxExperts && lane == 0) s.warp_act[warp] = __popc(ballot);
+    const uint32_t all = e < p.E ? s.mask[e] : 0u;
+    const int parts = (__popc(all) + NT * 8 - 1) / (NT * 8);
+    int sum = parts;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int below = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += below;
+    }
+    if (e < kMaxExperts && lane == 31) s.warp_parts[warp] = sum;
     __syncthreads();
     if (e < kMaxExperts) {
-      int base = 0;
-      for (int i = 0; i < warp; ++i) base += s.warp_act[i];
-      if (on) s.act[base + __popc(ballot & ((1u << lane) - 1u))] = static_cast<int16_t>(e);
-      if (e == kMaxExperts - 1) s.n_act = base + __popc(ballot);
+      int base = sum - parts;
+      for (int i = 0; i < warp; ++i) base += s.warp_parts[i];
+      uint32_t m = all;
+      for (int a = base; a < base + parts; ++a) {
+        s.act[a] = static_cast<int16_t>(e);
+        int c = 0;
+        for (; m != 0u && c < NT * 8; m &= m - 1u, ++c) s.tok[a][c] = static_cast<uint8_t>(__ffs(m) - 1);
+        s.count[a] = static_cast<uint8_t>(c);
+      }
+      if (e == kMaxExperts - 1) s.n_act = base + parts;
     }
     __syncthreads();
-    if (warp == 0) {  // rows of H: an expert's tokens one after the other
+    if (warp == 0) {  // rows of H: a part's tokens one after the other
       int base = 0;
       for (int a0 = 0; a0 < s.n_act; a0 += 32) {
         const int a = a0 + lane;
-        uint32_t m = a < s.n_act ? s.mask[s.act[a]] : 0u;
-        const int c = __popc(m);
-        int sum = c;
+        const int c = a < s.n_act ? s.count[a] : 0;
+        int rows = c;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
-          const int below = __shfl_up_sync(0xffffffffu, sum, o);
-          if (lane >= o) sum += below;
+          const int below = __shfl_up_sync(0xffffffffu, rows, o);
+          if (lane >= o) rows += below;
         }
-        if (a < s.n_act) {
-          s.row0[a] = static_cast<int16_t>(base + sum - c);
-          s.count[a] = static_cast<uint8_t>(c);
-          for (int i = 0; m != 0u; m &= m - 1u, ++i) s.tok[a][i] = static_cast<uint8_t>(__ffs(m) - 1);
-        }
-        base += __shfl_sync(0xffffffffu, sum, 31);
+        if (a < s.n_act) s.row0[a] = static_cast<int16_t>(base + rows - c);
+        base += __shfl_sync(0xffffffffu, rows, 31);
       }
     }
     __syncthreads();
@@ -340,47 +367,49 @@ struct Block {
     return ok;
   }
 
-  // Token warp: the `seg` bytes of weights from byte `at` of a row, as bytes
-  // of the count tokens' rows; row(i) is the i-th one.
-  template <typename F>
-  __device__ __forceinline__ void feed_tokens(int at, int seg, int count, F&& row) {
-    wait(&empty[pos.stage], pos.phase ^ 1u);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) return;
-    const int bytes = seg / 16 * kElems<WF> * 2;
-    uint8_t* dst = stage() + G::kWeightBytes;
-    for (int i = 0; i < count; ++i) {
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(row(i)) + static_cast<int64_t>(at) / 16 * kElems<WF> * 2;
+  // Token warp: the stages of a tile whose weights' rows are row_bytes long,
+  // for `count` tokens' rows; mine: this lane's (lane < count).
+  __device__ __forceinline__ void feed_tokens(int row_bytes, int count, const uint16_t* mine) {
+    for (int at = 0; at < row_bytes && ok; at += kSeg, pos.next()) {
+      wait(&empty[pos.stage], pos.phase ^ 1u);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      const int units = min(kSeg, row_bytes - at) / 16 * kElems<WF> * 2 / 16;  // of 16 bytes
+      const int first = at / 16 * kElems<WF> * 2 + lane * 16;
+      uint8_t* dst = stage() + G::kWeightBytes;
+#pragma unroll 2
+      for (int i = 0; i < count; ++i) {
+        const uint8_t* src =
+            reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(mine), i)) + first;
 #pragma unroll
-      for (int u = lane; u < G::kTokBytes / 16; u += 32)
-        if (u * 16 < bytes) cp_async_16(dst + swizzled(i * G::kTokLines + u / 8, u % 8), src + u * 16);
+        for (int u = 0; u < G::kTokBytes / 16; u += 32)
+          if (u + lane < units)
+            cp_async_16(dst + in_row<G::kTokLines>(swizzled((u + lane) / 8, lane % 8), i), src + u * 16);
+      }
+      cp_async_arrive(&full[pos.stage]);
     }
-    cp_async_arrive(&full[pos.stage]);
-    pos.next();
   }
 
   // Where a user's fragments stand in a stage: rows lo and hi of both m16
-  // halves, and the tokens of its columns.
+  // halves, and the tokens of its columns.  first_w, first_tok: those of the
+  // first row and token.
   struct Places {
     int w[4];
     int tok[NT][G::kStepElems / 8];
   };
-  __device__ __forceinline__ void place_rows(Places& at, const int (&row)[4]) const {
-    const int at_row = warp % kAlong * G::kStep + (lane & 3) * (G::kStep / 4);  // byte of the row's stretch
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      at.w[i] = swizzled(row[i] * G::kRowLines + at_row / 128, at_row % 128 / 16) + at_row % 16;
+  __device__ __forceinline__ void place_rows(Places& at, int r0, int r1, int r2, int r3) const {
+    at.w[0] = in_row<G::kRowLines>(first_w, r0);
+    at.w[1] = in_row<G::kRowLines>(first_w, r1);
+    at.w[2] = in_row<G::kRowLines>(first_w, r2);
+    at.w[3] = in_row<G::kRowLines>(first_w, r3);
   }
   __device__ __forceinline__ void place_tokens(Places& at, int count) const {
-    const int g = lane >> 2, q = lane & 3, along = warp % kAlong;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int row = min(n * 8 + g, count - 1);
+      const int row = min(n * 8 + (lane >> 2), count - 1);
 #pragma unroll
-      for (int i = 0; i < G::kStepElems / 8; ++i) {
-        const int unit = (along * 4 + q) * (G::kStepElems / 8) + i;
-        at.tok[n][i] = G::kWeightBytes + swizzled(row * G::kTokLines + unit / 8, unit % 8);
-      }
+      for (int i = 0; i < G::kStepElems / 8; ++i)
+        at.tok[n][i] = G::kWeightBytes + in_row<G::kTokLines>(first_tok[i], row);
     }
   }
 
@@ -474,9 +503,8 @@ struct Block {
   }
   __device__ __forceinline__ void feed_x(int row_bytes) {
     up_tiles([&](int a, int, int) {
-      for (int at = 0; at < row_bytes && ok; at += kSeg)
-        feed_tokens(at, min(kSeg, row_bytes - at), s.count[a],
-                    [&](int i) { return p.x + static_cast<int64_t>(s.tok[a][i]) * p.d; });
+      const int count = s.count[a];
+      feed_tokens(row_bytes, count, p.x + (lane < count ? static_cast<int64_t>(s.tok[a][lane]) * p.d : 0));
     });
   }
 
@@ -486,7 +514,7 @@ struct Block {
       const int e = s.act[a], count = s.count[a];
       const int f0 = min(g, rows - 1), f1 = min(8 + g, rows - 1);  // gate rows; up rows stand `rows` further
       Places at;
-      place_rows(at, {f0, rows + f0, f1, rows + f1});
+      place_rows(at, f0, rows + f0, f1, rows + f1);
       place_tokens(at, count);
       uint32_t zz[4] = {0, 0, 0, 0};
       if constexpr (WF == kWInt4) {
@@ -551,9 +579,8 @@ struct Block {
   }
   __device__ __forceinline__ void feed_h(int row_bytes) {
     down_tiles([&](int, int, int a) {
-      const uint16_t* h = p.h + static_cast<int64_t>(s.row0[a]) * p.f;
-      for (int at = 0; at < row_bytes && ok; at += kSeg)
-        feed_tokens(at, min(kSeg, row_bytes - at), s.count[a], [&](int i) { return h + static_cast<int64_t>(i) * p.f; });
+      const int count = s.count[a];
+      feed_tokens(row_bytes, count, p.h + static_cast<int64_t>(s.row0[a] + min(lane, count - 1)) * p.f);
     });
   }
   // After a second barrier that was not met: nobody will use the stages that
@@ -572,17 +599,19 @@ struct Block {
     const int g = lane >> 2, q = lane & 3;
     auto zero = [&]() {  // the warp's own sums
       float4* r = reinterpret_cast<float4*>(&s.red[warp][0][0]);
-      for (int i = lane; i < kRows * NT * 8 / 4; i += 32) r[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = lane; i < kRows * MT / 4; i += 32) r[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       __syncwarp();
     };
     zero();
+    Places at;
+    int row[4];
     down_tiles([&](int c, int rows, int a) {
       const int e = s.act[a], count = s.count[a];
-      int row[4];
+      if (a == 0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) row[i] = min(8 * i + g, rows - 1);
-      Places at;
-      place_rows(at, row);
+        for (int i = 0; i < 4; ++i) row[i] = min(8 * i + g, rows - 1);
+        place_rows(at, row[0], row[1], row[2], row[3]);
+      }
       place_tokens(at, count);
       const int64_t ch = static_cast<int64_t>(e) * p.d + c;
       uint32_t zz[4] = {0, 0, 0, 0};
@@ -600,6 +629,7 @@ struct Block {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
+            if (n * 8 + u >= count) break;
             const int i = n * 8 + 2 * q + u;
             if (i >= count) continue;
             const int t = s.tok[a][i];
@@ -614,7 +644,7 @@ struct Block {
       }
       if (a + 1 < s.n_act) return;
       named_bar_sync(kUserBar, kUsers);
-      for (int o = threadIdx.x; o < kRows * NT * 8; o += kUsers) {
+      for (int o = threadIdx.x; o < kRows * MT; o += kUsers) {
         const int r = o % kRows, t = o / kRows;
         if (t >= p.n || r >= rows) continue;
         float sum = 0.f;
@@ -632,13 +662,13 @@ struct Block {
   }
 };
 
-template <int WF, int NT>
+template <int WF, int NT, int MT>
 __global__ void __launch_bounds__(kThreads, 1)
     few_tokens_kernel(const __grid_constant__ FewMaps maps, const FewArgs p) {
-  using G = Geo<WF, NT>;
+  using G = Geo<WF, NT, MT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Block<WF, NT> b(p, maps, smem);
+  Block<WF, NT, MT> b(p, maps, smem);
   grid_dep_wait();
   const unsigned blocks = gridDim.x;
   const unsigned expected = blocks + static_cast<unsigned>(p.test_stall);
@@ -680,48 +710,51 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) grid_barrier_depart(p.bar + 2, blocks);
 }
 
-template <int WF, int NT>
+template <int WF, int NT, int MT>
 cudaError_t prepare(int* per_sm) {
-  auto kernel = few_tokens_kernel<WF, NT>;
+  auto kernel = few_tokens_kernel<WF, NT, MT>;
   const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<WF, NT>::kBytes);
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<WF, NT, MT>::kBytes);
   if (e != cudaSuccess) return e;
   int n = 0;
-  const cudaError_t o = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, Geo<WF, NT>::kBytes);
+  const cudaError_t o = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, Geo<WF, NT, MT>::kBytes);
   *per_sm = n < *per_sm ? n : *per_sm;
   return o;
 }
 
-template <int WF, int NT>
+template <int WF, int NT, int MT>
 cudaError_t launch(const FewMaps& m, const FewArgs& a, int grid, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = Geo<WF, NT>::kBytes;
+  cfg.dynamicSmemBytes = Geo<WF, NT, MT>::kBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_tokens_kernel<WF, NT>, m, a);
+  return cudaLaunchKernelEx(&cfg, few_tokens_kernel<WF, NT, MT>, m, a);
 }
 
 }  // namespace
 
 int few_format(bool quantised, WeightFormat wf) { return quantised ? static_cast<int>(wf) : kBf16; }
 
+template <int WF>
+static cudaError_t prepare_format(int* blocks_per_sm) {
+  cudaError_t e = prepare<WF, 1, 8>(blocks_per_sm);
+  if (e == cudaSuccess) e = prepare<WF, 1, 16>(blocks_per_sm);
+  return e == cudaSuccess ? prepare<WF, 2, 16>(blocks_per_sm) : e;
+}
+
 cudaError_t few_tokens_prepare(int format, int* blocks_per_sm) {
   *blocks_per_sm = 1;
-  auto both = [&](auto one, auto two) {
-    const cudaError_t e = one(blocks_per_sm);
-    return e == cudaSuccess ? two(blocks_per_sm) : e;
-  };
   switch (format) {
-    case kBf16: return both(prepare<kBf16, 1>, prepare<kBf16, 2>);
-    case kWInt8: return both(prepare<kWInt8, 1>, prepare<kWInt8, 2>);
-    case kWInt4: return both(prepare<kWInt4, 1>, prepare<kWInt4, 2>);
-    case kWFp8: return both(prepare<kWFp8, 1>, prepare<kWFp8, 2>);
+    case kBf16: return prepare_format<kBf16>(blocks_per_sm);
+    case kWInt8: return prepare_format<kWInt8>(blocks_per_sm);
+    case kWInt4: return prepare_format<kWInt4>(blocks_per_sm);
+    case kWFp8: return prepare_format<kWFp8>(blocks_per_sm);
   }
   return cudaErrorInvalidValue;
 }
@@ -747,15 +780,24 @@ bool few_token_maps(int format, const FewArgs& a, FewMaps* m) {
   return ok;
 }
 
+// More than 8 tokens: parts of up to 16 where experts have more than 4 of the
+// tokens on average.  Below, the few experts that have more than 8 are taken
+// in two parts, their weights read twice; the smaller stages leave half as
+// many again of them in flight.
+template <int WF>
+static cudaError_t launch_format(const FewMaps& m, const FewArgs& a, int grid, cudaStream_t s) {
+  if (a.n <= 8) return launch<WF, 1, 8>(m, a, grid, s);
+  return a.n * a.k > 4 * a.E ? launch<WF, 2, 16>(m, a, grid, s) : launch<WF, 1, 16>(m, a, grid, s);
+}
+
 cudaError_t launch_few_tokens(int format, const FewMaps& m, const FewArgs& a, int grid, cudaStream_t s) {
   if (a.n <= 0) return cudaSuccess;
   if (a.n > kMaxTokens || a.E > kMaxExperts || a.k > kMaxK || grid <= 0) return cudaErrorInvalidValue;
-  const bool two = a.n > 8;
   switch (format) {
-    case kBf16: return two ? launch<kBf16, 2>(m, a, grid, s) : launch<kBf16, 1>(m, a, grid, s);
-    case kWInt8: return two ? launch<kWInt8, 2>(m, a, grid, s) : launch<kWInt8, 1>(m, a, grid, s);
-    case kWInt4: return two ? launch<kWInt4, 2>(m, a, grid, s) : launch<kWInt4, 1>(m, a, grid, s);
-    case kWFp8: return two ? launch<kWFp8, 2>(m, a, grid, s) : launch<kWFp8, 1>(m, a, grid, s);
+    case kBf16: return launch_format<kBf16>(m, a, grid, s);
+    case kWInt8: return launch_format<kWInt8>(m, a, grid, s);
+    case kWInt4: return launch_format<kWInt4>(m, a, grid, s);
+    case kWFp8: return launch_format<kWFp8>(m, a, grid, s);
   }
   return cudaErrorInvalidValue;
 }

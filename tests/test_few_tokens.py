@@ -120,6 +120,29 @@ def test_matches_the_formulas(wdtype, n, d, f, E, k):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("wdtype", ["bf16", "int4"])
+@pytest.mark.parametrize("n", [8, 9, 16])
+def test_all_tokens_of_many_choose_the_same_experts(wdtype, n):
+    """More than 8 tokens at experts that are few of many: each expert is taken in parts."""
+    shape = synth.custom_shape("few", n, 512, 512, 48, 4, wdtype=wdtype, seed=14)
+    r = Run(shape)
+    bias = np.zeros(48, np.float32)
+    bias[[3, 17, 18, 40]] = [50, 40, 30, 20]
+    r.layer.bias = bias
+    w = {m: torch.from_numpy(getattr(r.layer, m)).cuda() for m in ("wr", "wg", "wu", "wd")}
+    if wdtype == "bf16":
+        w = {m: t.view(torch.bfloat16) for m, t in w.items()}
+    else:
+        w["wr"] = w["wr"].view(torch.bfloat16)
+    opt = {m: torch.from_numpy(getattr(r.layer, m)).cuda() if getattr(r.layer, m) is not None else None
+           for m in ("sg", "su", "sd", "zg", "zu", "zd")}
+    r.m = cb.MoELayer(n, 512, 512, 48, 4, w["wr"], w["wg"], w["wu"], w["wd"], router_bias=torch.from_numpy(bias).cuda(),
+                      s_gate=opt["sg"], s_up=opt["su"], s_down=opt["sd"], z_gate=opt["zg"], z_up=opt["zu"],
+                      z_down=opt["zd"], wdtype=wdtype)
+    check(r)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("router", ["raw", "hash"])
 @pytest.mark.parametrize("n,E,k", [(1, 8, 2), (11, 20, 3)])
 def test_other_routers(router, n, E, k):
