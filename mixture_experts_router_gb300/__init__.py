@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libcbmoe.so")
@@ -74,6 +75,10 @@ class cb_fp4_matmul_t(ctypes.Structure):
                 ("out", ctypes.c_void_p), ("ld_out", ctypes.c_int64), ("status", ctypes.c_void_p)]
 
 
+_FP4_MATMUL = struct.Struct("@2i3q6Pi4xPPqP")  # cb_fp4_matmul_t
+assert _FP4_MATMUL.size == ctypes.sizeof(cb_fp4_matmul_t)
+
+
 class CbMoeError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
         self.status = status
@@ -119,7 +124,7 @@ def load_library(path: str = LIB_PATH):
     lib.cb_fp4_scale_bytes.argtypes = [ctypes.c_int32, i64, i64, ctypes.POINTER(ctypes.c_uint64)]
     lib.cb_fp4_quantize.argtypes = [ctypes.c_int32, vp, ctypes.c_int32, i64, i64, i64, vp, vp, vp, vp]
     lib.cb_fp4_dequantize.argtypes = [ctypes.c_int32, vp, vp, vp, i64, i64, vp, ctypes.c_int32, i64, vp]
-    lib.cb_fp4_matmul.argtypes = [ctypes.POINTER(cb_fp4_matmul_t), vp]
+    lib.cb_fp4_matmul.argtypes = [vp, vp]
     for name in FP4_SYMBOLS:
         getattr(lib, name).restype = i32
     lib.cb_status_string.argtypes = [i32]
@@ -369,23 +374,68 @@ class MoELayer:
 
 
 # ------------------------------ 4-bit floats with block scales, over torch tensors
-def _check(st, what):
-    if st != CB_OK:
-        raise CbMoeError(st, what)
+# A decode step makes these calls with a few microseconds of GPU work each, so
+# the way to the library is kept short: torch is looked up once, and a call on
+# torch's current stream and device enters no context.
+_torch = None
+_FP4_TYPES = {}
+
+
+def _load_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _FP4_TYPES.update({torch.bfloat16: CB_T_BF16, torch.float32: CB_T_F32})
+        _torch = torch
+    return _torch
+
+
+def _stream_here(device, stream):
+    """torch's current stream on `device` (an index) as an int, or None where a context has to
+    be entered first: another stream is asked for, or another device is current."""
+    if device < 0:
+        raise ValueError("4-bit matrices are made from and kept in CUDA tensors")
+    if stream is None and device == _torch.cuda.current_device():
+        return _torch._C._cuda_getCurrentRawStream(device)
+    return None
+
+
+class _On:
+    """The device and the stream (torch's current one unless given) as a context."""
+
+    def __init__(self, device, stream):
+        self.device = _torch.cuda.device(device)
+        self.stream = _torch.cuda.stream(_torch.cuda.current_stream(device) if stream is None else stream)
+
+    def __enter__(self):
+        self.device.__enter__()
+        self.stream.__enter__()
+
+    def __exit__(self, *a):
+        self.stream.__exit__(*a)
+        self.device.__exit__(*a)
 
 
 def _fp4_type(dtype):
-    import torch
-    if dtype not in (torch.bfloat16, torch.float32):
+    kind = _FP4_TYPES.get(dtype)
+    if kind is None:
         raise ValueError(f"4-bit floats are made from and turned into bfloat16 or float32, not {dtype}")
-    return CB_T_BF16 if dtype == torch.bfloat16 else CB_T_F32
+    return kind
 
 
-def _row_stride(t, what):
-    """Elements between the rows of a 2-D CUDA tensor whose rows are contiguous."""
-    if t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: a 2-D CUDA tensor with contiguous rows is needed")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+def _fp4_scale_bytes(format, rows, cols):
+    """cb_fp4_scale_bytes in Python."""
+    if cols <= 0 or cols % 32:
+        raise CbMoeError(CB_ERR_INVALID_ARG, f"a 4-bit matrix of {cols} columns (a positive multiple of 32 is needed)")
+    return -(-rows // 128) * -(-cols // (4 * FP4_BLOCK[format])) * 512
+
+
+def _row_stride(t):
+    """Elements between the rows of a 2-D tensor whose rows are contiguous."""
+    s = t.stride()
+    if len(s) != 2 or (s[1] != 1 and t.shape[1] > 1):
+        raise ValueError(f"a 2-D tensor with contiguous rows is needed, not one of shape {tuple(t.shape)}, strides {s}")
+    return s[0] if s[0] >= t.shape[1] or t.shape[0] > 1 else t.shape[1]
 
 
 class Fp4Matrix:
@@ -394,70 +444,78 @@ class Fp4Matrix:
     `tensor_scale` (fp32 [1]).  One matrix per expert: codes [E][rows][cols / 2], scales of
     E arrays, tensor_scale [E]."""
 
+    __slots__ = ("format", "rows", "cols", "groups", "codes", "scales", "tensor_scale")
+
     def __init__(self, format, rows, cols, codes, scales, tensor_scale=None):
-        import torch
+        torch = _load_torch()
         if format not in FP4_FORMATS:
             raise ValueError(f"unknown 4-bit format {format!r}: one of {sorted(FP4_FORMATS)}")
-        self.format, self.rows, self.cols = format, int(rows), int(cols)
-        self.groups = int(codes.shape[0]) if codes.dim() == 3 else 1
-        st, need = cb_fp4_scale_bytes(FP4_FORMATS[format], self.rows, self.cols)
-        _check(st, "cb_fp4_scale_bytes")
-        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or \
-                tuple(codes.shape[-2:]) != (self.rows, self.cols // 2) or scales.numel() != need * self.groups or \
-                not (codes.is_contiguous() and scales.is_contiguous()):
-            raise ValueError(f"codes {tuple(codes.shape)} {codes.dtype}, scales {tuple(scales.shape)} {scales.dtype}: "
-                             f"not a contiguous {format} matrix of {self.rows} x {self.cols} ({need} scale bytes)")
-        if (tensor_scale is not None) != (format == "nv") or \
-                (tensor_scale is not None and (tensor_scale.dtype != torch.float32 or tensor_scale.numel() != self.groups
-                                               or not tensor_scale.is_contiguous())):
-            raise ValueError("format nv has one fp32 tensor scale per matrix, format mx none")
+        self.format, self.rows, self.cols = format, rows, cols
         self.codes, self.scales, self.tensor_scale = codes, scales, tensor_scale
-
-
-def _stream_of(stream, device):
-    """The stream to run on (torch's current one unless given), for use as a context too, so
-    that a result allocated within it belongs to it."""
-    import torch
-    return torch.cuda.current_stream(device) if stream is None else stream
+        shape = codes.shape
+        self.groups = groups = shape[0] if len(shape) == 3 else 1
+        need = _fp4_scale_bytes(format, rows, cols) * groups
+        if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8 or shape[-2:] != (rows, cols // 2) or \
+                scales.numel() != need or not (codes.is_contiguous() and scales.is_contiguous()):
+            raise ValueError(f"codes {tuple(shape)} {codes.dtype}, scales {tuple(scales.shape)} {scales.dtype}: not "
+                             f"{groups} contiguous {format} matrices of {rows} x {cols} ({need} scale bytes)")
+        if (tensor_scale is not None) != (format == "nv") or \
+                (tensor_scale is not None and (tensor_scale.dtype is not torch.float32 or
+                                               tensor_scale.numel() != groups or not tensor_scale.is_contiguous())):
+            raise ValueError("format nv has one fp32 tensor scale per matrix, format mx none")
 
 
 def fp4_quantize(x, format, tensor_scale=None, stream=None) -> Fp4Matrix:
     """x (2-D, bf16 or fp32, contiguous rows with any stride) as an Fp4Matrix; format "nv"
     takes tensor_scale, an fp32 CUDA tensor of one element, e.g. max|x| / (6 * 448).  Runs on
-    `stream`, or on torch's current stream."""
-    import torch
-    if format not in FP4_FORMATS:
+    `stream`, or on torch's current stream; its result belongs to that stream."""
+    torch = _load_torch()
+    fmt, kind, ld = FP4_FORMATS.get(format), _fp4_type(x.dtype), _row_stride(x)
+    if fmt is None:
         raise ValueError(f"unknown 4-bit format {format!r}: one of {sorted(FP4_FORMATS)}")
-    kind, ld = _fp4_type(x.dtype), _row_stride(x, "fp4_quantize")
-    rows, cols = int(x.shape[0]), int(x.shape[1])
-    if tensor_scale is not None and (tensor_scale.dtype != torch.float32 or tensor_scale.numel() != 1):
+    rows, cols = x.shape
+    nbytes = _fp4_scale_bytes(format, rows, cols)
+    if tensor_scale is not None and (tensor_scale.dtype is not torch.float32 or tensor_scale.numel() != 1):
         raise ValueError("tensor_scale: one fp32 element")
-    st, nbytes = cb_fp4_scale_bytes(FP4_FORMATS[format], rows, cols)
-    _check(st, "cb_fp4_quantize")
-    s = _stream_of(stream, x.device)
-    with torch.cuda.device(x.device), torch.cuda.stream(s):
-        codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=x.device)
-        scales = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-        _check(cb_fp4_quantize(FP4_FORMATS[format], x.data_ptr(), kind, rows, cols, ld, _ptr(tensor_scale),
-                               codes.data_ptr(), scales.data_ptr(), s.cuda_stream), "cb_fp4_quantize")
-    return Fp4Matrix(format, rows, cols, codes, scales, tensor_scale)
+    device = x.get_device()
+    s = _stream_here(device, stream)
+    if s is None:
+        with _On(device, stream):
+            return fp4_quantize(x, format, tensor_scale)
+    m = Fp4Matrix.__new__(Fp4Matrix)
+    m.format, m.rows, m.cols, m.groups, m.tensor_scale = format, rows, cols, 1, tensor_scale
+    m.codes = codes = x.new_empty((rows, cols // 2), dtype=torch.uint8)
+    m.scales = scales = x.new_empty(nbytes, dtype=torch.uint8)
+    st = (_lib or load_library()).cb_fp4_quantize(
+        fmt, x.data_ptr(), kind, rows, cols, ld, None if tensor_scale is None else tensor_scale.data_ptr(),
+        codes.data_ptr(), scales.data_ptr(), s)
+    if st != CB_OK:
+        raise CbMoeError(st, "cb_fp4_quantize")
+    return m
 
 
 def fp4_dequantize(m: Fp4Matrix, dtype=None, out=None, stream=None):
     """The values that m stands for, as bf16 (or `dtype`), or into `out` (2-D, contiguous rows
     with any stride)."""
-    import torch
+    torch = _load_torch()
+    codes, g = m.codes, m.tensor_scale
     if m.groups != 1:
         raise ValueError("fp4_dequantize: one matrix at a time")
-    s = _stream_of(stream, m.codes.device)
-    with torch.cuda.device(m.codes.device), torch.cuda.stream(s):
-        if out is None:
-            out = torch.empty((m.rows, m.cols), dtype=dtype or torch.bfloat16, device=m.codes.device)
-        elif tuple(out.shape) != (m.rows, m.cols) or (dtype is not None and out.dtype != dtype):
-            raise ValueError(f"out {tuple(out.shape)} {out.dtype} for a {m.rows} x {m.cols} matrix")
-        _check(cb_fp4_dequantize(FP4_FORMATS[m.format], m.codes.data_ptr(), m.scales.data_ptr(), _ptr(m.tensor_scale),
-                                 m.rows, m.cols, out.data_ptr(), _fp4_type(out.dtype),
-                                 _row_stride(out, "fp4_dequantize"), s.cuda_stream), "cb_fp4_dequantize")
+    if out is not None and (tuple(out.shape) != (m.rows, m.cols) or (dtype is not None and out.dtype != dtype)):
+        raise ValueError(f"out {tuple(out.shape)} {out.dtype} for a {m.rows} x {m.cols} matrix")
+    kind = _fp4_type((dtype or torch.bfloat16) if out is None else out.dtype)
+    device = codes.get_device()
+    s = _stream_here(device, stream)
+    if s is None:
+        with _On(device, stream):
+            return fp4_dequantize(m, dtype, out)
+    if out is None:
+        out = codes.new_empty((m.rows, m.cols), dtype=dtype or torch.bfloat16)
+    st = (_lib or load_library()).cb_fp4_dequantize(
+        FP4_FORMATS[m.format], codes.data_ptr(), m.scales.data_ptr(), None if g is None else g.data_ptr(), m.rows,
+        m.cols, out.data_ptr(), kind, _row_stride(out), s)
+    if st != CB_OK:
+        raise CbMoeError(st, "cb_fp4_dequantize")
     return out
 
 
@@ -466,21 +524,28 @@ def fp4_matmul(a: Fp4Matrix, b: Fp4Matrix, dtype=None, out=None, tile_offsets=No
     CUDA tensor [b.groups + 1], cb_routing_view_t's) rows 128 tile_offsets[e] .. 128
     tile_offsets[e + 1] of `a` meet b's e-th matrix; rows past the last are not written.
     `status`: an int32 CUDA tensor that receives CB_ERR_TIMEOUT if a device-side wait ran out."""
-    import torch
+    torch = _load_torch()
     if a.format != b.format or a.cols != b.cols or a.groups != 1:
         raise ValueError(f"fp4_matmul: {a.groups} x [{a.rows} x {a.cols}] {a.format} by [{b.rows} x {b.cols}] {b.format}")
     for name, t, n in (("tile_offsets", tile_offsets, b.groups + 1), ("status", status, 1)):
-        if t is not None and (t.dtype != torch.int32 or not t.is_cuda or t.numel() != n or not t.is_contiguous()):
+        if t is not None and (t.dtype is not torch.int32 or not t.is_cuda or t.numel() != n or not t.is_contiguous()):
             raise ValueError(f"fp4_matmul: {name} is a contiguous int32 CUDA tensor of {n}")
-    s = _stream_of(stream, a.codes.device)
-    with torch.cuda.device(a.codes.device), torch.cuda.stream(s):
-        if out is None:
-            out = torch.empty((a.rows, b.rows), dtype=dtype or torch.bfloat16, device=a.codes.device)
-        elif tuple(out.shape) != (a.rows, b.rows) or (dtype is not None and out.dtype != dtype):
-            raise ValueError(f"out {tuple(out.shape)} {out.dtype} for a {a.rows} x {b.rows} product")
-        p = cb_fp4_matmul_t(FP4_FORMATS[a.format], _fp4_type(out.dtype), a.rows, b.rows, a.cols, a.codes.data_ptr(),
-                            a.scales.data_ptr(), _ptr(a.tensor_scale), b.codes.data_ptr(), b.scales.data_ptr(),
-                            _ptr(b.tensor_scale), b.groups, _ptr(tile_offsets), out.data_ptr(),
-                            _row_stride(out, "fp4_matmul"), _ptr(status))
-        _check(cb_fp4_matmul(p, s.cuda_stream), "cb_fp4_matmul")
+    if out is not None and (tuple(out.shape) != (a.rows, b.rows) or (dtype is not None and out.dtype != dtype)):
+        raise ValueError(f"out {tuple(out.shape)} {out.dtype} for a {a.rows} x {b.rows} product")
+    kind = _fp4_type((dtype or torch.bfloat16) if out is None else out.dtype)
+    device = a.codes.get_device()
+    s = _stream_here(device, stream)
+    if s is None:
+        with _On(device, stream):
+            return fp4_matmul(a, b, dtype, out, tile_offsets, status)
+    if out is None:
+        out = a.codes.new_empty((a.rows, b.rows), dtype=dtype or torch.bfloat16)
+    nv = a.tensor_scale is not None
+    st = (_lib or load_library()).cb_fp4_matmul(_FP4_MATMUL.pack(
+        FP4_FORMATS[a.format], kind, a.rows, b.rows, a.cols, a.codes.data_ptr(), a.scales.data_ptr(),
+        a.tensor_scale.data_ptr() if nv else 0, b.codes.data_ptr(), b.scales.data_ptr(),
+        b.tensor_scale.data_ptr() if nv else 0, b.groups, 0 if tile_offsets is None else tile_offsets.data_ptr(),
+        out.data_ptr(), _row_stride(out), 0 if status is None else status.data_ptr()), s)
+    if st != CB_OK:
+        raise CbMoeError(st, "cb_fp4_matmul")
     return out

@@ -3,7 +3,8 @@
 //
 //   1. logits     l[t][e] = x[t] . Wr[e] + b[e]: one expert at a time per
 //                 block, the block's warps splitting d;
-//      -- grid barrier --
+//      -- grid barrier (none with few experts and tokens: every block then
+//         takes all the logits) --
 //   2. gate       every block takes the top-k of all n tokens from the n x E
 //                 logits (warp_gate) and lists the experts that any token chose;
 //   3. gate/up    H[t k + s][j] = bf16( SiLU(g) * u ), g and u the dot products
@@ -220,34 +221,63 @@ struct Block {
   }
 
   // ------------------------------------------------------------- 1. logits
+  // Few experts and tokens: every block takes all the logits itself, which
+  // is sooner than a barrier; a warp has one expert's share of d.
+  __device__ __forceinline__ static bool logits_here(const FewArgs& p) {
+    return p.ids == nullptr && p.E <= kUserWarps && p.n * p.E <= 32;
+  }
+  __device__ __forceinline__ void own_logits() {
+    const int per = kUserWarps / p.E, e = warp / per, part = warp % per;  // warps of an expert
+    if (user() && e < p.E) {
+      float sum[kMaxTokens];
+#pragma unroll
+      for (int t = 0; t < kMaxTokens; ++t) sum[t] = 0.f;
+#pragma unroll 4
+      for (int c = (part * 32 + lane) * 8; c < p.d; c += per * 256) add_products(e, c, sum);
+      put_logits(sum);
+    }
+    __syncthreads();
+    float v = 0.f;
+    const int i = threadIdx.x, te = i % p.E, t = i / p.E;
+    if (i < p.n * p.E) {
+      for (int w = 0; w < per; ++w) v += s.part[te * per + w][t];
+      v += p.bias != nullptr ? p.bias[te] : 0.f;
+    }
+    __syncthreads();
+    if (i < p.n * p.E) s.logit[i] = v;
+  }
+  __device__ __forceinline__ void add_products(int e, int c, float (&sum)[kMaxTokens]) const {
+    const uint4 wv = __ldg(reinterpret_cast<const uint4*>(p.wr + static_cast<int64_t>(e) * p.d + c));
+    const uint32_t wu[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+    for (int t = 0; t < kMaxTokens; ++t) {
+      if (t >= p.n) break;
+      const uint4 xv = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.d + c));
+      const uint32_t xu[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sum[t] = fmaf(__uint_as_float(xu[i] << 16), __uint_as_float(wu[i] << 16), sum[t]);
+        sum[t] = fmaf(__uint_as_float(xu[i] & 0xFFFF0000u), __uint_as_float(wu[i] & 0xFFFF0000u), sum[t]);
+      }
+    }
+  }
+  __device__ __forceinline__ void put_logits(float (&sum)[kMaxTokens]) {
+#pragma unroll
+    for (int t = 0; t < kMaxTokens; ++t) {
+      if (t >= p.n) break;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum[t] += __shfl_xor_sync(0xffffffffu, sum[t], o);
+      if (lane == 0) s.part[warp][t] = sum[t];
+    }
+  }
   __device__ __forceinline__ void logits() {
     for (int e = blockIdx.x; e < p.E; e += gridDim.x) {
       if (user()) {
         float sum[kMaxTokens];
 #pragma unroll
         for (int t = 0; t < kMaxTokens; ++t) sum[t] = 0.f;
-        for (int c = threadIdx.x * 8; c < p.d; c += kUsers * 8) {
-          const uint4 wv = __ldg(reinterpret_cast<const uint4*>(p.wr + static_cast<int64_t>(e) * p.d + c));
-          const uint32_t wu[4] = {wv.x, wv.y, wv.z, wv.w};
-#pragma unroll
-          for (int t = 0; t < kMaxTokens; ++t) {
-            if (t >= p.n) break;
-            const uint4 xv = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.d + c));
-            const uint32_t xu[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              sum[t] = fmaf(__uint_as_float(xu[i] << 16), __uint_as_float(wu[i] << 16), sum[t]);
-              sum[t] = fmaf(__uint_as_float(xu[i] & 0xFFFF0000u), __uint_as_float(wu[i] & 0xFFFF0000u), sum[t]);
-            }
-          }
-        }
-#pragma unroll
-        for (int t = 0; t < kMaxTokens; ++t) {
-          if (t >= p.n) break;
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) sum[t] += __shfl_xor_sync(0xffffffffu, sum[t], o);
-          if (lane == 0) s.part[warp][t] = sum[t];
-        }
+        for (int c = threadIdx.x * 8; c < p.d; c += kUsers * 8) add_products(e, c, sum);
+        put_logits(sum);
       }
       __syncthreads();
       if (threadIdx.x < p.n) {
@@ -262,7 +292,7 @@ struct Block {
   // --------------------------------------------------------------- 2. gate
   __device__ __forceinline__ void gate() {
     for (int e = threadIdx.x; e < kMaxExperts; e += kThreads) s.mask[e] = 0u;
-    if (p.ids == nullptr)
+    if (p.ids == nullptr && !logits_here(p))
       for (int i = threadIdx.x; i < p.n * p.E; i += kThreads) s.logit[i] = __ldcg(p.logits + i);
     __syncthreads();
     if (p.ids == nullptr) {
@@ -293,7 +323,8 @@ struct Block {
     const int e = threadIdx.x;
     const uint32_t all = e < p.E ? s.mask[e] : 0u;
     const int parts = (__popc(all) + NT * 8 - 1) / (NT * 8);
-    int sum = parts;
+    const int mine = parts | __popc(all) << 16;  // parts, and rows of H: scanned together
+    int sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
       const int below = __shfl_up_sync(0xffffffffu, sum, o);
@@ -302,32 +333,20 @@ struct Block {
     if (e < kMaxExperts && lane == 31) s.warp_parts[warp] = sum;
     __syncthreads();
     if (e < kMaxExperts) {
-      int base = sum - parts;
-      for (int i = 0; i < warp; ++i) base += s.warp_parts[i];
+      int before = sum - mine;
+      for (int i = 0; i < warp; ++i) before += s.warp_parts[i];
+      const int base = before & 0xFFFF;
+      int row = before >> 16;
       uint32_t m = all;
       for (int a = base; a < base + parts; ++a) {
         s.act[a] = static_cast<int16_t>(e);
         int c = 0;
         for (; m != 0u && c < NT * 8; m &= m - 1u, ++c) s.tok[a][c] = static_cast<uint8_t>(__ffs(m) - 1);
         s.count[a] = static_cast<uint8_t>(c);
+        s.row0[a] = static_cast<int16_t>(row);  // a part's tokens one after the other
+        row += c;
       }
       if (e == kMaxExperts - 1) s.n_act = base + parts;
-    }
-    __syncthreads();
-    if (warp == 0) {  // rows of H: a part's tokens one after the other
-      int base = 0;
-      for (int a0 = 0; a0 < s.n_act; a0 += 32) {
-        const int a = a0 + lane;
-        const int c = a < s.n_act ? s.count[a] : 0;
-        int rows = c;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-          const int below = __shfl_up_sync(0xffffffffu, rows, o);
-          if (lane >= o) rows += below;
-        }
-        if (a < s.n_act) s.row0[a] = static_cast<int16_t>(base + rows - c);
-        base += __shfl_sync(0xffffffffu, rows, 31);
-      }
     }
     __syncthreads();
   }
@@ -673,7 +692,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const unsigned blocks = gridDim.x;
   const unsigned expected = blocks + static_cast<unsigned>(p.test_stall);
   bool ok = true;
-  if (p.ids == nullptr) {
+  if (Block<WF, NT, MT>::logits_here(p)) {
+    __syncthreads();
+    b.own_logits();
+  } else if (p.ids == nullptr) {
     b.logits();
     ok = grid_barrier_wait(p.bar, expected, p.wait_limit_ns, p.err, &b.s.ok);
     if (threadIdx.x == 0) grid_barrier_depart(p.bar, blocks);

@@ -231,13 +231,13 @@ def test_a_token_keeps_to_itself():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("router", ["softmax", "hash"])
-def test_a_barrier_that_is_not_met_is_reported(router):
+@pytest.mark.parametrize("router,n", [("softmax", 6), ("softmax", 4), ("hash", 4)])
+def test_a_barrier_that_is_not_met_is_reported(router, n):
     """The handle's test flag makes the grid barriers wait for a block that does not exist, for
-    1 ms: the first one, or (the hash router's launch has no first) the one before the down
-    products, with copies already on their way.  The call ends, the status says why, and the
-    handle's barrier words are whole again: the next call ends the same way."""
-    shape = synth.with_router(synth.custom_shape("few", 4, 512, 1024, 8, 2, seed=6), router)
+    1 ms: the first one, or (launches of few logits, or of the hash router's, have no first) the
+    one before the down products, with copies already on their way.  The call ends, the status
+    says why, and the handle's barrier words are whole again: the next call ends the same way."""
+    shape = synth.with_router(synth.custom_shape("few", n, 512, 1024, 8, 2, seed=6), router)
     r = Run(shape, flags=cb.CB_FLAG_TEST_STALL_DISPATCH | cb.CB_FLAG_GUARDS)
     out = torch.empty(r.x.shape, dtype=torch.bfloat16, device="cuda")
     for _ in range(2):
