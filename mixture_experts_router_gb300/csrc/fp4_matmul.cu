@@ -5,9 +5,9 @@
 // elements; kind::mxf4nvf4: an e4m3 scale per 16) takes K = 64 codes per
 // instruction from shared memory and the scales of both operands from tensor
 // memory, and sums in fp32.  Codes arrive by TMA (128-byte swizzled rows of
-// K = 256), scales as whole 512-byte tiles of 128 rows x 4 blocks, the order
-// in which tcgen05.cp puts them into tensor memory: 4 columns per tile, the
-// same for each quarter of the lanes.  A row's tail past k is zero codes
+// K = 256), scales as whole 512-byte tiles of 128 rows x 4 blocks, each of
+// which becomes 4 columns of tensor memory, the same for each quarter of the
+// lanes.  A row's tail past k is zero codes
 // (TMA's fill); scale words past the array are not loaded, and no
 // instruction runs past k.
 //
@@ -22,7 +22,7 @@
 //    order.
 //
 // Per CTA: warp 0 TMA producer, warp 1 tensor memory and MMA issuer, warps
-// 2..5 epilogue.  Stage s of the ring has its own scale columns in tensor
+// 4..7 scales from shared into tensor memory, warps 8.. epilogue.  Stage s of the ring has its own scale columns in tensor
 // memory, so a stage's commit frees both.  All waits are bounded.
 #include <cuda_bf16.h>
 
@@ -37,8 +37,14 @@ constexpr int BP = 128;            // rows of the M side
 constexpr int BK = 256;            // elements per stage: 128 bytes of codes
 constexpr int ROW_BYTES = BK / 2;
 constexpr int STAGES = 4;
-constexpr int THREADS = 192;
-constexpr int EPI_WARP0 = 2;
+constexpr int SCALE_WARP0 = 4;     // 4 warps, one per quarter of the lanes
+constexpr int EPI_WARP0 = 8;
+// epilogue warps: a quarter of the lanes each, and with two per quarter half
+// of the columns
+template <int BN, bool SWAP>
+constexpr int EPI_WARPS = !SWAP && BN == 256 ? 8 : 4;
+template <int BN, bool SWAP>
+constexpr int THREADS = (EPI_WARP0 + EPI_WARPS<BN, SWAP>) * 32;
 constexpr int P_BYTES = BP * ROW_BYTES;
 
 constexpr int pow2_at_least(int v) {
@@ -99,8 +105,31 @@ struct Tiles {
   }
 };
 
+// One warp hands the accumulator back: its loads are done.
+__device__ __forceinline__ void release(uint64_t* tempty, int lane) {
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(tempty);
+}
+
+__device__ __forceinline__ void store_f32(float* o, const uint32_t (&v)[32], float alpha, int left, int vec) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float4 f = make_float4(alpha * __uint_as_float(v[4 * j]), alpha * __uint_as_float(v[4 * j + 1]),
+                                 alpha * __uint_as_float(v[4 * j + 2]), alpha * __uint_as_float(v[4 * j + 3]));
+    if (vec && 4 * j + 4 <= left) {
+      reinterpret_cast<float4*>(o)[j] = f;
+    } else {
+      if (4 * j < left) o[4 * j] = f.x;
+      if (4 * j + 1 < left) o[4 * j + 1] = f.y;
+      if (4 * j + 2 < left) o[4 * j + 2] = f.z;
+      if (4 * j + 3 < left) o[4 * j + 3] = f.w;
+    }
+  }
+}
+
 template <int FMT, int BN, bool SWAP>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__((THREADS<BN, SWAP>), 1)
     fp4_matmul_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
                       const Fp4MatmulArgs a, const int ksplit, const int vec) {
   using C = Cfg<FMT, BN>;
@@ -108,7 +137,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE);
   uint64_t* empty = full + STAGES;
-  uint64_t* tfull = empty + STAGES;
+  uint64_t* sfull = empty + STAGES;  // a stage's scales are in tensor memory
+  uint64_t* tfull = sfull + STAGES;
   uint64_t* tempty = tfull + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 1);
 
@@ -120,9 +150,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&sfull[s], 4);
     }
     mbar_init(tfull, 1);
-    mbar_init(tempty, 4);
+    mbar_init(tempty, EPI_WARPS<BN, SWAP>);
     fence_barrier_init();
     prefetch_tensormap(&tm_p);
     prefetch_tensormap(&tm_q);
@@ -194,25 +225,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_after();
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const int s = static_cast<int>(it % STAGES);
-          if (!mbar_wait(&full[s], static_cast<uint32_t>((it / STAGES) & 1), a.wait_limit_ns)) {
+          const uint32_t phase = static_cast<uint32_t>((it / STAGES) & 1);
+          if (!mbar_wait(&full[s], phase, a.wait_limit_ns) || !mbar_wait(&sfull[s], phase, a.wait_limit_ns)) {
             set_error(a.status, kErrTimeout);
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t st = smem_u32(smem + s * C::STAGE);
-          const uint32_t sf = st + P_BYTES + C::Q_BYTES;
           const uint32_t sfp = tmem + C::SF0 + static_cast<uint32_t>(s) * C::SF_COLS;
           const uint32_t sfq = sfp + 4 * C::W;
-          const int nw = min(C::W, words - kb * C::W);
-#pragma unroll
-          for (int w = 0; w < C::W; ++w)
-            if (w < nw) {
-              tc_copy_scales(sfp + 4 * w, scale_desc(sf + w * kScaleTileBytes));
-#pragma unroll
-              for (int j = 0; j < C::QT; ++j)
-                tc_copy_scales(sfq + 4 * (w * C::QT + j), scale_desc(sf + (1 + j) * C::SF_BYTES + w * kScaleTileBytes));
-            }
           const uint64_t pd = sw128_desc(st), qd = sw128_desc(st + P_BYTES);
           const int steps = min(4, (a.k - kb * BK + 63) / 64);
 #pragma unroll
@@ -232,9 +254,49 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_commit(tfull);
       }
     }
-  } else {
+  } else if (warp >= SCALE_WARP0 && warp < EPI_WARP0) {
+    // ------------------------------------------------ scales into tensor memory
+    // A quarter's lane i takes bytes [16 i, 16 i + 16) of every scale tile (the
+    // scales of rows i, i + 32, i + 64, i + 96): 4 columns, the same in each
+    // quarter.  (tcgen05.cp does this too, but in the MMA's own queue: its
+    // copies, 12 per stage of an NV product, took longer than the stage's MMAs.)
+    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    int64_t it = 0;
+    bool ok = true;
+    for (int i = worker; ok && i < tiles.total; i += workers)
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const int s = static_cast<int>(it % STAGES);
+        if (!mbar_wait(&full[s], static_cast<uint32_t>((it / STAGES) & 1), a.wait_limit_ns)) {
+          set_error(a.status, kErrTimeout);
+          ok = false;
+          break;
+        }
+        const uint8_t* sf = smem + s * C::STAGE + P_BYTES + C::Q_BYTES + lane * 16;
+        const uint32_t to = lanes + C::SF0 + static_cast<uint32_t>(s) * C::SF_COLS;
+        // words past the array hold an earlier stage's scales, which no MMA uses
+        uint32_t v[4 * C::W * (1 + C::QT)];
+#pragma unroll
+        for (int w = 0; w < C::W; ++w)
+#pragma unroll
+          for (int j = 0; j <= C::QT; ++j) {
+            const uint4 x = *reinterpret_cast<const uint4*>(sf + j * C::SF_BYTES + w * kScaleTileBytes);
+            const int c = j == 0 ? 4 * w : 4 * (C::W + w * C::QT + j - 1);
+            v[c] = x.x;
+            v[c + 1] = x.y;
+            v[c + 2] = x.z;
+            v[c + 3] = x.w;
+          }
+        tmem_store<4 * C::W * (1 + C::QT)>(to, v);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sfull[s]);
+      }
+  } else if (warp >= EPI_WARP0) {
     const int q = warp & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    constexpr int COLS = SWAP ? BN : BN / (EPI_WARPS<BN, SWAP> / 4);  // of this warp
+    const int col0 = SWAP ? 0 : (warp - EPI_WARP0) / 4 * COLS;
     uint32_t tphase = 0;
     for (int i = worker; i < tiles.total; i += workers, tphase ^= 1u) {
       const Tile t = tiles.at(i, a);
@@ -256,53 +318,48 @@ __global__ void __launch_bounds__(THREADS, 1)
       } else {
         const float alpha = FMT == kFp4Nv ? __ldg(a.a_tensor_scale) * __ldg(a.b_tensor_scale + t.e) : 1.f;
         const int row = t.p0 + q * 32 + lane;
+        const int first = t.q0 + col0;
+        if (a.out_f32) {
+          float* out = static_cast<float*>(a.out) + static_cast<int64_t>(row) * a.ld_out + first;
 #pragma unroll 1
-        for (int c0 = 0; c0 < BN; c0 += 32) {
-          if (t.q0 + c0 >= a.n) break;
-          uint32_t v[32];
-          tmem_load32(lanes + c0, v);
-          const int left = a.n - (t.q0 + c0);
-          const int64_t at = static_cast<int64_t>(row) * a.ld_out + t.q0 + c0;
-          if (row < a.m && a.out_f32) {
-            float* o = static_cast<float*>(a.out) + at;
+          for (int c0 = 0; c0 < COLS && first + c0 < a.n; c0 += 32) {
+            uint32_t v[32];
+            tmem_load32(lanes + col0 + c0, v);
+            if (row < a.m) store_f32(out + c0, v, alpha, a.n - first - c0, vec);
+            __syncwarp();  // whole again for the next load
+          }
+          release(tempty, lane);
+        } else {
+          // all columns as bf16 in registers, the accumulator handed on, then the stores
+          uint32_t h[COLS / 2];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 f = make_float4(alpha * __uint_as_float(v[4 * j]), alpha * __uint_as_float(v[4 * j + 1]),
-                                           alpha * __uint_as_float(v[4 * j + 2]), alpha * __uint_as_float(v[4 * j + 3]));
-              if (vec && 4 * j + 4 <= left) {
-                reinterpret_cast<float4*>(o)[j] = f;
-              } else {
-                if (4 * j < left) o[4 * j] = f.x;
-                if (4 * j + 1 < left) o[4 * j + 1] = f.y;
-                if (4 * j + 2 < left) o[4 * j + 2] = f.z;
-                if (4 * j + 3 < left) o[4 * j + 3] = f.w;
-              }
+          for (int c0 = 0; c0 < COLS; c0 += 32) {
+            uint32_t v[32];
+            tmem_load32(lanes + col0 + c0, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const __nv_bfloat162 b =
+                  __floats2bfloat162_rn(alpha * __uint_as_float(v[2 * j]), alpha * __uint_as_float(v[2 * j + 1]));
+              h[c0 / 2 + j] = *reinterpret_cast<const uint32_t*>(&b);
             }
-          } else if (row < a.m) {
-            uint16_t* o = static_cast<uint16_t*>(a.out) + at;
+          }
+          release(tempty, lane);
+          uint16_t* out = static_cast<uint16_t*>(a.out) + static_cast<int64_t>(row) * a.ld_out + first;
+          if (row < a.m) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t h[4];
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(alpha * __uint_as_float(v[8 * j + 2 * u]),
-                                                               alpha * __uint_as_float(v[8 * j + 2 * u + 1]));
-                h[u] = *reinterpret_cast<const uint32_t*>(&b);
-              }
-              if (vec && 8 * j + 8 <= left) {
-                reinterpret_cast<uint4*>(o)[j] = make_uint4(h[0], h[1], h[2], h[3]);
+            for (int c = 0; c < COLS; c += 8) {
+              const int left = a.n - first - c;
+              if (vec && left >= 8) {
+                *reinterpret_cast<uint4*>(out + c) = make_uint4(h[c / 2], h[c / 2 + 1], h[c / 2 + 2], h[c / 2 + 3]);
               } else {
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
-                  if (8 * j + u < left) o[8 * j + u] = static_cast<uint16_t>(h[u / 2] >> (16 * (u & 1)));
+                  if (u < left) out[c + u] = static_cast<uint16_t>(h[(c + u) / 2] >> (16 * (u & 1)));
               }
             }
           }
-          __syncwarp();  // whole again for the next load
+          __syncwarp();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(tempty);
       }
     }
   }
@@ -357,7 +414,7 @@ cudaError_t launch(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s) {
   const int64_t elem = a.out_f32 ? 4 : 2;
   const int vec = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && a.ld_out * elem % 16 == 0 ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.blockDim = dim3(THREADS<BN, SWAP>, 1, 1);
   cfg.dynamicSmemBytes = C::BYTES;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
