@@ -36,7 +36,6 @@ namespace {
 constexpr int BP = 128;            // rows of the M side
 constexpr int BK = 256;            // elements per stage: 128 bytes of codes
 constexpr int ROW_BYTES = BK / 2;
-constexpr int STAGES = 4;
 constexpr int SCALE_WARP0 = 4;     // 4 warps, one per quarter of the lanes
 constexpr int EPI_WARP0 = 8;
 // epilogue warps: a quarter of the lanes each, and with two per quarter half
@@ -53,8 +52,9 @@ constexpr int pow2_at_least(int v) {
   return p;
 }
 
-template <int FMT, int BN>
+template <int FMT, int BN, bool SWAP>
 struct Cfg {
+  static constexpr int STAGES = SWAP && BN >= 64 ? 3 : 4;  // (two CTAs per SM when swapped)
   static constexpr int W = BK / (4 * kFp4Block<FMT>);   // scale words per stage: 2 (MX) or 4 (NV)
   static constexpr int QT = (BN + 127) / 128;           // scale row tiles of the N side
   static constexpr int Q_BYTES = BN * ROW_BYTES;
@@ -65,7 +65,7 @@ struct Cfg {
   static constexpr int TMEM = pow2_at_least(SF0 + STAGES * SF_COLS);
   static constexpr int BYTES = STAGES * STAGE + 1024 + 256;
   static_assert(STAGE % 1024 == 0 && Q_BYTES % 1024 == 0 && BYTES <= 232448 && TMEM <= 512, "layout");
-  static_assert(STAGES * STAGE >= BN * BP * 4 || BN > 128, "the ring holds the partial sums");
+  static_assert(STAGES * STAGE >= BN * BP * 4 || !SWAP, "the ring holds the partial sums");
 };
 
 // A tile of the output: M-side rows from p0, N-side rows from q0.
@@ -112,27 +112,78 @@ __device__ __forceinline__ void release(uint64_t* tempty, int lane) {
   if (lane == 0) mbar_arrive(tempty);
 }
 
-__device__ __forceinline__ void store_f32(float* o, const uint32_t (&v)[32], float alpha, int left, int vec) {
+// Eight 16-byte chunks (4 registers each) of a lane's row become one chunk of
+// each of its 8-lane group's rows: h[4 i ..] of lane l is then chunk l % 8 of
+// row i of the group, and the group's 8 lanes store 128 contiguous bytes of a
+// row (a lane storing its own row's chunks would write half sectors of 32 rows
+// at a time, which took longer than the MMAs of k = 4096).
+__device__ __forceinline__ void transpose_chunks(uint32_t* h, int lane) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float4 f = make_float4(alpha * __uint_as_float(v[4 * j]), alpha * __uint_as_float(v[4 * j + 1]),
-                                 alpha * __uint_as_float(v[4 * j + 2]), alpha * __uint_as_float(v[4 * j + 3]));
-    if (vec && 4 * j + 4 <= left) {
-      reinterpret_cast<float4*>(o)[j] = f;
-    } else {
-      if (4 * j < left) o[4 * j] = f.x;
-      if (4 * j + 1 < left) o[4 * j + 1] = f.y;
-      if (4 * j + 2 < left) o[4 * j + 2] = f.z;
-      if (4 * j + 3 < left) o[4 * j + 3] = f.w;
+  for (int b = 1; b < 8; b *= 2) {
+    const bool upper = lane & b;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      if (c & b) continue;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        uint32_t& lo = h[4 * c + r];
+        uint32_t& hi = h[4 * (c | b) + r];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? lo : hi, b);
+        lo = upper ? got : lo;
+        hi = upper ? hi : got;
+      }
     }
   }
+}
+
+// A warp's 32 rows x 128 bytes, lane = row, h its 32 words: to out (the first
+// row's first byte, rows `pitch` bytes apart), `rows` of them, `elems`
+// elements of ELEM bytes each.  vec: rows start on 16 bytes.
+template <int ELEM>
+__device__ __forceinline__ void store_rows(uint8_t* out, int64_t pitch, uint32_t* h, int rows, int elems, int vec,
+                                           int lane) {
+  if (vec) {
+    constexpr int PER = 16 / ELEM;  // elements of a chunk
+    transpose_chunks(h, lane);
+    uint8_t* o = out + (lane & 24) * pitch + (lane & 7) * 16;
+    const int left = elems - (lane & 7) * PER;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if ((lane & 24) + i >= rows) continue;
+      if (left >= PER) {
+        *reinterpret_cast<uint4*>(o + i * pitch) = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+      } else {
+#pragma unroll
+        for (int u = 0; u < PER - 1; ++u) {
+          if (u >= left) break;
+          if constexpr (ELEM == 4)
+            reinterpret_cast<uint32_t*>(o + i * pitch)[u] = h[4 * i + u];
+          else
+            reinterpret_cast<uint16_t*>(o + i * pitch)[u] = static_cast<uint16_t>(h[4 * i + u / 2] >> (16 * (u & 1)));
+        }
+      }
+    }
+  } else if (lane < rows) {
+    uint8_t* o = out + lane * pitch;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if constexpr (ELEM == 4) {
+        if (i < elems) reinterpret_cast<uint32_t*>(o)[i] = h[i];
+      } else {
+        if (2 * i < elems) reinterpret_cast<uint16_t*>(o)[2 * i] = static_cast<uint16_t>(h[i]);
+        if (2 * i + 1 < elems) reinterpret_cast<uint16_t*>(o)[2 * i + 1] = static_cast<uint16_t>(h[i] >> 16);
+      }
+    }
+  }
+  __syncwarp();
 }
 
 template <int FMT, int BN, bool SWAP>
 __global__ void __launch_bounds__((THREADS<BN, SWAP>), 1)
     fp4_matmul_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
                       const Fp4MatmulArgs a, const int ksplit, const int vec) {
-  using C = Cfg<FMT, BN>;
+  using C = Cfg<FMT, BN, SWAP>;
+  constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE);
@@ -317,18 +368,20 @@ __global__ void __launch_bounds__((THREADS<BN, SWAP>), 1)
         }
       } else {
         const float alpha = FMT == kFp4Nv ? __ldg(a.a_tensor_scale) * __ldg(a.b_tensor_scale + t.e) : 1.f;
-        const int row = t.p0 + q * 32 + lane;
+        const int row0 = t.p0 + q * 32, rows = a.m - row0;  // the warp's rows (all 32 but in the last tile)
         const int first = t.q0 + col0;
         if (a.out_f32) {
-          float* out = static_cast<float*>(a.out) + static_cast<int64_t>(row) * a.ld_out + first;
+          uint8_t* out = static_cast<uint8_t*>(a.out) + (static_cast<int64_t>(row0) * a.ld_out + first) * 4;
 #pragma unroll 1
           for (int c0 = 0; c0 < COLS && first + c0 < a.n; c0 += 32) {
             uint32_t v[32];
             tmem_load32(lanes + col0 + c0, v);
-            if (row < a.m) store_f32(out + c0, v, alpha, a.n - first - c0, vec);
-            __syncwarp();  // whole again for the next load
+            if (c0 + 32 >= COLS || first + c0 + 32 >= a.n) release(tempty, lane);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(alpha * __uint_as_float(v[j]));
+            store_rows<4>(out + c0 * 4, a.ld_out * 4, v, rows, a.n - first - c0, vec, lane);
           }
-          release(tempty, lane);
+          if (first >= a.n) release(tempty, lane);
         } else {
           // all columns as bf16 in registers, the accumulator handed on, then the stores
           uint32_t h[COLS / 2];
@@ -344,21 +397,10 @@ __global__ void __launch_bounds__((THREADS<BN, SWAP>), 1)
             }
           }
           release(tempty, lane);
-          uint16_t* out = static_cast<uint16_t*>(a.out) + static_cast<int64_t>(row) * a.ld_out + first;
-          if (row < a.m) {
+          uint8_t* out = static_cast<uint8_t*>(a.out) + (static_cast<int64_t>(row0) * a.ld_out + first) * 2;
 #pragma unroll
-            for (int c = 0; c < COLS; c += 8) {
-              const int left = a.n - first - c;
-              if (vec && left >= 8) {
-                *reinterpret_cast<uint4*>(out + c) = make_uint4(h[c / 2], h[c / 2 + 1], h[c / 2 + 2], h[c / 2 + 3]);
-              } else {
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                  if (u < left) out[c + u] = static_cast<uint16_t>(h[(c + u) / 2] >> (16 * (u & 1)));
-              }
-            }
-          }
-          __syncwarp();
+          for (int c = 0; c < COLS; c += 64)
+            if (first + c < a.n) store_rows<2>(out + c * 2, a.ld_out * 2, h + c / 2, rows, a.n - first - c, vec, lane);
         }
       }
     }
@@ -367,20 +409,41 @@ __global__ void __launch_bounds__((THREADS<BN, SWAP>), 1)
   if constexpr (SWAP) {
     __syncwarp();
     cluster_sync();  // every rank's partial sums are in its shared memory
-    if (warp >= EPI_WARP0) {
-      const int r = (warp - EPI_WARP0) * 32 + lane;  // weight row of the tile
-      const int col = worker * BP + r;
-      const float alpha = FMT == kFp4Nv ? __ldg(a.a_tensor_scale) * __ldg(a.b_tensor_scale) : 1.f;
-      for (int t = rank; t < a.m; t += ksplit) {
-        const uint32_t at = smem_u32(reinterpret_cast<float*>(smem) + t * BP + r);
-        float v = 0.f;
-        for (int j = 0; j < ksplit; ++j) v += ld_shared_cluster_f32(mapa_shared(at, j));
-        if (col < a.n) {
-          const int64_t o = static_cast<int64_t>(t) * a.ld_out + col;
-          if (a.out_f32)
-            static_cast<float*>(a.out)[o] = alpha * v;
-          else
-            static_cast<uint16_t*>(a.out)[o] = __bfloat16_as_ushort(__float2bfloat16_rn(alpha * v));
+    // a token per warp, four output columns per lane; the ranks share the tokens
+    const int col = worker * BP + lane * 4;
+    const float alpha = FMT == kFp4Nv ? __ldg(a.a_tensor_scale) * __ldg(a.b_tensor_scale) : 1.f;
+    for (int t = rank + ksplit * warp; t < a.m; t += ksplit * (THREADS<BN, SWAP> / 32)) {
+      const uint32_t at = smem_u32(reinterpret_cast<float*>(smem) + t * BP + lane * 4);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int j = 0; j < ksplit; ++j) {
+        const float4 x = ld_shared_cluster_f32x4(mapa_shared(at, j));
+        v.x += x.x;
+        v.y += x.y;
+        v.z += x.z;
+        v.w += x.w;
+      }
+      const float f[4] = {alpha * v.x, alpha * v.y, alpha * v.z, alpha * v.w};
+      const int64_t o = static_cast<int64_t>(t) * a.ld_out + col;
+      if (a.out_f32) {
+        float* out = static_cast<float*>(a.out) + o;
+        if (vec && col + 4 <= a.n) {
+          *reinterpret_cast<float4*>(out) = make_float4(f[0], f[1], f[2], f[3]);
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (col + u < a.n) out[u] = f[u];
+        }
+      } else {
+        uint16_t* out = static_cast<uint16_t*>(a.out) + o;
+        const __nv_bfloat162 b0 = __floats2bfloat162_rn(f[0], f[1]), b1 = __floats2bfloat162_rn(f[2], f[3]);
+        const uint2 h = make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
+        if (vec && col + 4 <= a.n) {
+          *reinterpret_cast<uint2*>(out) = h;
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (col + u < a.n) out[u] = static_cast<uint16_t>((u < 2 ? h.x : h.y) >> (16 * (u & 1)));
         }
       }
     }
@@ -402,7 +465,7 @@ bool map_codes(CUtensorMap* m, const uint8_t* codes, int64_t rows, int k, int bo
 
 template <int FMT, int BN, bool SWAP>
 cudaError_t launch(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s) {
-  using C = Cfg<FMT, BN>;
+  using C = Cfg<FMT, BN, SWAP>;
   auto kernel = fp4_matmul_kernel<FMT, BN, SWAP>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
   if (e != cudaSuccess) return e;
@@ -421,7 +484,15 @@ cudaError_t launch(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s) {
   int ksplit = 1;
   if (SWAP) {
     const int tiles = (a.n + BP - 1) / BP, stages = (a.k + BK - 1) / BK;
-    while (ksplit < 8 && 4 * ksplit <= stages && 2 * ksplit * tiles <= 3 * num_sms) ksplit *= 2;
+    // CTAs enough for every SM, or for two per SM where they keep 4 stages
+    // each; all are resident at once (112 tiles of k = 4096: 9.6 us unsplit, 8.5
+    // in two, 11.7 in four; 32 tiles: 11.5, 8.9, 6.6, and 7.3 in eight)
+    while (ksplit < 8) {
+      const int64_t ctas = 2ll * ksplit * tiles;
+      const int each = stages / (2 * ksplit);
+      if (each < 2 || ctas > (each >= 4 ? 2 : 1) * num_sms) break;
+      ksplit *= 2;
+    }
     cfg.gridDim = dim3(tiles * ksplit, 1, 1);
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = ksplit;
