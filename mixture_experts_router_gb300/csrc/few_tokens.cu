@@ -19,7 +19,9 @@
 // a ring of stages of 512 (int4: 256) bytes per row, with the same stretch of the chosen
 // tokens' activations beside them.
 //
-//   warp 16     weights, one TMA copy per stage.  The tensor maps split a row
+// A block is two halves, each with a ring, two feeding warps and 8 users:
+//
+//   weights (1 thread)  one TMA copy per stage.  The tensor maps split a row
 //               into 128-byte chunks as a dimension of its own, so that one
 //               copy brings that much of every row of the tile; there is a
 //               map for each height.  A copy costs its SM about 55 ns and then
@@ -27,20 +29,24 @@
 //               bound the kernel (a bulk copy per row held it at 2 TB/s).  It
 //               runs ahead across tiles, experts and the second barrier: step
 //               4's weights do not wait for H.
-//   warp 17     tokens, by cp.async into the stage, in the weights' swizzle.
-//   warps 0-15  two sets of 8 that take the stages in turn; a warp owns an
-//               eighth of a stage's stretch, reads fragments with wide loads,
-//               widens quantised codes to bf16 exactly in registers and issues
-//               mma.sync m16n8k16 (A: weight rows, B: the expert's own tokens,
-//               in their order).  A dot product does not depend on the order
-//               of its terms, so a thread's k-slots are consecutive elements.
+//   tokens (1 warp)     by cp.async into the stage, in the weights' swizzle.
+//   users (8 warps)     a warp owns an eighth of a stage's stretch, reads
+//               fragments with wide loads, widens quantised codes to bf16
+//               exactly in registers and issues mma.sync m16n8k16 (A: weight
+//               rows, B: the expert's own tokens, in their order).  A dot
+//               product does not depend on the order of its terms, so a
+//               thread's k-slots are consecutive elements.
+//
+// The halves take a block's step-3 tiles in turn, so that one joins its
+// warps' sums while the other streams; in step 4 they take the experts in
+// turn (or, of few experts, half of k each).
 //
 // The balance: the parts' features (step 3) and the output columns
 // (step 4) are cut into one contiguous share per block, in steps of 4 (the
 // rows of the smallest copy).
 //
 // Every sum is fp32 in a fixed order (mma accumulators, experts in ascending
-// order, then the 16 warps in order), so results do not change from run to
+// order, then the warps in order), so results do not change from run to
 // run.  H is rounded to bf16 as everywhere in the layer: it is the MMA's
 // operand.  Rows past the tile's end and columns past the expert's tokens
 // read the last one again, and their sums are dropped.
@@ -58,18 +64,21 @@ namespace {
 
 constexpr int kUsers = 512;             // threads that use the ring
 constexpr int kUserWarps = kUsers / 32;
-constexpr int kWeightWarp = kUserWarps;
-constexpr int kTokenWarp = kUserWarps + 1;
-constexpr int kThreads = kUsers + 64;
+constexpr int kHalves = 2;
+constexpr int kWeightWarp = kUserWarps;             // one per half
+constexpr int kTokenWarp = kWeightWarp + kHalves;
+constexpr int kThreads = (kTokenWarp + kHalves) * 32;
 constexpr int kRows = 32;               // weight rows of a tile: two m16 fragments
-constexpr int kAlong = 8;               // warps along a row's stretch: a set
-constexpr int kSets = kUserWarps / kAlong;
+constexpr int kAlong = 8;               // warps along a row's stretch: a half's users
+constexpr int kFewParts = 8;            // parts below which the halves split k in step 4
 constexpr int kShareStep = kFewRowStep; // shares and tiles are multiples of this many rows
 constexpr int kMaxTokens = kFewTokens;
 constexpr int kMaxExperts = 256;
 constexpr int kMaxK = 16;
+constexpr int kLogitTokens = 4;
 constexpr int kMaxParts = kMaxTokens * kMaxK;
-constexpr uint32_t kUserBar = 1;        // named barrier of the ring's users
+constexpr uint32_t kUserBar = 1;        // named barriers: all users, and each half's
+constexpr uint32_t kHalfBar = 2;
 constexpr int kSmemLimit = 232448;
 
 // Weight formats of the kernel: the quantised ones as in WeightFormat.
@@ -115,12 +124,9 @@ struct Geo {
   static constexpr int kStage = kWeightBytes + NT * 8 * kTokBytes;
   static constexpr int kShared = (static_cast<int>(sizeof(Shared<NT, MT>)) + 256 + 1023) / 1024 * 1024;
   static constexpr int kFit = (kSmemLimit - kShared - 1024) / kStage;
-  // A whole number of turns of the sets: a stage always belongs to the same
-  // set, whose waits then see every phase of its barrier (a set that met a
-  // stage only every second time could take one phase for the other).
-  static constexpr int kStages = (kFit < 12 ? kFit : 12) / kSets * kSets;
-  static constexpr int kBytes = 1024 + kShared + kStages * kStage;
-  static_assert(kStages >= 4 && 16 * kStages <= 256 && kStage % 1024 == 0, "ring");
+  static constexpr int kStages = (kFit < 12 ? kFit : 12) / kHalves;  // of each half
+  static constexpr int kBytes = 1024 + kShared + kHalves * kStages * kStage;
+  static_assert(kStages >= 2 && 16 * kHalves * kStages <= 256 && kStage % 1024 == 0, "ring");
 };
 
 // Byte of 16-byte unit `unit` of 128-byte line `line` of a swizzled area.
@@ -178,8 +184,7 @@ struct Block {
   uint8_t* ring;
   RingPos<G::kStages> pos;  // the producer's, or a user's, place in the ring
   bool ok = true;           // no wait of this thread has run out
-  int turn = 0;             // set of warps that takes the next stage
-  const int warp, lane;
+  const int warp, lane, half;
   int first_w;
   int first_tok[G::kStepElems / 8];
 
@@ -187,11 +192,12 @@ struct Block {
       : p(p_),
         maps(maps_),
         s(*reinterpret_cast<Shared<NT, MT>*>(smem)),
-        full(reinterpret_cast<uint64_t*>(smem + G::kShared - 256)),
+        full(reinterpret_cast<uint64_t*>(smem + G::kShared - 256) + half_of_warp() * 2 * G::kStages),
         empty(full + G::kStages),
-        ring(smem + G::kShared),
+        ring(smem + G::kShared + half_of_warp() * G::kStages * G::kStage),
         warp(threadIdx.x / 32),
-        lane(threadIdx.x % 32) {
+        lane(threadIdx.x % 32),
+        half(half_of_warp()) {
     const int along = warp % kAlong, q = lane & 3;
     const int byte = along * G::kStep + q * (G::kStep / 4);  // of a row's stretch
     first_w = swizzled(byte / 128, byte % 128 / 16) + byte % 16;
@@ -201,12 +207,17 @@ struct Block {
       first_tok[i] = swizzled(unit / 8, unit % 8);
     }
     if (threadIdx.x == 0) {
-      for (int i = 0; i < G::kStages; ++i) {
-        mbar_init(&full[i], 1 + 32);  // the weights' announcement, the token warp's lanes
-        mbar_init(&empty[i], kAlong);
+      for (int i = 0; i < kHalves * G::kStages; ++i) {
+        uint64_t* bars = full + i / G::kStages * 2 * G::kStages + i % G::kStages;
+        mbar_init(bars, 1 + 32);  // full: the weights' announcement, the token warp's lanes
+        mbar_init(bars + G::kStages, kAlong);
       }
       fence_barrier_init();
     }
+  }
+  __device__ __forceinline__ static int half_of_warp() {
+    const int warp = threadIdx.x / 32;
+    return warp < kUserWarps ? warp / kAlong : (warp - kUserWarps) % kHalves;
   }
   __device__ __forceinline__ bool user() const { return warp < kUserWarps; }
 
@@ -221,20 +232,48 @@ struct Block {
   }
 
   // ------------------------------------------------------------- 1. logits
-  // Few experts and tokens: every block takes all the logits itself, which
-  // is sooner than a barrier; a warp has one expert's share of d.
+  // Four tokens at a time: their loads go out together.
+  // sum[i] += x[t0 + i] . Wr[e] over 8 elements from c, for the tokens there are
+  __device__ __forceinline__ void add_products(int e, int t0, int c, float (&sum)[kLogitTokens]) const {
+    const uint4 wv = __ldg(reinterpret_cast<const uint4*>(p.wr + static_cast<int64_t>(e) * p.d + c));
+    uint4 xv[kLogitTokens];
+#pragma unroll
+    for (int i = 0; i < kLogitTokens; ++i)
+      xv[i] = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(min(t0 + i, p.n - 1)) * p.d + c));
+    const uint32_t wu[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+    for (int i = 0; i < kLogitTokens; ++i) {
+      const uint32_t xu[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sum[i] = fmaf(__uint_as_float(xu[j] << 16), __uint_as_float(wu[j] << 16), sum[i]);
+        sum[i] = fmaf(__uint_as_float(xu[j] & 0xFFFF0000u), __uint_as_float(wu[j] & 0xFFFF0000u), sum[i]);
+      }
+    }
+  }
+  __device__ __forceinline__ void put_logits(int t0, float (&sum)[kLogitTokens]) {
+#pragma unroll
+    for (int i = 0; i < kLogitTokens; ++i) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+      if (lane == 0) s.part[warp][(t0 + i) % kMaxTokens] = sum[i];
+    }
+  }
+  // Few experts, tokens and elements: every block takes all the logits itself,
+  // which is sooner than a barrier; a warp has one expert's share of d.  (Of 8
+  // experts x d 256: 2.2 us against 3.3; x d 4096: 5.5 against 3.1, all blocks
+  // fetching the same rows.)
   __device__ __forceinline__ static bool logits_here(const FewArgs& p) {
-    return p.ids == nullptr && p.E <= kUserWarps && p.n * p.E <= 32;
+    return p.ids == nullptr && p.E <= kUserWarps && p.n * p.E <= 32 && p.E * p.d <= 8192;
   }
   __device__ __forceinline__ void own_logits() {
     const int per = kUserWarps / p.E, e = warp / per, part = warp % per;  // warps of an expert
     if (user() && e < p.E) {
-      float sum[kMaxTokens];
-#pragma unroll
-      for (int t = 0; t < kMaxTokens; ++t) sum[t] = 0.f;
-#pragma unroll 4
-      for (int c = (part * 32 + lane) * 8; c < p.d; c += per * 256) add_products(e, c, sum);
-      put_logits(sum);
+      for (int t0 = 0; t0 < p.n; t0 += kLogitTokens) {
+        float sum[kLogitTokens] = {};
+        for (int c = (part * 32 + lane) * 8; c < p.d; c += per * 256) add_products(e, t0, c, sum);
+        put_logits(t0, sum);
+      }
     }
     __syncthreads();
     float v = 0.f;
@@ -246,44 +285,22 @@ struct Block {
     __syncthreads();
     if (i < p.n * p.E) s.logit[i] = v;
   }
-  __device__ __forceinline__ void add_products(int e, int c, float (&sum)[kMaxTokens]) const {
-    const uint4 wv = __ldg(reinterpret_cast<const uint4*>(p.wr + static_cast<int64_t>(e) * p.d + c));
-    const uint32_t wu[4] = {wv.x, wv.y, wv.z, wv.w};
-#pragma unroll
-    for (int t = 0; t < kMaxTokens; ++t) {
-      if (t >= p.n) break;
-      const uint4 xv = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.d + c));
-      const uint32_t xu[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        sum[t] = fmaf(__uint_as_float(xu[i] << 16), __uint_as_float(wu[i] << 16), sum[t]);
-        sum[t] = fmaf(__uint_as_float(xu[i] & 0xFFFF0000u), __uint_as_float(wu[i] & 0xFFFF0000u), sum[t]);
-      }
-    }
-  }
-  __device__ __forceinline__ void put_logits(float (&sum)[kMaxTokens]) {
-#pragma unroll
-    for (int t = 0; t < kMaxTokens; ++t) {
-      if (t >= p.n) break;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum[t] += __shfl_xor_sync(0xffffffffu, sum[t], o);
-      if (lane == 0) s.part[warp][t] = sum[t];
-    }
-  }
+  // Otherwise an expert and up to four tokens per block, its warps splitting d.
   __device__ __forceinline__ void logits() {
-    for (int e = blockIdx.x; e < p.E; e += gridDim.x) {
+    const int items = p.E * ((p.n + kLogitTokens - 1) / kLogitTokens);
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+      const int e = item % p.E, t0 = item / p.E * kLogitTokens;
       if (user()) {
-        float sum[kMaxTokens];
-#pragma unroll
-        for (int t = 0; t < kMaxTokens; ++t) sum[t] = 0.f;
-        for (int c = threadIdx.x * 8; c < p.d; c += kUsers * 8) add_products(e, c, sum);
-        put_logits(sum);
+        float sum[kLogitTokens] = {};
+        for (int c = threadIdx.x * 8; c < p.d; c += kUsers * 8) add_products(e, t0, c, sum);
+        put_logits(t0, sum);
       }
       __syncthreads();
-      if (threadIdx.x < p.n) {
+      const int t = t0 + threadIdx.x;
+      if (threadIdx.x < kLogitTokens && t < p.n) {
         float v = 0.f;
-        for (int i = 0; i < kUserWarps; ++i) v += s.part[i][threadIdx.x];
-        p.logits[threadIdx.x * p.E + e] = v + (p.bias != nullptr ? p.bias[e] : 0.f);
+        for (int i = 0; i < kUserWarps; ++i) v += s.part[i][t];
+        p.logits[t * p.E + e] = v + (p.bias != nullptr ? p.bias[e] : 0.f);
       }
       __syncthreads();
     }
@@ -386,14 +403,14 @@ struct Block {
     return ok;
   }
 
-  // Token warp: the stages of a tile whose weights' rows are row_bytes long,
-  // for `count` tokens' rows; mine: this lane's (lane < count).
-  __device__ __forceinline__ void feed_tokens(int row_bytes, int count, const uint16_t* mine) {
-    for (int at = 0; at < row_bytes && ok; at += kSeg, pos.next()) {
+  // Token warp: the stages of a tile over the weights' bytes [at, end) of a
+  // row, for `count` tokens' rows; mine: this lane's (lane < count).
+  __device__ __forceinline__ void feed_tokens(int at, int end, int count, const uint16_t* mine) {
+    for (; at < end && ok; at += kSeg, pos.next()) {
       wait(&empty[pos.stage], pos.phase ^ 1u);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
-      const int units = min(kSeg, row_bytes - at) / 16 * kElems<WF> * 2 / 16;  // of 16 bytes
+      const int units = min(kSeg, end - at) / 16 * kElems<WF> * 2 / 16;  // of 16 bytes
       const int first = at / 16 * kElems<WF> * 2 + lane * 16;
       uint8_t* dst = stage() + G::kWeightBytes;
 #pragma unroll 2
@@ -432,20 +449,13 @@ struct Block {
     }
   }
 
-  // User: the tile's stages in order; the warp's set takes every second one.
-  // acc += its fragments of those, over the first `halves` m16 halves and
-  // n-tiles `tiles`.  True: it took one.
-  __device__ __forceinline__ bool use_stages(int row_bytes, int halves, int tiles, const Places& at,
+  // User: acc += its fragments of the tile's stages over the bytes [b, end)
+  // of a row, for the first `halves` m16 fragments and n-tiles `tiles`.
+  __device__ __forceinline__ void use_stages(int b, int end, int halves, int tiles, const Places& at,
                                              const uint32_t (&zz)[4], float (&acc)[2][NT][4]) {
-    bool took = false;
-    for (int b = 0; b < row_bytes; b += kSeg, turn ^= 1) {
-      if (turn != warp / kAlong) {
-        pos.next();
-        continue;
-      }
+    for (; b < end; b += kSeg) {
       wait(&full[pos.stage], pos.phase);
-      if (warp % kAlong * G::kStep < row_bytes - b) {
-        took = true;
+      if (warp % kAlong * G::kStep < end - b) {
         const uint8_t* st = stage();
         uint4 v[4];
 #pragma unroll
@@ -482,7 +492,6 @@ struct Block {
       if (lane == 0) mbar_arrive(&empty[pos.stage]);
       pos.next();
     }
-    return took;
   }
   __device__ __forceinline__ void clear(float (&v)[2][NT][4]) {
 #pragma unroll
@@ -492,17 +501,21 @@ struct Block {
   }
 
   // --------------------------------------------------------- 3. gate and up
-  // Calls f(active expert, first feature, features) for each tile of the
-  // block's share: at most 16 features of one interleave block of one expert.
+  // Calls f(part, first feature, features) for each tile of this half of the
+  // block's share: at most 16 features of one interleave block of one part,
+  // of a size that gives the halves equally many.
   template <typename F>
   __device__ __forceinline__ void up_tiles(F&& f) {
     const int64_t total = static_cast<int64_t>(s.n_act) * p.f / kShareStep;
     int j = static_cast<int>(total * blockIdx.x / gridDim.x) * kShareStep;
     const int end = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x) * kShareStep;
+    const int turns = (end - j + 16 * kHalves - 1) / (16 * kHalves);
+    const int size = turns > 0 ? (end - j + turns * kHalves * kShareStep - 1) / (turns * kHalves * kShareStep) * kShareStep
+                               : 0;
     int a = j / p.f, feat = j - a * p.f;
-    while (j < end) {
-      const int rows = min(16, min(end - j, p.gu_block - feat % p.gu_block));
-      f(a, feat, rows);
+    for (int i = 0; j < end; i ^= 1) {
+      const int rows = min(size, min(end - j, p.gu_block - feat % p.gu_block));
+      if (i == half) f(a, feat, rows);
       j += rows;
       feat += rows;
       if (feat == p.f) {
@@ -523,7 +536,7 @@ struct Block {
   __device__ __forceinline__ void feed_x(int row_bytes) {
     up_tiles([&](int a, int, int) {
       const int count = s.count[a];
-      feed_tokens(row_bytes, count, p.x + (lane < count ? static_cast<int64_t>(s.tok[a][lane]) * p.d : 0));
+      feed_tokens(0, row_bytes, count, p.x + (lane < count ? static_cast<int64_t>(s.tok[a][lane]) * p.d : 0));
     });
   }
 
@@ -545,8 +558,8 @@ struct Block {
       }
       float acc[2][NT][4];
       clear(acc);
-      use_stages(row_bytes, rows > 8 ? 2 : 1, count > 8 ? 2 : 1, at, zz, acc);
-      named_bar_sync(kUserBar, kUsers);  // the last tile's sums are read
+      use_stages(0, row_bytes, rows > 8 ? 2 : 1, count > 8 ? 2 : 1, at, zz, acc);
+      named_bar_sync(kHalfBar + half, kAlong * 32);  // the last tile's sums are read
       // row 16 m + r of a warp's sums: gate (r < 8) or up of feature 8 m + r % 8
 #pragma unroll
       for (int m = 0; m < 2; ++m)
@@ -556,15 +569,15 @@ struct Block {
           *reinterpret_cast<float2*>(&s.red[warp][16 * m + 8 + g][n * 8 + 2 * q]) =
               make_float2(acc[m][n][2], acc[m][n][3]);
         }
-      named_bar_sync(kUserBar, kUsers);
-      const int r = threadIdx.x % 16, t = threadIdx.x / 16;
+      named_bar_sync(kHalfBar + half, kAlong * 32);
+      const int r = threadIdx.x % 16, t = threadIdx.x % (kAlong * 32) / 16;
       if (t < count && r < rows) {
         const int row = (r & 8) * 2 + (r & 7);
         float gs = 0.f, us = 0.f;
 #pragma unroll
-        for (int w = 0; w < kUserWarps; ++w) {
-          gs += s.red[w][row][t];
-          us += s.red[w][row + 8][t];
+        for (int w = 0; w < kAlong; ++w) {
+          gs += s.red[half * kAlong + w][row][t];
+          us += s.red[half * kAlong + w][row + 8][t];
         }
         if constexpr (WF != kBf16) {
           const int64_t sc = static_cast<int64_t>(e) * p.f + feat0 + r;
@@ -578,40 +591,58 @@ struct Block {
   }
 
   // ------------------------------------------------- 4. down and combine
-  // Calls f(first column, columns, active expert) over the block's share:
-  // tiles of at most 32 output columns, all active experts for each.
-  template <typename F>
-  __device__ __forceinline__ void down_tiles(F&& f) {
+  // Calls f(first column, columns, part, first and last byte of a row) for
+  // this half of the block's share, tiles of at most 32 output columns, and
+  // done(first column, columns) after each: the halves take the parts in
+  // turn, or half of each row where there are few.
+  template <typename F, typename D>
+  __device__ __forceinline__ void down_tiles(int row_bytes, F&& f, D&& done) {
     const int64_t total = p.d / kShareStep;
     const int end = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x) * kShareStep;
-    for (int c = static_cast<int>(total * blockIdx.x / gridDim.x) * kShareStep; c < end; c += kRows)
-      for (int a = 0; a < s.n_act; ++a) f(c, min(kRows, end - c), a);
+    const bool split = s.n_act < kFewParts;
+    const int mid = (row_bytes + kSeg * kHalves - 1) / (kSeg * kHalves) * kSeg;
+    const int from = split && half == 1 ? mid : 0, to = split && half == 0 ? min(mid, row_bytes) : row_bytes;
+    for (int c = static_cast<int>(total * blockIdx.x / gridDim.x) * kShareStep; c < end; c += kRows) {
+      const int rows = min(kRows, end - c);
+      for (int a = split ? 0 : half; a < s.n_act; a += split ? 1 : kHalves)
+        if (from < to) f(c, rows, a, from, to);
+      done(c, rows);
+    }
   }
 
   __device__ __forceinline__ void feed_down(int row_bytes) {
-    down_tiles([&](int c, int rows, int a) {
-      const CUtensorMap* map = &maps.down[rows / kShareStep - 1];
-      const int row = s.act[a] * p.d + c;
-      for (int at = 0; at < row_bytes && open_stage(rows); at += kSeg, pos.next())
-        tma_load_3d(stage(), map, &full[pos.stage], 0, at / 128, row);
-    });
+    down_tiles(
+        row_bytes,
+        [&](int c, int rows, int a, int from, int to) {
+          const CUtensorMap* map = &maps.down[rows / kShareStep - 1];
+          const int row = s.act[a] * p.d + c;
+          for (int at = from; at < to && open_stage(rows); at += kSeg, pos.next())
+            tma_load_3d(stage(), map, &full[pos.stage], 0, at / 128, row);
+        },
+        [](int, int) {});
   }
   __device__ __forceinline__ void feed_h(int row_bytes) {
-    down_tiles([&](int, int, int a) {
-      const int count = s.count[a];
-      feed_tokens(row_bytes, count, p.h + static_cast<int64_t>(s.row0[a] + min(lane, count - 1)) * p.f);
-    });
+    down_tiles(
+        row_bytes,
+        [&](int, int, int a, int from, int to) {
+          const int count = s.count[a];
+          feed_tokens(from, to, count, p.h + static_cast<int64_t>(s.row0[a] + min(lane, count - 1)) * p.f);
+        },
+        [](int, int) {});
   }
   // After a second barrier that was not met: nobody will use the stages that
   // the weight warp opened ahead; see their copies land.
   __device__ __forceinline__ void drop_down(int row_bytes) {
     int left = G::kStages;
-    down_tiles([&](int, int, int) {
-      for (int at = 0; at < row_bytes && left > 0; at += kSeg, --left, pos.next()) {
-        mbar_arrive(&full[pos.stage]);
-        mbar_wait(&full[pos.stage], pos.phase, p.wait_limit_ns);
-      }
-    });
+    down_tiles(
+        row_bytes,
+        [&](int, int, int, int from, int to) {
+          for (int at = from; at < to && left > 0; at += kSeg, --left, pos.next()) {
+            mbar_arrive(&full[pos.stage]);
+            mbar_wait(&full[pos.stage], pos.phase, p.wait_limit_ns);
+          }
+        },
+        [](int, int) {});
   }
 
   __device__ __forceinline__ void down(int row_bytes) {
@@ -623,10 +654,11 @@ struct Block {
     };
     zero();
     Places at;
-    int row[4];
-    down_tiles([&](int c, int rows, int a) {
+    int row[4], placed = 0;
+    auto part = [&](int c, int rows, int a, int from, int to) {
       const int e = s.act[a], count = s.count[a];
-      if (a == 0) {
+      if (rows != placed) {
+        placed = rows;
 #pragma unroll
         for (int i = 0; i < 4; ++i) row[i] = min(8 * i + g, rows - 1);
         place_rows(at, row[0], row[1], row[2], row[3]);
@@ -642,26 +674,26 @@ struct Block {
       }
       float acc[2][NT][4];
       clear(acc);
-      // the warp's part of the expert, weighed and added to its tokens' sums
-      if (use_stages(row_bytes, rows > 16 ? 2 : 1, count > 8 ? 2 : 1, at, zz, acc)) {
+      use_stages(from, to, rows > 16 ? 2 : 1, count > 8 ? 2 : 1, at, zz, acc);
+      // the warp's share of the part, weighed and added to its tokens' sums
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            if (n * 8 + u >= count) break;
-            const int i = n * 8 + 2 * q + u;
-            if (i >= count) continue;
-            const int t = s.tok[a][i];
-            const float w = s.w[t * p.k + s.slot[e][t]];
+        for (int u = 0; u < 2; ++u) {
+          if (n * 8 + u >= count) break;
+          const int i = n * 8 + 2 * q + u;
+          if (i >= count) continue;
+          const int t = s.tok[a][i];
+          const float w = s.w[t * p.k + s.slot[e][t]];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              float& sum = s.red[warp][8 * r + g][t];
-              sum = fmaf(w * sc[r], acc[r / 2][n][(r & 1) * 2 + u], sum);
-            }
+          for (int r = 0; r < 4; ++r) {
+            float& sum = s.red[warp][8 * r + g][t];
+            sum = fmaf(w * sc[r], acc[r / 2][n][(r & 1) * 2 + u], sum);
           }
-        __syncwarp();
-      }
-      if (a + 1 < s.n_act) return;
+        }
+      __syncwarp();
+    };
+    down_tiles(row_bytes, part, [&](int c, int rows) {
       named_bar_sync(kUserBar, kUsers);
       for (int o = threadIdx.x; o < kRows * MT; o += kUsers) {
         const int r = o % kRows, t = o / kRows;
@@ -705,12 +737,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int up_bytes = p.d / kElems<WF> * 16, down_bytes = p.f / kElems<WF> * 16;
   if (ok) b.gate();
   // (a block that timed out above still meets the others at the second barrier)
-  if (b.warp == kWeightWarp) {
+  if (b.warp >= kWeightWarp && b.warp < kTokenWarp) {
     if (ok && b.lane == 0) {
       b.feed_gateup(up_bytes);
       b.feed_down(down_bytes);
     }
-  } else if (b.warp == kTokenWarp) {
+  } else if (b.warp >= kTokenWarp) {
     if (ok) {
       b.feed_x(up_bytes);
       bool met = true;
