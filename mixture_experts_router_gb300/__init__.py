@@ -484,8 +484,9 @@ def fp4_quantize(x, format, tensor_scale=None, stream=None) -> Fp4Matrix:
             return fp4_quantize(x, format, tensor_scale)
     m = Fp4Matrix.__new__(Fp4Matrix)
     m.format, m.rows, m.cols, m.groups, m.tensor_scale = format, rows, cols, 1, tensor_scale
-    m.codes = codes = x.new_empty((rows, cols // 2), dtype=torch.uint8)
-    m.scales = scales = x.new_empty(nbytes, dtype=torch.uint8)
+    where = x.device
+    m.codes = codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=where)
+    m.scales = scales = torch.empty(nbytes, dtype=torch.uint8, device=where)
     st = (_lib or load_library()).cb_fp4_quantize(
         fmt, x.data_ptr(), kind, rows, cols, ld, None if tensor_scale is None else tensor_scale.data_ptr(),
         codes.data_ptr(), scales.data_ptr(), s)
@@ -510,13 +511,18 @@ def fp4_dequantize(m: Fp4Matrix, dtype=None, out=None, stream=None):
         with _On(device, stream):
             return fp4_dequantize(m, dtype, out)
     if out is None:
-        out = codes.new_empty((m.rows, m.cols), dtype=dtype or torch.bfloat16)
+        out = torch.empty((m.rows, m.cols), dtype=dtype or torch.bfloat16, device=codes.device)
     st = (_lib or load_library()).cb_fp4_dequantize(
         FP4_FORMATS[m.format], codes.data_ptr(), m.scales.data_ptr(), None if g is None else g.data_ptr(), m.rows,
         m.cols, out.data_ptr(), kind, _row_stride(out), s)
     if st != CB_OK:
         raise CbMoeError(st, "cb_fp4_dequantize")
     return out
+
+
+def _check_int32(t, n, name):
+    if t.dtype is not _torch.int32 or not t.is_cuda or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous int32 CUDA tensor of {n} is needed")
 
 
 def fp4_matmul(a: Fp4Matrix, b: Fp4Matrix, dtype=None, out=None, tile_offsets=None, status=None, stream=None):
@@ -527,9 +533,10 @@ def fp4_matmul(a: Fp4Matrix, b: Fp4Matrix, dtype=None, out=None, tile_offsets=No
     torch = _load_torch()
     if a.format != b.format or a.cols != b.cols or a.groups != 1:
         raise ValueError(f"fp4_matmul: {a.groups} x [{a.rows} x {a.cols}] {a.format} by [{b.rows} x {b.cols}] {b.format}")
-    for name, t, n in (("tile_offsets", tile_offsets, b.groups + 1), ("status", status, 1)):
-        if t is not None and (t.dtype is not torch.int32 or not t.is_cuda or t.numel() != n or not t.is_contiguous()):
-            raise ValueError(f"fp4_matmul: {name} is a contiguous int32 CUDA tensor of {n}")
+    if tile_offsets is not None:
+        _check_int32(tile_offsets, b.groups + 1, "tile_offsets")
+    if status is not None:
+        _check_int32(status, 1, "status")
     if out is not None and (tuple(out.shape) != (a.rows, b.rows) or (dtype is not None and out.dtype != dtype)):
         raise ValueError(f"out {tuple(out.shape)} {out.dtype} for a {a.rows} x {b.rows} product")
     kind = _fp4_type((dtype or torch.bfloat16) if out is None else out.dtype)
@@ -539,7 +546,7 @@ def fp4_matmul(a: Fp4Matrix, b: Fp4Matrix, dtype=None, out=None, tile_offsets=No
         with _On(device, stream):
             return fp4_matmul(a, b, dtype, out, tile_offsets, status)
     if out is None:
-        out = a.codes.new_empty((a.rows, b.rows), dtype=dtype or torch.bfloat16)
+        out = torch.empty((a.rows, b.rows), dtype=dtype or torch.bfloat16, device=a.codes.device)
     nv = a.tensor_scale is not None
     st = (_lib or load_library()).cb_fp4_matmul(_FP4_MATMUL.pack(
         FP4_FORMATS[a.format], kind, a.rows, b.rows, a.cols, a.codes.data_ptr(), a.scales.data_ptr(),
