@@ -61,7 +61,7 @@ CB_API cb_status_t cb_fp4_scale_bytes(int32_t format, int64_t rows, int64_t cols
  * not start on 16 bytes are read in smaller pieces.
  * Errors: CB_ERR_INVALID_ARG (an unknown format or type, NULL, negative rows,
  * cols not a positive multiple of 32, ld < cols, a tensor_scale where there
- * is none or none where there is one), CB_ERR_ALIGNMENT (codes or scales not
+ * is none or none where there is one, x, codes and scales overlapping), CB_ERR_ALIGNMENT (codes or scales not
  * on 16 bytes, x not on its element's size, tensor_scale not on 4 bytes),
  * CB_ERR_UNSUPPORTED (2^31 row tiles or columns, or a wrong GPU),
  * CB_ERR_CUDA.

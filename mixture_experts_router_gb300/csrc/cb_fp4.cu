@@ -38,6 +38,11 @@ cb_status_t check_device(int* sms) {
   return major == 10 && minor == 3 ? CB_OK : CB_ERR_UNSUPPORTED;
 }
 
+bool overlap(const void* a, uint64_t an, const void* b, uint64_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return an > 0 && bn > 0 && x < y + bn && y < x + an;
+}
+
 // Arguments of the quantiser and its way back; x is its input or output.
 cb_status_t check_matrix(int32_t format, const void* x, int32_t type, int64_t rows, int64_t cols, int64_t ld,
                          const float* tensor_scale, const uint8_t* codes, const uint8_t* scales) {
@@ -48,14 +53,16 @@ cb_status_t check_matrix(int32_t format, const void* x, int32_t type, int64_t ro
   if (!on(codes, 16) || !on(scales, 16) || !on(x, type == CB_T_F32 ? 4 : 2) || !on(tensor_scale, 4))
     return CB_ERR_ALIGNMENT;
   // (the quotients first: a product of both sizes may pass 64 bits)
-  if (cols >= (1ll << 31) || rows / kScaleTileRows >= (1ll << 31) || fp4_tiles(rows, cols) >= (1ll << 31))
+  if (cols >= (1ll << 31) || rows / kScaleTileRows >= (1ll << 31) || fp4_tiles(rows, cols) >= (1ll << 31) ||
+      ld >= (1ll << 62) / (rows + 1))
     return CB_ERR_UNSUPPORTED;
+  if (rows > 0) {
+    const uint64_t xb = (static_cast<uint64_t>(rows - 1) * ld + cols) * (type == CB_T_F32 ? 4 : 2);
+    const uint64_t cb = static_cast<uint64_t>(rows) * cols / 2, sb = static_cast<uint64_t>(scale_bytes(format, rows, cols));
+    if (overlap(x, xb, codes, cb) || overlap(x, xb, scales, sb) || overlap(codes, cb, scales, sb))
+      return CB_ERR_INVALID_ARG;
+  }
   return CB_OK;
-}
-
-bool overlap(const void* a, uint64_t an, const void* b, uint64_t bn) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return an > 0 && bn > 0 && x < y + bn && y < x + an;
 }
 
 }  // namespace
@@ -114,6 +121,7 @@ cb_status_t cb_fp4_matmul(const cb_fp4_matmul_t* p, void* stream) {
     if (!on(q, 4)) return CB_ERR_ALIGNMENT;
   // tiles of the output are counted in 32 bits
   if ((p->m + 127) / 128 >= limit / ((p->n + 127) / 128)) return CB_ERR_UNSUPPORTED;
+  if (p->ld_out >= (1ll << 62) / p->m) return CB_ERR_UNSUPPORTED;
   const uint64_t out_bytes =
       (static_cast<uint64_t>(p->m - 1) * p->ld_out + p->n) * (p->out_type == CB_T_F32 ? 4 : 2);
   const uint64_t g = static_cast<uint64_t>(p->n_groups);

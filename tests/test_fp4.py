@@ -58,7 +58,7 @@ def test_scale_bytes(lib):
 
 
 def test_quantiser_refuses_bad_arguments_before_cuda(lib):
-    ok = dict(fmt=0, x=64, typ=0, rows=4, cols=64, ld=64, g=None, codes=128, scales=256)
+    ok = dict(fmt=0, x=0x1000, typ=0, rows=4, cols=64, ld=64, g=None, codes=0x2000, scales=0x3000)
 
     def both(**kw):
         a = {**ok, **kw}
@@ -66,11 +66,12 @@ def test_quantiser_refuses_bad_arguments_before_cuda(lib):
                 cb.cb_fp4_dequantize(a["fmt"], a["codes"], a["scales"], a["g"], a["rows"], a["cols"], a["x"], a["typ"], a["ld"])}
 
     for kw in (dict(fmt=2), dict(fmt=-1), dict(typ=2), dict(rows=-1), dict(cols=0), dict(cols=40), dict(ld=63),
-               dict(x=None), dict(codes=None), dict(scales=None), dict(g=64), dict(fmt=1)):
+               dict(x=None), dict(codes=None), dict(scales=None), dict(g=64), dict(fmt=1), dict(x=0x2000),
+               dict(x=0x3010), dict(codes=0x1010), dict(scales=0x2010), dict(x=0x1f00, ld=600)):
         assert both(**kw) == {cb.CB_ERR_INVALID_ARG}, kw
-    for kw in (dict(x=65), dict(typ=1, x=66), dict(codes=136), dict(scales=264), dict(fmt=1, g=66)):
+    for kw in (dict(x=0x1001), dict(typ=1, x=0x1002), dict(codes=0x2008), dict(scales=0x3008), dict(fmt=1, g=66)):
         assert both(**kw) == {cb.CB_ERR_ALIGNMENT}, kw
-    for kw in (dict(cols=1 << 31, ld=1 << 31), dict(rows=1 << 60), dict(rows=1 << 36, cols=1 << 20, ld=1 << 20)):
+    for kw in (dict(cols=1 << 31, ld=1 << 31), dict(rows=1 << 60), dict(rows=1 << 36, cols=1 << 20, ld=1 << 20), dict(ld=1 << 61)):
         assert both(**kw) == {cb.CB_ERR_UNSUPPORTED}, kw
     assert both(rows=0, x=None, codes=None, scales=None) == {cb.CB_OK}
 
