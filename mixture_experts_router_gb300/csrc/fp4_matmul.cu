@@ -13,7 +13,8 @@
 //
 // The two operands' roles.  The MMA's M side is 128 rows, its N side BN.
 //  * more than 128 rows of A, or experts: A's rows are the M side, BN rows of
-//    B the N side;
+//    B the N side; in large dense products 256 of A's rows against 256 of B's
+//    on a pair of SMs (below);
 //  * up to 128 rows of A ("swap"): B's rows (the weights) are the M side and
 //    all of A the N side, BN >= m of 16..128, so the 128-row side is never
 //    padding and a CTA streams its weight rows once.  What bounds these is
@@ -21,8 +22,8 @@
 //    k and adds its partial sums through distributed shared memory, in rank
 //    order.
 //
-// Per CTA: warp 0 TMA producer, warp 1 tensor memory and MMA issuer, warps
-// 4..7 scales from shared into tensor memory, warps 8.. epilogue.  Stage s of the ring has its own scale columns in tensor
+// Per CTA: warp 0 TMA producer, warp 1 tensor memory, scale copies and MMAs,
+// warps 4.. epilogue.  Stage s of the ring has its own scale columns in tensor
 // memory, so a stage's commit frees both.  All waits are bounded.
 #include <cuda_bf16.h>
 
@@ -36,8 +37,7 @@ namespace {
 constexpr int BP = 128;            // rows of the M side
 constexpr int BK = 256;            // elements per stage: 128 bytes of codes
 constexpr int ROW_BYTES = BK / 2;
-constexpr int SCALE_WARP0 = 4;     // 4 warps, one per quarter of the lanes
-constexpr int EPI_WARP0 = 8;
+constexpr int EPI_WARP0 = 4;
 // epilogue warps: a quarter of the lanes each, and with two per quarter half
 // of the columns
 template <int BN, bool SWAP>
@@ -102,6 +102,42 @@ struct Tiles {
       t.e = lo;
     }
     return t;
+  }
+};
+
+// The MMA warp's place in the ring.  The whole warp walks it, so that its
+// addresses are uniform values, and an elected lane issues: an MMA or a copy of
+// scales then takes 37 cycles to issue, by a lane that walks alone 80 and
+// more, which made a stage's copies take longer than its MMAs.
+template <int STAGES>
+struct Issuer {
+  uint64_t* full;
+  const Fp4MatmulArgs& a;
+  int s = 0;
+  uint32_t phase = 0;
+  bool ready = false, ok = true;
+  const bool leader;
+  __device__ __forceinline__ Issuer(uint64_t* full_, const Fp4MatmulArgs& a_)
+      : full(full_), a(a_), leader(elect_one()) {}
+
+  // All lanes or none; false once a wait has run out.
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+    ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, a.wait_limit_ns));
+    if (!ok) set_error(a.status, kErrTimeout);
+    return ok;
+  }
+  __device__ __forceinline__ bool wait_stage() {
+    if (!__all_sync(0xffffffffu, ready) && !wait(full + s, phase)) return false;
+    tc_fence_after();
+    return true;
+  }
+  __device__ __forceinline__ void next() {
+    __syncwarp();
+    if (++s == STAGES) {
+      s = 0;
+      phase ^= 1u;
+    }
+    ready = mbar_test(full + s, phase);
   }
 };
 
@@ -178,6 +214,47 @@ __device__ __forceinline__ void store_rows(uint8_t* out, int64_t pitch, uint32_t
   __syncwarp();
 }
 
+// An epilogue warp's part of a tile: 32 rows from row0, COLS columns from
+// `first`, from tensor memory at `acc`.  done(): the accumulator is read.
+template <int FMT, int COLS, typename F>
+__device__ __forceinline__ void store_tile(const Fp4MatmulArgs& a, uint32_t acc, int row0, int first, int e, int vec,
+                                           int lane, F&& done) {
+  const float alpha = FMT == kFp4Nv ? __ldg(a.a_tensor_scale) * __ldg(a.b_tensor_scale + e) : 1.f;
+  const int rows = a.m - row0;  // the warp's rows (all 32 but in the last tiles)
+  if (a.out_f32) {
+    uint8_t* out = static_cast<uint8_t*>(a.out) + (static_cast<int64_t>(row0) * a.ld_out + first) * 4;
+#pragma unroll 1
+    for (int c0 = 0; c0 < COLS && first + c0 < a.n; c0 += 32) {
+      uint32_t v[32];
+      tmem_load32(acc + c0, v);
+      if (c0 + 32 >= COLS || first + c0 + 32 >= a.n) done();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(alpha * __uint_as_float(v[j]));
+      store_rows<4>(out + c0 * 4, a.ld_out * 4, v, rows, a.n - first - c0, vec, lane);
+    }
+    if (first >= a.n) done();
+  } else {
+    // all columns as bf16 in registers, the accumulator handed on, then the stores
+    uint32_t h[COLS / 2];
+#pragma unroll
+    for (int c0 = 0; c0 < COLS; c0 += 32) {
+      uint32_t v[32];
+      tmem_load32(acc + c0, v);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const __nv_bfloat162 b =
+            __floats2bfloat162_rn(alpha * __uint_as_float(v[2 * j]), alpha * __uint_as_float(v[2 * j + 1]));
+        h[c0 / 2 + j] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+    }
+    done();
+    uint8_t* out = static_cast<uint8_t*>(a.out) + (static_cast<int64_t>(row0) * a.ld_out + first) * 2;
+#pragma unroll
+    for (int c = 0; c < COLS; c += 64)
+      if (first + c < a.n) store_rows<2>(out + c * 2, a.ld_out * 2, h + c / 2, rows, a.n - first - c, vec, lane);
+  }
+}
+
 template <int FMT, int BN, bool SWAP>
 __global__ void __launch_bounds__((THREADS<BN, SWAP>), 1)
     fp4_matmul_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
@@ -188,8 +265,7 @@ __global__ void __launch_bounds__((THREADS<BN, SWAP>), 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE);
   uint64_t* empty = full + STAGES;
-  uint64_t* sfull = empty + STAGES;  // a stage's scales are in tensor memory
-  uint64_t* tfull = sfull + STAGES;
+  uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 1);
 
@@ -201,7 +277,6 @@ __global__ void __launch_bounds__((THREADS<BN, SWAP>), 1)
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&sfull[s], 4);
     }
     mbar_init(tfull, 1);
     mbar_init(tempty, EPI_WARPS<BN, SWAP>);
@@ -264,85 +339,45 @@ __global__ void __launch_bounds__((THREADS<BN, SWAP>), 1)
           set_error(a.status, kErrTimeout);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int64_t it = 0;
-      uint32_t tphase = 0;
-      bool ok = true;
-      for (int i = worker; ok && i < tiles.total; i += workers, tphase ^= 1u) {
-        if (!mbar_wait(tempty, tphase ^ 1u, a.wait_limit_ns)) {
-          set_error(a.status, kErrTimeout);
-          break;
-        }
-        tc_fence_after();
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int s = static_cast<int>(it % STAGES);
-          const uint32_t phase = static_cast<uint32_t>((it / STAGES) & 1);
-          if (!mbar_wait(&full[s], phase, a.wait_limit_ns) || !mbar_wait(&sfull[s], phase, a.wait_limit_ns)) {
-            set_error(a.status, kErrTimeout);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t st = smem_u32(smem + s * C::STAGE);
-          const uint32_t sfp = tmem + C::SF0 + static_cast<uint32_t>(s) * C::SF_COLS;
-          const uint32_t sfq = sfp + 4 * C::W;
-          const uint64_t pd = sw128_desc(st), qd = sw128_desc(st + P_BYTES);
-          const int steps = min(4, (a.k - kb * BK + 63) / 64);
+    Issuer<STAGES> is(full, a);
+    const uint64_t desc0 = sw128_desc(smem_u32(smem)), sdesc0 = scale_desc(smem_u32(smem + P_BYTES + C::Q_BYTES));
+    uint32_t tphase = 0;
+    for (int i = worker; is.ok && i < tiles.total; i += workers, tphase ^= 1u) {
+      if (!is.wait(tempty, tphase ^ 1u)) break;
+      tc_fence_after();
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!is.wait_stage()) break;
+        const uint64_t pd = desc0 + is.s * (C::STAGE / 16), qd = pd + P_BYTES / 16;
+        const uint64_t sd = sdesc0 + is.s * (C::STAGE / 16);
+        const uint32_t sfp = tmem + C::SF0 + static_cast<uint32_t>(is.s) * C::SF_COLS;
+        const uint32_t sfq = sfp + 4 * C::W;
+        if (is.leader) {
+          // words past the array are an earlier stage's, which no MMA uses
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j < steps) {
-              const uint32_t acc = (kb != kb0 || j != 0) ? 1u : 0u;
-              if constexpr (FMT == kFp4Mx)
-                tc_mma_mx4(tmem, pd + 2 * j, qd + 2 * j, idesc_fp4(BP, BN, true, (j & 1) * 2), sfp + 4 * (j / 2),
-                           sfq + 4 * C::QT * (j / 2), acc);
-              else
-                tc_mma_nv4(tmem, pd + 2 * j, qd + 2 * j, idesc_fp4(BP, BN, false, 0), sfp + 4 * j,
-                           sfq + 4 * C::QT * j, acc);
-            }
-          tc_commit(&empty[s]);
+          for (int w = 0; w < C::W; ++w) {
+            tc_copy_scales(sfp + 4 * w, sd + w * (kScaleTileBytes / 16));
+#pragma unroll
+            for (int j = 0; j < C::QT; ++j)
+              tc_copy_scales(sfq + 4 * (w * C::QT + j), sd + ((1 + j) * C::SF_BYTES + w * kScaleTileBytes) / 16);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (j > 0 && kb * BK + j * 64 >= a.k) break;
+            const uint32_t acc = (kb != kb0 || j != 0) ? 1u : 0u;
+            if constexpr (FMT == kFp4Mx)
+              tc_mma_mx4(tmem, pd + 2 * j, qd + 2 * j, idesc_fp4(BP, BN, true, (j & 1) * 2), sfp + 4 * (j / 2),
+                         sfq + 4 * C::QT * (j / 2), acc);
+            else
+              tc_mma_nv4(tmem, pd + 2 * j, qd + 2 * j, idesc_fp4(BP, BN, false, 0), sfp + 4 * j, sfq + 4 * C::QT * j,
+                         acc);
+          }
+          tc_commit(&empty[is.s]);
         }
-        if (!ok) break;
-        tc_commit(tfull);
+        is.next();
       }
+      if (is.ok && is.leader) tc_commit(tfull);
+      __syncwarp();
     }
-  } else if (warp >= SCALE_WARP0 && warp < EPI_WARP0) {
-    // ------------------------------------------------ scales into tensor memory
-    // A quarter's lane i takes bytes [16 i, 16 i + 16) of every scale tile (the
-    // scales of rows i, i + 32, i + 64, i + 96): 4 columns, the same in each
-    // quarter.  (tcgen05.cp does this too, but in the MMA's own queue: its
-    // copies, 12 per stage of an NV product, took longer than the stage's MMAs.)
-    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    int64_t it = 0;
-    bool ok = true;
-    for (int i = worker; ok && i < tiles.total; i += workers)
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const int s = static_cast<int>(it % STAGES);
-        if (!mbar_wait(&full[s], static_cast<uint32_t>((it / STAGES) & 1), a.wait_limit_ns)) {
-          set_error(a.status, kErrTimeout);
-          ok = false;
-          break;
-        }
-        const uint8_t* sf = smem + s * C::STAGE + P_BYTES + C::Q_BYTES + lane * 16;
-        const uint32_t to = lanes + C::SF0 + static_cast<uint32_t>(s) * C::SF_COLS;
-        // words past the array hold an earlier stage's scales, which no MMA uses
-        uint32_t v[4 * C::W * (1 + C::QT)];
-#pragma unroll
-        for (int w = 0; w < C::W; ++w)
-#pragma unroll
-          for (int j = 0; j <= C::QT; ++j) {
-            const uint4 x = *reinterpret_cast<const uint4*>(sf + j * C::SF_BYTES + w * kScaleTileBytes);
-            const int c = j == 0 ? 4 * w : 4 * (C::W + w * C::QT + j - 1);
-            v[c] = x.x;
-            v[c + 1] = x.y;
-            v[c + 2] = x.z;
-            v[c + 3] = x.w;
-          }
-        tmem_store<4 * C::W * (1 + C::QT)>(to, v);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sfull[s]);
-      }
   } else if (warp >= EPI_WARP0) {
     const int q = warp & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
@@ -367,41 +402,7 @@ __global__ void __launch_bounds__((THREADS<BN, SWAP>), 1)
           for (int j = 0; j < 16; ++j) part[(c0 + j) * BP + q * 32 + lane] = __uint_as_float(v[j]);
         }
       } else {
-        const float alpha = FMT == kFp4Nv ? __ldg(a.a_tensor_scale) * __ldg(a.b_tensor_scale + t.e) : 1.f;
-        const int row0 = t.p0 + q * 32, rows = a.m - row0;  // the warp's rows (all 32 but in the last tile)
-        const int first = t.q0 + col0;
-        if (a.out_f32) {
-          uint8_t* out = static_cast<uint8_t*>(a.out) + (static_cast<int64_t>(row0) * a.ld_out + first) * 4;
-#pragma unroll 1
-          for (int c0 = 0; c0 < COLS && first + c0 < a.n; c0 += 32) {
-            uint32_t v[32];
-            tmem_load32(lanes + col0 + c0, v);
-            if (c0 + 32 >= COLS || first + c0 + 32 >= a.n) release(tempty, lane);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(alpha * __uint_as_float(v[j]));
-            store_rows<4>(out + c0 * 4, a.ld_out * 4, v, rows, a.n - first - c0, vec, lane);
-          }
-          if (first >= a.n) release(tempty, lane);
-        } else {
-          // all columns as bf16 in registers, the accumulator handed on, then the stores
-          uint32_t h[COLS / 2];
-#pragma unroll
-          for (int c0 = 0; c0 < COLS; c0 += 32) {
-            uint32_t v[32];
-            tmem_load32(lanes + col0 + c0, v);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const __nv_bfloat162 b =
-                  __floats2bfloat162_rn(alpha * __uint_as_float(v[2 * j]), alpha * __uint_as_float(v[2 * j + 1]));
-              h[c0 / 2 + j] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-          }
-          release(tempty, lane);
-          uint8_t* out = static_cast<uint8_t*>(a.out) + (static_cast<int64_t>(row0) * a.ld_out + first) * 2;
-#pragma unroll
-          for (int c = 0; c < COLS; c += 64)
-            if (first + c < a.n) store_rows<2>(out + c * 2, a.ld_out * 2, h + c / 2, rows, a.n - first - c, vec, lane);
-        }
+        store_tile<FMT, COLS>(a, lanes + col0, t.p0 + q * 32, t.q0 + col0, t.e, vec, lane, [&]() { release(tempty, lane); });
       }
     }
   }
@@ -458,9 +459,186 @@ __global__ void __launch_bounds__((THREADS<BN, SWAP>), 1)
   }
 }
 
+// ------------------------------------------------------------------- CTA pairs
+// A cluster of two CTAs takes 256 rows of A (128 each) against 256 rows of B
+// with the 2-SM MMA.  Each stages half of B's rows and the tensor cores read
+// both halves: 38 KB a stage (NV) against 54.
+//
+// Barriers: both CTAs' copies complete the even CTA's `full`; the MMA's
+// commits arrive on `empty` and `tfull` of both; the epilogue warps of both
+// arrive on the even CTA's `tempty`.
+template <int FMT>
+struct PairCfg {
+  static constexpr int STAGES = 5, BN = 256, EPI = 8, THREADS = (EPI_WARP0 + EPI) * 32;
+  static constexpr int W = BK / (4 * kFp4Block<FMT>);
+  static constexpr int Q_BYTES = BN / 2 * ROW_BYTES;
+  static constexpr int SF_BYTES = W * kScaleTileBytes;
+  static constexpr int STAGE = P_BYTES + Q_BYTES + 3 * SF_BYTES;
+  static constexpr int SF_COLS = W * 4 * 3;  // per stage: own rows of A, two row tiles of B
+  static constexpr int TMEM = 512;
+  static constexpr int BYTES = STAGES * STAGE + 1024 + 256;
+  static_assert(STAGE % 1024 == 0 && BYTES <= 232448 && BN + STAGES * SF_COLS <= TMEM, "layout");
+};
+
+template <int FMT>
+__global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
+    fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
+                           const __grid_constant__ CUtensorMap tm_ps, const __grid_constant__ CUtensorMap tm_qs,
+                           const Fp4MatmulArgs a, const int vec) {
+  using C = PairCfg<FMT>;
+  constexpr int STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 1);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const bool even = rank == 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(tfull, 1);
+    mbar_init(tempty, 2 * C::EPI);
+    fence_barrier_init();
+    prefetch_tensormap(&tm_p);
+    prefetch_tensormap(&tm_q);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, C::TMEM);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dep_wait();
+
+  const int pt = (a.m + 2 * BP - 1) / (2 * BP), total = pt * ((a.n + C::BN - 1) / C::BN);
+  const int first = blockIdx.x / 2, step = gridDim.x / 2;
+  const int stages = (a.k + BK - 1) / BK;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint32_t full_even = mapa_shared(smem_u32(full), 0);
+      int64_t it = 0;
+      bool ok = true;
+      for (int i = first; ok && i < total; i += step) {
+        const int p0 = (i % pt * 2 + rank) * BP, q0 = i / pt * C::BN;
+        for (int kb = 0; kb < stages; ++kb, ++it) {
+          const int s = static_cast<int>(it % STAGES);
+          if (!mbar_wait(&empty[s], static_cast<uint32_t>(((it / STAGES) & 1) ^ 1), a.wait_limit_ns)) {
+            set_error(a.status, kErrTimeout);
+            ok = false;
+            break;
+          }
+          uint8_t* st = smem + s * C::STAGE;
+          uint8_t* sf = st + P_BYTES + C::Q_BYTES;
+          if (even) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE);
+          const uint32_t bar = full_even + static_cast<uint32_t>(s * 8);
+          tma_load_2d_pair(st, &tm_p, bar, kb * ROW_BYTES, p0);
+          tma_load_2d_pair(st + P_BYTES, &tm_q, bar, kb * ROW_BYTES, q0 + rank * BP);
+          tma_load_2d_pair(sf, &tm_ps, bar, kb * (C::SF_BYTES / 8), p0 / BP);
+          tma_load_2d_pair(sf + C::SF_BYTES, &tm_qs, bar, kb * (C::SF_BYTES / 8), q0 / BP);
+        }
+      }
+      // no copy may still be in flight into shared memory at exit (the even
+      // CTA's `full` counts both CTAs' copies)
+      for (int64_t j = (it > STAGES ? it - STAGES : 0); even && j < it; ++j)
+        if (!mbar_wait(&full[j % STAGES], static_cast<uint32_t>((j / STAGES) & 1), a.wait_limit_ns))
+          set_error(a.status, kErrTimeout);
+    }
+  } else if (warp == 1 && even) {
+    Issuer<STAGES> is(full, a);
+    const uint64_t desc0 = sw128_desc(smem_u32(smem)), sdesc0 = scale_desc(smem_u32(smem + P_BYTES + C::Q_BYTES));
+    uint32_t tphase = 0;
+    for (int i = first; is.ok && i < total; i += step, tphase ^= 1u) {
+      if (!is.wait(tempty, tphase ^ 1u)) break;
+      tc_fence_after();
+      for (int kb = 0; kb < stages; ++kb) {
+        if (!is.wait_stage()) break;
+        const uint64_t pd = desc0 + is.s * (C::STAGE / 16), qd = pd + P_BYTES / 16;
+        const uint64_t sd = sdesc0 + is.s * (C::STAGE / 16);
+        const uint32_t sfp = tmem + C::BN + static_cast<uint32_t>(is.s) * C::SF_COLS;
+        const uint32_t sfq = sfp + 4 * C::W;
+        if (is.leader) {
+#pragma unroll
+          for (int w = 0; w < C::W; ++w) {
+            tc_copy_scales_pair(sfp + 4 * w, sd + w * (kScaleTileBytes / 16));
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              tc_copy_scales_pair(sfq + 4 * (2 * w + j), sd + ((1 + j) * C::SF_BYTES + w * kScaleTileBytes) / 16);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (j > 0 && kb * BK + j * 64 >= a.k) break;
+            const uint32_t acc = (kb | j) != 0 ? 1u : 0u;
+            if constexpr (FMT == kFp4Mx)
+              tc_mma_mx4_pair(tmem, pd + 2 * j, qd + 2 * j, idesc_fp4(2 * BP, C::BN, true, (j & 1) * 2),
+                              sfp + 4 * (j / 2), sfq + 8 * (j / 2), acc);
+            else
+              tc_mma_nv4_pair(tmem, pd + 2 * j, qd + 2 * j, idesc_fp4(2 * BP, C::BN, false, 0), sfp + 4 * j,
+                              sfq + 8 * j, acc);
+          }
+          tc_commit_pair_multicast(&empty[is.s], 3);
+        }
+        is.next();
+      }
+      if (is.ok && is.leader) tc_commit_pair_multicast(tfull, 3);
+      __syncwarp();
+    }
+  } else if (warp >= EPI_WARP0) {
+    const int q = warp & 3, col0 = (warp - EPI_WARP0) / 4 * 128;
+    const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(col0);
+    const uint32_t tempty_even = mapa_shared(smem_u32(tempty), 0);
+    uint32_t tphase = 0;
+    for (int i = first; i < total; i += step, tphase ^= 1u) {
+      if (!mbar_wait(tfull, tphase, a.wait_limit_ns)) {
+        set_error(a.status, kErrTimeout);
+        break;
+      }
+      tc_fence_after();
+      store_tile<FMT, 128>(a, acc, (i % pt * 2 + rank) * BP + q * 32, i / pt * C::BN + col0, 0, vec, lane, [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(tempty_even);
+      });
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, C::TMEM);
+  }
+}
+
 bool map_codes(CUtensorMap* m, const uint8_t* codes, int64_t rows, int k, int box) {
   return make_tmap(m, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, static_cast<uint64_t>(k / 2),
                    static_cast<uint64_t>(rows), ROW_BYTES, static_cast<uint32_t>(box));
+}
+
+// Scale tiles as 8-byte elements, rows of one row tile each; a box is a stage's
+// words of `box` row tiles.
+template <int FMT>
+bool map_scales(CUtensorMap* m, const uint8_t* scales, int64_t rows, int k, int box) {
+  const uint64_t words = static_cast<uint64_t>((k / kFp4Block<FMT> + 3) / 4);
+  return make_tmap(m, scales, CU_TENSOR_MAP_DATA_TYPE_UINT64, 8, words * (kScaleTileBytes / 8),
+                   static_cast<uint64_t>((rows + 127) / 128), BK / (4 * kFp4Block<FMT>) * (kScaleTileBytes / 8),
+                   static_cast<uint32_t>(box), CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// Whether the output's rows start on 16 bytes.
+int rows_on_16(const Fp4MatmulArgs& a) {
+  return (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && a.ld_out * (a.out_f32 ? 4 : 2) % 16 == 0 ? 1 : 0;
 }
 
 template <int FMT, int BN, bool SWAP>
@@ -474,8 +652,7 @@ cudaError_t launch(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s) {
   if (!map_codes(&tp, SWAP ? a.b_codes : a.a_codes, SWAP ? b_rows : a.m, a.k, BP) ||
       !map_codes(&tq, SWAP ? a.a_codes : a.b_codes, SWAP ? a.m : b_rows, a.k, BN))
     return cudaErrorInvalidValue;
-  const int64_t elem = a.out_f32 ? 4 : 2;
-  const int vec = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && a.ld_out * elem % 16 == 0 ? 1 : 0;
+  const int vec = rows_on_16(a);
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(THREADS<BN, SWAP>, 1, 1);
   cfg.dynamicSmemBytes = C::BYTES;
@@ -508,6 +685,33 @@ cudaError_t launch(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s) {
 }
 
 template <int FMT>
+cudaError_t launch_pair(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s) {
+  using C = PairCfg<FMT>;
+  auto kernel = fp4_matmul_pair_kernel<FMT>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
+  if (e != cudaSuccess) return e;
+  CUtensorMap tp, tq, tps, tqs;
+  if (!map_codes(&tp, a.a_codes, a.m, a.k, BP) || !map_codes(&tq, a.b_codes, a.n, a.k, BP) ||
+      !map_scales<FMT>(&tps, a.a_scales, a.m, a.k, 1) || !map_scales<FMT>(&tqs, a.b_scales, a.n, a.k, 2))
+    return cudaErrorInvalidValue;
+  const int64_t tiles = static_cast<int64_t>((a.m + 2 * BP - 1) / (2 * BP)) * ((a.n + C::BN - 1) / C::BN);
+  const int64_t pairs = num_sms / 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)), 1, 1);
+  cfg.blockDim = dim3(C::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = C::BYTES;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, tp, tq, tps, tqs, a, rows_on_16(a));
+}
+
+template <int FMT>
 cudaError_t launch_format(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s) {
   if (a.tile_offsets == nullptr && a.m <= 128) {
     if (a.m <= 16) return launch<FMT, 16, true>(a, num_sms, s);
@@ -517,7 +721,8 @@ cudaError_t launch_format(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s) {
   }
   // 128-column tiles while the 256-column ones would leave SMs without a tile
   const int64_t wide = static_cast<int64_t>((a.m + BP - 1) / BP) * ((a.n + 255) / 256);
-  return wide < num_sms ? launch<FMT, 128, false>(a, num_sms, s) : launch<FMT, 256, false>(a, num_sms, s);
+  if (wide < num_sms) return launch<FMT, 128, false>(a, num_sms, s);
+  return a.tile_offsets != nullptr ? launch<FMT, 256, false>(a, num_sms, s) : launch_pair<FMT>(a, num_sms, s);
 }
 
 }  // namespace

@@ -119,6 +119,16 @@ def test_python_refusals(lib):
             cb.Fp4Matrix(*args)
     with pytest.raises(cb.CbMoeError):
         cb.Fp4Matrix("mx", 2, 40, u(2, 20), u(512))
+    class Elsewhere:
+        device = "cuda:1"
+
+        def get_device(self):
+            return 1
+
+    for t in (torch.zeros(2), Elsewhere()):
+        with pytest.raises(ValueError):
+            cb._check_device(0, None, t)
+    cb._check_device(1, None, Elsewhere())
     with pytest.raises(ValueError):
         cb.fp4_matmul(m, cb.Fp4Matrix("mx", 2, 96, u(2, 48), u(512)))
     with pytest.raises(ValueError):
@@ -375,6 +385,56 @@ def test_experts_products(fmt, counts, n, k):
                 ref, _ = expected(a, b, fmt, e, rows)
                 assert torch.equal(out[rows], torch.from_numpy(ref).to(dtype).cuda()), e
         assert (out[int(ends[-1]) * 128:] == 7.0).all()
+
+
+# sizes of 152 tiles of 128 x 256 and more: odd numbers of 128-row tiles, ends inside each kind of
+# tile, rows of 8 bytes and of 16, k inside and past a stage of 256
+LARGE = [(2432, 2304, 96), (2500, 4008, 544), (5100, 1030, 1184), (129, 20000, 32), (19600, 130, 288), (4100, 4097, 256)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("m,n,k", LARGE)
+def test_large_products_are_exact(fmt, m, n, k):
+    """As above, against 64-bit products on the GPU."""
+    rng = np.random.default_rng(m + n + k)
+    a, b = random_matrix(rng, m, k, fmt, True), random_matrix(rng, n, k, fmt, True)
+    x, y = (torch.from_numpy(decode64(t, fmt)).cuda() for t in (a, b))
+    ref = x @ y.T
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for dtype in (torch.float32, torch.bfloat16):
+        out = torch.full((m, n + 24), 7.0, dtype=dtype, device="cuda")
+        cb.fp4_matmul(a, b, out=out[:, :n], status=status)
+        assert torch.equal(out[:, :n], ref.to(dtype)) and (out[:, n:] == 7.0).all()
+    assert int(status) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_many_experts_products_are_exact(fmt):
+    rng = np.random.default_rng(8)
+    counts, n, k = [130, 0, 5, 700, 128, 1] * 5, 2100, 416
+    ends = np.r_[0, np.cumsum([-(-c // 128) for c in counts])]
+    a, b = random_matrix(rng, int(ends[-1]) * 128, k, fmt, True), random_matrix(rng, n, k, fmt, True, groups=len(counts))
+    got = cb.fp4_matmul(a, b, dtype=torch.float32, tile_offsets=torch.from_numpy(ends.astype(np.int32)).cuda())
+    x = torch.from_numpy(decode64(a, fmt)).cuda()
+    for e in range(len(counts)):
+        rows = slice(int(ends[e]) * 128, int(ends[e + 1]) * 128)
+        assert torch.equal(got[rows].double(), x[rows] @ torch.from_numpy(decode64(b, fmt, e)).cuda().T), e
+
+
+@pytest.mark.gpu
+def test_tensors_on_several_devices_are_refused():
+    x = torch.randn(4, 64, device="cuda")
+    m, u = cb.fp4_quantize(x, "mx"), cb.fp4_quantize(x, "nv", torch.ones(1, device="cuda"))
+    on_cpu = cb.Fp4Matrix("mx", 4, 64, m.codes.cpu(), m.scales.cpu())
+    for call in (lambda: cb.Fp4Matrix("mx", 4, 64, m.codes, m.scales.cpu()),
+                 lambda: cb.Fp4Matrix("nv", 4, 64, u.codes, u.scales, u.tensor_scale.cpu()),
+                 lambda: cb.fp4_quantize(x, "nv", torch.ones(1)), lambda: cb.fp4_dequantize(m, out=torch.zeros(4, 64)),
+                 lambda: cb.fp4_matmul(m, on_cpu), lambda: cb.fp4_matmul(on_cpu, m),
+                 lambda: cb.fp4_matmul(m, m, out=torch.zeros(4, 4))):
+        with pytest.raises(ValueError):
+            call()
 
 
 @pytest.mark.gpu
