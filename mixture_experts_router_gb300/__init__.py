@@ -400,6 +400,12 @@ def _stream_here(device, stream):
     return None
 
 
+def _check_device(device, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensors on several devices: {t.device} beside device {device}")
+
+
 class _On:
     """The device and the stream (torch's current one unless given) as a context."""
 
@@ -463,6 +469,7 @@ class Fp4Matrix:
                 (tensor_scale is not None and (tensor_scale.dtype is not torch.float32 or
                                                tensor_scale.numel() != groups or not tensor_scale.is_contiguous())):
             raise ValueError("format nv has one fp32 tensor scale per matrix, format mx none")
+        _check_device(codes.get_device(), scales, tensor_scale)
 
 
 def fp4_quantize(x, format, tensor_scale=None, stream=None) -> Fp4Matrix:
@@ -478,6 +485,7 @@ def fp4_quantize(x, format, tensor_scale=None, stream=None) -> Fp4Matrix:
     if tensor_scale is not None and (tensor_scale.dtype is not torch.float32 or tensor_scale.numel() != 1):
         raise ValueError("tensor_scale: one fp32 element")
     device = x.get_device()
+    _check_device(device, tensor_scale)
     s = _stream_here(device, stream)
     if s is None:
         with _On(device, stream):
@@ -506,6 +514,7 @@ def fp4_dequantize(m: Fp4Matrix, dtype=None, out=None, stream=None):
         raise ValueError(f"out {tuple(out.shape)} {out.dtype} for a {m.rows} x {m.cols} matrix")
     kind = _fp4_type((dtype or torch.bfloat16) if out is None else out.dtype)
     device = codes.get_device()
+    _check_device(device, out)
     s = _stream_here(device, stream)
     if s is None:
         with _On(device, stream):
@@ -541,6 +550,7 @@ def fp4_matmul(a: Fp4Matrix, b: Fp4Matrix, dtype=None, out=None, tile_offsets=No
         raise ValueError(f"out {tuple(out.shape)} {out.dtype} for a {a.rows} x {b.rows} product")
     kind = _fp4_type((dtype or torch.bfloat16) if out is None else out.dtype)
     device = a.codes.get_device()
+    _check_device(device, b.codes, out, tile_offsets, status)
     s = _stream_here(device, stream)
     if s is None:
         with _On(device, stream):
