@@ -395,7 +395,7 @@ def _stream_here(device, stream):
     be entered first: another stream is asked for, or another device is current."""
     if device < 0:
         raise ValueError("4-bit matrices are made from and kept in CUDA tensors")
-    if stream is None and device == _torch.cuda.current_device():
+    if stream is None and device == _torch._C._cuda_getDevice():
         return _torch._C._cuda_getCurrentRawStream(device)
     return None
 
@@ -485,7 +485,8 @@ def fp4_quantize(x, format, tensor_scale=None, stream=None) -> Fp4Matrix:
     if tensor_scale is not None and (tensor_scale.dtype is not torch.float32 or tensor_scale.numel() != 1):
         raise ValueError("tensor_scale: one fp32 element")
     device = x.get_device()
-    _check_device(device, tensor_scale)
+    if tensor_scale is not None:
+        _check_device(device, tensor_scale)
     s = _stream_here(device, stream)
     if s is None:
         with _On(device, stream):
@@ -514,7 +515,8 @@ def fp4_dequantize(m: Fp4Matrix, dtype=None, out=None, stream=None):
         raise ValueError(f"out {tuple(out.shape)} {out.dtype} for a {m.rows} x {m.cols} matrix")
     kind = _fp4_type((dtype or torch.bfloat16) if out is None else out.dtype)
     device = codes.get_device()
-    _check_device(device, out)
+    if out is not None:
+        _check_device(device, out)
     s = _stream_here(device, stream)
     if s is None:
         with _On(device, stream):
@@ -550,7 +552,8 @@ def fp4_matmul(a: Fp4Matrix, b: Fp4Matrix, dtype=None, out=None, tile_offsets=No
         raise ValueError(f"out {tuple(out.shape)} {out.dtype} for a {a.rows} x {b.rows} product")
     kind = _fp4_type((dtype or torch.bfloat16) if out is None else out.dtype)
     device = a.codes.get_device()
-    _check_device(device, b.codes, out, tile_offsets, status)
+    if b.codes.get_device() != device or out is not None or tile_offsets is not None or status is not None:
+        _check_device(device, b.codes, out, tile_offsets, status)
     s = _stream_here(device, stream)
     if s is None:
         with _On(device, stream):

@@ -1,4 +1,5 @@
 // Host side of the C ABI in cb_fp4.h: argument validation and the launches.
+#include <atomic>
 #include <cstdlib>
 #include <cstring>
 
@@ -26,16 +27,29 @@ bool known_format(int32_t f) { return f == CB_FP4_MX || f == CB_FP4_NV; }
 bool known_type(int32_t t) { return t == CB_T_BF16 || t == CB_T_F32; }
 
 // The current device: this library's kernels are for compute capability 10.3.
+// A device's SM count is asked for once (0: not
+// yet; negative: a wrong GPU).
 cb_status_t check_device(int* sms) {
-  int dev = 0, major = 0, minor = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
     return CB_ERR_CUDA;
   }
-  return major == 10 && minor == 3 ? CB_OK : CB_ERR_UNSUPPORTED;
+  int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      cudaGetLastError();
+      return CB_ERR_CUDA;
+    }
+    if (major != 10 || minor != 3) n = -1;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  }
+  *sms = n;
+  return n > 0 ? CB_OK : CB_ERR_UNSUPPORTED;
 }
 
 bool overlap(const void* a, uint64_t an, const void* b, uint64_t bn) {

@@ -27,6 +27,8 @@
 // memory, so a stage's commit frees both.  All waits are bounded.
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "fp4.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -641,11 +643,47 @@ int rows_on_16(const Fp4MatmulArgs& a) {
   return (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && a.ld_out * (a.out_f32 ? 4 : 2) % 16 == 0 ? 1 : 0;
 }
 
+// Allows a kernel its shared memory, once per device (bits of `done`).
+template <typename K>
+cudaError_t allow_shared(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+// A launch in a cluster of `cluster` CTAs that may begin (up to
+// grid_dep_wait) while the kernel before it in the stream ends.
+template <typename K, typename... Args>
+cudaError_t launch_cluster(K kernel, unsigned grid, unsigned threads, size_t smem, unsigned cluster, cudaStream_t s,
+                           const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int FMT, int BN, bool SWAP>
 cudaError_t launch(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s) {
   using C = Cfg<FMT, BN, SWAP>;
   auto kernel = fp4_matmul_kernel<FMT, BN, SWAP>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_shared(kernel, C::BYTES, done);
   if (e != cudaSuccess) return e;
   CUtensorMap tp, tq;
   const int64_t b_rows = static_cast<int64_t>(a.n) * a.n_groups;
@@ -653,11 +691,7 @@ cudaError_t launch(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s) {
       !map_codes(&tq, SWAP ? a.a_codes : a.b_codes, SWAP ? a.m : b_rows, a.k, BN))
     return cudaErrorInvalidValue;
   const int vec = rows_on_16(a);
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(THREADS<BN, SWAP>, 1, 1);
-  cfg.dynamicSmemBytes = C::BYTES;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  int64_t grid;
   int ksplit = 1;
   if (SWAP) {
     const int tiles = (a.n + BP - 1) / BP, stages = (a.k + BK - 1) / BK;
@@ -670,25 +704,21 @@ cudaError_t launch(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s) {
       if (each < 2 || ctas > (each >= 4 ? 2 : 1) * num_sms) break;
       ksplit *= 2;
     }
-    cfg.gridDim = dim3(tiles * ksplit, 1, 1);
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ksplit;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    grid = static_cast<int64_t>(tiles) * ksplit;
   } else {
     const int64_t tiles = static_cast<int64_t>((a.m + BP - 1) / BP) * ((a.n + BN - 1) / BN);
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles < num_sms ? tiles : num_sms), 1, 1);
+    grid = tiles < num_sms ? tiles : num_sms;
   }
-  return cudaLaunchKernelEx(&cfg, kernel, tp, tq, a, ksplit, vec);
+  return launch_cluster(kernel, static_cast<unsigned>(grid), THREADS<BN, SWAP>, C::BYTES, SWAP ? ksplit : 0, s, tp, tq,
+                        a, ksplit, vec);
 }
 
 template <int FMT>
 cudaError_t launch_pair(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s) {
   using C = PairCfg<FMT>;
   auto kernel = fp4_matmul_pair_kernel<FMT>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_shared(kernel, C::BYTES, done);
   if (e != cudaSuccess) return e;
   CUtensorMap tp, tq, tps, tqs;
   if (!map_codes(&tp, a.a_codes, a.m, a.k, BP) || !map_codes(&tq, a.b_codes, a.n, a.k, BP) ||
@@ -696,19 +726,8 @@ cudaError_t launch_pair(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s) {
     return cudaErrorInvalidValue;
   const int64_t tiles = static_cast<int64_t>((a.m + 2 * BP - 1) / (2 * BP)) * ((a.n + C::BN - 1) / C::BN);
   const int64_t pairs = num_sms / 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)), 1, 1);
-  cfg.blockDim = dim3(C::THREADS, 1, 1);
-  cfg.dynamicSmemBytes = C::BYTES;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, tp, tq, tps, tqs, a, rows_on_16(a));
+  return launch_cluster(kernel, static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)), C::THREADS, C::BYTES, 2, s, tp,
+                        tq, tps, tqs, a, rows_on_16(a));
 }
 
 template <int FMT>

@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const T* x, int6
   const bool in = col < cols;
   for (int i = threadIdx.x; i < kScaleTiles<FMT> * kScaleTileBytes / 16; i += kThreads)
     reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
+  grid_dep_wait();
   NvScale nv{};
   if constexpr (FMT == kFp4Nv) {
     nv.g = __ldg(tensor_scale);
@@ -222,6 +223,7 @@ __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const uint8_t*
   const int64_t row0 = (blockIdx.x / col_tiles) * kTileRows;
   const int64_t col = (blockIdx.x % col_tiles) * kTileCols + threadIdx.x % 32 * 8;
   if (col >= cols) return;
+  grid_dep_wait();
   const int64_t scale_cols = (cols / kFp4Block<FMT> + 3) / 4;
   const int64_t j = col / kFp4Block<FMT>;
   const uint8_t* sp = scales + ((row0 / kTileRows) * scale_cols + j / 4) * kScaleTileBytes;
@@ -310,11 +312,13 @@ int64_t fp4_tiles(int64_t rows, int64_t cols) {
 }
 
 cudaError_t launch_fp4_quantize(const Fp4Args& a, cudaStream_t s) {
+  PdlScope pdl(true, 0);
   if (a.format == kFp4Mx) return a.f32 ? quantize<kFp4Mx, float>(a, s) : quantize<kFp4Mx, uint16_t>(a, s);
   return a.f32 ? quantize<kFp4Nv, float>(a, s) : quantize<kFp4Nv, uint16_t>(a, s);
 }
 
 cudaError_t launch_fp4_dequantize(const Fp4Args& a, cudaStream_t s) {
+  PdlScope pdl(true, 0);
   if (a.format == kFp4Mx) return a.f32 ? dequantize<kFp4Mx, float>(a, s) : dequantize<kFp4Mx, uint16_t>(a, s);
   return a.f32 ? dequantize<kFp4Nv, float>(a, s) : dequantize<kFp4Nv, uint16_t>(a, s);
 }
