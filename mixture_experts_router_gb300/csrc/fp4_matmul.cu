@@ -42,10 +42,10 @@ constexpr int ROW_BYTES = BK / 2;
 constexpr int EPI_WARP0 = 4;
 // epilogue warps: a quarter of the lanes each, and with two per quarter half
 // of the columns
-template <int BN, bool SWAP>
-constexpr int EPI_WARPS = !SWAP && BN == 256 ? 8 : 4;
-template <int BN, bool SWAP>
-constexpr int THREADS = (EPI_WARP0 + EPI_WARPS<BN, SWAP>) * 32;
+template <bool SWAP>
+constexpr int EPI_WARPS = SWAP ? 4 : 8;
+template <bool SWAP>
+constexpr int THREADS = (EPI_WARP0 + EPI_WARPS<SWAP>) * 32;
 constexpr int P_BYTES = BP * ROW_BYTES;
 
 constexpr int pow2_at_least(int v) {
@@ -174,46 +174,97 @@ __device__ __forceinline__ void transpose_chunks(uint32_t* h, int lane) {
   }
 }
 
-// A warp's 32 rows x 128 bytes, lane = row, h its 32 words: to out (the first
-// row's first byte, rows `pitch` bytes apart), `rows` of them, `elems`
-// elements of ELEM bytes each.  vec: rows start on 16 bytes.
-template <int ELEM>
-__device__ __forceinline__ void store_rows(uint8_t* out, int64_t pitch, uint32_t* h, int rows, int elems, int vec,
-                                           int lane) {
-  if (vec) {
-    constexpr int PER = 16 / ELEM;  // elements of a chunk
-    transpose_chunks(h, lane);
-    uint8_t* o = out + (lane & 24) * pitch + (lane & 7) * 16;
-    const int left = elems - (lane & 7) * PER;
+// The same word by word: h[i] of lane l becomes word l of row i.
+__device__ __forceinline__ void transpose_words(uint32_t* h, int lane) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if ((lane & 24) + i >= rows) continue;
-      if (left >= PER) {
-        *reinterpret_cast<uint4*>(o + i * pitch) = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
-      } else {
+  for (int b = 1; b < 32; b *= 2) {
+    const bool upper = lane & b;
 #pragma unroll
-        for (int u = 0; u < PER - 1; ++u) {
-          if (u >= left) break;
-          if constexpr (ELEM == 4)
-            reinterpret_cast<uint32_t*>(o + i * pitch)[u] = h[4 * i + u];
-          else
-            reinterpret_cast<uint16_t*>(o + i * pitch)[u] = static_cast<uint16_t>(h[4 * i + u / 2] >> (16 * (u & 1)));
-        }
-      }
+    for (int c = 0; c < 32; ++c) {
+      if (c & b) continue;
+      uint32_t& lo = h[c];
+      uint32_t& hi = h[c | b];
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? lo : hi, b);
+      lo = upper ? got : lo;
+      hi = upper ? hi : got;
     }
-  } else if (lane < rows) {
-    uint8_t* o = out + lane * pitch;
+  }
+}
+
+// A warp's 32 rows x 128 bytes, lane = row, h its 32 words: to out (the first
+// row's first byte, rows `pitch` bytes apart and on 16 bytes), `rows` of them,
+// `elems` elements of ELEM bytes each.
+template <int ELEM>
+__device__ __forceinline__ void store_rows(uint8_t* out, int64_t pitch, uint32_t* h, int rows, int elems, int lane) {
+  constexpr int PER = 16 / ELEM;  // elements of a chunk
+  transpose_chunks(h, lane);
+  uint8_t* o = out + (lane & 24) * pitch + (lane & 7) * 16;
+  const int left = elems - (lane & 7) * PER;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if constexpr (ELEM == 4) {
-        if (i < elems) reinterpret_cast<uint32_t*>(o)[i] = h[i];
-      } else {
-        if (2 * i < elems) reinterpret_cast<uint16_t*>(o)[2 * i] = static_cast<uint16_t>(h[i]);
-        if (2 * i + 1 < elems) reinterpret_cast<uint16_t*>(o)[2 * i + 1] = static_cast<uint16_t>(h[i] >> 16);
+  for (int i = 0; i < 8; ++i) {
+    if ((lane & 24) + i >= rows) continue;
+    if (left >= PER) {
+      *reinterpret_cast<uint4*>(o + i * pitch) = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < PER - 1; ++u) {
+        if (u >= left) break;
+        if constexpr (ELEM == 4)
+          reinterpret_cast<uint32_t*>(o + i * pitch)[u] = h[4 * i + u];
+        else
+          reinterpret_cast<uint16_t*>(o + i * pitch)[u] = static_cast<uint16_t>(h[4 * i + u / 2] >> (16 * (u & 1)));
       }
     }
   }
   __syncwarp();
+}
+
+// The same for rows that start anywhere, a row's 128 bytes by the whole warp in
+// words of 4 bytes.  A row of 2-byte elements that starts between two words
+// is moved up by an element first: its words then hold elements 2 l - 1 and
+// 2 l, the one before the first from `carry`, the last 128 bytes' last
+// element; the ends of the warp's columns (`begin`, `end`) are single elements.
+// (Element by element, a lane per row, 4096 x 14331 x 4096 took 542 us.)
+template <int ELEM>
+__device__ __forceinline__ void store_any_rows(uint8_t* out, int64_t pitch, uint32_t* h, int rows, int elems,
+                                               uint32_t& carry, bool begin, bool end, int lane) {
+  const auto moved = [&](int row) {
+    return ELEM == 2 ? static_cast<int>(reinterpret_cast<uintptr_t>(out + row * pitch) >> 1 & 1) : 0;
+  };
+  if constexpr (ELEM == 2) {
+    const int mine = moved(lane);
+    const uint32_t before = carry;
+    carry = h[31];
+#pragma unroll
+    for (int j = 31; j >= 0; --j) h[j] = __funnelshift_rc(j > 0 ? h[j - 1] : before, h[j], 32 - 16 * mine);
+    if (end && mine && lane < rows && elems >= 64)
+      *reinterpret_cast<uint16_t*>(out + lane * pitch + 126) = static_cast<uint16_t>(carry >> 16);
+  }
+  transpose_words(h, lane);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    if (i >= rows) break;
+    if constexpr (ELEM == 4) {
+      if (lane < elems) *reinterpret_cast<uint32_t*>(out + i * pitch + lane * 4) = h[i];
+    } else {
+      const int up = moved(i), e = 2 * lane - up;  // the word's first element
+      uint8_t* o = out + i * pitch + e * 2;
+      if (begin && e < 0) {
+        if (elems > 0) *reinterpret_cast<uint16_t*>(o + 2) = static_cast<uint16_t>(h[i] >> 16);
+      } else if (e + 1 < elems) {
+        *reinterpret_cast<uint32_t*>(o) = h[i];
+      } else if (e < elems) {
+        *reinterpret_cast<uint16_t*>(o) = static_cast<uint16_t>(h[i]);
+      }
+    }
+  }
+  __syncwarp();
+}
+
+// Two accumulators times alpha as a pair of bf16.
+__device__ __forceinline__ uint32_t bf16_pair(float alpha, uint32_t a, uint32_t b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(alpha * __uint_as_float(a), alpha * __uint_as_float(b));
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // An epilogue warp's part of a tile: 32 rows from row0, COLS columns from
@@ -223,16 +274,36 @@ __device__ __forceinline__ void store_tile(const Fp4MatmulArgs& a, uint32_t acc,
                                            int lane, F&& done) {
   const float alpha = FMT == kFp4Nv ? __ldg(a.a_tensor_scale) * __ldg(a.b_tensor_scale + e) : 1.f;
   const int rows = a.m - row0;  // the warp's rows (all 32 but in the last tiles)
-  if (a.out_f32) {
-    uint8_t* out = static_cast<uint8_t*>(a.out) + (static_cast<int64_t>(row0) * a.ld_out + first) * 4;
+  const int elem = a.out_f32 ? 4 : 2;
+  uint8_t* out = static_cast<uint8_t*>(a.out) + (static_cast<int64_t>(row0) * a.ld_out + first) * elem;
+  const int64_t pitch = a.ld_out * elem;
+  if (a.out_f32 || !vec) {
+    // 128 bytes of each row at a time
+    const int step = a.out_f32 ? 32 : 64;
+    uint32_t carry = 0;
 #pragma unroll 1
-    for (int c0 = 0; c0 < COLS && first + c0 < a.n; c0 += 32) {
+    for (int c0 = 0; c0 < COLS && first + c0 < a.n; c0 += step) {
       uint32_t v[32];
       tmem_load32(acc + c0, v);
-      if (c0 + 32 >= COLS || first + c0 + 32 >= a.n) done();
+      const bool last = c0 + step >= COLS || first + c0 + step >= a.n;
+      if (a.out_f32) {
+        if (last) done();
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(alpha * __uint_as_float(v[j]));
-      store_rows<4>(out + c0 * 4, a.ld_out * 4, v, rows, a.n - first - c0, vec, lane);
+        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(alpha * __uint_as_float(v[j]));
+        if (vec)
+          store_rows<4>(out + c0 * 4, pitch, v, rows, a.n - first - c0, lane);
+        else
+          store_any_rows<4>(out + c0 * 4, pitch, v, rows, a.n - first - c0, carry, c0 == 0, last, lane);
+      } else {
+        uint32_t u[32];
+        tmem_load32(acc + c0 + 32, u);
+        if (last) done();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = bf16_pair(alpha, v[2 * j], v[2 * j + 1]);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[16 + j] = bf16_pair(alpha, u[2 * j], u[2 * j + 1]);
+        store_any_rows<2>(out + c0 * 2, pitch, v, rows, a.n - first - c0, carry, c0 == 0, last, lane);
+      }
     }
     if (first >= a.n) done();
   } else {
@@ -243,22 +314,17 @@ __device__ __forceinline__ void store_tile(const Fp4MatmulArgs& a, uint32_t acc,
       uint32_t v[32];
       tmem_load32(acc + c0, v);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const __nv_bfloat162 b =
-            __floats2bfloat162_rn(alpha * __uint_as_float(v[2 * j]), alpha * __uint_as_float(v[2 * j + 1]));
-        h[c0 / 2 + j] = *reinterpret_cast<const uint32_t*>(&b);
-      }
+      for (int j = 0; j < 16; ++j) h[c0 / 2 + j] = bf16_pair(alpha, v[2 * j], v[2 * j + 1]);
     }
     done();
-    uint8_t* out = static_cast<uint8_t*>(a.out) + (static_cast<int64_t>(row0) * a.ld_out + first) * 2;
 #pragma unroll
     for (int c = 0; c < COLS; c += 64)
-      if (first + c < a.n) store_rows<2>(out + c * 2, a.ld_out * 2, h + c / 2, rows, a.n - first - c, vec, lane);
+      if (first + c < a.n) store_rows<2>(out + c * 2, pitch, h + c / 2, rows, a.n - first - c, lane);
   }
 }
 
 template <int FMT, int BN, bool SWAP>
-__global__ void __launch_bounds__((THREADS<BN, SWAP>), 1)
+__global__ void __launch_bounds__((THREADS<SWAP>), 1)
     fp4_matmul_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
                       const Fp4MatmulArgs a, const int ksplit, const int vec) {
   using C = Cfg<FMT, BN, SWAP>;
@@ -281,7 +347,7 @@ __global__ void __launch_bounds__((THREADS<BN, SWAP>), 1)
       mbar_init(&empty[s], 1);
     }
     mbar_init(tfull, 1);
-    mbar_init(tempty, EPI_WARPS<BN, SWAP>);
+    mbar_init(tempty, EPI_WARPS<SWAP>);
     fence_barrier_init();
     prefetch_tensormap(&tm_p);
     prefetch_tensormap(&tm_q);
@@ -383,7 +449,7 @@ __global__ void __launch_bounds__((THREADS<BN, SWAP>), 1)
   } else if (warp >= EPI_WARP0) {
     const int q = warp & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    constexpr int COLS = SWAP ? BN : BN / (EPI_WARPS<BN, SWAP> / 4);  // of this warp
+    constexpr int COLS = SWAP ? BN : BN / (EPI_WARPS<SWAP> / 4);  // of this warp
     const int col0 = SWAP ? 0 : (warp - EPI_WARP0) / 4 * COLS;
     uint32_t tphase = 0;
     for (int i = worker; i < tiles.total; i += workers, tphase ^= 1u) {
@@ -415,7 +481,7 @@ __global__ void __launch_bounds__((THREADS<BN, SWAP>), 1)
     // a token per warp, four output columns per lane; the ranks share the tokens
     const int col = worker * BP + lane * 4;
     const float alpha = FMT == kFp4Nv ? __ldg(a.a_tensor_scale) * __ldg(a.b_tensor_scale) : 1.f;
-    for (int t = rank + ksplit * warp; t < a.m; t += ksplit * (THREADS<BN, SWAP> / 32)) {
+    for (int t = rank + ksplit * warp; t < a.m; t += ksplit * (THREADS<SWAP> / 32)) {
       const uint32_t at = smem_u32(reinterpret_cast<float*>(smem) + t * BP + lane * 4);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -709,7 +775,7 @@ cudaError_t launch(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s) {
     const int64_t tiles = static_cast<int64_t>((a.m + BP - 1) / BP) * ((a.n + BN - 1) / BN);
     grid = tiles < num_sms ? tiles : num_sms;
   }
-  return launch_cluster(kernel, static_cast<unsigned>(grid), THREADS<BN, SWAP>, C::BYTES, SWAP ? ksplit : 0, s, tp, tq,
+  return launch_cluster(kernel, static_cast<unsigned>(grid), THREADS<SWAP>, C::BYTES, SWAP ? ksplit : 0, s, tp, tq,
                         a, ksplit, vec);
 }
 
@@ -738,10 +804,19 @@ cudaError_t launch_format(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s) {
     if (a.m <= 64) return launch<FMT, 64, true>(a, num_sms, s);
     return launch<FMT, 128, true>(a, num_sms, s);
   }
-  // 128-column tiles while the 256-column ones would leave SMs without a tile
-  const int64_t wide = static_cast<int64_t>((a.m + BP - 1) / BP) * ((a.n + 255) / 256);
-  if (wide < num_sms) return launch<FMT, 128, false>(a, num_sms, s);
-  return a.tile_offsets != nullptr ? launch<FMT, 256, false>(a, num_sms, s) : launch_pair<FMT>(a, num_sms, s);
+  // 128-column tiles where one for each SM is enough (512 x 4096 x 4096, 128 of
+  // them: 9.2 us against 10.8; 768 x 4096 x 4096, 192: 13.9 against 11.1);
+  // beyond, pairs for dense products of more than a round of wide tiles that
+  // are long enough for their set-up (nv, k = 4096: 1024 x 14336, 25.9 us
+  // against 27.8, 4096 x 14336, 82 against 97; k = 512: 2048 x 4096, 8.9
+  // against 8.0, 3000 x 14336, 27.4 against 26.6).  Experts keep single CTAs:
+  // of an odd number of row tiles a pair wastes half (2.8 row tiles each: 37.9
+  // us against 31.8; 10.4: 74.5 against 77.8).
+  const int64_t row_tiles = (a.m + BP - 1) / BP;
+  if (row_tiles * ((a.n + 127) / 128) <= num_sms) return launch<FMT, 128, false>(a, num_sms, s);
+  if (a.tile_offsets == nullptr && a.k >= 1024 && row_tiles * ((a.n + 255) / 256) > num_sms)
+    return launch_pair<FMT>(a, num_sms, s);
+  return launch<FMT, 256, false>(a, num_sms, s);
 }
 
 }  // namespace
