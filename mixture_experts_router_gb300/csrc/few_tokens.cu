@@ -139,7 +139,13 @@ __device__ __forceinline__ int in_row(int first, int row) {
 }
 
 // Elements 8 i .. 8 i + 7 of a thread's 16 bytes of a weight row as four bf16
-// pairs, in memory order.
+// pairs, in the order of pair_up: memory order, but for int4 and fp8 the
+// pairs that masks take out of a word without moving bytes.
+//   int4: elements m and m + 4.  A nibble n in a half word under 0x4300 is
+// 128 + n, minus 128 + z exactly n - z (11 instructions for 8 elements; in
+// memory order, by bytes, 15).
+//   fp8: elements m and m + 2.  Sign and magnitude of an e4m3 byte at bits 15
+// and 10-4 are its value times 2^-120 (as in fp8x4_to_bf16x4).
 template <int WF>
 __device__ __forceinline__ void widen8(const uint4& v, int i, uint32_t zz, uint32_t (&o)[4]) {
   const uint32_t in[4] = {v.x, v.y, v.z, v.w};
@@ -147,16 +153,39 @@ __device__ __forceinline__ void widen8(const uint4& v, int i, uint32_t zz, uint3
 #pragma unroll
     for (int j = 0; j < 4; ++j) o[j] = in[j];
   } else if constexpr (WF == kWInt4) {
-    int4x8_minus_zero_to_bf16(in[i], zz, o);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t n;
+      asm("lop3.b32 %0, %1, 0x000F000F, 0x43004300, 0xEA;" : "=r"(n) : "r"(in[i] >> (4 * j)));
+      asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(o[j]) : "r"(n), "r"(zz));
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      if constexpr (WF == kWFp8)
-        fp8x4_to_bf16x4(in[2 * i + j], o[2 * j], o[2 * j + 1]);
-      else
-        int8x4_to_bf16x4_fma(in[2 * i + j], o[2 * j], o[2 * j + 1]);
+      const uint32_t w = in[2 * i + j];
+      if constexpr (WF == kWFp8) {
+        uint32_t a, b;
+        asm("lop3.b32 %0, %1, 0x80008000, %2, 0xEA;" : "=r"(a) : "r"(w << 8), "r"((w << 4) & 0x07F007F0u));
+        asm("lop3.b32 %0, %1, 0x80008000, %2, 0xEA;" : "=r"(b) : "r"(w), "r"((w >> 4) & 0x07F007F0u));
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[2 * j]) : "r"(a), "r"(0x7B807B80u));
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[2 * j + 1]) : "r"(b), "r"(0x7B807B80u));
+      } else {
+        int8x4_to_bf16x4_fma(w, o[2 * j], o[2 * j + 1]);
+      }
     }
   }
+}
+// Eight elements of a token in the same pairs.
+template <int WF>
+__device__ __forceinline__ uint4 pair_up(const uint4& t) {
+  if constexpr (WF == kWInt4)
+    return make_uint4(__byte_perm(t.x, t.z, 0x5410), __byte_perm(t.x, t.z, 0x7632), __byte_perm(t.y, t.w, 0x5410),
+                      __byte_perm(t.y, t.w, 0x7632));
+  else if constexpr (WF == kWFp8)
+    return make_uint4(__byte_perm(t.x, t.y, 0x5410), __byte_perm(t.x, t.y, 0x7632), __byte_perm(t.z, t.w, 0x5410),
+                      __byte_perm(t.z, t.w, 0x7632));
+  else
+    return t;
 }
 
 // A stretch of the ring's stages, one after the other.
@@ -472,7 +501,7 @@ struct Block {
           uint4 t[NT];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            if (n == 0 || n < tiles) t[n] = *reinterpret_cast<const uint4*>(st + at.tok[n][i]);
+            if (n == 0 || n < tiles) t[n] = pair_up<WF>(*reinterpret_cast<const uint4*>(st + at.tok[n][i]));
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             if (m == 1 && halves < 2) break;
