@@ -97,7 +97,7 @@ cb_status_t cb_fp4_quantize(int32_t format, const void* x, int32_t x_type, int64
   if ((st = check_device(&sms)) != CB_OK) return st;
   if (fault_injected("launch")) return CB_ERR_CUDA;
   const Fp4Args a{format, x_type == CB_T_F32, const_cast<void*>(x), rows, cols, ld, tensor_scale, codes, scales};
-  return launch_fp4_quantize(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CB_OK : CB_ERR_CUDA;
+  return launch_fp4_quantize(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CB_OK : CB_ERR_CUDA;
 }
 
 cb_status_t cb_fp4_dequantize(int32_t format, const uint8_t* codes, const uint8_t* scales, const float* tensor_scale,
@@ -109,7 +109,7 @@ cb_status_t cb_fp4_dequantize(int32_t format, const uint8_t* codes, const uint8_
   if (fault_injected("launch")) return CB_ERR_CUDA;
   const Fp4Args a{format, out_type == CB_T_F32, out, rows, cols, ld, tensor_scale, const_cast<uint8_t*>(codes),
                   const_cast<uint8_t*>(scales)};
-  return launch_fp4_dequantize(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CB_OK : CB_ERR_CUDA;
+  return launch_fp4_dequantize(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CB_OK : CB_ERR_CUDA;
 }
 
 cb_status_t cb_fp4_matmul(const cb_fp4_matmul_t* p, void* stream) {

@@ -86,7 +86,7 @@ struct cb_moe {
   uint16_t* few_h;         // the few-token layer's H, logits and (hash router) experts
   float* few_logits;
   int32_t* few_ids;
-  FewMaps few_maps;
+  FewMaps few_maps[2];
   int32_t few_grid;        // blocks of its cooperative launch
   bool fused_combine;      // the CTA-pair down GEMM adds its rows into the token sums
   const void* tm_x_src;    // x pointer tm_x was encoded for
@@ -886,7 +886,7 @@ cb_status_t cb_moe_init(const cb_moe_config_t* cfg, const cb_moe_weights_t* wts,
   int few_per_sm = 0;
   ok = ok && few_tokens_prepare(few_format(int8w, weight_format(*cfg)), &few_per_sm) == cudaSuccess;
   h->few_grid = std::min(few_per_sm, 1) * h->num_sms;
-  ok = ok && few_token_maps(few_format(int8w, weight_format(*cfg)), few_args(h), &h->few_maps);
+  ok = ok && few_token_maps(few_format(int8w, weight_format(*cfg)), few_args(h), h->few_maps);
   // router: tcgen05 for wide expert counts, the mma.sync split-K router for
   // E <= 16 (bound by reading x, where more CTAs help); CB_MOE_ROUTER=tc|mma
   // overrides the choice

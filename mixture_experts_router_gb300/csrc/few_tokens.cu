@@ -16,8 +16,8 @@
 // most 16 tokens an expert's 128-row tiles of the large kernels would be
 // nearly all padding.  So a tile here is at most 32 weight rows (in step 3, 16
 // features' gate and up rows; in step 4, 32 output columns), streamed through
-// a ring of stages of 512 (int4: 256) bytes per row, with the same stretch of the chosen
-// tokens' activations beside them.
+// a ring of stages of 512 (int4 with 16 tokens: 256) bytes per row, with the same
+// stretch of the chosen tokens' activations beside them.
 //
 // A block is two halves, each with a ring, two feeding warps and 8 users:
 //
@@ -107,14 +107,15 @@ struct Shared {
   int ok;
 };
 
-// Bytes of a row per stage; int4's, with four times as many bytes of tokens
-// beside them, are fewer.
-template <int WF>
-constexpr int kSeg = WF == kWInt4 ? 256 : 512;
+// Bytes of a row per stage; int4's with 16 tokens, four times as many bytes
+// each beside them, are fewer.  (With 8 tokens 256 bytes are slower too: 16
+// tokens over 64 experts 170 us against 162.)
+template <int WF, int NT>
+constexpr int kSeg = WF == kWInt4 && NT == 2 ? 256 : 512;
 
 template <int WF, int NT, int MT>
 struct Geo {
-  static constexpr int kSeg = cbmoe::kSeg<WF>;
+  static constexpr int kSeg = cbmoe::kSeg<WF, NT>;
   static constexpr int kRowLines = kSeg / 128;
   static constexpr int kWeightBytes = kRows * kSeg;
   static constexpr int kStep = kSeg / kAlong;             // bytes of a row per warp
@@ -842,10 +843,11 @@ cudaError_t few_tokens_prepare(int format, int* blocks_per_sm) {
   return cudaErrorInvalidValue;
 }
 
-bool few_token_maps(int format, const FewArgs& a, FewMaps* m) {
+template <int NT>
+static bool part_maps(int format, const FewArgs& a, FewMaps* m) {
   const uint64_t elems = format == kBf16 ? kElems<kBf16> : format == kWInt4 ? kElems<kWInt4> : kElems<kWInt8>;
   const uint64_t up = a.d / elems * 16, down = a.f / elems * 16, blk = a.gu_block;
-  const cuuint32_t lines = (format == kWInt4 ? kSeg<kWInt4> : kSeg<kBf16>) / 128;
+  const cuuint32_t lines = (format == kWInt4 ? kSeg<kWInt4, NT> : kSeg<kBf16, NT>) / 128;
   // rows of bytes as (byte of a 128-byte chunk, chunk, row[, gate or up, interleave block])
   const cuuint64_t up_dims[5] = {128, up / 128, blk, 2, static_cast<uint64_t>(a.E) * a.f / blk};
   const cuuint64_t up_strides[4] = {128, up, blk * up, 2 * blk * up};
@@ -863,17 +865,21 @@ bool few_token_maps(int format, const FewArgs& a, FewMaps* m) {
   return ok;
 }
 
+bool few_token_maps(int format, const FewArgs& a, FewMaps (&m)[2]) {
+  return part_maps<1>(format, a, &m[0]) && part_maps<2>(format, a, &m[1]);
+}
+
 // More than 8 tokens: parts of up to 16 where experts have more than 4 of the
 // tokens on average.  Below, the few experts that have more than 8 are taken
 // in two parts, their weights read twice; the smaller stages leave half as
 // many again of them in flight.
 template <int WF>
-static cudaError_t launch_format(const FewMaps& m, const FewArgs& a, int grid, cudaStream_t s) {
-  if (a.n <= 8) return launch<WF, 1, 8>(m, a, grid, s);
-  return a.n * a.k > 4 * a.E ? launch<WF, 2, 16>(m, a, grid, s) : launch<WF, 1, 16>(m, a, grid, s);
+static cudaError_t launch_format(const FewMaps (&m)[2], const FewArgs& a, int grid, cudaStream_t s) {
+  if (a.n <= 8) return launch<WF, 1, 8>(m[0], a, grid, s);
+  return a.n * a.k > 4 * a.E ? launch<WF, 2, 16>(m[1], a, grid, s) : launch<WF, 1, 16>(m[0], a, grid, s);
 }
 
-cudaError_t launch_few_tokens(int format, const FewMaps& m, const FewArgs& a, int grid, cudaStream_t s) {
+cudaError_t launch_few_tokens(int format, const FewMaps (&m)[2], const FewArgs& a, int grid, cudaStream_t s) {
   if (a.n <= 0) return cudaSuccess;
   if (a.n > kMaxTokens || a.E > kMaxExperts || a.k > kMaxK || grid <= 0) return cudaErrorInvalidValue;
   switch (format) {

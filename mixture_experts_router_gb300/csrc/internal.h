@@ -328,8 +328,8 @@ struct FewMaps {
   CUtensorMap gate_up[16 / kFewRowStep];
   CUtensorMap down[32 / kFewRowStep];
 };
-bool few_token_maps(int format, const FewArgs& a, FewMaps* m);
-cudaError_t launch_few_tokens(int format, const FewMaps& m, const FewArgs& a, int grid, cudaStream_t s);
+bool few_token_maps(int format, const FewArgs& a, FewMaps (&m)[2]);
+cudaError_t launch_few_tokens(int format, const FewMaps (&m)[2], const FewArgs& a, int grid, cudaStream_t s);
 
 // ------------------------------------------- 4-bit floats with block scales
 struct Fp4Args {
@@ -341,9 +341,9 @@ struct Fp4Args {
   uint8_t* codes;
   uint8_t* scales;
 };
-int64_t fp4_tiles(int64_t rows, int64_t cols);  // blocks of either launch
-cudaError_t launch_fp4_quantize(const Fp4Args& a, cudaStream_t s);
-cudaError_t launch_fp4_dequantize(const Fp4Args& a, cudaStream_t s);
+int64_t fp4_tiles(int64_t rows, int64_t cols);  // of 128 x 256 elements
+cudaError_t launch_fp4_quantize(const Fp4Args& a, int num_sms, cudaStream_t s);
+cudaError_t launch_fp4_dequantize(const Fp4Args& a, int num_sms, cudaStream_t s);
 
 struct Fp4MatmulArgs {
   int32_t format;
