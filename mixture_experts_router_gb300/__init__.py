@@ -453,23 +453,30 @@ class Fp4Matrix:
     __slots__ = ("format", "rows", "cols", "groups", "codes", "scales", "tensor_scale")
 
     def __init__(self, format, rows, cols, codes, scales, tensor_scale=None):
-        torch = _load_torch()
+        torch = _torch or _load_torch()
         if format not in FP4_FORMATS:
             raise ValueError(f"unknown 4-bit format {format!r}: one of {sorted(FP4_FORMATS)}")
-        self.format, self.rows, self.cols = format, rows, cols
-        self.codes, self.scales, self.tensor_scale = codes, scales, tensor_scale
-        shape = codes.shape
-        self.groups = groups = shape[0] if len(shape) == 3 else 1
+        self.format = format
+        self.rows = rows
+        self.cols = cols
+        self.codes = codes
+        self.scales = scales
+        self.tensor_scale = tensor_scale
+        shape, kind, device = codes.shape, torch.uint8, codes.get_device()
+        dims = len(shape)
+        self.groups = groups = shape[0] if dims == 3 else 1
         need = _fp4_scale_bytes(format, rows, cols) * groups
-        if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8 or shape[-2:] != (rows, cols // 2) or \
-                scales.numel() != need or not (codes.is_contiguous() and scales.is_contiguous()):
+        if dims not in (2, 3) or shape[-2] != rows or shape[-1] != cols // 2 or scales.numel() != need or \
+                codes.dtype is not kind or scales.dtype is not kind or \
+                not (codes.is_contiguous() and scales.is_contiguous()):
             raise ValueError(f"codes {tuple(shape)} {codes.dtype}, scales {tuple(scales.shape)} {scales.dtype}: not "
                              f"{groups} contiguous {format} matrices of {rows} x {cols} ({need} scale bytes)")
         if (tensor_scale is not None) != (format == "nv") or \
                 (tensor_scale is not None and (tensor_scale.dtype is not torch.float32 or
                                                tensor_scale.numel() != groups or not tensor_scale.is_contiguous())):
             raise ValueError("format nv has one fp32 tensor scale per matrix, format mx none")
-        _check_device(codes.get_device(), scales, tensor_scale)
+        if scales.get_device() != device or (tensor_scale is not None and tensor_scale.get_device() != device):
+            _check_device(device, scales, tensor_scale)
 
 
 def fp4_quantize(x, format, tensor_scale=None, stream=None) -> Fp4Matrix:
