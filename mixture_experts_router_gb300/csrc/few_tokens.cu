@@ -16,8 +16,8 @@
 // most 16 tokens an expert's 128-row tiles of the large kernels would be
 // nearly all padding.  So a tile here is at most 32 weight rows (in step 3, 16
 // features' gate and up rows; in step 4, 32 output columns), streamed through
-// a ring of stages of 512 (int4 with 16 tokens: 256) bytes per row, with the same
-// stretch of the chosen tokens' activations beside them.
+// a ring of stages of 512 (int4 with 16 tokens: 256) bytes per row, with the
+// same stretch of the chosen tokens' activations beside them.
 //
 // A block is two halves, each with a ring, two feeding warps and 8 users:
 //
@@ -44,6 +44,12 @@
 // The balance: the parts' features (step 3) and the output columns
 // (step 4) are cut into one contiguous share per block, in steps of 4 (the
 // rows of the smallest copy).
+//
+// Measured on the GPU alone, d x f x experts, bf16 if not said: 1 token of 2 of
+// 8 of 4096 x 14336, 112 us and 8 tokens 379 (6.3 and 6.7 TB/s); 3 tokens of 4
+// of 128 of 2048 x 768, 33 us (half of it start and barriers); 16 tokens of 6
+// of 64 of 4096 x 1536, int8, 196 us (4.9 TB/s: widening) and int4 162; 1 token
+// of 2 of 8 of 256 x 512, 12 us (launch and phases).
 //
 // Every sum is fp32 in a fixed order (mma accumulators, experts in ascending
 // order, then the warps in order), so results do not change from run to

@@ -7,9 +7,8 @@
 // memory, and sums in fp32.  Codes arrive by TMA (128-byte swizzled rows of
 // K = 256), scales as whole 512-byte tiles of 128 rows x 4 blocks, each of
 // which becomes 4 columns of tensor memory, the same for each quarter of the
-// lanes.  A row's tail past k is zero codes
-// (TMA's fill); scale words past the array are not loaded, and no
-// instruction runs past k.
+// lanes.  A row's tail past k is zero codes (TMA's fill); scale words past the
+// array are not used, and no instruction runs past k.
 //
 // The two operands' roles.  The MMA's M side is 128 rows, its N side BN.
 //  * more than 128 rows of A, or experts: A's rows are the M side, BN rows of
@@ -25,6 +24,12 @@
 // Per CTA: warp 0 TMA producer, warp 1 tensor memory, scale copies and MMAs,
 // warps 4.. epilogue.  Stage s of the ring has its own scale columns in tensor
 // memory, so a stage's commit frees both.  All waits are bounded.
+//
+// Measured on the GPU alone (inputs larger than L2 in turn or as large as they
+// are): 1 x 14336 x 4096 7.6 us, 64 x 4096 x 14336 9.8 us (the weights at 4.3
+// and 3.2 TB/s: launch, first loads and the joining are most of both), 64
+// experts of 1536 x 4096 in 84 row tiles 53 us (4.6 TB/s), 4096 x 14336 x 4096
+// 82 us and 8192^3 164 us (nv) or 157 us (mx): 5.9, 6.7 and 7.0 PFLOP/s.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -530,7 +535,11 @@ __global__ void __launch_bounds__((THREADS<SWAP>), 1)
 // ------------------------------------------------------------------- CTA pairs
 // A cluster of two CTAs takes 256 rows of A (128 each) against 256 rows of B
 // with the 2-SM MMA.  Each stages half of B's rows and the tensor cores read
-// both halves: 38 KB a stage (NV) against 54.
+// both halves: 38 KB a stage (NV) against 54.  What bounds it is that feed: a
+// stage takes 306 ns, 124 bytes/ns and SM (64 a cycle), its four MMAs about
+// 190.  The accumulator is single, scales having the rest of tensor memory;
+// handing it over costs 0.7 us a tile, and the output's stores share the feed
+// (4096 x 14336 x 4096 without them: 68 us instead of 82).
 //
 // Barriers: both CTAs' copies complete the even CTA's `full`; the MMA's
 // commits arrive on `empty` and `tfull` of both; the epilogue warps of both
@@ -761,13 +770,13 @@ cudaError_t launch(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s) {
   int ksplit = 1;
   if (SWAP) {
     const int tiles = (a.n + BP - 1) / BP, stages = (a.k + BK - 1) / BK;
-    // CTAs enough for every SM, or for two per SM where they keep 4 stages
-    // each; all are resident at once (112 tiles of k = 4096: 9.6 us unsplit, 8.5
-    // in two, 11.7 in four; 32 tiles: 11.5, 8.9, 6.6, and 7.3 in eight)
+    // CTAs enough for every SM, or for half of them twice where they keep 4
+    // stages each (112 tiles of 16 stages: 9.7 us unsplit, 9.3 in two, 12.4 in
+    // four; 32 tiles of 56 stages: 23.8, 15.3, 11.5 in four and 12.3 in eight)
     while (ksplit < 8) {
       const int64_t ctas = 2ll * ksplit * tiles;
       const int each = stages / (2 * ksplit);
-      if (each < 2 || ctas > (each >= 4 ? 2 : 1) * num_sms) break;
+      if (each < 2 || ctas > (each >= 4 ? num_sms + num_sms / 2 : num_sms)) break;
       ksplit *= 2;
     }
     grid = static_cast<int64_t>(tiles) * ksplit;
