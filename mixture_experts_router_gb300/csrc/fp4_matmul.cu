@@ -731,8 +731,9 @@ cudaError_t allow_shared(K kernel, int bytes, std::atomic<uint64_t>& done) {
   return e;
 }
 
-// A launch in a cluster of `cluster` CTAs that may begin (up to
-// grid_dep_wait) while the kernel before it in the stream ends.
+// A launch in clusters of `cluster` CTAs (0: none).  It follows arbitrary work
+// of the caller, so it does not begin before that has ended: a kernel that
+// let it begin and allocated tensor memory only then could wait for it.
 template <typename K, typename... Args>
 cudaError_t launch_cluster(K kernel, unsigned grid, unsigned threads, size_t smem, unsigned cluster, cudaStream_t s,
                            const Args&... args) {
@@ -741,15 +742,13 @@ cudaError_t launch_cluster(K kernel, unsigned grid, unsigned threads, size_t sme
   cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  cfg.numAttrs = cluster > 0 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

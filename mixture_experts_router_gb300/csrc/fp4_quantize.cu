@@ -343,14 +343,12 @@ int64_t fp4_tiles(int64_t rows, int64_t cols) {
 }
 
 cudaError_t launch_fp4_quantize(const Fp4Args& a, int num_sms, cudaStream_t s) {
-  PdlScope pdl(true, 0);
   return with_types(a, num_sms, [&](auto fmt, auto t, auto vec, auto parts) {
     return quantize<decltype(fmt)::value, decltype(t), decltype(vec)::value, decltype(parts)::value>(a, s);
   });
 }
 
 cudaError_t launch_fp4_dequantize(const Fp4Args& a, int num_sms, cudaStream_t s) {
-  PdlScope pdl(true, 0);
   return with_types(a, num_sms, [&](auto fmt, auto t, auto vec, auto parts) {
     return dequantize<decltype(fmt)::value, decltype(t), decltype(vec)::value, decltype(parts)::value>(a, s);
   });
