@@ -26,10 +26,10 @@
 // memory, so a stage's commit frees both.  All waits are bounded.
 //
 // Measured on the GPU alone (inputs larger than L2 in turn or as large as they
-// are): 1 x 14336 x 4096 7.6 us, 64 x 4096 x 14336 9.8 us (the weights at 4.3
-// and 3.2 TB/s: launch, first loads and the joining are most of both), 64
+// are): 1 x 14336 x 4096 8.0 us, 64 x 4096 x 14336 10.1 us (the weights at 4.1
+// and 3.1 TB/s: launch, first loads and the joining are most of both), 64
 // experts of 1536 x 4096 in 84 row tiles 53 us (4.6 TB/s), 4096 x 14336 x 4096
-// 82 us and 8192^3 164 us (nv) or 157 us (mx): 5.9, 6.7 and 7.0 PFLOP/s.
+// 81 us and 8192^3 164 us (nv) or 157 us (mx): 5.9, 6.7 and 7.0 PFLOP/s.
 #include <cuda_bf16.h>
 
 #include <atomic>

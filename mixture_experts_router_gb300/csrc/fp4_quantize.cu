@@ -1,7 +1,7 @@
 // Quantisation to 4-bit floating point with block scales and its way back.
 //
 // Bound by memory: 2 or 4 bytes an element in, half a byte and a 16th or 32nd
-// out (28672 x 4096 bf16, mx: 54 us, 5.5 TB/s, and 48 us, 6.2 TB/s, back).  A
+// out (28672 x 4096 bf16, mx: 55 us, 5.4 TB/s, and 49 us, 6.1 TB/s, back).  A
 // block of 256 threads takes a tile of 128 rows x 256 columns, a thread 8
 // consecutive elements of 16 rows (16 bytes of bf16, so a warp reads 512-byte
 // runs), kBatch rows' loads ahead of their arithmetic.  The largest magnitude
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const T* x, int6
                                                                 uint8_t* scales, int64_t col_tiles) {
   constexpr int LANES = kFp4Block<FMT> / 8;  // lanes that share a block
   __shared__ __align__(16) uint8_t tile[kScaleTiles<FMT> * kScaleTileBytes];
-  const unsigned at = blockIdx.x / PARTS, part = blockIdx.x % PARTS;
+  const int at = static_cast<int>(blockIdx.x / PARTS), part = static_cast<int>(blockIdx.x % PARTS);
   const int64_t row0 = (at / col_tiles) * kTileRows;
   const int64_t col0 = (at % col_tiles) * kTileCols;
   const int lane = threadIdx.x % 32;
@@ -166,8 +166,8 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const T* x, int6
   }
   __syncthreads();
   const int first = threadIdx.x / 32;
-  for (int b = part * (kTileBatches / PARTS); b < (part + 1) * (kTileBatches / PARTS); ++b) {
-    const int i0 = b * kBatch;
+  const int i_first = part * kBatch, i_end = PARTS == 1 ? kTileRows / kRowsAtOnce : i_first + kBatch;
+  for (int i0 = i_first; i0 < i_end; i0 += kBatch) {
     if (row0 + i0 * kRowsAtOnce >= rows) break;
     Eight<T, VEC> v[kBatch];
 #pragma unroll
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const uint8_t*
                                                                   const float* tensor_scale, int64_t rows,
                                                                   int64_t cols, T* out, int64_t ld,
                                                                   int64_t col_tiles) {
-  const unsigned at = blockIdx.x / PARTS, part = blockIdx.x % PARTS;
+  const int at = static_cast<int>(blockIdx.x / PARTS), part = static_cast<int>(blockIdx.x % PARTS);
   const int64_t row0 = (at / col_tiles) * kTileRows;
   const int64_t col = (at % col_tiles) * kTileCols + threadIdx.x % 32 * 8;
   if (col >= cols) return;
@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const uint8_t*
   float g = 1.f;
   if constexpr (FMT == kFp4Nv) g = __ldg(tensor_scale);
   const int first = threadIdx.x / 32;
-  for (int b = part * (kTileBatches / PARTS); b < (part + 1) * (kTileBatches / PARTS); ++b) {
-    const int i0 = b * kBatch;
+  const int i_first = part * kBatch, i_end = PARTS == 1 ? kTileRows / kRowsAtOnce : i_first + kBatch;
+  for (int i0 = i_first; i0 < i_end; i0 += kBatch) {
     uint32_t c[kBatch], s[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
