@@ -529,10 +529,13 @@ def fp4_dequantize(m: Fp4Matrix, dtype=None, out=None, stream=None):
         with _On(device, stream):
             return fp4_dequantize(m, dtype, out)
     if out is None:
-        out = torch.empty((m.rows, m.cols), dtype=dtype or torch.bfloat16, device=codes.device)
+        ld = m.cols
+        out = torch.empty((m.rows, ld), dtype=dtype or torch.bfloat16, device=codes.device)
+    else:
+        ld = _row_stride(out)
     st = (_lib or load_library()).cb_fp4_dequantize(
         FP4_FORMATS[m.format], codes.data_ptr(), m.scales.data_ptr(), None if g is None else g.data_ptr(), m.rows,
-        m.cols, out.data_ptr(), kind, _row_stride(out), s)
+        m.cols, out.data_ptr(), kind, ld, s)
     if st != CB_OK:
         raise CbMoeError(st, "cb_fp4_dequantize")
     return out
@@ -565,14 +568,18 @@ def fp4_matmul(a: Fp4Matrix, b: Fp4Matrix, dtype=None, out=None, tile_offsets=No
     if s is None:
         with _On(device, stream):
             return fp4_matmul(a, b, dtype, out, tile_offsets, status)
+    rows, cols = a.rows, b.rows
     if out is None:
-        out = torch.empty((a.rows, b.rows), dtype=dtype or torch.bfloat16, device=a.codes.device)
+        ld = cols
+        out = torch.empty((rows, cols), dtype=dtype or torch.bfloat16, device=a.codes.device)
+    else:
+        ld = _row_stride(out)
     nv = a.tensor_scale is not None
     st = (_lib or load_library()).cb_fp4_matmul(_FP4_MATMUL.pack(
-        FP4_FORMATS[a.format], kind, a.rows, b.rows, a.cols, a.codes.data_ptr(), a.scales.data_ptr(),
+        FP4_FORMATS[a.format], kind, rows, cols, a.cols, a.codes.data_ptr(), a.scales.data_ptr(),
         a.tensor_scale.data_ptr() if nv else 0, b.codes.data_ptr(), b.scales.data_ptr(),
         b.tensor_scale.data_ptr() if nv else 0, b.groups, 0 if tile_offsets is None else tile_offsets.data_ptr(),
-        out.data_ptr(), _row_stride(out), 0 if status is None else status.data_ptr()), s)
+        out.data_ptr(), ld, 0 if status is None else status.data_ptr()), s)
     if st != CB_OK:
         raise CbMoeError(st, "cb_fp4_matmul")
     return out
