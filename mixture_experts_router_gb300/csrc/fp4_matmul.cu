@@ -537,7 +537,7 @@ __global__ void __launch_bounds__((THREADS<SWAP>), 1)
 // with the 2-SM MMA.  Each stages half of B's rows and the tensor cores read
 // both halves: 38 KB a stage (NV) against 54.  What bounds it is that feed: a
 // stage takes 306 ns, 124 bytes/ns and SM (64 a cycle), its four MMAs about
-// 190.  The accumulator is single, scales having the rest of tensor memory;
+// 190 (from issuing each twice).  The accumulator is single, scales having the rest of tensor memory;
 // handing it over costs 0.7 us a tile, and the output's stores share the feed
 // (4096 x 14336 x 4096 without them: 68 us instead of 82).
 //
