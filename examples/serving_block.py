@@ -55,9 +55,15 @@ class ServingBlock:
         self.dense, self.d, self.graphs = dense, d, {}
 
     def prompt(self, x):
-        out = torch.empty(x.shape, dtype=torch.float32, device=x.device)
-        self.layer.forward(x, out, stream=torch.cuda.current_stream(), f32out=True)
-        return (out + self.dense(x)).bfloat16()
+        """Up to prompt_tokens tokens: the handle's forward takes exactly that many, so a shorter
+        prompt is padded with rows of zeros, whose results are dropped."""
+        n, T = x.shape[0], self.layer.cfg.n_tokens
+        if n > T:
+            raise ValueError(f"a prompt of {n} tokens for a handle of {T}")
+        rows = x if n == T else torch.cat([x, x.new_zeros((T - n, self.d))])
+        out = torch.empty((T, self.d), dtype=torch.float32, device=x.device)
+        self.layer.forward(rows, out, stream=torch.cuda.current_stream(), f32out=True)
+        return (out[:n] + self.dense(x)).bfloat16()
 
     def _decode(self, x):
         out = torch.empty(x.shape, dtype=torch.float32, device=x.device)
@@ -101,7 +107,9 @@ class Fp4Experts:
 
     def __call__(self, x, layer):
         """x as in layer's last forward, whose routing is used."""
-        T, k, E = x.shape[0], layer.cfg.top_k, layer.cfg.n_experts
+        T, k, E = layer.cfg.n_tokens, layer.cfg.top_k, layer.cfg.n_experts
+        if x.shape[0] != T:
+            raise ValueError(f"{x.shape[0]} rows for the routing of {T} tokens")
         v, grab = layer.routing(), {}
         for name, n, dtype in (("ids", T * k, torch.int32), ("w", T * k, torch.float32), ("inv", T * k, torch.int32),
                                ("offsets", E + 1, torch.int32), ("tile_offsets", E + 1, torch.int32)):

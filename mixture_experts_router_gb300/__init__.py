@@ -298,6 +298,14 @@ class MoELayer:
         self.handle = h
 
     def forward(self, x, out, stream=None, f32out=False):
+        """The layer for the handle's T tokens: x bf16 (or int16 bits), out bf16 (fp32 with f32out),
+        contiguous and of T d elements (more are left alone).  Runs on `stream`, or on the legacy
+        default stream."""
+        need = self.cfg.n_tokens * self.cfg.d_model
+        for name, t, size in (("x", x, 2), ("out", out, 4 if f32out else 2)):
+            if not t.is_contiguous() or t.numel() * t.element_size() < need * size:
+                raise ValueError(f"forward: {name} {tuple(t.shape)} {t.dtype} is not contiguous or holds less than "
+                                 f"{self.cfg.n_tokens} x {self.cfg.d_model} elements of {size} bytes")
         s = 0 if stream is None else stream.cuda_stream
         fn = cb_moe_forward_f32out if f32out else cb_moe_forward
         st = fn(self.handle, x.data_ptr(), out.data_ptr(), s)

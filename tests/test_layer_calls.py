@@ -1,0 +1,88 @@
+"""What MoELayer's calls and examples/serving_block.py refuse before anything reaches the library, and
+that they run where the caller says.  Most of it needs no GPU: the handle is a stand-in."""
+import os
+import sys
+import types
+
+import pytest
+import torch
+
+import mixture_experts_router_gb300 as cb
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+
+
+class Reached(Exception):
+    """The call got as far as the library."""
+
+
+def layer(T, d, device=0):
+    """A MoELayer that stands for a handle of T tokens; nothing is on a GPU."""
+    m = cb.MoELayer.__new__(cb.MoELayer)
+    m.handle, m.cfg = None, cb.cb_moe_config_t(T, d, 256, 4, 2, cb.CB_W_BF16, device, 0, 0, 0)
+    return m
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The library's forwards, replaced by a record of what reached them."""
+    got = []
+    for name in ("cb_moe_forward", "cb_moe_forward_f32out", "cb_moe_forward_few", "cb_moe_forward_few_f32out"):
+        monkeypatch.setattr(cb, name, lambda *a, name=name: got.append((name,) + a) or cb.CB_OK)
+    return got
+
+
+def bf16(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+# ---------------------------------------------------------------- forward
+def test_forward_refuses_tensors_that_it_would_run_past(calls):
+    m = layer(20, 256)
+    ok, f32 = bf16(20, 256), torch.zeros(20, 256)
+    m.forward(ok, ok.clone())
+    m.forward(bf16(33, 256), bf16(33, 256))                              # the first 20 rows
+    m.forward(torch.zeros(20 * 256, dtype=torch.int16), ok)              # bits, any shape
+    m.forward(ok, f32, f32out=True)
+    assert len(calls) == 4
+    short, gaps = bf16(19, 256), bf16(20, 512)[:, ::2]
+    for x, out, kind in ((short, ok, False), (ok, short, False), (ok, ok.clone(), True), (gaps, ok, False), (ok, gaps, False),
+                         (bf16(1, 256).expand(20, 256), ok, False)):
+        with pytest.raises(ValueError):
+            m.forward(x, out, f32out=kind)
+    assert len(calls) == 4
+
+
+# ---------------------------------------------------------------- example
+def test_serving_block_takes_prompts_up_to_its_handles_tokens(calls, monkeypatch):
+    import serving_block as sb
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=5))
+    block = sb.ServingBlock.__new__(sb.ServingBlock)
+    block.layer, block.d, block.dense = layer(20, 256), 256, lambda x: torch.zeros(x.shape[0], 256)
+    for n in (20, 7, 0):
+        assert block.prompt(bf16(n, 256)).shape == (n, 256)
+    assert [c[0] for c in calls] == ["cb_moe_forward_f32out"] * 3
+    with pytest.raises(ValueError):
+        block.prompt(bf16(21, 256))
+
+
+def test_fp4_experts_refuse_rows_that_were_not_routed():
+    import serving_block as sb
+    for n in (19, 21):
+        with pytest.raises(ValueError):
+            sb.Fp4Experts.__call__(None, bf16(n, 256), layer(20, 256))
+
+
+@pytest.mark.gpu
+def test_prompts_of_several_lengths():
+    """A short prompt is the full one whose other rows are zeros (the routed experts' part: k = 2, so
+    that the order of a token's additions does not matter)."""
+    import serving_block as sb
+    block, _, _ = sb.random_block(d=512, f=256, E=8, top_k=2, dense_f=256, prompt_tokens=100)
+    block.dense = lambda x: torch.zeros(x.shape, device="cuda")
+    x = torch.randn(100, 512, device="cuda").bfloat16()
+    for n in (1, 37, 99):
+        padded = torch.cat([x[:n], torch.zeros_like(x[n:])])
+        got, want = block.prompt(x[:n]), block.prompt(padded)[:n]
+        assert torch.equal(got, want) and got.abs().max() > 0
+    assert block.layer.last_error() == cb.CB_OK
