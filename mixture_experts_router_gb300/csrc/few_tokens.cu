@@ -786,6 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         met = b.poll(expected);
         __threadfence();
       }
+      __syncwarp();  // the other lanes read other blocks' H too (a vote orders no memory)
       if (__all_sync(0xffffffffu, met))
         b.feed_h(down_bytes);
       else

@@ -274,3 +274,21 @@ def test_zero_and_refused_sizes():
         del os.environ["CB_MOE_INJECT_FAULT"]
     torch.cuda.synchronize()
     assert r.m.last_error() == cb.CB_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("wdtype", ["bf16", "int8", "int4", "fp8"])
+@pytest.mark.parametrize("n", [3, 14])
+def test_every_run_reads_its_own_intermediate_values(wdtype, n):
+    """Runs in turn on two inputs without a pause between them: a block that read another block's H
+    before it was written would find the other input's there."""
+    r = Run(synth.custom_shape("few", n, 512, 2048, 16, 4, wdtype=wdtype, seed=17))
+    xs = [r.x, (r.x.view(torch.bfloat16).float() * -0.5).bfloat16().view(r.x.dtype)]
+    want = [r.few(f32=True, x=x) for x in xs]
+    assert not torch.equal(*want)
+    outs = [torch.empty_like(want[0]) for _ in range(200)]
+    for i, out in enumerate(outs):
+        r.m.forward_few(xs[i % 2], out, f32out=True)
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, want[i % 2]) for i, out in enumerate(outs))
+    assert r.m.last_error() == cb.CB_OK
