@@ -220,6 +220,7 @@ struct Block {
   uint8_t* ring;
   RingPos<G::kStages> pos;  // the producer's, or a user's, place in the ring
   bool ok = true;           // no wait of this thread has run out
+  int opened = 0;           // the weight thread's last stages, at most the whole ring
   const int warp, lane, half;
   int first_w;
   int first_tok[G::kStepElems / 8];
@@ -435,8 +436,25 @@ struct Block {
   // nothing may be copied.
   __device__ __forceinline__ bool open_stage(int rows) {
     wait(&empty[pos.stage], pos.phase ^ 1u);
-    if (ok) mbar_arrive_expect_tx(&full[pos.stage], static_cast<uint32_t>(rows * kSeg));
+    if (ok) {
+      mbar_arrive_expect_tx(&full[pos.stage], static_cast<uint32_t>(rows * kSeg));
+      opened = min(opened + 1, G::kStages);
+    }
     return ok;
+  }
+  // No copy may still be in flight into shared memory at exit.  (The users see
+  // the copies land, unless one of their waits ran out.)
+  __device__ __forceinline__ void see_copies_land() {
+    RingPos<G::kStages> last = pos;
+    if ((last.stage -= opened) < 0) {
+      last.stage += G::kStages;
+      last.phase ^= 1u;
+    }
+    for (; opened > 0; --opened, last.next())
+      if (!mbar_wait(&full[last.stage], last.phase, p.wait_limit_ns)) {
+        set_error(p.err, kErrTimeout);
+        break;
+      }
   }
 
   // Token warp: the stages of a tile over the weights' bytes [at, end) of a
@@ -777,6 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && b.lane == 0) {
       b.feed_gateup(up_bytes);
       b.feed_down(down_bytes);
+      b.see_copies_land();
     }
   } else if (b.warp >= kTokenWarp) {
     if (ok) {

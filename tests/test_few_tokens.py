@@ -292,3 +292,21 @@ def test_every_run_reads_its_own_intermediate_values(wdtype, n):
     torch.cuda.synchronize()
     assert all(torch.equal(out, want[i % 2]) for i, out in enumerate(outs))
     assert r.m.last_error() == cb.CB_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("wdtype", ["bf16", "int8", "int4", "fp8"])
+@pytest.mark.parametrize("n", [3, 14])
+def test_a_launch_that_gave_up_leaves_nothing_behind(wdtype, n):
+    """Rows of several rings' length, so that the weights' copies are ahead when the barrier's wait
+    runs out: the launch sees them land, and other launches right after it are right."""
+    shape = synth.custom_shape("few", n, 512, 4096, 8, 2, wdtype=wdtype, seed=23)
+    stalled, r = Run(shape, flags=cb.CB_FLAG_TEST_STALL_DISPATCH | cb.CB_FLAG_GUARDS), Run(shape)
+    want = r.few(f32=True)
+    out, lost = torch.empty_like(want), torch.empty_like(want)
+    for _ in range(3):
+        stalled.m.forward_few(stalled.x, lost, f32out=True)
+        r.m.forward_few(r.x, out, f32out=True)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and r.m.last_error() == cb.CB_OK
+        assert stalled.m.last_error() == cb.CB_ERR_TIMEOUT and stalled.m.check_guards() == cb.CB_OK
