@@ -315,13 +315,18 @@ class MoELayer:
 
     def forward_few(self, x, out, stream=None, f32out=False):
         """The layer for x.shape[0] <= CB_MOE_MAX_FEW tokens, whatever T the handle was made for.
-        x bf16 (or int16 bits) and out bf16 (fp32 with f32out), both contiguous [n][d] on the
+        x bf16 (or int16 bits) and out the same (fp32 with f32out), both contiguous [n][d] on the
         handle's device."""
+        torch, device = _torch or _load_torch(), self.cfg.device
         if x.shape != out.shape or x.dim() != 2 or x.shape[1] != self.cfg.d_model:
             raise ValueError(f"forward_few: x {tuple(x.shape)}, out {tuple(out.shape)}, d = {self.cfg.d_model}")
-        if not (x.is_contiguous() and out.is_contiguous()) or x.element_size() != 2 or \
-                out.element_size() != (4 if f32out else 2):
-            raise ValueError("forward_few: x is contiguous bf16, out contiguous bf16 (fp32 with f32out)")
+        bits = (torch.bfloat16, torch.int16)
+        if x.dtype not in bits or (out.dtype is not torch.float32 if f32out else out.dtype not in bits) or \
+                not (x.is_contiguous() and out.is_contiguous()):
+            raise ValueError(f"forward_few: x {x.dtype}, out {out.dtype}: contiguous bf16 (or its bits as int16) are "
+                             f"needed, out fp32 with f32out and only then")
+        if x.get_device() != device or out.get_device() != device:
+            raise ValueError(f"forward_few: x on {x.device}, out on {out.device}, the handle on device {device}")
         s = 0 if stream is None else stream.cuda_stream
         fn = cb_moe_forward_few_f32out if f32out else cb_moe_forward_few
         st = fn(self.handle, x.data_ptr(), int(x.shape[0]), out.data_ptr(), s)

@@ -53,6 +53,49 @@ def test_forward_refuses_tensors_that_it_would_run_past(calls):
     assert len(calls) == 4
 
 
+# ------------------------------------------------------------ forward_few
+class On:
+    """A tensor said to be on a CUDA device: what the call asks of one."""
+
+    def __init__(self, t, device=0):
+        self.t, self.device = t, f"cuda:{device}"
+        self.shape, self.dtype, self.index = t.shape, t.dtype, device
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return self.index
+
+
+def test_forward_few_refuses_other_types(calls):
+    """float16 has bf16's size, and its bits would be read as bf16's."""
+    m, x = layer(20, 256), On(bf16(3, 256))
+    stream = types.SimpleNamespace(cuda_stream=5)
+    m.forward_few(x, On(bf16(3, 256)), stream=stream)
+    m.forward_few(On(torch.zeros(3, 256, dtype=torch.int16)), On(torch.zeros(3, 256, dtype=torch.int16)), stream=stream)
+    m.forward_few(x, On(torch.zeros(3, 256)), stream=stream, f32out=True)
+    assert len(calls) == 3
+    for a, b, f32 in ((torch.float16, torch.bfloat16, False), (torch.bfloat16, torch.float16, False),
+                      (torch.bfloat16, torch.float32, False), (torch.bfloat16, torch.int32, True),
+                      (torch.bfloat16, torch.bfloat16, True), (torch.uint8, torch.bfloat16, False)):
+        with pytest.raises(ValueError):
+            m.forward_few(On(torch.zeros(3, 256, dtype=a)), On(torch.zeros(3, 256, dtype=b)), stream=stream, f32out=f32)
+    assert len(calls) == 3
+
+
+def test_forward_few_refuses_other_devices(calls):
+    """A host tensor's address, or another GPU's, never reaches the kernel."""
+    x = bf16(3, 256)
+    stream = types.SimpleNamespace(cuda_stream=5)
+    layer(20, 256, device=1).forward_few(On(x, 1), On(x.clone(), 1), stream=stream)
+    assert len(calls) == 1
+    for a, b in ((x, x.clone()), (On(x), x.clone()), (x, On(x)), (On(x, 1), On(x)), (On(x), On(x, 1))):
+        with pytest.raises(ValueError):
+            layer(20, 256).forward_few(a, b, stream=stream)
+    assert len(calls) == 1
+
+
 # ---------------------------------------------------------------- example
 def test_serving_block_takes_prompts_up_to_its_handles_tokens(calls, monkeypatch):
     import serving_block as sb
