@@ -316,7 +316,7 @@ class MoELayer:
     def forward_few(self, x, out, stream=None, f32out=False):
         """The layer for x.shape[0] <= CB_MOE_MAX_FEW tokens, whatever T the handle was made for.
         x bf16 (or int16 bits) and out the same (fp32 with f32out), both contiguous [n][d] on the
-        handle's device."""
+        handle's device.  Runs on `stream`, or on torch's current stream there, as the 4-bit calls do."""
         torch, device = _torch or _load_torch(), self.cfg.device
         if x.shape != out.shape or x.dim() != 2 or x.shape[1] != self.cfg.d_model:
             raise ValueError(f"forward_few: x {tuple(x.shape)}, out {tuple(out.shape)}, d = {self.cfg.d_model}")
@@ -327,7 +327,7 @@ class MoELayer:
                              f"needed, out fp32 with f32out and only then")
         if x.get_device() != device or out.get_device() != device:
             raise ValueError(f"forward_few: x on {x.device}, out on {out.device}, the handle on device {device}")
-        s = 0 if stream is None else stream.cuda_stream
+        s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
         fn = cb_moe_forward_few_f32out if f32out else cb_moe_forward_few
         st = fn(self.handle, x.data_ptr(), int(x.shape[0]), out.data_ptr(), s)
         if st != CB_OK:

@@ -96,6 +96,35 @@ def test_forward_few_refuses_other_devices(calls):
     assert len(calls) == 1
 
 
+def test_forward_few_runs_on_the_current_stream(calls, monkeypatch):
+    """As the 4-bit calls beside it do: its input was written there."""
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 100 + device, raising=False)
+    x = bf16(3, 256)
+    layer(20, 256).forward_few(On(x), On(x.clone()))
+    layer(20, 256, device=1).forward_few(On(x, 1), On(x.clone(), 1))
+    layer(20, 256).forward_few(On(x), On(x.clone()), stream=types.SimpleNamespace(cuda_stream=5))
+    assert [c[-1] for c in calls] == [100, 101, 5]
+
+
+@pytest.mark.gpu
+def test_forward_few_follows_its_input_on_a_side_stream():
+    import gpu_harness as gh
+    import synth
+    s = synth.custom_shape("few", 5, 512, 512, 8, 2, seed=2)
+    lay = synth.make_layer(s)
+    m = cb.MoELayer(s.T, s.d, s.f, s.E, s.k, *(gh.to_dev(getattr(lay, n)) for n in ("wr", "wg", "wu", "wd")))
+    x = gh.to_dev(lay.x)
+    want, y, out = torch.empty_like(x), torch.zeros_like(x), torch.empty_like(x)
+    m.forward_few(x, want)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        torch.cuda._sleep(20_000_000)                # y is written some 10 ms from now
+        y.copy_(x)
+        m.forward_few(y, out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
 # ---------------------------------------------------------------- example
 def test_serving_block_takes_prompts_up_to_its_handles_tokens(calls, monkeypatch):
     import serving_block as sb
