@@ -110,11 +110,11 @@ class Fp4Experts:
         T, k, E = layer.cfg.n_tokens, layer.cfg.top_k, layer.cfg.n_experts
         if x.shape[0] != T:
             raise ValueError(f"{x.shape[0]} rows for the routing of {T} tokens")
-        v, grab = layer.routing(), {}
+        v, grab, here = layer.routing(), {}, torch.cuda.current_stream()
         for name, n, dtype in (("ids", T * k, torch.int32), ("w", T * k, torch.float32), ("inv", T * k, torch.int32),
                                ("offsets", E + 1, torch.int32), ("tile_offsets", E + 1, torch.int32)):
             grab[name] = torch.empty(n, dtype=dtype, device=x.device)
-            cb.copy_from_device(grab[name], getattr(v, name), 4 * n)
+            cb.copy_from_device(grab[name], getattr(v, name), 4 * n, stream=here)
         ids, tiles = grab["ids"].long(), grab["tile_offsets"]
         rows = 128 * ((T * k + 127 * E) // 128 + 1)       # room for every expert's padding
         at = 128 * tiles[ids].long() + grab["inv"].long() - grab["offsets"][ids].long()   # row of each (token, slot)

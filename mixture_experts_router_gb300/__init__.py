@@ -234,9 +234,11 @@ def cb_fp4_matmul(args: cb_fp4_matmul_t, stream: int = 0) -> int:
 _cudart = None
 
 
-def copy_from_device(dst_tensor, src_ptr: int, nbytes: int) -> None:
+def copy_from_device(dst_tensor, src_ptr: int, nbytes: int, stream=None) -> None:
     """Copy nbytes of library-owned device memory (e.g. a cb_routing_view_t
-    array) into a torch CUDA tensor, with the CUDA runtime torch has loaded."""
+    array) into a torch CUDA tensor, with the CUDA runtime torch has loaded:
+    in order on `stream`, or on the legacy default stream, which side streams
+    do not wait for."""
     global _cudart
     if _cudart is None:
         import glob
@@ -256,9 +258,12 @@ def copy_from_device(dst_tensor, src_ptr: int, nbytes: int) -> None:
             raise RuntimeError("no CUDA runtime library found")
         lib.cudaMemcpy.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int]
         lib.cudaMemcpy.restype = ctypes.c_int
+        lib.cudaMemcpyAsync.argtypes = lib.cudaMemcpy.argtypes + [ctypes.c_void_p]
+        lib.cudaMemcpyAsync.restype = ctypes.c_int
         _cudart = lib
     if nbytes:
-        rc = _cudart.cudaMemcpy(dst_tensor.data_ptr(), src_ptr, nbytes, 3)  # device to device
+        args = dst_tensor.data_ptr(), src_ptr, nbytes, 3  # device to device
+        rc = _cudart.cudaMemcpy(*args) if stream is None else _cudart.cudaMemcpyAsync(*args, stream.cuda_stream)
         if rc != 0:
             raise RuntimeError(f"cudaMemcpy failed ({rc})")
 

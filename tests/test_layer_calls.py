@@ -145,6 +145,58 @@ def test_fp4_experts_refuse_rows_that_were_not_routed():
             sb.Fp4Experts.__call__(None, bf16(n, 256), layer(20, 256))
 
 
+class Runtime:
+    """The CUDA runtime's copies, recorded."""
+
+    def __init__(self):
+        self.streams = []
+
+    def cudaMemcpy(self, dst, src, n, kind):
+        self.streams.append("legacy")
+        return 0
+
+    def cudaMemcpyAsync(self, dst, src, n, kind, stream):
+        self.streams.append(stream)
+        return 0
+
+
+def test_copies_of_the_routing_run_where_they_are_used(monkeypatch):
+    import serving_block as sb
+    rt = Runtime()
+    monkeypatch.setattr(cb, "_cudart", rt)
+    cb.copy_from_device(torch.zeros(4), 64, 16)
+    cb.copy_from_device(torch.zeros(4), 64, 16, stream=types.SimpleNamespace(cuda_stream=9))
+    cb.copy_from_device(torch.zeros(4), 64, 0, stream=types.SimpleNamespace(cuda_stream=9))
+    assert rt.streams == ["legacy", 9]
+    # the example, up to its first use of what it copied
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=7))
+    m = layer(20, 256)
+    m.routing = lambda: types.SimpleNamespace(ids=64, w=64, inv=64, offsets=64, tile_offsets=64)
+    monkeypatch.setattr(torch.Tensor, "long", lambda t: (_ for _ in ()).throw(Reached()))
+    with pytest.raises(Reached):
+        sb.Fp4Experts.__call__(None, bf16(20, 256), m)
+    assert rt.streams[2:] == [7] * 5
+
+
+@pytest.mark.gpu
+def test_fp4_experts_on_a_side_stream():
+    """The routing that a forward on a side stream is still to write."""
+    import serving_block as sb
+    block, routed, _ = sb.random_block(d=512, f=256, E=12, top_k=3, dense_f=256, prompt_tokens=90, seed=3)
+    experts = sb.Fp4Experts(*routed[1:])
+    x, other = (torch.randn(90, 512, device="cuda").bfloat16() for _ in range(2))
+    block.prompt(x)
+    want = experts(x, block.layer)
+    block.prompt(other)                              # another routing in the meantime
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        torch.cuda._sleep(20_000_000)
+        block.prompt(x)
+        got = experts(x, block.layer)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
 @pytest.mark.gpu
 def test_prompts_of_several_lengths():
     """A short prompt is the full one whose other rows are zeros (the routed experts' part: k = 2, so
