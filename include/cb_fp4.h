@@ -49,8 +49,9 @@ CB_API cb_status_t cb_fp4_scale_bytes(int32_t format, int64_t rows, int64_t cols
  * scales.  Per block with a = its largest magnitude:
  *   MX: e = floor(log2 a) - 2, clamped to -127..125 (-127 for a = 0), scale 2^e;
  *   NV: s = the e4m3 value nearest a / (6 g), ties to the even code, at most
- *       448; g = *tensor_scale (device fp32, > 0), a value such as
- *       max|x| / (6 * 448) that puts the largest block scale at 448.
+ *       448; g = *tensor_scale (device fp32), a value such as
+ *       max|x| / (6 * 448) that puts the largest block scale at 448.  Where g
+ *       is not above 0 (that formula's value for zeros) s = 0.
  * Each element is the nearest v of x / scale, ties to the even code,
  * magnitudes past 6 becoming 6.  The quotients are rounded as if computed
  * exactly, so a result depends on nothing but x and g.  (x / scale is 0 where

@@ -160,7 +160,9 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const T* x, int6
   grid_dep_wait();
   NvScale nv{};
   if constexpr (FMT == kFp4Nv) {
-    nv.g = __ldg(tensor_scale);
+    // the g of a matrix of zeros is 0: as an infinite one, it leaves every scale and code 0
+    const float g = __ldg(tensor_scale);
+    nv.g = g > 0.f ? g : __uint_as_float(0x7F800000u);
     nv.six_g = 6.f * nv.g;
     nv.wide = !(nv.g > 0x1p-80f && nv.g < 0x1p+80f);
   }

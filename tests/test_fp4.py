@@ -515,3 +515,26 @@ def test_offsets_past_32_bits():
     w = cb.fp4_quantize(torch.randn(24, cols, device="cuda").bfloat16(), "mx")
     del x, back
     assert torch.equal(cb.fp4_matmul(big, w)[-128:], cb.fp4_matmul(small, w)[-128:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("top", [0.0, 2.0 ** -140])
+@pytest.mark.parametrize("rows,cols", [(3, 96), (140, 320)])
+def test_nv_scale_of_zeros(dtype, top, rows, cols):
+    """max|x| / (6 * 448) is 0 for zeros, and for values that it cannot tell from them: zeros
+    throughout, and a product with them is 0; a block that is not finite is NaN as ever."""
+    x = torch.full((rows, cols), top, device="cuda").to(dtype)
+    g = (x.float().abs().amax() / (6 * 448)).reshape(1)
+    assert float(g) == 0.0
+    q = cb.fp4_quantize(x, "nv", g)
+    assert int(q.codes.max()) == 0 and int(q.scales.max()) == 0
+    assert torch.equal(cb.fp4_dequantize(q, dtype), torch.zeros_like(x))
+    w = cb.fp4_quantize(torch.randn(40, cols, device="cuda"), "nv", torch.tensor([0.002], device="cuda"))
+    for a, b, shape in ((q, w, (rows, 40)), (w, q, (40, rows))):
+        assert torch.equal(cb.fp4_matmul(a, b), torch.zeros(shape, dtype=torch.bfloat16, device="cuda"))
+    x[1, 40] = float("nan")
+    y = cb.fp4_dequantize(cb.fp4_quantize(x, "nv", g), torch.float32)
+    want = torch.zeros_like(x, dtype=torch.bool)
+    want[1, 32:48] = True
+    assert torch.equal(torch.isnan(y), want)
