@@ -81,7 +81,9 @@ CB_API cb_status_t cb_fp4_dequantize(int32_t format, const uint8_t *codes, const
 /*
  * out [m][n] = A B^T, A [m][k] and B [n][k] both of `format`:
  *   out[i][j] = g_a g_b sum_l A[i][l] B[j][l],
- * fp32 sums on the tensor core, rounded once to out_type.
+ * fp32 sums on the tensor core.  MX: rounded once, to out_type.  NV: g_a g_b
+ * and its product with the sum are rounded to fp32 each (neither leaves its
+ * range where the result does not), then to out_type.
  *
  * Experts' products: with n_groups = E >= 1 and tile_offsets (device int32
  * [E + 1], ascending from 0), B is E matrices and rows

@@ -266,9 +266,47 @@ __device__ __forceinline__ void store_any_rows(uint8_t* out, int64_t pitch, uint
   __syncwarp();
 }
 
-// Two accumulators times alpha as a pair of bf16.
-__device__ __forceinline__ uint32_t bf16_pair(float alpha, uint32_t a, uint32_t b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(alpha * __uint_as_float(a), alpha * __uint_as_float(b));
+// The two matrices' scales (NV) as factors of the fp32 sums: first, then second.
+// second is 1 and first their product, unless that leaves fp32's normal range
+// where a result need not: then first has the significant bits with an
+// exponent that keeps the sums' products normal (a sum other than 0 lies
+// between 2^-20 and 2^60), and second is a power of two.
+struct MatrixScale {
+  float first = 1.f, second = 1.f;
+  __device__ __forceinline__ static MatrixScale of(float ga, float gb) {
+    MatrixScale m;
+    m.first = ga * gb;
+    const float size = fabsf(m.first);
+    if (!(size >= 0x1p-126f && size < __uint_as_float(0x7F800000u)) && isfinite(ga) && isfinite(gb)) {
+      int ea, eb;
+      const float bits = frexpf(ga, &ea) * frexpf(gb, &eb);  // 0, or from 1/4 to 1
+      const int e = min(max(ea + eb, -90), 60);
+      m.first = ldexpf(bits, e);
+      m.second = ldexpf(1.f, min(ea + eb - e, 127));  // (0 and 2^127: results below and past fp32)
+    }
+    return m;
+  }
+  // sums[i] as the bits of a float
+  template <int N>
+  __device__ __forceinline__ void apply(uint32_t (&sums)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) sums[i] = __float_as_uint(first * __uint_as_float(sums[i]));
+    if (second != 1.f) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) sums[i] = __float_as_uint(second * __uint_as_float(sums[i]));
+    }
+  }
+};
+
+template <int FMT>
+__device__ __forceinline__ MatrixScale matrix_scale(const Fp4MatmulArgs& a, int e) {
+  if constexpr (FMT == kFp4Nv) return MatrixScale::of(__ldg(a.a_tensor_scale), __ldg(a.b_tensor_scale + e));
+  return MatrixScale{};
+}
+
+// Two floats' bits as a pair of bf16.
+__device__ __forceinline__ uint32_t bf16_pair(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(a), __uint_as_float(b));
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
@@ -277,7 +315,7 @@ __device__ __forceinline__ uint32_t bf16_pair(float alpha, uint32_t a, uint32_t 
 template <int FMT, int COLS, typename F>
 __device__ __forceinline__ void store_tile(const Fp4MatmulArgs& a, uint32_t acc, int row0, int first, int e, int vec,
                                            int lane, F&& done) {
-  const float alpha = FMT == kFp4Nv ? __ldg(a.a_tensor_scale) * __ldg(a.b_tensor_scale + e) : 1.f;
+  const MatrixScale g = matrix_scale<FMT>(a, e);
   const int rows = a.m - row0;  // the warp's rows (all 32 but in the last tiles)
   const int elem = a.out_f32 ? 4 : 2;
   uint8_t* out = static_cast<uint8_t*>(a.out) + (static_cast<int64_t>(row0) * a.ld_out + first) * elem;
@@ -293,8 +331,7 @@ __device__ __forceinline__ void store_tile(const Fp4MatmulArgs& a, uint32_t acc,
       const bool last = c0 + step >= COLS || first + c0 + step >= a.n;
       if (a.out_f32) {
         if (last) done();
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(alpha * __uint_as_float(v[j]));
+        g.apply(v);
         if (vec)
           store_rows<4>(out + c0 * 4, pitch, v, rows, a.n - first - c0, lane);
         else
@@ -303,10 +340,12 @@ __device__ __forceinline__ void store_tile(const Fp4MatmulArgs& a, uint32_t acc,
         uint32_t u[32];
         tmem_load32(acc + c0 + 32, u);
         if (last) done();
+        g.apply(v);
+        g.apply(u);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = bf16_pair(alpha, v[2 * j], v[2 * j + 1]);
+        for (int j = 0; j < 16; ++j) v[j] = bf16_pair(v[2 * j], v[2 * j + 1]);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[16 + j] = bf16_pair(alpha, u[2 * j], u[2 * j + 1]);
+        for (int j = 0; j < 16; ++j) v[16 + j] = bf16_pair(u[2 * j], u[2 * j + 1]);
         store_any_rows<2>(out + c0 * 2, pitch, v, rows, a.n - first - c0, carry, c0 == 0, last, lane);
       }
     }
@@ -318,8 +357,9 @@ __device__ __forceinline__ void store_tile(const Fp4MatmulArgs& a, uint32_t acc,
     for (int c0 = 0; c0 < COLS; c0 += 32) {
       uint32_t v[32];
       tmem_load32(acc + c0, v);
+      g.apply(v);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) h[c0 / 2 + j] = bf16_pair(alpha, v[2 * j], v[2 * j + 1]);
+      for (int j = 0; j < 16; ++j) h[c0 / 2 + j] = bf16_pair(v[2 * j], v[2 * j + 1]);
     }
     done();
 #pragma unroll
@@ -485,7 +525,7 @@ __global__ void __launch_bounds__((THREADS<SWAP>), 1)
     cluster_sync();  // every rank's partial sums are in its shared memory
     // a token per warp, four output columns per lane; the ranks share the tokens
     const int col = worker * BP + lane * 4;
-    const float alpha = FMT == kFp4Nv ? __ldg(a.a_tensor_scale) * __ldg(a.b_tensor_scale) : 1.f;
+    const MatrixScale g = matrix_scale<FMT>(a, 0);
     for (int t = rank + ksplit * warp; t < a.m; t += ksplit * (THREADS<SWAP> / 32)) {
       const uint32_t at = smem_u32(reinterpret_cast<float*>(smem) + t * BP + lane * 4);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -497,12 +537,13 @@ __global__ void __launch_bounds__((THREADS<SWAP>), 1)
         v.z += x.z;
         v.w += x.w;
       }
-      const float f[4] = {alpha * v.x, alpha * v.y, alpha * v.z, alpha * v.w};
+      uint32_t f[4] = {__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)};
+      g.apply(f);
       const int64_t o = static_cast<int64_t>(t) * a.ld_out + col;
       if (a.out_f32) {
-        float* out = static_cast<float*>(a.out) + o;
+        uint32_t* out = static_cast<uint32_t*>(a.out) + o;
         if (vec && col + 4 <= a.n) {
-          *reinterpret_cast<float4*>(out) = make_float4(f[0], f[1], f[2], f[3]);
+          *reinterpret_cast<uint4*>(out) = make_uint4(f[0], f[1], f[2], f[3]);
         } else {
 #pragma unroll
           for (int u = 0; u < 4; ++u)
@@ -510,8 +551,7 @@ __global__ void __launch_bounds__((THREADS<SWAP>), 1)
         }
       } else {
         uint16_t* out = static_cast<uint16_t*>(a.out) + o;
-        const __nv_bfloat162 b0 = __floats2bfloat162_rn(f[0], f[1]), b1 = __floats2bfloat162_rn(f[2], f[3]);
-        const uint2 h = make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
+        const uint2 h = make_uint2(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]));
         if (vec && col + 4 <= a.n) {
           *reinterpret_cast<uint2*>(out) = h;
         } else {

@@ -538,3 +538,31 @@ def test_nv_scale_of_zeros(dtype, top, rows, cols):
     want = torch.zeros_like(x, dtype=torch.bool)
     want[1, 32:48] = True
     assert torch.equal(torch.isnan(y), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ga,gb", [(0.01, 0.003), (1e-23, 1e-23), (1e-23, -1e-23), (1e20, 1e20), (3e38, 3e38), (1e-40, 1e-5),
+                                   (2.0 ** -140, 2.0 ** -100), (1e-45, 1e-45), (0.0, 1e30), (1e-30, 1e37)])
+@pytest.mark.parametrize("m,n,k,gap", [(4, 130, 160, 0), (200, 256, 96, 0), (200, 77, 96, 0), (2500, 1030, 96, 2), (2500, 2000, 1024, 0),
+                                       (2500, 2001, 1024, 0)])
+def test_matrix_scales_whose_product_leaves_fp32(m, n, k, gap, ga, gb):
+    """The sums themselves are exact here.  Rounded after them: the product of the two scales and the
+    scaled sum to fp32 (a smallest step apart at most where it is not normal), then to the output's
+    type.  Sums of 0 stay 0, whatever the scales."""
+    rng = np.random.default_rng(m + n + k)
+    a, b = random_matrix(rng, m, k, "nv", True), random_matrix(rng, n, k, "nv", True)
+    a.codes[1] = 0
+    sums = torch.from_numpy(decode64(a, "nv")).cuda() @ torch.from_numpy(decode64(b, "nv")).cuda().T
+    a.tensor_scale.fill_(ga)
+    b.tensor_scale.fill_(gb)
+    ref = sums * (a.tensor_scale.double() * b.tensor_scale.double())
+    for dtype in (torch.float32, torch.bfloat16):
+        out = torch.empty((m, n + gap), dtype=dtype, device="cuda")[:, :n]
+        got = cb.fp4_matmul(a, b, out=out).double()
+        step, tiny = torch.finfo(dtype).eps / 2, 2.0 ** -149 + (2.0 ** -134 if dtype == torch.bfloat16 else 0)
+        tol = ref.abs() * (step + 3 * 2.0 ** -24) + tiny
+        top = torch.finfo(dtype).max
+        past, within = ref.abs() > top + tol, ref.abs() < top - tol
+        assert ((got - ref).abs() <= tol)[within].all()
+        assert torch.equal(got[past], torch.copysign(torch.full_like(ref, float("inf")), ref)[past])
+        assert (got[1] == 0).all()
