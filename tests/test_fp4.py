@@ -566,3 +566,75 @@ def test_matrix_scales_whose_product_leaves_fp32(m, n, k, gap, ga, gb):
         assert ((got - ref).abs() <= tol)[within].all()
         assert torch.equal(got[past], torch.copysign(torch.full_like(ref, float("inf")), ref)[past])
         assert (got[1] == 0).all()
+
+
+# ------------------------------------------- forms that only large matrices take
+def sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def nearest_on_gpu(grid, v):
+    """nearest() as torch operations, in 64 bits."""
+    g = torch.tensor(grid, dtype=torch.float64, device=v.device)
+    i = torch.searchsorted(g, v.contiguous()).clamp_(1, len(g) - 1)
+    low, high = v - g[i - 1], g[i] - v
+    return torch.where((low < high) | ((low == high) & ((i - 1) % 2 == 0)), i - 1, i)
+
+
+def two_to(e):
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
+def quantise_on_gpu(x, fmt, g):
+    """quantise64() as torch operations: codes, and scale bytes in their stored order."""
+    v = x.double().view(x.shape[0], -1, BLOCK[fmt])
+    finite = torch.isfinite(v).all(-1)
+    v = torch.where(finite[..., None], v, 0.0)
+    top = v.abs().amax(-1)
+    if fmt == "mx":
+        byte = torch.where(top > 0, torch.frexp(top).exponent.long() - 1 - 2 + 127, 0).clamp(0, 252)
+        unit = two_to(byte - 127)
+    else:
+        byte = nearest_on_gpu(E4M3, top / (6 * g))
+        unit = torch.tensor(E4M3, device=x.device)[byte] * g
+    code = nearest_on_gpu(E2M1, torch.where(unit[..., None] > 0, v.abs() / unit[..., None], 0.0))
+    byte = torch.where(finite, byte, 255 if fmt == "mx" else 127)
+    r, c = -(-byte.shape[0] // 128), -(-byte.shape[1] // 4)
+    tiles = torch.zeros((r * 128, c * 4), dtype=torch.uint8, device=x.device)
+    tiles[:byte.shape[0], :byte.shape[1]] = byte.to(torch.uint8)
+    return code.view(x.shape), tiles.view(r, 4, 32, c, 4).permute(0, 3, 2, 1, 4).reshape(-1), v.view(x.shape) < 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols,gap", [(1300, 14336, 0), (19600, 544, 0), (19600, 544, 1), (39000, 32, 3)])
+def test_matrices_of_whole_tiles(fmt, dtype, rows, cols, gap):
+    """Two tiles of 128 x 256 and more per SM, each by one block: rows that start on 16 bytes and
+    rows that do not, tiles cut at the ends, both ways, bit for bit."""
+    assert -(-rows // 128) * -(-cols // 256) >= 2 * sms()
+    gen = torch.Generator(device="cuda").manual_seed(rows + cols + gap)
+    x = torch.randn((rows, cols), generator=gen, device="cuda") * torch.exp(2 * torch.randn((rows, 1), generator=gen, device="cuda"))
+    x[:, ::3] = torch.round(x[:, ::3] * 4) / 4                      # ties among them
+    x[rows // 2] = 0
+    x[rows - 1, cols - 1], x[5, 17] = float("nan"), float("-inf")
+    wide = torch.full((rows, cols + gap), 9.0, device="cuda", dtype=dtype)
+    wide[:, :cols] = x.to(dtype)
+    x = wide[:, :cols]
+    scale = None if fmt == "mx" else (x.float().abs().nan_to_num(0, 0).amax() / (6 * 448)).reshape(1)
+    m = cb.fp4_quantize(x, fmt, scale)
+    code, scales, negative = quantise_on_gpu(x, fmt, None if fmt == "mx" else scale.double())
+    got = torch.stack([m.codes & 15, m.codes >> 4], -1).view(rows, cols)
+    assert torch.equal(m.scales, scales)
+    assert torch.equal(got.long() & 7, code)
+    assert torch.equal((got >> 3 == 1)[code > 0], negative[code > 0])
+    # and back: the values of the form for few tiles, 512 rows at a time (its tests are above)
+    back = torch.full((rows, cols + gap), 9.0, device="cuda", dtype=dtype)
+    cb.fp4_dequantize(m, out=back[:, :cols])
+    assert (back[:, cols:] == 9.0).all()
+    per = m.scales.numel() // -(-rows // 128)
+    assert 4 * -(-cols // 256) < 2 * sms()
+    for r in range(0, rows, 512):
+        end = min(r + 512, rows)
+        part = cb.Fp4Matrix(fmt, end - r, cols, m.codes[r:end], m.scales[r // 128 * per:-(-end // 128) * per], scale)
+        assert torch.equal(cb.fp4_dequantize(part, dtype).nan_to_num(-1), back[r:end, :cols].nan_to_num(-1)), r
