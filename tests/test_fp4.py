@@ -638,3 +638,30 @@ def test_matrices_of_whole_tiles(fmt, dtype, rows, cols, gap):
         end = min(r + 512, rows)
         part = cb.Fp4Matrix(fmt, end - r, cols, m.codes[r:end], m.scales[r // 128 * per:-(-end // 128) * per], scale)
         assert torch.equal(cb.fp4_dequantize(part, dtype).nan_to_num(-1), back[r:end, :cols].nan_to_num(-1)), r
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("m,n,k,gap", [
+    (2400, 2304, 1024, 24),      # 19 row tiles: the last pair's odd CTA has none; whole column tiles; rows on 16 bytes
+    (2432, 2344, 1120, 24),      # the last column tile ends in its first half; k ends inside an instruction
+    (2300, 2504, 1312, 24),      # ... in its second half; 18 row tiles, the last one cut
+    (2400, 2501, 1056, 24),      # rows on any byte
+    (2400, 2304, 1024, 0),       # no gap between the rows
+])
+def test_products_on_cta_pairs_are_exact(fmt, m, n, k, gap):
+    """Dense products of k >= 1024 and more tiles of 128 x 256 than SMs run on pairs of SMs (the large
+    products above, but for 5100 x 1030 x 1184, are shorter and run on single ones); more tiles of
+    256 x 256 than pairs, so that accumulators are handed on."""
+    assert k >= 1024 and -(-m // 128) * -(-n // 256) > sms() and -(-m // 256) * -(-n // 256) > sms() // 2
+    rng = np.random.default_rng(m + n + k)
+    a, b = random_matrix(rng, m, k, fmt, True), random_matrix(rng, n, k, fmt, True)
+    x, y = (torch.from_numpy(decode64(t, fmt)).cuda() for t in (a, b))
+    ref = x @ y.T
+    assert float((x.abs() @ y.abs().T).max()) < 2.0 ** 20
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for dtype in (torch.float32, torch.bfloat16):
+        out = torch.full((m, n + gap), 7.0, dtype=dtype, device="cuda")
+        cb.fp4_matmul(a, b, out=out[:, :n], status=status)
+        assert torch.equal(out[:, :n], ref.to(dtype)) and (out[:, n:] == 7.0).all()
+    assert int(status) == 0
