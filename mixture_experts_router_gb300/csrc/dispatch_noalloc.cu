@@ -47,29 +47,30 @@ constexpr int kMaxDevices = 64;
 
 static __device__ __align__(256) int32_t g_dispatch_scratch[kScratchWords];
 
-using CtxGetCurrentFn = CUresult (*)(CUcontext*);
-
-// cuCtxGetCurrent through the runtime's driver entry points (the library
-// links no driver library), or nullptr if it cannot be had.
-CtxGetCurrentFn ctx_get_current() {
-  static CtxGetCurrentFn fn = [] {
+// The id of the current context, unique while the process lives, or 0 where it
+// cannot be had (through the runtime's driver entry points: the library links
+// no driver library).  The context's handle would not do: the primary context
+// has the same one again after cudaDeviceReset.
+unsigned long long current_context() {
+  using GetCurrent = CUresult (*)(CUcontext*);
+  using GetId = CUresult (*)(CUcontext, unsigned long long*);
+  const auto entry = [](const char* name, unsigned int version) -> void* {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &p, 4000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      return static_cast<CtxGetCurrentFn>(nullptr);
-    }
-    return reinterpret_cast<CtxGetCurrentFn>(p);
-  }();
-  return fn;
-}
-
-CUcontext current_context() {
+    if (cudaGetDriverEntryPointByVersion(name, &p, version, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return p;
+    cudaGetLastError();
+    return nullptr;
+  };
+  static const GetCurrent get_current = reinterpret_cast<GetCurrent>(entry("cuCtxGetCurrent", 4000));
+  static const GetId get_id = reinterpret_cast<GetId>(entry("cuCtxGetId", 12000));
   CUcontext c = nullptr;
-  CtxGetCurrentFn fn = ctx_get_current();
-  if (fn == nullptr || fn(&c) != CUDA_SUCCESS) return nullptr;
-  return c;
+  unsigned long long id = 0;
+  if (get_current == nullptr || get_id == nullptr || get_current(&c) != CUDA_SUCCESS || c == nullptr ||
+      get_id(c, &id) != CUDA_SUCCESS)
+    return 0;
+  return id;
 }
 
 // Device address of g_dispatch_scratch on `device` (the current device), or
@@ -78,7 +79,7 @@ CUcontext current_context() {
 // name the context the set-up runs on every call.
 int32_t* scratch_on(int device) {
   struct Entry {
-    CUcontext ctx;
+    unsigned long long ctx;
     int32_t* addr;
   };
   static std::mutex mu;
@@ -86,12 +87,12 @@ int32_t* scratch_on(int device) {
   if (device < 0 || device >= kMaxDevices) return nullptr;
   std::lock_guard<std::mutex> lock(mu);
   Entry& en = cache[device];
-  const CUcontext before = current_context();
-  if (before != nullptr && en.ctx == before && en.addr != nullptr) return en.addr;
+  const unsigned long long before = current_context();
+  if (before != 0 && en.ctx == before && en.addr != nullptr) return en.addr;
   void* p = nullptr;
   if (cudaGetSymbolAddress(&p, g_dispatch_scratch) != cudaSuccess || dispatch_prepare() != cudaSuccess) {
     cudaGetLastError();
-    en = Entry{nullptr, nullptr};
+    en = Entry{0, nullptr};
     return nullptr;
   }
   en = Entry{current_context(), static_cast<int32_t*>(p)};
