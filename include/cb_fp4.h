@@ -25,8 +25,9 @@
  * Conventions are those of cb_moe.h: device pointers, 16-byte aligned where
  * not said otherwise, work enqueued on `stream` of the current device,
  * arguments checked before anything is enqueued, no allocation and no
- * synchronisation.  All calls can be captured into a graph.  The calls keep
- * no state: they are safe from several threads and on several streams.
+ * synchronisation (but in cb_fp4_last_error).  The others can be captured into
+ * a graph.  The calls keep no state but a device's error word: they are safe
+ * from several threads and on several streams.
  */
 #ifndef CB_FP4_H
 #define CB_FP4_H
@@ -108,9 +109,10 @@ typedef struct {
   const int32_t *tile_offsets;  /* device [n_groups + 1], or NULL               */
   void *out;                    /* row stride ld_out elements, on 16 bytes      */
   int64_t ld_out;               /* >= n                                         */
-  int32_t *status;              /* device int32 or NULL: CB_ERR_TIMEOUT is put
-                                   there if a device-side wait ran past its
-                                   bound (out is then garbage); else untouched  */
+  int32_t *status;              /* device int32: CB_ERR_TIMEOUT is put there if
+                                   a device-side wait ran past its bound (out
+                                   is then garbage); else untouched.  NULL: the
+                                   device's own word, see cb_fp4_last_error     */
 } cb_fp4_matmul_t;
 
 /* Errors: CB_ERR_INVALID_ARG (NULL, an unknown format or type, negative sizes,
@@ -119,6 +121,12 @@ typedef struct {
  * CB_ERR_UNSUPPORTED (a size of 2^31 or more, n_groups n of 2^31 or more, a
  * wrong GPU), CB_ERR_CUDA. */
 CB_API cb_status_t cb_fp4_matmul(const cb_fp4_matmul_t *args, void *stream);
+
+/* Synchronise the current device, return what its products without a status
+ * word of their own ran into since the last such call (CB_OK or
+ * CB_ERR_TIMEOUT), and clear it.  CB_ERR_UNSUPPORTED (a wrong GPU),
+ * CB_ERR_CUDA. */
+CB_API cb_status_t cb_fp4_last_error(void);
 
 #ifdef __cplusplus
 }

@@ -35,7 +35,7 @@ ABI_SYMBOLS = ("cb_moe_init", "cb_moe_forward", "cb_moe_forward_f32out", "cb_moe
 
 CB_MOE_MAX_FEW = 16
 # every symbol include/cb_fp4.h declares
-FP4_SYMBOLS = ("cb_fp4_scale_bytes", "cb_fp4_quantize", "cb_fp4_dequantize", "cb_fp4_matmul")
+FP4_SYMBOLS = ("cb_fp4_scale_bytes", "cb_fp4_quantize", "cb_fp4_dequantize", "cb_fp4_matmul", "cb_fp4_last_error")
 CB_FP4_MX, CB_FP4_NV = 0, 1
 CB_T_BF16, CB_T_F32 = 0, 1
 FP4_FORMATS = {"mx": CB_FP4_MX, "nv": CB_FP4_NV}
@@ -125,6 +125,7 @@ def load_library(path: str = LIB_PATH):
     lib.cb_fp4_quantize.argtypes = [ctypes.c_int32, vp, ctypes.c_int32, i64, i64, i64, vp, vp, vp, vp]
     lib.cb_fp4_dequantize.argtypes = [ctypes.c_int32, vp, vp, vp, i64, i64, vp, ctypes.c_int32, i64, vp]
     lib.cb_fp4_matmul.argtypes = [vp, vp]
+    lib.cb_fp4_last_error.argtypes = []
     for name in FP4_SYMBOLS:
         getattr(lib, name).restype = i32
     lib.cb_status_string.argtypes = [i32]
@@ -228,6 +229,10 @@ def cb_fp4_dequantize(fmt, codes_ptr, scales_ptr, tensor_scale_ptr, rows, cols, 
 
 def cb_fp4_matmul(args: cb_fp4_matmul_t, stream: int = 0) -> int:
     return load_library().cb_fp4_matmul(ctypes.byref(args), stream)
+
+
+def cb_fp4_last_error() -> int:
+    return load_library().cb_fp4_last_error()
 
 
 # ------------------------------------------------------- torch convenience
@@ -568,7 +573,8 @@ def fp4_matmul(a: Fp4Matrix, b: Fp4Matrix, dtype=None, out=None, tile_offsets=No
     """a b^T ([a.rows][b.rows], bf16 or `dtype`, or into `out`).  With `tile_offsets` (int32
     CUDA tensor [b.groups + 1], cb_routing_view_t's) rows 128 tile_offsets[e] .. 128
     tile_offsets[e + 1] of `a` meet b's e-th matrix; rows past the last are not written.
-    `status`: an int32 CUDA tensor that receives CB_ERR_TIMEOUT if a device-side wait ran out."""
+    `status`: an int32 CUDA tensor that receives CB_ERR_TIMEOUT if a device-side wait ran out and the
+    result is garbage; without one fp4_last_error says so."""
     torch = _load_torch()
     if a.format != b.format or a.cols != b.cols or a.groups != 1:
         raise ValueError(f"fp4_matmul: {a.groups} x [{a.rows} x {a.cols}] {a.format} by [{b.rows} x {b.cols}] {b.format}")
@@ -601,3 +607,11 @@ def fp4_matmul(a: Fp4Matrix, b: Fp4Matrix, dtype=None, out=None, tile_offsets=No
     if st != CB_OK:
         raise CbMoeError(st, "cb_fp4_matmul")
     return out
+
+
+def fp4_last_error(device=None):
+    """Waits for the GPU (torch's current one unless given); CB_OK, or CB_ERR_TIMEOUT if since the
+    last such call a product without a `status` gave up a device-side wait."""
+    torch = _load_torch()
+    with torch.cuda.device(torch.cuda.current_device() if device is None else device):
+        return cb_fp4_last_error()

@@ -13,9 +13,11 @@ namespace {
 
 bool on(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
-bool fault_injected(const char* what) {
+// Testing only: what CB_MOE_INJECT_FAULT asks for.
+enum Fault { kNoFault, kLaunch, kStall };
+Fault injected_fault() {
   const char* v = std::getenv("CB_MOE_INJECT_FAULT");
-  return v != nullptr && std::strcmp(v, what) == 0;
+  return v == nullptr ? kNoFault : std::strcmp(v, "launch") == 0 ? kLaunch : std::strcmp(v, "stall") == 0 ? kStall : kNoFault;
 }
 
 int64_t scale_bytes(int32_t format, int64_t rows, int64_t cols) {
@@ -95,7 +97,7 @@ cb_status_t cb_fp4_quantize(int32_t format, const void* x, int32_t x_type, int64
   if (st != CB_OK || rows == 0) return st;
   int sms;
   if ((st = check_device(&sms)) != CB_OK) return st;
-  if (fault_injected("launch")) return CB_ERR_CUDA;
+  if (injected_fault() == kLaunch) return CB_ERR_CUDA;
   const Fp4Args a{format, x_type == CB_T_F32, const_cast<void*>(x), rows, cols, ld, tensor_scale, codes, scales};
   return launch_fp4_quantize(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CB_OK : CB_ERR_CUDA;
 }
@@ -106,7 +108,7 @@ cb_status_t cb_fp4_dequantize(int32_t format, const uint8_t* codes, const uint8_
   if (st != CB_OK || rows == 0) return st;
   int sms;
   if ((st = check_device(&sms)) != CB_OK) return st;
-  if (fault_injected("launch")) return CB_ERR_CUDA;
+  if (injected_fault() == kLaunch) return CB_ERR_CUDA;
   const Fp4Args a{format, out_type == CB_T_F32, out, rows, cols, ld, tensor_scale, const_cast<uint8_t*>(codes),
                   const_cast<uint8_t*>(scales)};
   return launch_fp4_dequantize(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CB_OK : CB_ERR_CUDA;
@@ -147,7 +149,8 @@ cb_status_t cb_fp4_matmul(const cb_fp4_matmul_t* p, void* stream) {
   int sms = 0;
   const cb_status_t st = check_device(&sms);
   if (st != CB_OK) return st;
-  if (fault_injected("launch")) return CB_ERR_CUDA;
+  const Fault fault = injected_fault();
+  if (fault == kLaunch) return CB_ERR_CUDA;
   Fp4MatmulArgs a{};
   a.format = p->format;
   a.out_f32 = p->out_type == CB_T_F32;
@@ -166,7 +169,18 @@ cb_status_t cb_fp4_matmul(const cb_fp4_matmul_t* p, void* stream) {
   a.ld_out = p->ld_out;
   a.status = p->status;
   a.wait_limit_ns = kWaitLimitNs;
+  if (fault == kStall) {
+    a.test_stall = 1;
+    a.wait_limit_ns = 1000000ull;  // 1 ms
+  }
   return launch_fp4_matmul(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CB_OK : CB_ERR_CUDA;
+}
+
+cb_status_t cb_fp4_last_error(void) {
+  int sms, code = 0;
+  const cb_status_t st = check_device(&sms);
+  if (st != CB_OK) return st;
+  return take_fp4_error(&code) == cudaSuccess ? static_cast<cb_status_t>(code) : CB_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -112,6 +112,13 @@ struct Tiles {
   }
 };
 
+// What launches without a status word of their own ran into.
+__device__ int g_error;
+
+__device__ __forceinline__ void timed_out(const Fp4MatmulArgs& a) {
+  set_error(a.status != nullptr ? a.status : &g_error, kErrTimeout);
+}
+
 // The MMA warp's place in the ring.  The whole warp walks it, so that its
 // addresses are uniform values, and an elected lane issues: an MMA or a copy of
 // scales then takes 37 cycles to issue, by a lane that walks alone 80 and
@@ -130,7 +137,7 @@ struct Issuer {
   // All lanes or none; false once a wait has run out.
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
     ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, a.wait_limit_ns));
-    if (!ok) set_error(a.status, kErrTimeout);
+    if (!ok) timed_out(a);
     return ok;
   }
   __device__ __forceinline__ bool wait_stage() {
@@ -391,7 +398,7 @@ __global__ void __launch_bounds__((THREADS<SWAP>), 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(tfull, 1);
+    mbar_init(tfull, 1 + a.test_stall);
     mbar_init(tempty, EPI_WARPS<SWAP>);
     fence_barrier_init();
     prefetch_tensormap(&tm_p);
@@ -429,7 +436,7 @@ __global__ void __launch_bounds__((THREADS<SWAP>), 1)
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const int s = static_cast<int>(it % STAGES);
           if (!mbar_wait(&empty[s], static_cast<uint32_t>(((it / STAGES) & 1) ^ 1), a.wait_limit_ns)) {
-            set_error(a.status, kErrTimeout);
+            timed_out(a);
             ok = false;
             break;
           }
@@ -449,7 +456,7 @@ __global__ void __launch_bounds__((THREADS<SWAP>), 1)
       // no copy may still be in flight into shared memory at exit
       for (int64_t j = (it > STAGES ? it - STAGES : 0); j < it; ++j)
         if (!mbar_wait(&full[j % STAGES], static_cast<uint32_t>((j / STAGES) & 1), a.wait_limit_ns))
-          set_error(a.status, kErrTimeout);
+          timed_out(a);
     }
   } else if (warp == 1) {
     Issuer<STAGES> is(full, a);
@@ -500,7 +507,7 @@ __global__ void __launch_bounds__((THREADS<SWAP>), 1)
     for (int i = worker; i < tiles.total; i += workers, tphase ^= 1u) {
       const Tile t = tiles.at(i, a);
       if (!mbar_wait(tfull, tphase, a.wait_limit_ns)) {
-        set_error(a.status, kErrTimeout);
+        timed_out(a);
         break;
       }
       tc_fence_after();
@@ -620,7 +627,7 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(tfull, 1);
+    mbar_init(tfull, 1 + a.test_stall);
     mbar_init(tempty, 2 * C::EPI);
     fence_barrier_init();
     prefetch_tensormap(&tm_p);
@@ -651,7 +658,7 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
         for (int kb = 0; kb < stages; ++kb, ++it) {
           const int s = static_cast<int>(it % STAGES);
           if (!mbar_wait(&empty[s], static_cast<uint32_t>(((it / STAGES) & 1) ^ 1), a.wait_limit_ns)) {
-            set_error(a.status, kErrTimeout);
+            timed_out(a);
             ok = false;
             break;
           }
@@ -669,7 +676,7 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
       // CTA's `full` counts both CTAs' copies)
       for (int64_t j = (it > STAGES ? it - STAGES : 0); even && j < it; ++j)
         if (!mbar_wait(&full[j % STAGES], static_cast<uint32_t>((j / STAGES) & 1), a.wait_limit_ns))
-          set_error(a.status, kErrTimeout);
+          timed_out(a);
     }
   } else if (warp == 1 && even) {
     Issuer<STAGES> is(full, a);
@@ -717,7 +724,7 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
     uint32_t tphase = 0;
     for (int i = first; i < total; i += step, tphase ^= 1u) {
       if (!mbar_wait(tfull, tphase, a.wait_limit_ns)) {
-        set_error(a.status, kErrTimeout);
+        timed_out(a);
         break;
       }
       tc_fence_after();
@@ -868,6 +875,13 @@ cudaError_t launch_format(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s) {
 }
 
 }  // namespace
+
+cudaError_t take_fp4_error(int* code) {
+  const int none = 0;
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(code, g_error, sizeof(int));
+  return e == cudaSuccess && *code != 0 ? cudaMemcpyToSymbol(g_error, &none, sizeof(int)) : e;
+}
 
 cudaError_t launch_fp4_matmul(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s) {
   return a.format == kFp4Mx ? launch_format<kFp4Mx>(a, num_sms, s) : launch_format<kFp4Nv>(a, num_sms, s);

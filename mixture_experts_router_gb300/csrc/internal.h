@@ -359,10 +359,13 @@ struct Fp4MatmulArgs {
   const int32_t* tile_offsets;
   void* out;
   int64_t ld_out;
-  int32_t* status;
+  int32_t* status;       // or nullptr: the device's own word
   uint64_t wait_limit_ns;
+  int32_t test_stall;    // test only: the epilogues wait for a tile that is never said to be done
 };
 cudaError_t launch_fp4_matmul(const Fp4MatmulArgs& a, int num_sms, cudaStream_t s);
+// the current device's own status word, cleared (waits for the device)
+cudaError_t take_fp4_error(int* code);
 
 // 2-D row-major tensor [outer][inner] with a box of box_outer x box_inner
 // elements, 128-byte swizzled (MMA operands) unless said otherwise.

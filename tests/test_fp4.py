@@ -665,3 +665,23 @@ def test_products_on_cta_pairs_are_exact(fmt, m, n, k, gap):
         cb.fp4_matmul(a, b, out=out[:, :n], status=status)
         assert torch.equal(out[:, :n], ref.to(dtype)) and (out[:, n:] == 7.0).all()
     assert int(status) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(4, 256, 256), (200, 256, 256), (2400, 2304, 1024)])
+def test_a_wait_that_runs_out_is_reported(monkeypatch, m, n, k):
+    """The library's stall makes the epilogues wait, for 1 ms, for a tile that is never said to be
+    done (swapped products, single CTAs, pairs).  The call ends and the status says why: the
+    caller's own word, or without one the device's; the next product is right."""
+    rng = np.random.default_rng(m)
+    a, b = random_matrix(rng, m, k, "mx", True), random_matrix(rng, n, k, "mx", True)
+    want = cb.fp4_matmul(a, b)
+    assert cb.fp4_last_error() == cb.CB_OK
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    monkeypatch.setenv("CB_MOE_INJECT_FAULT", "stall")
+    cb.fp4_matmul(a, b, status=status)
+    assert cb.fp4_last_error() == cb.CB_OK and int(status) == cb.CB_ERR_TIMEOUT
+    cb.fp4_matmul(a, b)
+    monkeypatch.delenv("CB_MOE_INJECT_FAULT")
+    assert cb.fp4_last_error() == cb.CB_ERR_TIMEOUT and cb.fp4_last_error() == cb.CB_OK
+    assert torch.equal(cb.fp4_matmul(a, b), want) and cb.fp4_last_error() == cb.CB_OK
