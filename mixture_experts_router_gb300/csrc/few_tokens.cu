@@ -774,7 +774,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Block<WF, NT, MT> b(p, maps, smem);
-  grid_dep_wait();
   const unsigned blocks = gridDim.x;
   const unsigned expected = blocks + static_cast<unsigned>(p.test_stall);
   bool ok = true;

@@ -412,7 +412,6 @@ __global__ void __launch_bounds__((THREADS<SWAP>), 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  grid_dep_wait();
 
   const Tiles<BN, SWAP> tiles(a);
   const int stages = (a.k + BK - 1) / BK;
@@ -642,7 +641,6 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  grid_dep_wait();
 
   const int pt = (a.m + 2 * BP - 1) / (2 * BP), total = pt * ((a.n + C::BN - 1) / C::BN);
   const int first = blockIdx.x / 2, step = gridDim.x / 2;

@@ -17,12 +17,13 @@ constexpr int kErrDevice = 7;
 // Default bound on any device-side wait.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
-// Kernel launches of this library go through launch_kernel.  Inside a
+// Kernel launches of this library go through launch_kernel, but for those that
+// are never begun early (cooperative ones, the 4-bit products).  Inside a
 // PdlScope that is on, every launch after the first `plain_first` ones
 // carries programmatic stream serialization: the kernel may start (and run
 // its prologue) while the previous one in the stream finishes.  Every kernel
-// of the library calls grid_dep_wait before it reads what an earlier kernel
-// wrote, so the results do not depend on it.
+// launched so calls grid_dep_wait before it reads what an earlier kernel
+// wrote, and the results do not depend on it.
 struct PdlScope {
   static bool& flag() {
     static thread_local bool on = false;
