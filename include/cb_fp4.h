@@ -73,8 +73,9 @@ CB_API cb_status_t cb_fp4_quantize(int32_t format, const void *x, int32_t x_type
                                    void *stream);
 
 /* The way back: out [rows][cols] (out_type, row stride ld) = the values that
- * the codes and scales stand for, v s exactly in fp32, times g rounded once to
- * fp32, rounded once more to bf16 where out_type says so.  Errors as above. */
+ * the codes and scales stand for, v s exactly in fp32 (infinite past its range,
+ * which the quantiser's scales do not reach), times g rounded once to fp32,
+ * rounded once more to bf16 where out_type says so.  Errors as above. */
 CB_API cb_status_t cb_fp4_dequantize(int32_t format, const uint8_t *codes, const uint8_t *scales,
                                      const float *tensor_scale, int64_t rows, int64_t cols, void *out,
                                      int32_t out_type, int64_t ld, void *stream);

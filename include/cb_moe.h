@@ -196,7 +196,8 @@ CB_API cb_status_t cb_moe_forward_f32out(cb_moe_t *h, const void *x, float *out,
  * fp32) [n_tokens][d], device pointers as for cb_moe_forward.  The same
  * formulas in the same precision (bf16 H, fp32 sums, another order of them),
  * every weight format and router mode.  One kernel launch (two with the hash
- * router), which reads the weights of the chosen experts once.  The routing
+ * router), which reads the weights of the chosen experts once (of an expert
+ * that more than 8 tokens chose, twice, where n_tokens k <= 4 E).  The routing
  * of cb_moe_routing and the stage times stay those of the last full forward.
  * Asynchronous on `stream`, ordered after the handle's other forwards as
  * cb_moe_forward is; it can be captured into a graph.  Errors:

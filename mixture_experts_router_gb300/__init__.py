@@ -471,7 +471,8 @@ class Fp4Matrix:
     """A matrix of 4-bit floats with block scales, as include/cb_fp4.h lays it out: `codes`
     uint8 [rows][cols / 2] and `scales` uint8; format "mx" or "nv", the latter with
     `tensor_scale` (fp32 [1]).  One matrix per expert: codes [E][rows][cols / 2], scales of
-    E arrays, tensor_scale [E]."""
+    E arrays, tensor_scale [E].  The tensors are kept as they are given, not copied: writing another
+    scale into the caller's tensor_scale changes the matrix."""
 
     __slots__ = ("format", "rows", "cols", "groups", "codes", "scales", "tensor_scale")
 
@@ -504,8 +505,9 @@ class Fp4Matrix:
 
 def fp4_quantize(x, format, tensor_scale=None, stream=None) -> Fp4Matrix:
     """x (2-D, bf16 or fp32, contiguous rows with any stride) as an Fp4Matrix; format "nv"
-    takes tensor_scale, an fp32 CUDA tensor of one element, e.g. max|x| / (6 * 448).  Runs on
-    `stream`, or on torch's current stream; its result belongs to that stream."""
+    takes tensor_scale, an fp32 CUDA tensor of one element, e.g. max|x| / (6 * 448), which the
+    matrix keeps (0, as for zeros: every value is 0).  Runs on `stream`, or on torch's current
+    stream; its result belongs to that stream."""
     torch = _load_torch()
     fmt, kind, ld = FP4_FORMATS.get(format), _fp4_type(x.dtype), _row_stride(x)
     if fmt is None:

@@ -12,12 +12,13 @@
 //      -- grid barrier --
 //   4. down and combine   out[t][c] = sum_s w[t][s] (H[t k + s] . Wd[ids[t][s]][c]).
 //
-// What bounds it: the chosen experts' weights, read once from HBM; with at
-// most 16 tokens an expert's 128-row tiles of the large kernels would be
-// nearly all padding.  So a tile here is at most 32 weight rows (in step 3, 16
-// features' gate and up rows; in step 4, 32 output columns), streamed through
-// a ring of stages of 512 (int4 with 16 tokens: 256) bytes per row, with the
-// same stretch of the chosen tokens' activations beside them.
+// What bounds it: the chosen experts' weights, read once from HBM (of an expert
+// in two parts, twice: see launch_format); with at most 16 tokens an expert's
+// 128-row tiles of the large kernels would be nearly all padding.  So a tile
+// here is at most 32 weight rows (in step 3, 16 features' gate and up rows; in
+// step 4, 32 output columns), streamed through a ring of stages of 512 (int4
+// with 16 tokens: 256) bytes per row, with the same stretch of the chosen
+// tokens' activations beside them.
 //
 // A block is two halves, each with a ring, two feeding warps and 8 users:
 //

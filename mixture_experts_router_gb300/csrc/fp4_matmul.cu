@@ -23,7 +23,9 @@
 //
 // Per CTA: warp 0 TMA producer, warp 1 tensor memory, scale copies and MMAs,
 // warps 4.. epilogue.  Stage s of the ring has its own scale columns in tensor
-// memory, so a stage's commit frees both.  All waits are bounded.
+// memory, so a stage's commit frees both.  Every wait on a barrier in memory is
+// bounded; the allocation of tensor memory and the clusters' barriers are not
+// (they wait for CTAs whose own waits are).
 //
 // Measured on the GPU alone (inputs larger than L2 in turn or as large as they
 // are): 1 x 14336 x 4096 8.0 us, 64 x 4096 x 14336 10.1 us (the weights at 4.1

@@ -1,7 +1,10 @@
 // Quantisation to 4-bit floating point with block scales and its way back.
 //
 // Bound by memory: 2 or 4 bytes an element in, half a byte and a 16th or 32nd
-// out (28672 x 4096 bf16, mx: 55 us, 5.4 TB/s, and 49 us, 6.1 TB/s, back).  A
+// out (28672 x 4096 bf16, mx: 55 us, 5.4 TB/s, and 49 us, 6.1 TB/s, back).  NV is
+// bound by its arithmetic (two conversions of each element) and, in bf16, by
+// the elements next to a border, which are common there: 89 to 234 us by the
+// data and g, with L2 flushed before (mx alike: 63), fp32 98 (mx: 94).  A
 // block of 256 threads takes a tile of 128 rows x 256 columns, a thread 8
 // consecutive elements of 16 rows (16 bytes of bf16, so a warp reads 512-byte
 // runs), kBatch rows' loads ahead of their arithmetic.  The largest magnitude
