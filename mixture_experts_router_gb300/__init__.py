@@ -40,6 +40,13 @@ CB_FP4_MX, CB_FP4_NV = 0, 1
 CB_T_BF16, CB_T_F32 = 0, 1
 FP4_FORMATS = {"mx": CB_FP4_MX, "nv": CB_FP4_NV}
 FP4_BLOCK = {"mx": 32, "nv": 16}
+# every symbol include/cb_serve.h declares
+SERVE_SYMBOLS = ("cb_rms_norm", "cb_route", "cb_int4_matmul_few")
+CB_NORM_MAX_COLS, CB_FP8_COLS, CB_ROUTE_MAX_GROUPS, CB_INT4_MAX_ROWS = 32768, 128, 32, CB_MOE_MAX_FEW
+CB_SCORE_SIGMOID, CB_SCORE_SOFTMAX = 0, 1
+CB_GROUP_TOP2, CB_GROUP_MAX = 0, 1
+SCORES = {"sigmoid": CB_SCORE_SIGMOID, "softmax": CB_SCORE_SOFTMAX}
+GROUP_SCORES = {"top2": CB_GROUP_TOP2, "max": CB_GROUP_MAX}
 CB_ROUTER_SOFTMAX_TOPK, CB_ROUTER_RAW_LOGITS, CB_ROUTER_HASH = 0, 1, 2
 CB_MAX_HASH_DIMS = 8
 ROUTER_MODES = {"softmax": CB_ROUTER_SOFTMAX_TOPK, "raw": CB_ROUTER_RAW_LOGITS, "hash": CB_ROUTER_HASH}
@@ -77,6 +84,39 @@ class cb_fp4_matmul_t(ctypes.Structure):
 
 _FP4_MATMUL = struct.Struct("@2i3q6Pi4xPPqP")  # cb_fp4_matmul_t
 assert _FP4_MATMUL.size == ctypes.sizeof(cb_fp4_matmul_t)
+
+
+class cb_rms_norm_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64), ("weight", ctypes.c_void_p),
+                ("sum", ctypes.c_void_p), ("ld_sum", ctypes.c_int64), ("out", ctypes.c_void_p), ("ld_out", ctypes.c_int64),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("x_type", ctypes.c_int32), ("weight_type", ctypes.c_int32), ("out_type", ctypes.c_int32)]
+
+
+class cb_route_t(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int64), ("logits", ctypes.c_void_p), ("ld_logits", ctypes.c_int64),
+                ("bias", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("w", ctypes.c_void_p), ("scale", ctypes.c_float),
+                ("logits_type", ctypes.c_int32), ("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("n_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_score", ctypes.c_int32), ("renormalise", ctypes.c_int32)]
+
+
+class cb_int4_matmul_t(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_scales", ctypes.c_void_p), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("w", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("status", ctypes.c_void_p),
+                ("ld_x", ctypes.c_int64), ("ld_out", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("n_tokens", ctypes.c_int32), ("top_k", ctypes.c_int32), ("n_experts", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("x_per_slot", ctypes.c_int32), ("swiglu", ctypes.c_int32),
+                ("out_type", ctypes.c_int32)]
+
+
+# the same layouts for calls that are made every few microseconds
+_RMS_NORM, _ROUTE, _INT4 = struct.Struct("@2qPqPqPPqPqPPf3i"), struct.Struct("@qPq3Pf8i4x"), struct.Struct("@9P4q7i4x")
+for _s, _t in ((_RMS_NORM, cb_rms_norm_t), (_ROUTE, cb_route_t), (_INT4, cb_int4_matmul_t)):
+    assert _s.size == ctypes.sizeof(_t), _t
 
 
 class CbMoeError(RuntimeError):
@@ -127,6 +167,9 @@ def load_library(path: str = LIB_PATH):
     lib.cb_fp4_matmul.argtypes = [vp, vp]
     lib.cb_fp4_last_error.argtypes = []
     for name in FP4_SYMBOLS:
+        getattr(lib, name).restype = i32
+    for name in SERVE_SYMBOLS:
+        getattr(lib, name).argtypes = [vp, vp]
         getattr(lib, name).restype = i32
     lib.cb_status_string.argtypes = [i32]
     lib.cb_status_string.restype = ctypes.c_char_p
@@ -233,6 +276,18 @@ def cb_fp4_matmul(args: cb_fp4_matmul_t, stream: int = 0) -> int:
 
 def cb_fp4_last_error() -> int:
     return load_library().cb_fp4_last_error()
+
+
+def cb_rms_norm(args: cb_rms_norm_t, stream: int = 0) -> int:
+    return load_library().cb_rms_norm(ctypes.byref(args), stream)
+
+
+def cb_route(args: cb_route_t, stream: int = 0) -> int:
+    return load_library().cb_route(ctypes.byref(args), stream)
+
+
+def cb_int4_matmul_few(args: cb_int4_matmul_t, stream: int = 0) -> int:
+    return load_library().cb_int4_matmul_few(ctypes.byref(args), stream)
 
 
 # ------------------------------------------------------- torch convenience
@@ -417,7 +472,7 @@ def _stream_here(device, stream):
     """torch's current stream on `device` (an index) as an int, or None where a context has to
     be entered first: another stream is asked for, or another device is current."""
     if device < 0:
-        raise ValueError("4-bit matrices are made from and kept in CUDA tensors")
+        raise ValueError("CUDA tensors are needed")
     if stream is None and device == _torch._C._cuda_getDevice():
         return _torch._C._cuda_getCurrentRawStream(device)
     return None
@@ -617,3 +672,217 @@ def fp4_last_error(device=None):
     torch = _load_torch()
     with torch.cuda.device(torch.cuda.current_device() if device is None else device):
         return cb_fp4_last_error()
+
+
+# ----------------------------------------------- around the layer, over torch tensors
+class Fp8Rows:
+    """Rows of e4m3 codes (torch.float8_e4m3fn, or its bytes as uint8, [rows][cols]) with an fp32 scale per
+    row and 128 columns ([rows][ceil(cols / 128)]), both contiguous: X = scale * code.  The tensors
+    are kept as they are given."""
+
+    __slots__ = ("codes", "scales", "rows", "cols")
+
+    def __init__(self, codes, scales):
+        torch = _torch or _load_torch()
+        self.codes = codes
+        self.scales = scales
+        shape = codes.shape
+        if len(shape) != 2 or codes.dtype not in (torch.float8_e4m3fn, torch.uint8) or scales.dtype is not torch.float32 or \
+                tuple(scales.shape) != (shape[0], -(-shape[1] // CB_FP8_COLS)) or \
+                not (codes.is_contiguous() and scales.is_contiguous()):
+            raise ValueError(f"codes {tuple(shape)} {codes.dtype}, scales {tuple(scales.shape)} {scales.dtype}: not "
+                             f"contiguous e4m3 rows with an fp32 scale per {CB_FP8_COLS} columns")
+        self.rows, self.cols = shape
+        _check_device(codes.get_device(), scales)
+
+
+class RmsNormed:
+    """What rms_norm returns: `out`, `fp8` (Fp8Rows) and `sum`, None where not asked for."""
+
+    __slots__ = ("out", "fp8", "sum")
+
+    def __init__(self, out, fp8, sum):
+        self.out, self.fp8, self.sum = out, fp8, sum
+
+
+def rms_norm(x, weight, eps=1e-6, residual=None, want="out", dtype=None, out=None, sum=None, stream=None) -> RmsNormed:
+    """y = h / sqrt(mean(h^2) + eps) * weight over the rows of h = x + residual (2-D, bf16 or fp32, contiguous
+    rows with any stride; h = x without a residual), as cb_rms_norm.  want: "out" (y in x's type or
+    `dtype`, or into `out`), "fp8" (y as Fp8Rows) or "both".  With a residual h is returned too, in x's
+    type (into `sum`, which may be x or residual itself).  `out` may be x itself."""
+    torch = _torch or _load_torch()
+    kind, wkind = _FP4_TYPES.get(x.dtype), _FP4_TYPES.get(weight.dtype)
+    if kind is None or wkind is None:
+        raise ValueError(f"rms_norm: x {x.dtype}, weight {weight.dtype}: bfloat16 or float32 are needed")
+    if want not in ("out", "fp8", "both"):
+        raise ValueError(f"rms_norm: want {want!r} is none of 'out', 'fp8', 'both'")
+    ld, (rows, cols), device = _row_stride(x), x.shape, x.get_device()
+    if weight.dim() != 1 or weight.shape[0] != cols or not weight.is_contiguous():
+        raise ValueError(f"rms_norm: a weight of {tuple(weight.shape)} for {cols} columns")
+    if out is not None and (want == "fp8" or out.shape != x.shape or (dtype is not None and out.dtype != dtype)):
+        raise ValueError(f"rms_norm: out {tuple(out.shape)} {out.dtype} for rows of {tuple(x.shape)}, want {want!r}")
+    okind = _FP4_TYPES.get((dtype or x.dtype) if out is None else out.dtype)
+    if okind is None:
+        raise ValueError("rms_norm: a result in bfloat16 or float32")
+    if residual is None and sum is not None:
+        raise ValueError("rms_norm: a sum without a residual")
+    for t in (residual, sum):
+        if t is not None and (t.dtype != x.dtype or t.shape != x.shape):
+            raise ValueError(f"rms_norm: residual or sum {tuple(t.shape)} {t.dtype} beside x {tuple(x.shape)} {x.dtype}")
+    _check_device(device, weight, residual, out, sum)
+    s = _stream_here(device, stream)
+    if s is None:
+        with _On(device, stream):
+            return rms_norm(x, weight, eps, residual, want, dtype, out, sum)
+    where, fp8 = x.device, None
+    if want != "fp8" and out is None:
+        out = torch.empty((rows, cols), dtype=dtype or x.dtype, device=where)
+    if residual is not None and sum is None:
+        sum = torch.empty((rows, cols), dtype=x.dtype, device=where)
+    if want != "out":
+        fp8 = Fp8Rows.__new__(Fp8Rows)
+        fp8.rows, fp8.cols = rows, cols
+        fp8.codes = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=where)
+        fp8.scales = torch.empty((rows, -(-cols // CB_FP8_COLS)), dtype=torch.float32, device=where)
+    st = (_lib or load_library()).cb_rms_norm(_RMS_NORM.pack(
+        rows, cols, x.data_ptr(), ld,
+        *((0, 0) if residual is None else (residual.data_ptr(), _row_stride(residual))), weight.data_ptr(),
+        *((0, 0) if sum is None else (sum.data_ptr(), _row_stride(sum))),
+        *((0, 0) if out is None else (out.data_ptr(), _row_stride(out))),
+        *((0, 0) if fp8 is None else (fp8.codes.data_ptr(), fp8.scales.data_ptr())), eps, kind, wkind, okind), s)
+    if st != CB_OK:
+        raise CbMoeError(st, "cb_rms_norm")
+    return RmsNormed(out, fp8, sum)
+
+
+def route(logits, top_k, score="sigmoid", bias=None, groups=1, top_groups=None, group_score="top2", renormalise=True,
+          scale=1.0, stream=None):
+    """(ids int32 [T][top_k], w fp32 [T][top_k]) from logits [T][E] (bf16 or fp32, contiguous rows with any
+    stride), as cb_route: the top_k experts by score ("sigmoid" or "softmax") + bias (fp32 [E]) of the best
+    `top_groups` (all unless given) of `groups` groups of consecutive experts (by "top2" or "max"); weights
+    are the scores, divided by their sum with `renormalise`, times `scale`."""
+    torch = _torch or _load_torch()
+    kind, how, by = _FP4_TYPES.get(logits.dtype), SCORES.get(score), GROUP_SCORES.get(group_score)
+    if kind is None or how is None or by is None:
+        raise ValueError(f"route: logits {logits.dtype} (bfloat16 or float32), score {score!r} (one of {sorted(SCORES)}), "
+                         f"group_score {group_score!r} (one of {sorted(GROUP_SCORES)})")
+    ld, (tokens, experts), device = _row_stride(logits), logits.shape, logits.get_device()
+    if bias is not None:
+        if bias.dtype is not torch.float32 or bias.numel() != experts or not bias.is_contiguous():
+            raise ValueError(f"route: a contiguous fp32 bias of {experts} is needed")
+        _check_device(device, bias)
+    s = _stream_here(device, stream)
+    if s is None:
+        with _On(device, stream):
+            return route(logits, top_k, score, bias, groups, top_groups, group_score, renormalise, scale)
+    if top_k < 1:
+        raise CbMoeError(CB_ERR_INVALID_ARG, f"route: top_k = {top_k}")
+    where = logits.device
+    ids = torch.empty((tokens, top_k), dtype=torch.int32, device=where)
+    w = torch.empty((tokens, top_k), dtype=torch.float32, device=where)
+    st = (_lib or load_library()).cb_route(_ROUTE.pack(
+        tokens, logits.data_ptr(), ld, 0 if bias is None else bias.data_ptr(), ids.data_ptr(), w.data_ptr(), scale, kind,
+        experts, top_k, how, groups, groups if top_groups is None else top_groups, by, 1 if renormalise else 0), s)
+    if st != CB_OK:
+        raise CbMoeError(st, "cb_route")
+    return ids, w
+
+
+class Int4Matrix:
+    """4-bit integer weights with a scale and a zero point per group of 32, 64 or 128 elements of a row, as
+    include/cb_serve.h lays them out: codes uint8 [rows][cols / 2] (element 2i in the low nibble), scales
+    fp32 [cols / group][rows], zeros uint8 of the same shape, or None for 8 everywhere.  One matrix per
+    expert: codes [E][rows][cols / 2], scales and zeros [E][cols / group][rows].  The tensors are kept as
+    they are given."""
+
+    __slots__ = ("rows", "cols", "group", "experts", "codes", "scales", "zeros")
+
+    def __init__(self, codes, scales, zeros=None):
+        torch = _torch or _load_torch()
+        self.codes, self.scales, self.zeros = codes, scales, zeros
+        shape, meta = codes.shape, scales.shape
+        dims = len(shape)
+        self.experts = shape[0] if dims == 3 else None
+        if dims not in (2, 3) or len(meta) != dims or codes.dtype is not torch.uint8 or scales.dtype is not torch.float32 or \
+                (dims == 3 and meta[0] != shape[0]) or meta[-1] != shape[-2] or meta[-2] == 0 or \
+                (zeros is not None and (zeros.dtype is not torch.uint8 or zeros.shape != meta or not zeros.is_contiguous())) \
+                or not (codes.is_contiguous() and scales.is_contiguous()):
+            raise ValueError(f"codes {tuple(shape)} {codes.dtype}, scales {tuple(meta)} {scales.dtype}: not contiguous "
+                             f"4-bit weights [..][rows][cols / 2] with scales (and zeros alike) [..][cols / group][rows]")
+        self.rows, self.cols = shape[-2], 2 * shape[-1]
+        self.group = self.cols // meta[-2]
+        if self.group not in (32, 64, 128) or self.group * meta[-2] != self.cols:
+            raise ValueError(f"{meta[-2]} groups in {self.cols} columns: groups of 32, 64 or 128 are needed")
+        _check_device(codes.get_device(), scales, zeros)
+
+
+def int4_matmul_few(x, m: Int4Matrix, ids=None, weights=None, swiglu=False, dtype=None, out=None, status=None,
+                    stream=None):
+    """x m^T for 1 to CB_INT4_MAX_ROWS rows of x (bf16, contiguous rows, or Fp8Rows), in bf16 or `dtype`
+    (or into `out`), as cb_int4_matmul_few.  One matrix: [T][rows].  With ids (int32 CUDA tensor [T][k]) each row
+    meets its experts' matrices: [T][k][rows]; x may then be [T][k][cols] (Fp8Rows: T k rows), a row per slot.  With
+    weights too (fp32 [T][k]) their weighted sum: [T][rows].  swiglu: the rows are gates, then the values they
+    open: half as many columns.  `status`: an int32 CUDA tensor that receives CB_ERR_DEVICE where an id is no expert
+    (that row is NaN)."""
+    torch = _torch or _load_torch()
+    if isinstance(x, Fp8Rows):
+        data, scales, ld = x.codes, x.scales, x.cols
+        x_rows, cols, per_slot = x.rows, x.cols, False
+        if ids is not None and x_rows != ids.shape[0]:
+            per_slot = True
+    else:
+        data, scales, per_slot = x, None, x.dim() == 3
+        if x.dtype is not torch.bfloat16 or x.dim() not in (2, 3):
+            raise ValueError(f"int4_matmul_few: x {tuple(x.shape)} {x.dtype}: rows of bfloat16, or Fp8Rows, are needed")
+        if per_slot:
+            if ids is None or not x.is_contiguous():
+                raise ValueError("int4_matmul_few: a contiguous x of [T][k][cols] comes with ids")
+            x_rows, cols = x.shape[0] * x.shape[1], x.shape[2]
+            ld = cols
+        else:
+            (x_rows, cols), ld = x.shape, _row_stride(x)
+    if cols != m.cols:
+        raise ValueError(f"int4_matmul_few: rows of {cols} by a matrix of {m.cols} columns")
+    if (ids is not None) != (m.experts is not None):
+        raise ValueError("int4_matmul_few: ids and a matrix per expert come together")
+    device = data.get_device()
+    tokens, top = x_rows, 1
+    if ids is not None:
+        if ids.dim() != 2 or ids.dtype is not torch.int32 or not ids.is_contiguous():
+            raise ValueError("int4_matmul_few: ids: a contiguous int32 CUDA tensor [T][k] is needed")
+        tokens, top = ids.shape
+        if x_rows != (tokens * top if per_slot else tokens) or (per_slot and scales is None and x.shape[0] != tokens):
+            raise ValueError(f"int4_matmul_few: {x_rows} rows of x for ids of {tuple(ids.shape)}")
+        if weights is not None and (weights.dtype is not torch.float32 or weights.shape != ids.shape or
+                                    not weights.is_contiguous()):
+            raise ValueError(f"int4_matmul_few: weights: a contiguous fp32 tensor of {tuple(ids.shape)} is needed")
+    if weights is not None and (ids is None or swiglu):
+        raise ValueError("int4_matmul_few: weights come with ids and without swiglu")
+    width = m.rows // 2 if swiglu else m.rows
+    shape = (tokens, width) if ids is None or weights is not None else (tokens, top, width)
+    if out is not None and (tuple(out.shape) != shape or (dtype is not None and out.dtype != dtype) or
+                            (len(shape) == 3 and not out.is_contiguous())):
+        raise ValueError(f"int4_matmul_few: out {tuple(out.shape)} {out.dtype} for a result of {shape}")
+    kind = _FP4_TYPES.get((dtype or torch.bfloat16) if out is None else out.dtype)
+    if kind is None:
+        raise ValueError("int4_matmul_few: a result in bfloat16 or float32")
+    if status is not None:
+        _check_int32(status, 1, "status")
+    _check_device(device, m.codes, ids, weights, out, status)
+    s = _stream_here(device, stream)
+    if s is None:
+        with _On(device, stream):
+            return int4_matmul_few(x, m, ids, weights, swiglu, dtype, out, status)
+    if out is None:
+        out, ld_out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=data.device), width
+    else:
+        ld_out = width if len(shape) == 3 else _row_stride(out)
+    st = (_lib or load_library()).cb_int4_matmul_few(_INT4.pack(
+        data.data_ptr(), 0 if scales is None else scales.data_ptr(), m.codes.data_ptr(), m.scales.data_ptr(),
+        0 if m.zeros is None else m.zeros.data_ptr(), 0 if ids is None else ids.data_ptr(),
+        0 if weights is None else weights.data_ptr(), out.data_ptr(), 0 if status is None else status.data_ptr(),
+        ld, ld_out, m.rows, m.cols, tokens, top, m.experts or 1, m.group, 1 if per_slot else 0, 1 if swiglu else 0,
+        kind), s)
+    if st != CB_OK:
+        raise CbMoeError(st, "cb_int4_matmul_few")
+    return out

@@ -28,32 +28,6 @@ int64_t scale_bytes(int32_t format, int64_t rows, int64_t cols) {
 bool known_format(int32_t f) { return f == CB_FP4_MX || f == CB_FP4_NV; }
 bool known_type(int32_t t) { return t == CB_T_BF16 || t == CB_T_F32; }
 
-// The current device: this library's kernels are for compute capability 10.3.
-// A device's SM count is asked for once (0: not
-// yet; negative: a wrong GPU).
-cb_status_t check_device(int* sms) {
-  static std::atomic<int> known[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) {
-    cudaGetLastError();
-    return CB_ERR_CUDA;
-  }
-  int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
-  if (n == 0) {
-    int major = 0, minor = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-      cudaGetLastError();
-      return CB_ERR_CUDA;
-    }
-    if (major != 10 || minor != 3) n = -1;
-    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
-  }
-  *sms = n;
-  return n > 0 ? CB_OK : CB_ERR_UNSUPPORTED;
-}
-
 bool overlap(const void* a, uint64_t an, const void* b, uint64_t bn) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return an > 0 && bn > 0 && x < y + bn && y < x + an;
@@ -83,6 +57,32 @@ cb_status_t check_matrix(int32_t format, const void* x, int32_t type, int64_t ro
 
 }  // namespace
 
+// The current device: this library's kernels are for compute capability 10.3.
+// A device's SM count is asked for once (0: not
+// yet; negative: a wrong GPU).
+int cbmoe::check_device(int* sms) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return CB_ERR_CUDA;
+  }
+  int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      cudaGetLastError();
+      return CB_ERR_CUDA;
+    }
+    if (major != 10 || minor != 3) n = -1;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  }
+  *sms = n;
+  return n > 0 ? CB_OK : CB_ERR_UNSUPPORTED;
+}
+
 extern "C" {
 
 cb_status_t cb_fp4_scale_bytes(int32_t format, int64_t rows, int64_t cols, uint64_t* bytes) {
@@ -96,7 +96,7 @@ cb_status_t cb_fp4_quantize(int32_t format, const void* x, int32_t x_type, int64
   cb_status_t st = check_matrix(format, x, x_type, rows, cols, ld, tensor_scale, codes, scales);
   if (st != CB_OK || rows == 0) return st;
   int sms;
-  if ((st = check_device(&sms)) != CB_OK) return st;
+  if ((st = static_cast<cb_status_t>(check_device(&sms))) != CB_OK) return st;
   if (injected_fault() == kLaunch) return CB_ERR_CUDA;
   const Fp4Args a{format, x_type == CB_T_F32, const_cast<void*>(x), rows, cols, ld, tensor_scale, codes, scales};
   return launch_fp4_quantize(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CB_OK : CB_ERR_CUDA;
@@ -107,7 +107,7 @@ cb_status_t cb_fp4_dequantize(int32_t format, const uint8_t* codes, const uint8_
   cb_status_t st = check_matrix(format, out, out_type, rows, cols, ld, tensor_scale, codes, scales);
   if (st != CB_OK || rows == 0) return st;
   int sms;
-  if ((st = check_device(&sms)) != CB_OK) return st;
+  if ((st = static_cast<cb_status_t>(check_device(&sms))) != CB_OK) return st;
   if (injected_fault() == kLaunch) return CB_ERR_CUDA;
   const Fp4Args a{format, out_type == CB_T_F32, out, rows, cols, ld, tensor_scale, const_cast<uint8_t*>(codes),
                   const_cast<uint8_t*>(scales)};
@@ -147,7 +147,7 @@ cb_status_t cb_fp4_matmul(const cb_fp4_matmul_t* p, void* stream) {
       overlap(p->out, out_bytes, p->b_scales, g * scale_bytes(p->format, p->n, p->k)))
     return CB_ERR_INVALID_ARG;
   int sms = 0;
-  const cb_status_t st = check_device(&sms);
+  const cb_status_t st = static_cast<cb_status_t>(check_device(&sms));
   if (st != CB_OK) return st;
   const Fault fault = injected_fault();
   if (fault == kLaunch) return CB_ERR_CUDA;
@@ -178,7 +178,7 @@ cb_status_t cb_fp4_matmul(const cb_fp4_matmul_t* p, void* stream) {
 
 cb_status_t cb_fp4_last_error(void) {
   int sms, code = 0;
-  const cb_status_t st = check_device(&sms);
+  const cb_status_t st = static_cast<cb_status_t>(check_device(&sms));
   if (st != CB_OK) return st;
   return take_fp4_error(&code) == cudaSuccess ? static_cast<cb_status_t>(code) : CB_ERR_CUDA;
 }

@@ -368,6 +368,68 @@ cudaError_t launch_fp4_matmul(const Fp4MatmulArgs& a, int num_sms, cudaStream_t 
 // the current device's own status word, cleared (waits for the device)
 cudaError_t take_fp4_error(int* code);
 
+// ------------------------------------------------ around the layer (cb_serve.h)
+struct NormArgs {
+  int64_t rows;
+  int32_t cols;
+  const void* x;
+  int64_t ld_x;
+  const void* residual;
+  int64_t ld_residual;
+  const void* weight;
+  void* sum;
+  int64_t ld_sum;
+  void* out;
+  int64_t ld_out;
+  uint8_t* codes;
+  float* scales;
+  float eps;
+  int32_t f32;         // x, residual and sum are fp32 (else bf16)
+  int32_t weight_f32, out_f32;
+};
+cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t s);
+
+struct RouteArgs {
+  int32_t n_tokens, n_experts, top_k;
+  const void* logits;
+  int64_t ld;
+  const float* bias;
+  int32_t* ids;
+  float* w;
+  float scale;
+  int32_t f32;         // logits are fp32 (else bf16)
+  int32_t softmax;     // else sigmoid
+  int32_t n_groups, top_groups, group_max;
+  int32_t renormalise;
+};
+cudaError_t launch_route(const RouteArgs& a, int num_sms, cudaStream_t s);
+
+struct Int4Args {
+  int32_t pairs, top, n_experts;  // pairs: rows of out before the weighted sum
+  int32_t n, k;
+  const void* x;
+  int64_t ld_x;
+  const float* x_scales;
+  int32_t x_per_slot;
+  const uint8_t* codes;
+  const float* scales;
+  const uint8_t* zeros;
+  const int32_t* ids;
+  const float* w;
+  int32_t swiglu;
+  void* out;
+  int64_t ld_out;
+  int32_t out_f32;
+  int32_t* status;
+  int32_t nx;          // set by the launch: rows of x that a stage has room for,
+  int32_t ks;          //   and warps that share a tile
+};
+cudaError_t launch_int4_few(int group, const Int4Args& a, int num_sms, cudaStream_t s);
+
+// The current device's SMs; CB_ERR_UNSUPPORTED on a GPU that is none of this
+// library's (cb_status_t).
+int check_device(int* sms);
+
 // 2-D row-major tensor [outer][inner] with a box of box_outer x box_inner
 // elements, 128-byte swizzled (MMA operands) unless said otherwise.
 bool make_tmap(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t elem_bytes, uint64_t inner,

@@ -1,0 +1,239 @@
+// Root-mean-square norm with the residual's addition, written in x's type, as
+// e4m3 rows with an fp32 scale per 128 columns, or both:
+//
+//   h = x + r,  y = h / sqrt(mean h^2 + eps) * g,  s = max|y| / 448,  code = e4m3(y / s).
+//
+// Bound by memory: every element is read and written once, a row staying in
+// registers between its sum of squares and its results.  R threads share a row
+// (a power of two from 32), each holding up to 4 times 8 elements.  Rows that
+// start on 16 bytes: a thread's elements are 8 in a row (16 bytes of bf16),
+// 16 lanes a scale's 128 columns.  Others: an element of every 32 (a warp's
+// loads are whole lines), a warp's first 4 and last 4 steps a scale's columns.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace cbmoe {
+namespace {
+
+constexpr int kMaxThreads = 1024;
+constexpr int kBlock = 256;  // threads of a block that holds several rows
+
+__device__ __forceinline__ float bf16_to_f32(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+__device__ __forceinline__ uint16_t f32_to_bf16(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+
+// Eight elements of one thread: consecutive from p (VEC: on 16 bytes), or
+// every 32nd from p of which those below `left` exist.
+template <bool F32, bool VEC>
+__device__ __forceinline__ void load8(const void* base, int64_t at, int left, float (&v)[8]) {
+  if constexpr (VEC) {
+    if constexpr (F32) {
+      const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+      const float4 a = q[0], b = q[1];
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+      const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
+      const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(u[i] << 16);
+        v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = 0.f;
+      if (i * 32 < left) {
+        if constexpr (F32)
+          v[i] = static_cast<const float*>(base)[at + i * 32];
+        else
+          v[i] = bf16_to_f32(static_cast<const uint16_t*>(base)[at + i * 32]);
+      }
+    }
+  }
+}
+template <bool F32, bool VEC>
+__device__ __forceinline__ void store8(void* base, int64_t at, int left, const float (&v)[8]) {
+  if constexpr (VEC) {
+    if constexpr (F32) {
+      float4* q = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+      q[0] = make_float4(v[0], v[1], v[2], v[3]);
+      q[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      uint32_t u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = f32_to_bf16(v[2 * i]) | static_cast<uint32_t>(f32_to_bf16(v[2 * i + 1])) << 16;
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i * 32 < left) {
+        if constexpr (F32)
+          static_cast<float*>(base)[at + i * 32] = v[i];
+        else
+          static_cast<uint16_t*>(base)[at + i * 32] = f32_to_bf16(v[i]);
+      }
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void load8(bool f32, const void* base, int64_t at, int left, float (&v)[8]) {
+  if (f32)
+    load8<true, VEC>(base, at, left, v);
+  else
+    load8<false, VEC>(base, at, left, v);
+}
+
+// The scale of a group whose largest magnitude has the bits `top`, and what
+// its elements are multiplied by (0: divide by the scale, which is too small
+// for a reciprocal).
+struct GroupScale {
+  float scale, inverse;
+  bool finite;
+};
+__device__ __forceinline__ GroupScale group_scale(uint32_t top) {
+  GroupScale r;
+  r.finite = top < 0x7F800000u;
+  r.scale = r.finite ? __uint_as_float(top) / 448.f : __int_as_float(0x7FC00000);
+  r.inverse = r.scale > 1e-30f ? 1.f / r.scale : 0.f;
+  return r;
+}
+__device__ __forceinline__ float scaled(float y, const GroupScale& s) {
+  if (s.inverse > 0.f) return y * s.inverse;
+  return s.scale > 0.f ? y / s.scale : 0.f;  // (a NaN scale: zero)
+}
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+
+template <int STEPS, bool F32, bool VEC>
+__global__ void __launch_bounds__(kMaxThreads, 1) rms_norm_kernel(const NormArgs a, const int per_row) {
+  __shared__ float partial[32];
+  const int rows_here = blockDim.x / per_row, tid = threadIdx.x % per_row, lane = threadIdx.x % 32;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * rows_here + threadIdx.x / per_row;
+  const bool on = row < a.rows;
+  // the first of a step's eight columns of this thread, and how many columns there are from it
+  int col[STEPS];
+  float h[STEPS][8];
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const int chunk = i * per_row + tid;  // of 8 columns
+    col[i] = VEC ? chunk * 8 : chunk / 32 * 256 + lane;
+    const int left = a.cols - col[i];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[i][j] = 0.f;
+    if (on && left > 0) {
+      load8<F32, VEC>(a.x, row * a.ld_x + col[i], left, h[i]);
+      if (a.residual != nullptr) {
+        float r[8];
+        load8<F32, VEC>(a.residual, row * a.ld_residual + col[i], left, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] += r[j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = fmaf(h[i][j], h[i][j], sum);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (per_row > 32) {
+    if (lane == 0) partial[threadIdx.x / 32] = sum;
+    __syncthreads();
+    const int first = threadIdx.x / per_row * (per_row / 32);
+    sum = 0.f;
+    for (int i = 0; i < per_row / 32; ++i) sum += partial[first + i];
+  }
+  const float factor = 1.f / sqrtf(sum / static_cast<float>(a.cols) + a.eps);
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const int left = on ? a.cols - col[i] : 0;
+    float y[8] = {};
+    if (left > 0) {
+      if (a.sum != nullptr) store8<F32, VEC>(a.sum, row * a.ld_sum + col[i], left, h[i]);
+      load8<VEC>(a.weight_f32 != 0, a.weight, col[i], left, y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] *= h[i][j] * factor;
+      if (a.out != nullptr) {
+        if (a.out_f32)
+          store8<true, VEC>(a.out, row * a.ld_out + col[i], left, y);
+        else
+          store8<false, VEC>(a.out, row * a.ld_out + col[i], left, y);
+      }
+    }
+    if (a.codes != nullptr) {  // (the same for all threads)
+      const int groups = (a.cols + 127) / 128;
+      uint32_t top[VEC ? 1 : 2] = {};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t& t = top[VEC ? 0 : j / 4];
+        t = max(t, __float_as_uint(y[j]) & 0x7FFFFFFFu);
+      }
+      if constexpr (VEC) {
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) top[0] = max(top[0], __shfl_xor_sync(0xffffffffu, top[0], o));
+        if (left > 0) {
+          const GroupScale s = group_scale(top[0]);
+          uint32_t u[2] = {};
+          if (s.finite) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[j / 2] |= e4m3x2(scaled(y[2 * j], s), scaled(y[2 * j + 1], s)) << (j % 2 * 16);
+          }
+          *reinterpret_cast<uint2*>(a.codes + row * a.cols + col[i]) = make_uint2(u[0], u[1]);
+          if (lane % 16 == 0) a.scales[row * groups + col[i] / 128] = s.scale;
+        }
+      } else {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const GroupScale s = group_scale(__reduce_max_sync(0xffffffffu, top[b]));
+          if (b * 128 < left) {
+            if (lane == 0) a.scales[row * groups + col[i] / 128 + b] = s.scale;
+#pragma unroll
+            for (int j = 4 * b; j < 4 * b + 4; ++j)
+              if (j * 32 < left)
+                a.codes[row * a.cols + col[i] + j * 32] =
+                    s.finite ? static_cast<uint8_t>(e4m3x2(scaled(y[j], s), 0.f)) : uint8_t{0};
+          }
+        }
+      }
+    }
+  }
+}
+
+template <int STEPS, bool F32, bool VEC>
+cudaError_t launch(const NormArgs& a, int per_row, cudaStream_t s) {
+  const int threads = per_row < kBlock ? kBlock : per_row, rows_here = threads / per_row;
+  const unsigned grid = static_cast<unsigned>((a.rows + rows_here - 1) / rows_here);
+  return launch_kernel(rms_norm_kernel<STEPS, F32, VEC>, dim3(grid), dim3(threads), 0, s, a, per_row);
+}
+template <bool F32, bool VEC>
+cudaError_t launch_steps(const NormArgs& a, cudaStream_t s) {
+  const int chunks = (a.cols + 255) / 256 * 32;  // of 8 columns; unaligned rows take them by warps
+  int per_row = 32;
+  while (per_row < kMaxThreads && per_row < chunks) per_row *= 2;
+  // two steps of 8 per thread where that still fills a block
+  const int steps = (chunks + per_row - 1) / per_row;
+  if (steps <= 1) return launch<1, F32, VEC>(a, per_row, s);
+  if (steps <= 2) return launch<2, F32, VEC>(a, per_row, s);
+  return launch<4, F32, VEC>(a, per_row, s);
+}
+
+bool on16(const void* p, int64_t ld, int size) {
+  return p == nullptr || ((reinterpret_cast<uintptr_t>(p) | static_cast<uint64_t>(ld) * size) & 15u) == 0;
+}
+
+}  // namespace
+
+cudaError_t launch_rms_norm(const NormArgs& a, int, cudaStream_t s) {
+  const int size = a.f32 ? 4 : 2;
+  const bool vec = a.cols % 8 == 0 && on16(a.x, a.ld_x, size) && on16(a.residual, a.ld_residual, size) &&
+                   on16(a.sum, a.ld_sum, size) && on16(a.weight, 0, 1) && on16(a.out, a.ld_out, a.out_f32 ? 4 : 2) &&
+                   (reinterpret_cast<uintptr_t>(a.codes) & 7u) == 0;
+  if (a.f32) return vec ? launch_steps<true, true>(a, s) : launch_steps<true, false>(a, s);
+  return vec ? launch_steps<false, true>(a, s) : launch_steps<false, false>(a, s);
+}
+
+}  // namespace cbmoe
