@@ -210,6 +210,26 @@ CB_API cb_status_t cb_moe_forward_few(cb_moe_t *h, const void *x, int32_t n_toke
 CB_API cb_status_t cb_moe_forward_few_f32out(cb_moe_t *h, const void *x, int32_t n_tokens, float *out, void *stream);
 
 /*
+ * The same passes on a routing that the caller has (cb_route's, say) in place
+ * of the handle's router: ids int32 [n_tokens][top_k], w fp32 [n_tokens][top_k]
+ * (device, 4-byte aligned, read while the call runs on the stream), out = sum_s
+ * w[t][s] Y[row(t,s)].  The experts of a token have to be distinct and in
+ * [0, n_experts): a token's output row is NaN where they are not, and
+ * cb_moe_last_error returns CB_ERR_DEVICE.  Any handle, its router mode
+ * notwithstanding.  One launch more than the dispatch's, the two GEMMs' and the
+ * combine's, none more in the few-token forms; cb_moe_routing gives the
+ * routing of cb_moe_forward_routed as of any full forward.  Errors as above.
+ */
+CB_API cb_status_t cb_moe_forward_routed(cb_moe_t *h, const void *x, const int32_t *ids, const float *w, void *out,
+                                         void *stream);
+CB_API cb_status_t cb_moe_forward_routed_f32out(cb_moe_t *h, const void *x, const int32_t *ids, const float *w,
+                                                float *out, void *stream);
+CB_API cb_status_t cb_moe_forward_few_routed(cb_moe_t *h, const void *x, int32_t n_tokens, const int32_t *ids,
+                                             const float *w, void *out, void *stream);
+CB_API cb_status_t cb_moe_forward_few_routed_f32out(cb_moe_t *h, const void *x, int32_t n_tokens, const int32_t *ids,
+                                                    const float *w, float *out, void *stream);
+
+/*
  * Same pass from host memory: x_host (bf16 [T][d]) in, out_host (bf16 [T][d])
  * back.  The input copy, the layer and the output copy run on three streams
  * of the handle, through two handle-owned device staging slots that

@@ -30,7 +30,9 @@ STAGE_NAMES = ("router", "dispatch", "gateup_gemm", "down_gemm", "combine")
 ABI_SYMBOLS = ("cb_moe_init", "cb_moe_forward", "cb_moe_forward_f32out", "cb_moe_forward_host",
                "cb_moe_routing", "cb_moe_stage_times", "cb_moe_last_error", "cb_moe_device_bytes",
                "cb_moe_free", "cb_status_string", "cb_moe_dispatch_noalloc", "cb_moe_kernels_per_forward",
-               "cb_moe_set_stage_timing", "cb_moe_check_guards", "cb_moe_forward_few", "cb_moe_forward_few_f32out")
+               "cb_moe_set_stage_timing", "cb_moe_check_guards", "cb_moe_forward_few", "cb_moe_forward_few_f32out",
+               "cb_moe_forward_routed", "cb_moe_forward_routed_f32out", "cb_moe_forward_few_routed",
+               "cb_moe_forward_few_routed_f32out")
 
 
 CB_MOE_MAX_FEW = 16
@@ -144,6 +146,10 @@ def load_library(path: str = LIB_PATH):
     lib.cb_moe_forward_host.argtypes = [vp, vp, vp, vp]
     lib.cb_moe_forward_few.argtypes = [vp, vp, ctypes.c_int32, vp, vp]
     lib.cb_moe_forward_few_f32out.argtypes = [vp, vp, ctypes.c_int32, vp, vp]
+    lib.cb_moe_forward_routed.argtypes = [vp, vp, vp, vp, vp, vp]
+    lib.cb_moe_forward_routed_f32out.argtypes = [vp, vp, vp, vp, vp, vp]
+    lib.cb_moe_forward_few_routed.argtypes = [vp, vp, ctypes.c_int32, vp, vp, vp, vp]
+    lib.cb_moe_forward_few_routed_f32out.argtypes = [vp, vp, ctypes.c_int32, vp, vp, vp, vp]
     lib.cb_moe_routing.argtypes = [vp, ctypes.POINTER(cb_routing_view_t)]
     lib.cb_moe_stage_times.argtypes = [vp, ctypes.POINTER(ctypes.c_float), ctypes.c_int32]
     lib.cb_moe_last_error.argtypes = [vp]
@@ -158,7 +164,8 @@ def load_library(path: str = LIB_PATH):
     for name in ("cb_moe_init", "cb_moe_forward", "cb_moe_forward_f32out", "cb_moe_forward_host",
                  "cb_moe_routing", "cb_moe_stage_times", "cb_moe_last_error", "cb_moe_device_bytes",
                  "cb_moe_free", "cb_moe_kernels_per_forward", "cb_moe_set_stage_timing", "cb_moe_check_guards",
-                 "cb_moe_forward_few", "cb_moe_forward_few_f32out"):
+                 "cb_moe_forward_few", "cb_moe_forward_few_f32out", "cb_moe_forward_routed", "cb_moe_forward_routed_f32out",
+                 "cb_moe_forward_few_routed", "cb_moe_forward_few_routed_f32out"):
         getattr(lib, name).restype = i32
     i64 = ctypes.c_int64
     lib.cb_fp4_scale_bytes.argtypes = [ctypes.c_int32, i64, i64, ctypes.POINTER(ctypes.c_uint64)]
@@ -203,6 +210,24 @@ def cb_moe_forward_few(handle, x_ptr: int, n_tokens: int, out_ptr: int, stream: 
 
 def cb_moe_forward_few_f32out(handle, x_ptr: int, n_tokens: int, out_ptr: int, stream: int = 0) -> int:
     return load_library().cb_moe_forward_few_f32out(handle, x_ptr, n_tokens, out_ptr, stream)
+
+
+def cb_moe_forward_routed(handle, x_ptr: int, ids_ptr: int, w_ptr: int, out_ptr: int, stream: int = 0) -> int:
+    return load_library().cb_moe_forward_routed(handle, x_ptr, ids_ptr, w_ptr, out_ptr, stream)
+
+
+def cb_moe_forward_routed_f32out(handle, x_ptr: int, ids_ptr: int, w_ptr: int, out_ptr: int, stream: int = 0) -> int:
+    return load_library().cb_moe_forward_routed_f32out(handle, x_ptr, ids_ptr, w_ptr, out_ptr, stream)
+
+
+def cb_moe_forward_few_routed(handle, x_ptr: int, n_tokens: int, ids_ptr: int, w_ptr: int, out_ptr: int,
+                              stream: int = 0) -> int:
+    return load_library().cb_moe_forward_few_routed(handle, x_ptr, n_tokens, ids_ptr, w_ptr, out_ptr, stream)
+
+
+def cb_moe_forward_few_routed_f32out(handle, x_ptr: int, n_tokens: int, ids_ptr: int, w_ptr: int, out_ptr: int,
+                                     stream: int = 0) -> int:
+    return load_library().cb_moe_forward_few_routed_f32out(handle, x_ptr, n_tokens, ids_ptr, w_ptr, out_ptr, stream)
 
 
 def cb_moe_forward_host(handle, x_host_ptr: int, out_host_ptr: int, stream: int = 0) -> int:
@@ -362,26 +387,43 @@ class MoELayer:
             raise CbMoeError(st, "cb_moe_init")
         self.handle = h
 
-    def forward(self, x, out, stream=None, f32out=False):
+    def _check_given(self, routing, n):
+        """The caller's routing (ids int32, w fp32, both [n][k] on the handle's device), e.g. route()'s."""
+        torch, k = _torch or _load_torch(), self.cfg.top_k
+        ids, w = routing
+        for name, t, kind in (("ids", ids, torch.int32), ("w", w, torch.float32)):
+            if t.dtype is not kind or tuple(t.shape) != (n, k) or not t.is_contiguous() or t.get_device() != self.cfg.device:
+                raise ValueError(f"routing: {name} {tuple(t.shape)} {t.dtype} on {t.device}: contiguous {kind} of "
+                                 f"{(n, k)} on device {self.cfg.device} is needed")
+        return ids.data_ptr(), w.data_ptr()
+
+    def forward(self, x, out, stream=None, f32out=False, routing=None):
         """The layer for the handle's T tokens: x bf16 (or int16 bits), out bf16 (fp32 with f32out),
         contiguous and of T d elements (more are left alone).  Runs on `stream`, or on the legacy
-        default stream."""
+        default stream.  routing: (ids, w) in place of the handle's router, as cb_moe_forward_routed;
+        made on another stream, they are the caller's to wait for."""
         need = self.cfg.n_tokens * self.cfg.d_model
         for name, t, size in (("x", x, 2), ("out", out, 4 if f32out else 2)):
             if not t.is_contiguous() or t.numel() * t.element_size() < need * size:
                 raise ValueError(f"forward: {name} {tuple(t.shape)} {t.dtype} is not contiguous or holds less than "
                                  f"{self.cfg.n_tokens} x {self.cfg.d_model} elements of {size} bytes")
         s = 0 if stream is None else stream.cuda_stream
-        fn = cb_moe_forward_f32out if f32out else cb_moe_forward
-        st = fn(self.handle, x.data_ptr(), out.data_ptr(), s)
+        if routing is not None:
+            ids, w = self._check_given(routing, self.cfg.n_tokens)
+            fn = cb_moe_forward_routed_f32out if f32out else cb_moe_forward_routed
+            st = fn(self.handle, x.data_ptr(), ids, w, out.data_ptr(), s)
+        else:
+            fn = cb_moe_forward_f32out if f32out else cb_moe_forward
+            st = fn(self.handle, x.data_ptr(), out.data_ptr(), s)
         if st != CB_OK:
             raise CbMoeError(st, "cb_moe_forward")
         return out
 
-    def forward_few(self, x, out, stream=None, f32out=False):
+    def forward_few(self, x, out, stream=None, f32out=False, routing=None):
         """The layer for x.shape[0] <= CB_MOE_MAX_FEW tokens, whatever T the handle was made for.
         x bf16 (or int16 bits) and out the same (fp32 with f32out), both contiguous [n][d] on the
-        handle's device.  Runs on `stream`, or on torch's current stream there, as the 4-bit calls do."""
+        handle's device.  Runs on `stream`, or on torch's current stream there, as the 4-bit calls do.
+        routing: (ids, w) in place of the handle's router, as cb_moe_forward_few_routed."""
         torch, device = _torch or _load_torch(), self.cfg.device
         if x.shape != out.shape or x.dim() != 2 or x.shape[1] != self.cfg.d_model:
             raise ValueError(f"forward_few: x {tuple(x.shape)}, out {tuple(out.shape)}, d = {self.cfg.d_model}")
@@ -393,8 +435,13 @@ class MoELayer:
         if x.get_device() != device or out.get_device() != device:
             raise ValueError(f"forward_few: x on {x.device}, out on {out.device}, the handle on device {device}")
         s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
-        fn = cb_moe_forward_few_f32out if f32out else cb_moe_forward_few
-        st = fn(self.handle, x.data_ptr(), int(x.shape[0]), out.data_ptr(), s)
+        if routing is not None:
+            ids, w = self._check_given(routing, x.shape[0])
+            fn = cb_moe_forward_few_routed_f32out if f32out else cb_moe_forward_few_routed
+            st = fn(self.handle, x.data_ptr(), int(x.shape[0]), ids, w, out.data_ptr(), s)
+        else:
+            fn = cb_moe_forward_few_f32out if f32out else cb_moe_forward_few
+            st = fn(self.handle, x.data_ptr(), int(x.shape[0]), out.data_ptr(), s)
         if st != CB_OK:
             raise CbMoeError(st, "cb_moe_forward_few")
         return out

@@ -48,6 +48,7 @@ struct cb_moe {
   int* err;
   unsigned int* coop_bar;  // grid barrier of the cooperative dispatch
   int32_t coop_blocks;     // > 0: the dispatch's own ranking runs as one cooperative launch
+  int32_t routed_blocks;   // the same for a given routing
   uint64_t guard_off[48];  // CB_FLAG_GUARDS: offsets of the guard bands in the block
   int32_t n_guards;
   uint16_t *x_stage[2], *out_stage[2];  // host-buffer forwards: double-buffered device copies of x and out
@@ -79,7 +80,7 @@ struct cb_moe {
     const void* b;
     bool timing;           // captured with the stage events
     cudaGraphExec_t exec;
-  } graphs[4];             // bf16 forward, fp32-out forward, host-buffer forward (two staging slots)
+  } graphs[6];             // bf16 forward, fp32-out forward, host-buffer forward (two staging slots), given routings (two)
   bool gather_a;           // gate/up GEMM gathers its rows from x (no Xp copy)
   bool int8_tm;            // int8 GEMMs convert their weights into tensor memory
   bool use_pdl;            // programmatic dependent launch between the forward's kernels
@@ -307,7 +308,8 @@ FewArgs few_args(const cb_moe_t* h) {
   return a;
 }
 
-cb_status_t enqueue_forward(cb_moe_t* h, const void* x, void* out, bool f32out, cudaStream_t s) {
+// given: the routing is in the handle already.
+cb_status_t enqueue_forward(cb_moe_t* h, const void* x, void* out, bool f32out, cudaStream_t s, bool given = false) {
   const cb_moe_config_t& c = h->cfg;
   if (fault_injected("launch")) return CB_ERR_CUDA;
   // the forward's first kernel follows arbitrary work of the caller and is
@@ -346,7 +348,9 @@ cb_status_t enqueue_forward(cb_moe_t* h, const void* x, void* out, bool f32out, 
     ra.local_rank = h->inv;
   }
   ra.raw_weights = c.router_mode == CB_ROUTER_RAW_LOGITS ? 1 : 0;
-  if (c.router_mode == CB_ROUTER_HASH) {
+  if (given) {
+    if (!mark(1)) return CB_ERR_CUDA;
+  } else if (c.router_mode == CB_ROUTER_HASH) {
     if (launch_router_hash(hash_router_args(h, x, c.n_tokens, h->ids, h->w), s) != cudaSuccess || !mark(1)) return CB_ERR_CUDA;
   } else if (h->router_tc) {
     if (h->tm_x_src != x) {
@@ -393,7 +397,11 @@ cb_status_t enqueue_forward(cb_moe_t* h, const void* x, void* out, bool f32out, 
     da.test_stall = 1;
     da.wait_limit_ns = 1000000ull;  // 1 ms
   }
-  if (h->rd_grid > 0 && c.router_mode != CB_ROUTER_HASH) {
+  if (given) {
+    da.rank_block = 0;
+    da.coop_blocks = h->routed_blocks;
+    if (launch_dispatch(da, s) != cudaSuccess || !mark(2)) return CB_ERR_CUDA;
+  } else if (h->rd_grid > 0 && c.router_mode != CB_ROUTER_HASH) {
     // router and dispatch in one launch: the router stage ends with it and
     // the dispatch stage is empty
     ra.blk_counts = nullptr;
@@ -636,11 +644,13 @@ bool mark_last_forward(cb_moe_t* h, cudaStream_t s) {
   return true;
 }
 
-// A device forward (bf16 or fp32 output) on the caller's stream.
-template <class Body>
-cb_status_t device_forward(cb_moe_t* h, int slot, const void* x, void* out, cudaStream_t s, Body body) {
+// A device forward (bf16 or fp32 output) on the caller's stream; `before` is
+// enqueued in front of it, outside of its graph.
+template <class Before, class Body>
+cb_status_t device_forward(cb_moe_t* h, int slot, const void* x, void* out, cudaStream_t s, Before before, Body body) {
   const bool cap = capturing(s);
   if (!cap && !wait_last_forward(h, s)) return CB_ERR_CUDA;
+  if (!before(s)) return CB_ERR_CUDA;
   const cb_status_t st = run_graphed(h, slot, x, out, s, body);
   if (st == CB_OK && !cap && !mark_last_forward(h, s)) return CB_ERR_CUDA;
   return st;
@@ -648,7 +658,8 @@ cb_status_t device_forward(cb_moe_t* h, int slot, const void* x, void* out, cuda
 
 // The few-token layer on the caller's stream: the hash router's kernel where
 // the handle has one, and the one launch that is the rest.
-cb_status_t few_forward(cb_moe_t* h, const void* x, int32_t n, void* out, bool f32out, void* stream) {
+cb_status_t few_forward(cb_moe_t* h, const void* x, int32_t n, const int32_t* ids, const float* w, void* out, bool f32out,
+                        void* stream) {
   if (h == nullptr || n < 0) return CB_ERR_INVALID_ARG;
   if (n > CB_MOE_MAX_FEW) return CB_ERR_UNSUPPORTED;
   if (n == 0) return CB_OK;
@@ -672,7 +683,9 @@ cb_status_t few_forward(cb_moe_t* h, const void* x, int32_t n, void* out, bool f
     a.test_stall = 1;
     a.wait_limit_ns = 1000000ull;  // 1 ms
   }
-  if (c.router_mode == CB_ROUTER_HASH) {
+  a.ids = ids;
+  a.w = w;
+  if (ids == nullptr && c.router_mode == CB_ROUTER_HASH) {
     a.ids = h->few_ids;
     const HashRouterArgs ha =
         hash_router_args(h, x, n, h->few_ids, reinterpret_cast<float*>(h->few_ids + kFewTokens));
@@ -681,6 +694,56 @@ cb_status_t few_forward(cb_moe_t* h, const void* x, int32_t n, void* out, bool f
   if (launch_few_tokens(format, h->few_maps, a, h->few_grid, s) != cudaSuccess) return CB_ERR_CUDA;
   if (!cap && !mark_last_forward(h, s)) return CB_ERR_CUDA;
   return CB_OK;
+}
+
+// A forward of the handle's n_tokens on the caller's stream, on the caller's
+// routing if ids is one.
+cb_status_t full_forward(cb_moe_t* h, const void* x, const int32_t* ids, const float* w, void* out, bool f32out,
+                         void* stream) {
+  const cb_status_t st = check_forward_args(h, x, out, h != nullptr ? h->cfg.n_tokens : 0, f32out ? 4 : 2);
+  if (st != CB_OK) return st;
+  const cb_moe_config_t& c = h->cfg;
+  if (c.n_tokens == 0) return CB_OK;
+  if (fault_injected("launch")) return CB_ERR_CUDA;
+  DeviceGuard guard(c.device);
+  if (!guard.ok) return CB_ERR_CUDA;
+  const bool given = ids != nullptr;
+  return device_forward(
+      h, (given ? 4 : 0) + (f32out ? 1 : 0), x, out, static_cast<cudaStream_t>(stream),
+      [&](cudaStream_t s) {
+        return !given || launch_given_routing(ids, w, c.n_tokens, c.top_k, c.n_experts, h->ids, h->w, h->err, s) ==
+                             cudaSuccess;
+      },
+      [&](cudaStream_t s) { return enqueue_forward(h, x, out, f32out, s, given); });
+}
+
+// A routing as an argument: 4-byte aligned words [n][top_k] that out does not overlap.
+cb_status_t check_routing(const cb_moe_t* h, const int32_t* ids, const float* w, int64_t n, const void* out,
+                          uint64_t out_elem_bytes) {
+  if (h == nullptr || ids == nullptr || w == nullptr) return CB_ERR_INVALID_ARG;
+  const uint64_t bytes = static_cast<uint64_t>(n) * h->cfg.top_k * 4;
+  const uintptr_t o = reinterpret_cast<uintptr_t>(out), end = o + static_cast<uint64_t>(n) * h->cfg.d_model * out_elem_bytes;
+  for (const void* p : {static_cast<const void*>(ids), static_cast<const void*>(w)}) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    if (a % 4 != 0) return CB_ERR_ALIGNMENT;
+    if (a < end && o < a + bytes) return CB_ERR_INVALID_ARG;
+  }
+  return CB_OK;
+}
+
+cb_status_t full_routed(cb_moe_t* h, const void* x, const int32_t* ids, const float* w, void* out, bool f32out,
+                        void* stream) {
+  if (h != nullptr && h->cfg.n_tokens == 0) return full_forward(h, x, nullptr, nullptr, out, f32out, stream);
+  const cb_status_t st = check_routing(h, ids, w, h != nullptr ? h->cfg.n_tokens : 0, out, f32out ? 4 : 2);
+  return st != CB_OK ? st : full_forward(h, x, ids, w, out, f32out, stream);
+}
+cb_status_t few_routed(cb_moe_t* h, const void* x, int32_t n, const int32_t* ids, const float* w, void* out, bool f32out,
+                       void* stream) {
+  if (n > 0 && n <= CB_MOE_MAX_FEW) {
+    const cb_status_t st = check_routing(h, ids, w, n, out, f32out ? 4 : 2);
+    if (st != CB_OK) return st;
+  }
+  return few_forward(h, x, n, ids, w, out, f32out, stream);
 }
 
 }  // namespace
@@ -1002,11 +1065,13 @@ cb_status_t cb_moe_init(const cb_moe_config_t* cfg, const cb_moe_weights_t* wts,
     const char* dv = std::getenv("CB_MOE_DISPATCH");
     const bool coop_pref = dv != nullptr ? std::strcmp(dv, "coop") == 0 : routed <= kCoopMaxPairs;
     h->coop_blocks = 0;
-    if (h->rank_block == 0 && h->rd_grid == 0 && cfg->n_experts <= 256 && coop_pref) {
+    h->routed_blocks = 0;
+    if (cfg->n_experts <= 256 && coop_pref) {
       int g = dispatch_coop_max_blocks(h->num_sms);
       g = std::min(g, kFusedScanWords / cfg->n_experts);  // rows of counts the chunk buffer holds
       g = std::min(g, cfg->n_tokens);
-      h->coop_blocks = std::max(g, 0);
+      h->routed_blocks = std::max(g, 0);
+      if (h->rank_block == 0 && h->rd_grid == 0) h->coop_blocks = h->routed_blocks;
     }
   }
   ok = ok && make_tmap(&h->tm_wr, h->wr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d, E, 64,
@@ -1049,33 +1114,39 @@ cb_status_t cb_moe_init(const cb_moe_config_t* cfg, const cb_moe_weights_t* wts,
 }
 
 cb_status_t cb_moe_forward(cb_moe_t* h, const void* x, void* out, void* stream) {
-  const cb_status_t st = check_forward_args(h, x, out, h != nullptr ? h->cfg.n_tokens : 0, 2);
-  if (st != CB_OK) return st;
-  if (h->cfg.n_tokens == 0) return CB_OK;
-  if (fault_injected("launch")) return CB_ERR_CUDA;
-  DeviceGuard guard(h->cfg.device);
-  if (!guard.ok) return CB_ERR_CUDA;
-  return device_forward(h, 0, x, out, static_cast<cudaStream_t>(stream),
-                        [&](cudaStream_t s) { return enqueue_forward(h, x, out, false, s); });
+  return full_forward(h, x, nullptr, nullptr, out, false, stream);
 }
 
 cb_status_t cb_moe_forward_f32out(cb_moe_t* h, const void* x, float* out, void* stream) {
-  const cb_status_t st = check_forward_args(h, x, out, h != nullptr ? h->cfg.n_tokens : 0, 4);
-  if (st != CB_OK) return st;
-  if (h->cfg.n_tokens == 0) return CB_OK;
-  if (fault_injected("launch")) return CB_ERR_CUDA;
-  DeviceGuard guard(h->cfg.device);
-  if (!guard.ok) return CB_ERR_CUDA;
-  return device_forward(h, 1, x, out, static_cast<cudaStream_t>(stream),
-                        [&](cudaStream_t s) { return enqueue_forward(h, x, out, true, s); });
+  return full_forward(h, x, nullptr, nullptr, out, true, stream);
+}
+
+cb_status_t cb_moe_forward_routed(cb_moe_t* h, const void* x, const int32_t* ids, const float* w, void* out,
+                                  void* stream) {
+  return full_routed(h, x, ids, w, out, false, stream);
+}
+
+cb_status_t cb_moe_forward_routed_f32out(cb_moe_t* h, const void* x, const int32_t* ids, const float* w, float* out,
+                                         void* stream) {
+  return full_routed(h, x, ids, w, out, true, stream);
 }
 
 cb_status_t cb_moe_forward_few(cb_moe_t* h, const void* x, int32_t n_tokens, void* out, void* stream) {
-  return few_forward(h, x, n_tokens, out, false, stream);
+  return few_forward(h, x, n_tokens, nullptr, nullptr, out, false, stream);
 }
 
 cb_status_t cb_moe_forward_few_f32out(cb_moe_t* h, const void* x, int32_t n_tokens, float* out, void* stream) {
-  return few_forward(h, x, n_tokens, out, true, stream);
+  return few_forward(h, x, n_tokens, nullptr, nullptr, out, true, stream);
+}
+
+cb_status_t cb_moe_forward_few_routed(cb_moe_t* h, const void* x, int32_t n_tokens, const int32_t* ids, const float* w,
+                                      void* out, void* stream) {
+  return few_routed(h, x, n_tokens, ids, w, out, false, stream);
+}
+
+cb_status_t cb_moe_forward_few_routed_f32out(cb_moe_t* h, const void* x, int32_t n_tokens, const int32_t* ids,
+                                             const float* w, float* out, void* stream) {
+  return few_routed(h, x, n_tokens, ids, w, out, true, stream);
 }
 
 cb_status_t cb_moe_forward_host(cb_moe_t* h, const void* x_host, void* out_host, void* stream) {

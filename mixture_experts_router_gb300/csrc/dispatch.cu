@@ -612,6 +612,38 @@ cudaError_t launch_dispatch_ranks(const DispatchArgs& a, int scan_words, cudaStr
   return e;
 }
 
+// A thread a token; it compares each expert with the token's others.
+__global__ void __launch_bounds__(kThreads) given_routing_kernel(const int32_t* __restrict__ ids,
+                                                                 const float* __restrict__ w, int32_t T, int32_t k,
+                                                                 int32_t E, int32_t* ids_out, float* w_out, int* err) {
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  if (t >= T) return;
+  constexpr int kMost = 16;
+  int id[kMost];
+  bool ok = true;
+#pragma unroll
+  for (int s = 0; s < kMost; ++s) {
+    id[s] = s < k ? __ldg(ids + t * k + s) : -1 - s;
+    if (s < k) ok = ok && id[s] >= 0 && id[s] < E;
+#pragma unroll
+    for (int u = 0; u < s; ++u) ok = ok && id[s] != id[u];
+  }
+  if (!ok) set_error(err, kErrDevice);
+#pragma unroll
+  for (int s = 0; s < kMost; ++s)
+    if (s < k) {
+      ids_out[t * k + s] = ok ? id[s] : s;
+      w_out[t * k + s] = ok ? __ldg(w + t * k + s) : __int_as_float(0x7FC00000);
+    }
+}
+
+cudaError_t launch_given_routing(const int32_t* ids, const float* w, int32_t T, int32_t k, int32_t E, int32_t* ids_out,
+                                 float* w_out, int* err, cudaStream_t s) {
+  if (k > 16) return cudaErrorInvalidValue;
+  return launch_kernel(given_routing_kernel, dim3((T + kThreads - 1) / kThreads), dim3(kThreads), 0, s, ids, w, T, k, E,
+                       ids_out, w_out, err);
+}
+
 cudaError_t dispatch_prepare() {
   return cudaFuncSetAttribute(dispatch_scan_blocks, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               kFusedScanWords * 4);

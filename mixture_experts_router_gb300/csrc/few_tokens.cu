@@ -367,11 +367,26 @@ struct Block {
           atomicOr(&s.mask[id], 1u << warp);
         }
       }
-    } else if (threadIdx.x < p.n) {  // the hash router's experts: one per token, weight 1
-      const int id = p.ids[threadIdx.x];
-      s.w[threadIdx.x] = 1.f;
-      s.slot[id][threadIdx.x] = 0;
-      atomicOr(&s.mask[id], 1u << threadIdx.x);
+    } else if (threadIdx.x < p.n) {  // given experts
+      const int t = threadIdx.x;
+      const uint32_t bit = 1u << t;
+      const int32_t* ids = p.ids + t * p.k;
+      int good = 0;  // slots in order that are in range and new
+      for (; good < p.k; ++good) {
+        const int id = ids[good];
+        if (id < 0 || id >= p.E || (atomicOr(&s.mask[id], bit) & bit) != 0u) break;
+        s.slot[id][t] = static_cast<uint8_t>(good);
+        s.w[t * p.k + good] = p.w != nullptr ? p.w[t * p.k + good] : 1.f;
+      }
+      if (good < p.k) {  // experts 0 .. k - 1 with NaN weights instead
+        if (blockIdx.x == 0) set_error(p.err, kErrDevice);
+        for (int i = 0; i < good; ++i) atomicAnd(&s.mask[ids[i]], ~bit);
+        for (int i = 0; i < p.k; ++i) {
+          s.slot[i][t] = static_cast<uint8_t>(i);
+          s.w[t * p.k + i] = __int_as_float(0x7FC00000);
+          atomicOr(&s.mask[i], bit);
+        }
+      }
     }
     __syncthreads();
     // the parts: an expert's tokens in order, NT x 8 at most to a part

@@ -200,6 +200,12 @@ cudaError_t route_dispatch_tc_prepare();  // one-time function attributes
 cudaError_t launch_route_dispatch_tc(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const RouterArgs& r,
                                      const DispatchArgs& a, int grid, int box_rows, cudaStream_t s);
 
+// The caller's routing [T][k] into the handle's.  A token whose experts are
+// not distinct and in range gets experts 0 .. k - 1 with NaN weights, and err
+// kErrDevice.
+cudaError_t launch_given_routing(const int32_t* ids, const float* w, int32_t T, int32_t k, int32_t E, int32_t* ids_out,
+                                 float* w_out, int* err, cudaStream_t s);
+
 // ----------------------------------------------------------------- combine
 struct CombineArgs {
   const float* y;        // fp32 [max_mtiles*kTileM][d]
@@ -304,7 +310,8 @@ struct FewArgs {
   const uint16_t* wr;    // bf16 [E][d]
   const float* bias;     // [E] or nullptr
   int32_t raw_weights;   // 1: w = the selected raw logits (no softmax)
-  const int32_t* ids;    // the hash router's [n] experts (k = 1, weights 1), else nullptr: routed here
+  const int32_t* ids;    // given experts [n][k] (the hash router's, k = 1, or the caller's), else nullptr: routed here
+  const float* w;        // their weights [n][k], or nullptr: all 1
   const void* wgu;       // the handle's gate/up rows, interleaved in blocks of gu_block
   const void* wd;
   int32_t gu_block;
