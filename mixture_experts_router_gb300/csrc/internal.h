@@ -429,7 +429,8 @@ struct Int4Args {
   int32_t out_f32;
   int32_t* status;
   int32_t nx;          // set by the launch: rows of x that a stage has room for,
-  int32_t ks;          //   and warps that share a tile
+  int32_t ks;          //   warps that share a tile, stages of a warp's ring
+  int32_t depth;
 };
 cudaError_t launch_int4_few(int group, const Int4Args& a, int num_sms, cudaStream_t s);
 
