@@ -120,7 +120,8 @@ CB_API cb_status_t cb_route(const cb_route_t *args, void *stream);
  *   y[r][j] = sum_i x[r][i] W[j][i],
  * x in bf16, or e4m3 codes with a scale per row and 128 columns (cb_rms_norm's).
  * The integers code - zero are exact operands and every group's sum meets its
- * scale in fp32: nothing is rounded before the result.
+ * scale in fp32: nothing is rounded before the result.  (Elements of bf16 x
+ * from 2^62 on count as infinite, and what is below 2^-57 may be lost.)
  *
  * One matrix (n_experts = 1, ids NULL): out [n_tokens][n].  With ids
  * [n_tokens][top_k] (device, in [0, n_experts)) one matrix per expert, and
@@ -135,6 +136,7 @@ CB_API cb_status_t cb_route(const cb_route_t *args, void *stream);
  * unrounded sums.  Not with weights.
  */
 #define CB_INT4_MAX_ROWS CB_MOE_MAX_FEW
+#define CB_INT4_MAX_K 49152 /* with ids; eight times as much without */
 typedef struct {
   const void *x;          /* bf16 [rows][k], or e4m3 with x_scales; row stride ld_x elements */
   const float *x_scales;  /* [rows][ceil(k / 128)], or NULL: x is bf16           */
@@ -161,8 +163,8 @@ typedef struct {
  * ids or with swiglu, x_per_slot without ids, out overlapping an input),
  * CB_ERR_ALIGNMENT (x, codes, scales, zeros: 16 bytes; x's rows: 16 bytes (8 in 8 bits);
  * out: its element; the others: 4), CB_ERR_UNSUPPORTED (more than
- * CB_INT4_MAX_ROWS tokens, 16 slots or 256 experts, n or k above 2^24, a wrong
- * GPU), CB_ERR_CUDA. */
+ * CB_INT4_MAX_ROWS tokens, 16 slots or 256 experts, n above 2^24, k above
+ * CB_INT4_MAX_K, a wrong GPU), CB_ERR_CUDA. */
 CB_API cb_status_t cb_int4_matmul_few(const cb_int4_matmul_t *args, void *stream);
 
 #ifdef __cplusplus

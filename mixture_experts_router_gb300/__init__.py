@@ -44,7 +44,8 @@ FP4_FORMATS = {"mx": CB_FP4_MX, "nv": CB_FP4_NV}
 FP4_BLOCK = {"mx": 32, "nv": 16}
 # every symbol include/cb_serve.h declares
 SERVE_SYMBOLS = ("cb_rms_norm", "cb_route", "cb_int4_matmul_few")
-CB_NORM_MAX_COLS, CB_FP8_COLS, CB_ROUTE_MAX_GROUPS, CB_INT4_MAX_ROWS = 32768, 128, 32, CB_MOE_MAX_FEW
+CB_NORM_MAX_COLS, CB_FP8_COLS, CB_ROUTE_MAX_GROUPS = 32768, 128, 32
+CB_INT4_MAX_ROWS, CB_INT4_MAX_K = CB_MOE_MAX_FEW, 49152
 CB_SCORE_SIGMOID, CB_SCORE_SOFTMAX = 0, 1
 CB_GROUP_TOP2, CB_GROUP_MAX = 0, 1
 SCORES = {"sigmoid": CB_SCORE_SIGMOID, "softmax": CB_SCORE_SOFTMAX}

@@ -158,7 +158,8 @@ cb_status_t cb_int4_matmul_few(const cb_int4_matmul_t* p, void* stream) {
   if (!by_expert && (p->top_k != 1 || p->n_experts != 1)) return CB_ERR_INVALID_ARG;
   const int64_t cols = swiglu ? p->n / 2 : p->n;
   if (p->ld_x < p->k || p->ld_out < cols) return CB_ERR_INVALID_ARG;
-  if (p->n_tokens > CB_INT4_MAX_ROWS || p->top_k > 16 || p->n_experts > 256 || p->n > (1 << 24) || p->k > (1 << 24) ||
+  if (p->n_tokens > CB_INT4_MAX_ROWS || p->top_k > 16 || p->n_experts > 256 || p->n > (1 << 24) ||
+      p->k > (by_expert ? CB_INT4_MAX_K : 8 * CB_INT4_MAX_K) ||
       p->ld_x > (1ll << 48) || p->ld_out > (1ll << 48))
     return CB_ERR_UNSUPPORTED;
   if (p->n_tokens == 0) return CB_OK;

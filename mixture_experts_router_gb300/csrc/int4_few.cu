@@ -1,38 +1,59 @@
 // A few rows (1 to 16) by 4-bit integer weights with a scale and a zero point
 // per group of 32, 64 or 128 elements of a row:
 //
-//   y[t][j] = sum_g s[g][j] sum_{i in g} x[t][i] (q[j][i] - z[g][j]),
+//   y[t][j] = sum_g s[g][j] ( sum_{i in g} x[t][i] q[j][i]  -  z[g][j] sum_{i in g} x[t][i] ),
 //
 // one matrix, or one per expert with the experts of each row given; then the
-// rows as they are, silu(gate) * up, or the weighted sum over a row's experts.
+// rows as they are, silu(gate) * up (rows_kernel), or the weighted sum over a
+// row's experts (sum_kernel).
 //
 // What bounds it: the weights, read once from HBM (of an expert with more rows
 // than a part holds, once per part), and the instructions that widen them.
-// A warp takes tiles of 32 weight rows (SwiGLU: 16 features' gate and up
-// rows), a stage of 256 elements (128 bytes of a row) at a time, through a ring
-// in shared memory of its own that cp.async fills: with no thread but its own
-// 32 to wait for, a warp needs no barrier to keep its loads in flight across
-// stages, tiles and experts.  A stage brings the tile's codes, scales and zero
-// points and the same stretch of its rows of x.  The codes become bf16 (8-bit
-// x: fp16) exactly in registers and go through mma.sync m16n8k16 (A: weight
-// rows, B: up to 8 rows of x per n-tile); a group's sum is taken from zero and
-// joins the tile's sum with its scale, in fp32, so that no weight is rounded.
+// Both kernels take tiles of 32 weight rows (SwiGLU: 16 features' gate and up
+// rows) in stages of 128 elements, 64 bytes of a row: codes, scales and zero
+// points come by cp.async into a ring in shared memory that belongs to one
+// warp.  With no thread but its own 32 to wait for, a warp needs no barrier to
+// keep its loads in flight across stages, tiles and experts.
+//
+// Widening.  A bf16 word with bits only in its low byte is that byte times
+// 2^-133: its subnormals and its lowest normal numbers have one spacing.  So a
+// code is an MMA operand as soon as its neighbours are masked away: n 2^-133 in
+// bits 0-3, 16 n 2^-133 in bits 4-7 (for which x is given as x / 16), and after
+// one shift by 8 bits the other two of each half word: 5 instructions for 8
+// codes and none of them rounds.  (128 + n minus 128 + z, as an ordinary bf16
+// number, takes 11.)  x is multiplied by 2^64 to keep the sums in fp32's
+// normal range.  8-bit x goes the same way in fp16, whose spacing is 2^-24 and
+// which holds every e4m3 number and its sixteenth.  The tensor core takes
+// subnormal operands exactly (measured: 256 byte values, both types).
+//   The zero points' sum over x comes from one more MMA per 16 elements, whose
+// weights are all 1.  A group's sums are taken from zero and join the tile's
+// with their scale, in fp32: no weight is rounded.
 //
 // Layouts.  A dot product does not depend on the order of its terms: within a
 // group thread q of a quad owns a quarter of the group's consecutive elements,
 // so it reads its codes in one piece of 4, 8 or 16 bytes.  The 16-byte units
-// of a row stand at unit ^ key(row), the units of x in the order in which the
-// quads read them: no bank conflicts either way.  Row 2g and 2g + 1 of each
-// half of a tile are lane group g's, so its scales and zero points are pairs.
+// of a row stand at unit ^ key(row): no bank conflicts.  Rows 2g and 2g + 1 of
+// each half of a tile are lane group g's, so its scales and zero points are
+// pairs.
 //
-// Warps: `ks` of a block's eight share a tile, taking its stages in turn, where
-// there would be fewer tiles than warps; their sums are joined in order.  The
-// weighted sum has one tile per block at a time, all experts' stages going to
-// the eight warps in turn.  All sums are in a fixed order.
+// rows_kernel keeps a part's rows of x in shared memory, in the order of the
+// MMA's operands, and walks its share of the tiles; `ks` of a block's sixteen
+// warps share a tile, neighbours in k, so that 64 ks bytes of each row are
+// read together.  (x in the ring beside the codes cost as much as the codes:
+// all blocks read the same few lines of L2; 8 rows by two of 8 experts of
+// 28672 x 4096, loads alone, 113 us against 66 without.)  Where one matrix
+// has so long rows that x does not fit, a cluster of blocks splits k: each
+// keeps its stretch of x and the sums of a batch of tiles, which are joined
+// over distributed shared memory.
+//   sum_kernel has one tile per block at a time and all its experts' parts; each
+// pair has its own row of x there, which comes through the ring.
+//
+// All sums are in a fixed order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include "internal.h"
@@ -42,38 +63,32 @@
 namespace cbmoe {
 namespace {
 
+constexpr int kWarps = 16;
+constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 32;            // weight rows of a tile: two m16 fragments
+constexpr int kStageK = 128;         // elements of a row in a stage
+constexpr int kRowBytes = kStageK / 2;
 constexpr int kMaxPairs = 256;       // (row of x, slot)
 constexpr int kMaxExperts = 256;
 constexpr int kRedStride = 36;       // floats: the fragments' stores meet no bank twice
-constexpr int kMaxTokens = kFewTokens;
-constexpr int kWarpsOfSm = 16;       // in blocks of 8, or of 16 for the weighted sum
-constexpr int kMaxDepth = 4;
+constexpr int kMaxDepth = 6;
+constexpr int kMaxCluster = 8;
+constexpr int kXBytes = 2 * kStageK; // of a row of x in a stage, as MMA operands
+constexpr int kMaskBytes = kMaxExperts * kMaxPairs / 8;
 
-// One of the kernel's forms: groups of GROUP elements, NT n-tiles of 8 rows of
-// x to a part, SK elements of a row in a stage, x in 8 bits or not, WARPS to a block.
-template <int GROUP_, int NT_, int SK_, bool F8_, int WARPS_>
-struct Form {
-  static constexpr int kGroup = GROUP_, NT = NT_, SK = SK_, kWarps = WARPS_;
-  static constexpr bool F8 = F8_;
-  static constexpr int kThreads = kWarps * 32;
-  static constexpr int kRowBytes = SK / 2;
-  static constexpr int kGroups = SK / kGroup;            // of a stage
-  static constexpr int kWords = kGroup / 32;             // of codes, to a thread, row and group
-  // a row of x in a stage; for neighbours' reads to meet no bank twice 8-bit
-  // rows are padded, and of 16-bit ones every other has its 64-byte halves swapped
-  static constexpr int kTokBytes = F8 ? SK + 32 : 2 * SK;
-  static constexpr int kScales = kRows * kRowBytes;      // where the scales, zero points and x stand
-  static constexpr int kZeros = kScales + kGroups * kRows * 4;
-  static constexpr int kX = kZeros + kGroups * kRows;
-  // bytes of a stage with nx rows of x (and 8-bit rows' scales behind them)
-  __host__ __device__ static constexpr int stage(int nx) {
-    return (kX + nx * (kTokBytes + (F8 ? SK / 32 : 0)) + 127) / 128 * 128;
-  }
-  static_assert(kX + (NT == 1 ? 1 : 9) * kTokBytes >= NT * 8 * kRedStride * 4, "a tile's sums fit a stage");
-};
+// A stage: codes, scales, zero points (and in sum_kernel rows of x).
+constexpr int kScales = kRows * kRowBytes;
+template <int GROUP>
+constexpr int kGroups = kStageK / GROUP;
+template <int GROUP>
+constexpr int kZeros = kScales + kGroups<GROUP> * kRows * 4;
+template <int GROUP>
+constexpr int kStage = (kZeros<GROUP> + kGroups<GROUP> * kRows + 127) / 128 * 128;
+// a row of x in sum_kernel's ring; for neighbours' reads to meet no bank twice
+// 8-bit rows are padded, and of 16-bit ones every other has its 64-byte halves swapped
+template <bool F8>
+constexpr int kRingX = F8 ? kStageK + 32 : 2 * kStageK;
 
-template <int WARPS>
 struct Shared {
   uint8_t pair[kMaxPairs];      // pairs by expert, then in order,
   uint8_t row[kMaxPairs];       //   and their rows of x
@@ -81,7 +96,7 @@ struct Shared {
   int16_t first[kMaxPairs];     //   first entry of `pair`
   uint8_t count[kMaxPairs];     //   and number of them
   uint32_t bad[kMaxPairs / 32]; // pairs whose expert does not exist
-  int red[WARPS];               // where a warp has its sums of a tile, in the dynamic array
+  int red[kWarps];              // where a warp has its sums of a tile, in the dynamic array
   int warp_parts[kMaxExperts / 32];
   int n_parts;
 };
@@ -93,9 +108,15 @@ __device__ __forceinline__ void cp_async_8(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait_pending() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// All but the n newest groups have landed.
+__device__ __forceinline__ void cp_async_wait_pending(int n) {
+  switch (n) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+  }
 }
 
 template <bool F8>
@@ -128,444 +149,237 @@ __device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// Eight codes of a word minus their zero point, pairs of elements m and m + 4.
-// bf16: a nibble n in a half word under 0x4300 is 128 + n.  fp16: under 0x6400
-// 1024 + n, and one bit field further up 1024 + 16 n, so two shifts fewer:
-// (1024 + 16 n) / 16 - (64 + z).  All of it is exact.
+// Eight codes as operands, pairs of elements m and m + 4: 0 and 2 in units of
+// 2^-133 (fp16: 2^-24), 1 and 3 in sixteenths of it.
+__device__ __forceinline__ void widen(uint32_t v, uint32_t (&o)[4]) {
+  o[0] = v & 0x000F000Fu;
+  o[1] = v & 0x00F000F0u;
+  o[2] = v >> 8 & 0x000F000Fu;
+  o[3] = v >> 8 & 0x00F000F0u;
+}
+constexpr uint32_t kOnes = 0x00010001u, kSixteens = 0x00100010u;
+// What undoes the operands' units: 2^133 2^-64, or 2^24.
 template <bool F8>
-struct Zero {
-  uint32_t a, b;
-  // byte `at` of v is the zero point
-  __device__ __forceinline__ void set(uint32_t v, int at) {
-    a = __byte_perm(v, F8 ? 0x64u : 0x43u, at == 0 ? 0x4040 : 0x4141);
-    if constexpr (F8) b = __byte_perm(v << 4, 0xD4u, at == 0 ? 0x4040 : 0x4141);  // -(64 + z)
-  }
-};
-template <bool F8>
-__device__ __forceinline__ void widen(uint32_t v, const Zero<F8>& z, uint32_t (&o)[4]) {
-  if constexpr (F8) {
+constexpr float kUnit = F8 ? 16777216.f : 590295810358705651712.f;
+
+// Eight elements of x as operands to match.
+__device__ __forceinline__ void x_bf16(const uint4& e, uint32_t (&b)[4]) {
+  const uint32_t p[4] = {__byte_perm(e.x, e.z, 0x5410), __byte_perm(e.x, e.z, 0x7632), __byte_perm(e.y, e.w, 0x5410),
+                         __byte_perm(e.y, e.w, 0x7632)};
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      uint32_t lo, hi;
-      asm("lop3.b32 %0, %1, 0x000F000F, 0x64006400, 0xEA;" : "=r"(lo) : "r"(v >> (8 * j)));
-      asm("lop3.b32 %0, %1, 0x00F000F0, 0x64006400, 0xEA;" : "=r"(hi) : "r"(v >> (8 * j)));
-      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o[2 * j]) : "r"(lo), "r"(z.a));
-      asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o[2 * j + 1]) : "r"(hi), "r"(0x2C002C00u), "r"(z.b));
-    }
-  } else {
+  for (int i = 0; i < 4; ++i)  // times 2^64 or 2^60
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(b[i]) : "r"(p[i]), "r"(i % 2 == 0 ? 0x5F805F80u : 0x5D805D80u));
+}
+__device__ __forceinline__ void x_e4m3(const uint2& e, uint32_t (&b)[4]) {
+  const uint32_t lo = __byte_perm(e.x, e.y, 0x5140), hi = __byte_perm(e.x, e.y, 0x7362);
+  const uint16_t h[4] = {static_cast<uint16_t>(lo), static_cast<uint16_t>(lo >> 16), static_cast<uint16_t>(hi),
+                         static_cast<uint16_t>(hi >> 16)};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t n;
-      asm("lop3.b32 %0, %1, 0x000F000F, 0x43004300, 0xEA;" : "=r"(n) : "r"(v >> (4 * j)));
-      asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(o[j]) : "r"(n), "r"(z.a));
-    }
+  for (int i = 0; i < 4; ++i) {
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b[i]) : "h"(h[i]));
+    if (i % 2 == 1) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(b[i]) : "r"(0x2C002C00u));  // a sixteenth
   }
 }
 
-template <class F>
-struct Worker {
-  static constexpr int NT = F::NT, SK = F::SK, GROUP = F::kGroup, kWords = F::kWords, kWarps = F::kWarps;
-  static constexpr bool F8 = F::F8;
-  static constexpr int kPer = F::kRowBytes / 16;  // 16-byte units of a row in a stage
-  const Int4Args& p;
-  Shared<kWarps>& s;
-  uint8_t* const dynamic;
-  const int warp, lane, g, q;
-  const int bytes;        // of a stage
-  const int nst;          // stages of a row
-  const int tiles;        // of a matrix
-  const int row_bytes;
-  const int ring;         // this warp's, in the dynamic array
-  int slot_in = 0, slot_out = 0;
-  int ks = 1;             // warps that share a tile
+// The lane group's place among the 16-byte units of its rows: what differs
+// between neighbours is first the widest reads' own bit.
+__device__ __forceinline__ int unit_key(int g) { return (g & 2) | g >> 2; }
 
-  // Where the loads stand: the tile, its part, the stage; and this lane's
-  // codes, scales and zero points of the tile.
-  struct Place {
-    int sub, part, tile, st;
-    const uint8_t *lo, *hi;     // codes of the tile's rows of the first and the second fragment
-    int64_t scales, zeros;      // elements
-  };
-  Place in;
-  int end, step;          // of the walk over the tiles
-
-  __device__ __forceinline__ Worker(const Int4Args& p_, Shared<kWarps>& s_, uint8_t* smem)
-      : p(p_),
-        s(s_),
-        dynamic(smem),
-        warp(threadIdx.x / 32),
-        lane(threadIdx.x % 32),
-        g(threadIdx.x % 32 >> 2),
-        q(threadIdx.x & 3),
-        bytes(F::stage(p_.nx)),
-        nst((p_.k + SK - 1) / SK),
-        tiles(((p_.swiglu ? p_.n / 2 : p_.n) + tile_out(p_) - 1) / tile_out(p_)),
-        row_bytes(p_.k / 2),
-        ring(static_cast<int>(threadIdx.x / 32) * p_.depth * F::stage(p_.nx)) {}
-  __device__ __forceinline__ static int tile_out(const Int4Args& p) { return p.swiglu ? kRows / 2 : kRows; }
-
-  // The lane group's place among the 16-byte units of its rows: what differs
-  // between neighbours is first the widest reads' own bit.
-  __device__ __forceinline__ static int unit_key(int g) {
-    return kPer == 8 ? (g & 1) << 2 | (g & 2) | g >> 2 : (g & 2) | g >> 2;
-  }
-
-  // ------------------------------------------------------------- the walk
-  __device__ __forceinline__ void at_tile(Place& a) const {
-    const int e = s.act[a.part];
-    const int r0 = p.swiglu ? a.tile * (kRows / 2) : a.tile * kRows, second = p.swiglu ? p.n / 2 : kRows / 2;
-    const bool both = p.swiglu || r0 + kRows / 2 < p.n;  // else the second fragment is the first again
-    const int64_t matrix = static_cast<int64_t>(e) * p.n;
-    a.lo = p.codes + (matrix + r0 + 2 * (lane / kPer)) * row_bytes + lane % kPer * 16;
-    a.hi = both ? a.lo + static_cast<int64_t>(second) * row_bytes : a.lo;
-    const int64_t meta = static_cast<int64_t>(e) * (p.k / GROUP) * p.n + r0;
-    const int up = both ? second : 0;
-    a.scales = meta + (lane % 8 >= 4 ? up : 0) + lane % 4 * 4 + static_cast<int64_t>(lane / 8) * p.n;
-    a.zeros = meta + (lane % 4 >= 2 ? up : 0) + lane % 2 * 8 + static_cast<int64_t>(lane / 4) * p.n;
-  }
-  __device__ __forceinline__ bool any(const Place& a) const { return a.sub < end; }
-  // rows(): a tile is a part's
-  __device__ __forceinline__ void start_row(Place& a, int sub) const {
-    a.sub = sub;
-    if (sub >= end) return;
-    a.part = sub / tiles;
-    a.tile = sub - a.part * tiles;
-    a.st = warp % ks;
-    at_tile(a);
-  }
-  // weighted(): a tile's parts, `kWarps / ks` warps apart, one after the other
-  __device__ __forceinline__ void start_sum(Place& a, int sub) const {
-    a.sub = sub;
-    a.tile = sub;
-    a.part = warp / ks;
-    a.st = warp % ks;
-    if (a.part >= s.n_parts) a.sub = end;  // (in every tile)
-    if (any(a)) at_tile(a);
-  }
-  __device__ __forceinline__ void next(Place& a) const {
-    a.st += ks;
-    if (a.st < nst) return;
-    if (p.w == nullptr) {
-      start_row(a, a.sub + step);
-    } else {
-      a.st = warp % ks;
-      a.part += kWarps / ks;
-      if (a.part >= s.n_parts)
-        start_sum(a, a.sub + step);
-      else
-        at_tile(a);
-    }
-  }
-
-  // -------------------------------------------------------------- a stage
-  __device__ __forceinline__ void issue() {
-    if (any(in)) {
-      uint8_t* dst = dynamic + ring + slot_in * bytes;
-      const int k0 = in.st * SK, left = p.k - k0;
-      if (lane % kPer * 32 < left) {
-        // row j of lane group h stands at row 8 j + h: rows 2 h and 2 h + 1 of each fragment
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int j = kPer == 8 ? i >> 1 : i, h = kPer == 8 ? (i & 1) * 4 + lane / kPer : lane / kPer;
-          const int off = (j & 1) * row_bytes + (kPer == 8 ? (i & 1) * 8 * row_bytes : 0);
-          cp_async_16(dst + (j * 8 + h) * F::kRowBytes + ((lane % kPer ^ unit_key(h)) << 4),
-                      (j < 2 ? in.lo : in.hi) + (k0 / 2 + off));
-        }
-      }
-      // scales: 4 rows to a lane; zero points: 8
-      const int64_t before = static_cast<int64_t>(in.st * F::kGroups) * p.n;
-#pragma unroll
-      for (int i = 0; i < (F::kGroups + 3) / 4; ++i) {
-        const int gi = i * 4 + lane / 8;
-        if (gi < F::kGroups && gi * GROUP < left)
-          cp_async_16(dst + F::kScales + (i * 32 + lane) * 16, p.scales + in.scales + before + static_cast<int64_t>(i * 4) * p.n);
-      }
-      if (p.zeros != nullptr && lane / 4 < F::kGroups && lane / 4 * GROUP < left)
-        cp_async_8(dst + F::kZeros + lane * 8, p.zeros + in.zeros + before);
-      // x: 8 elements to a lane, in the order in which the quads read them
-      const int count = s.count[in.part], first = s.first[in.part];
-      constexpr int kUnits = GROUP / 8, kLanes = SK / 8;  // of a group; of a row of x
-      const int u = lane % kLanes;
-      const int at = u / kUnits * kUnits + u % kWords * 4 + u % kUnits / kWords;
-      uint8_t* x = dst + F::kX;
-      if (u * 8 < left)
-        for (int t = lane / kLanes; t < count; t += 32 / kLanes) {
-          const int64_t from = s.row[first + t] * p.ld_x + k0 + u * 8;
-          if constexpr (F8)
-            cp_async_8(x + t * F::kTokBytes + at * 8, static_cast<const uint8_t*>(p.x) + from);
-          else
-            cp_async_16(x + t * F::kTokBytes + ((at ^ (t & 1) << 2) << 4), static_cast<const uint16_t*>(p.x) + from);
-        }
-      if constexpr (F8) {
-        constexpr int kScales = SK / 128;
-        const int t = lane / kScales, h = lane % kScales;
-        if (t < count && h * 128 < left)
-          cp_async_4(x + p.nx * F::kTokBytes + lane * 4,
-                     p.x_scales + static_cast<int64_t>(s.row[first + t]) * ((p.k + 127) / 128) + k0 / 128 + h);
-      }
-      next(in);
-    }
-    cp_async_commit();
-    slot_in = slot_in + 1 == p.depth ? 0 : slot_in + 1;
-  }
-
-  __device__ __forceinline__ void clear(float (&v)[2][NT][4]) const {
+template <int NT>
+struct Sums {  // m16n8 fragments: [fragment][n-tile]
+  float v[2][NT][4];
+  __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int n = 0; n < NT; ++n) v[m][n][0] = v[m][n][1] = v[m][n][2] = v[m][n][3] = 0.f;
   }
+};
 
-  // acc += the oldest stage in the ring, which is stage st of a part of `count` rows.
-  __device__ __forceinline__ void take(int st, int count, float (&acc)[2][NT][4]) {
-    if (p.depth == 2)
-      cp_async_wait_pending<0>();
-    else if (p.depth == 3)
-      cp_async_wait_pending<1>();
-    else
-      cp_async_wait_pending<2>();
-    __syncwarp();
-    issue();
-    const uint8_t* src = dynamic + ring + slot_out * bytes;
-    slot_out = slot_out + 1 == p.depth ? 0 : slot_out + 1;
-    const int groups = (p.k - st * SK) / GROUP;
-    const uint8_t* codes = src + g * F::kRowBytes;
-    const int unit = ((q * kWords / 4 ^ unit_key(g)) << 4) + q * kWords % 4 * 4;
-    const uint8_t* x[NT][2];  // 16-bit rows: for the units in even and in odd halves
-    const float* xs[NT][2];
+// acc += the first `groups` groups of a stage.  fetch(n, i, b): n-tile n's
+// operands for this lane's i-th word of codes.  wide: the second n-tile too.
+// x_scale: of the lane's two columns of each n-tile.
+template <int GROUP, int NT, bool F8, typename Fetch>
+__device__ __forceinline__ void add_stage(const uint8_t* stage, int groups, bool has_zeros, bool wide, Fetch&& fetch,
+                                          const float (&x_scale)[NT][2], Sums<NT>& acc) {
+  constexpr int kWords = GROUP / 32;  // of a thread, row and group
+  const int g = threadIdx.x % 32 >> 2, q = threadIdx.x & 3;
+  const uint8_t* codes = stage + g * kRowBytes;
+  const int unit = ((q * kWords / 4 ^ unit_key(g)) << 4) + q * kWords % 4 * 4;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int t = min(n * 8 + g, count - 1), swap = F8 ? 0 : (t & 1) << 6;
-      x[n][0] = src + F::kX + t * F::kTokBytes + q * (F8 ? 8 : 16) + swap;
-      x[n][1] = x[n][0] - 2 * swap;
-      if constexpr (F8)
+  for (int gi = 0; gi < kGroups<GROUP>; ++gi) {
+    if (gi >= groups) break;
+    uint32_t v[4][kWords];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          xs[n][i] = reinterpret_cast<const float*>(src + F::kX + p.nx * F::kTokBytes) +
-                     min(n * 8 + 2 * q + i, count - 1) * (SK / 128);
+    for (int j = 0; j < 4; ++j) {
+      const uint8_t* at = codes + (unit ^ gi * GROUP / 2) + j * 8 * kRowBytes;
+      if constexpr (kWords == 4) {
+        const uint4 w = *reinterpret_cast<const uint4*>(at);
+        v[j][0] = w.x, v[j][1] = w.y, v[j][2] = w.z, v[j][3] = w.w;
+      } else if constexpr (kWords == 2) {
+        const uint2 w = *reinterpret_cast<const uint2*>(at);
+        v[j][0] = w.x, v[j][1] = w.y;
+      } else {
+        v[j][0] = *reinterpret_cast<const uint32_t*>(at);
+      }
     }
-    const bool wide = count > 8;
+    float sum[2][NT][4], all[NT][4];  // all: x's own sums, in every row
 #pragma unroll
-    for (int gi = 0; gi < F::kGroups; ++gi) {
-      if (gi >= groups) break;
-      uint32_t v[4][kWords];
+    for (int w = 0; w < kWords; ++w) {
+      uint32_t b[NT][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint8_t* at = codes + (unit ^ gi * GROUP / 2) + j * 8 * F::kRowBytes;
-        if constexpr (kWords == 4) {
-          const uint4 w = *reinterpret_cast<const uint4*>(at);
-          v[j][0] = w.x, v[j][1] = w.y, v[j][2] = w.z, v[j][3] = w.w;
-        } else if constexpr (kWords == 2) {
-          const uint2 w = *reinterpret_cast<const uint2*>(at);
-          v[j][0] = w.x, v[j][1] = w.y;
-        } else {
-          v[j][0] = *reinterpret_cast<const uint32_t*>(at);
-        }
-      }
-      Zero<F8> zz[4];
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        uint32_t z = 0x0808u;
-        if (p.zeros != nullptr) z = *reinterpret_cast<const uint16_t*>(src + F::kZeros + gi * kRows + m * 16 + 2 * g);
-        zz[2 * m].set(z, 0);
-        zz[2 * m + 1].set(z, 1);
-      }
-      float sum[2][NT][4];
-#pragma unroll
-      for (int w = 0; w < kWords; ++w) {
-        uint32_t b[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (n > 0 && !wide) break;
-          const uint8_t* at = x[n][F8 ? 0 : (gi * (GROUP / 32) + w) & 1] + (gi * (GROUP / 8) + w * 4) * (F8 ? 8 : 16);
-          if constexpr (F8) {
-            const uint2 e = *reinterpret_cast<const uint2*>(at);
-            const uint32_t lo = __byte_perm(e.x, e.y, 0x5140), hi = __byte_perm(e.x, e.y, 0x7362);
-            const uint16_t h[4] = {static_cast<uint16_t>(lo), static_cast<uint16_t>(lo >> 16), static_cast<uint16_t>(hi),
-                                   static_cast<uint16_t>(hi >> 16)};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b[n][i]) : "h"(h[i]));
-          } else {
-            const uint4 e = *reinterpret_cast<const uint4*>(at);
-            b[n][0] = __byte_perm(e.x, e.z, 0x5410);
-            b[n][1] = __byte_perm(e.x, e.z, 0x7632);
-            b[n][2] = __byte_perm(e.y, e.w, 0x5410);
-            b[n][3] = __byte_perm(e.y, e.w, 0x7632);
-          }
-        }
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          uint32_t a0[4], a1[4];
-          widen<F8>(v[2 * m][w], zz[2 * m], a0);
-          widen<F8>(v[2 * m + 1][w], zz[2 * m + 1], a1);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if (n > 0 && !wide) break;
-            if (w == 0)
-              mma_first<F8>(sum[m][n], a0[0], a1[0], a0[1], a1[1], b[n][0], b[n][1]);
-            else
-              mma<F8>(sum[m][n], a0[0], a1[0], a0[1], a1[1], b[n][0], b[n][1]);
-            mma<F8>(sum[m][n], a0[2], a1[2], a0[3], a1[3], b[n][2], b[n][3]);
-          }
-        }
+      for (int n = 0; n < NT; ++n) {
+        if (n > 0 && !wide) break;
+        fetch(n, gi * kWords + w, b[n]);
+        if (w == 0)
+          mma_first<F8>(all[n], kOnes, kOnes, kSixteens, kSixteens, b[n][0], b[n][1]);
+        else
+          mma<F8>(all[n], kOnes, kOnes, kSixteens, kSixteens, b[n][0], b[n][1]);
+        mma<F8>(all[n], kOnes, kOnes, kSixteens, kSixteens, b[n][2], b[n][3]);
       }
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        const float2 sc = *reinterpret_cast<const float2*>(src + F::kScales + (gi * kRows + m * 16 + 2 * g) * 4);
+        uint32_t a0[4], a1[4];
+        widen(v[2 * m][w], a0);
+        widen(v[2 * m + 1][w], a1);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           if (n > 0 && !wide) break;
-          float* c = acc[m][n];
-          const float* t = sum[m][n];
-          if constexpr (F8) {  // x's scale first, then the weights'
-            const float x0 = xs[n][0][gi * GROUP / 128], x1 = xs[n][1][gi * GROUP / 128];
-            c[0] = fmaf(sc.x, x0 * t[0], c[0]);
-            c[1] = fmaf(sc.x, x1 * t[1], c[1]);
-            c[2] = fmaf(sc.y, x0 * t[2], c[2]);
-            c[3] = fmaf(sc.y, x1 * t[3], c[3]);
-          } else {
-            c[0] = fmaf(sc.x, t[0], c[0]);
-            c[1] = fmaf(sc.x, t[1], c[1]);
-            c[2] = fmaf(sc.y, t[2], c[2]);
-            c[3] = fmaf(sc.y, t[3], c[3]);
-          }
+          if (w == 0)
+            mma_first<F8>(sum[m][n], a0[0], a1[0], a0[1], a1[1], b[n][0], b[n][1]);
+          else
+            mma<F8>(sum[m][n], a0[0], a1[0], a0[1], a1[1], b[n][0], b[n][1]);
+          mma<F8>(sum[m][n], a0[2], a1[2], a0[3], a1[3], b[n][2], b[n][3]);
         }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      float2 sc = *reinterpret_cast<const float2*>(stage + kScales + (gi * kRows + m * 16 + 2 * g) * 4);
+      sc.x *= kUnit<F8>;
+      sc.y *= kUnit<F8>;
+      uint32_t z = 0x0808u;
+      if (has_zeros) z = *reinterpret_cast<const uint16_t*>(stage + kZeros<GROUP> + gi * kRows + m * 16 + 2 * g);
+      // 2^23 + z as a float's bits, less 2^23
+      const float z0 = __uint_as_float(__byte_perm(z, 0x4B000000u, 0x7650)) - 8388608.f;
+      const float z1 = __uint_as_float(__byte_perm(z, 0x4B000000u, 0x7651)) - 8388608.f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (n > 0 && !wide) break;
+        float* c = acc.v[m][n];
+        float t[4] = {fmaf(-z0, all[n][0], sum[m][n][0]), fmaf(-z0, all[n][1], sum[m][n][1]),
+                      fmaf(-z1, all[n][0], sum[m][n][2]), fmaf(-z1, all[n][1], sum[m][n][3])};
+        if constexpr (F8) {
+          t[0] *= x_scale[n][0];
+          t[1] *= x_scale[n][1];
+          t[2] *= x_scale[n][0];
+          t[3] *= x_scale[n][1];
+        }
+        c[0] = fmaf(sc.x, t[0], c[0]);
+        c[1] = fmaf(sc.x, t[1], c[1]);
+        c[2] = fmaf(sc.y, t[2], c[2]);
+        c[3] = fmaf(sc.y, t[3], c[3]);
       }
     }
   }
+}
 
-  // The tile's sums of this warp, [row of x][weight row], into the stage that
-  // it used last: nothing is loaded there before the next one is taken.
-  __device__ __forceinline__ float* put_sums(const float (&acc)[2][NT][4], int count) {
-    const int at = ring + (slot_out == 0 ? p.depth - 1 : slot_out - 1) * bytes;
-    float* red = reinterpret_cast<float*>(dynamic + at);
+// What both kernels' warps have: their ring and a tile's codes in it.
+template <int GROUP>
+struct Ring {
+  const Int4Args& p;
+  uint8_t* const base;    // of this warp
+  const int bytes;        // of a stage
+  const int lane;
+  const int row_bytes;
+  int slot_in = 0, slot_out = 0;
+
+  __device__ __forceinline__ Ring(const Int4Args& p_, uint8_t* base_, int bytes_)
+      : p(p_), base(base_), bytes(bytes_), lane(threadIdx.x % 32), row_bytes(p_.k / 2) {}
+
+  // This lane's codes, scales and zero points of a tile.
+  struct Tile {
+    const uint8_t *lo, *hi;     // codes of the tile's rows of the first and the second fragment
+    int64_t scales, zeros;      // elements
+  };
+  __device__ __forceinline__ Tile tile(int expert, int index) const {
+    const int r0 = p.swiglu ? index * (kRows / 2) : index * kRows, second = p.swiglu ? p.n / 2 : kRows / 2;
+    const bool both = p.swiglu || r0 + kRows / 2 < p.n;  // else the second fragment is the first again
+    Tile t;
+    t.lo = p.codes + (static_cast<int64_t>(expert) * p.n + r0 + 2 * (lane / 4)) * row_bytes + lane % 4 * 16;
+    t.hi = both ? t.lo + static_cast<int64_t>(second) * row_bytes : t.lo;
+    const int64_t meta = static_cast<int64_t>(expert) * (p.k / GROUP) * p.n + r0;
+    const int up = both ? second : 0;
+    t.scales = meta + (lane % 8 >= 4 ? up : 0) + lane % 4 * 4 + static_cast<int64_t>(lane / 8) * p.n;
+    t.zeros = meta + (lane % 4 >= 2 ? up : 0) + lane % 2 * 8 + static_cast<int64_t>(lane / 4) * p.n;
+    return t;
+  }
+  // Stage st of a tile into the next slot, whose address is returned.
+  __device__ __forceinline__ uint8_t* load(const Tile& t, int st) {
+    uint8_t* dst = base + slot_in * bytes;
+    const int k0 = st * kStageK, left = p.k - k0;
+    if (lane % 4 * 32 < left) {
+      // row j of lane group h stands at row 8 j + h: rows 2 h and 2 h + 1 of each fragment
+      const int h = lane / 4;
+      uint8_t* to = dst + h * kRowBytes + ((lane % 4 ^ unit_key(h)) << 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        cp_async_16(to + j * 8 * kRowBytes, (j < 2 ? t.lo : t.hi) + (k0 / 2 + (j & 1) * row_bytes));
+    }
+    // scales: 4 rows to a lane; zero points: 8
+    const int64_t before = static_cast<int64_t>(st * kGroups<GROUP>) * p.n;
+    if (lane / 8 < kGroups<GROUP> && lane / 8 * GROUP < left)
+      cp_async_16(dst + kScales + lane * 16, p.scales + t.scales + before);
+    if (p.zeros != nullptr && lane / 4 < kGroups<GROUP> && lane / 4 * GROUP < left)
+      cp_async_8(dst + kZeros<GROUP> + lane * 8, p.zeros + t.zeros + before);
+    return dst;
+  }
+  // Ends the loads into a slot (there may be none).
+  __device__ __forceinline__ void commit() {
+    cp_async_commit();
+    slot_in = slot_in + 1 == p.depth ? 0 : slot_in + 1;
+  }
+  // The oldest slot, landed for the whole warp, which has also read the one before it.
+  __device__ __forceinline__ const uint8_t* wait() {
+    cp_async_wait_pending(p.depth - 2);
+    __syncwarp();
+    const uint8_t* src = base + slot_out * bytes;
+    slot_out = slot_out + 1 == p.depth ? 0 : slot_out + 1;
+    return src;
+  }
+  // A tile's sums, [row of x][weight row], into the slot that was read last:
+  // nothing is loaded there before the next wait.
+  template <int NT>
+  __device__ __forceinline__ float* put(const Sums<NT>& acc, bool wide) {
+    float* red = reinterpret_cast<float*>(base + (slot_out == 0 ? p.depth - 1 : slot_out - 1) * bytes);
     __syncwarp();  // all lanes have read it
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      if (n > 0 && count <= 8) break;
+      if (n > 0 && !wide) break;
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        float* to = red + (n * 8 + 2 * q) * kRedStride + 16 * m + 2 * g;
-        *reinterpret_cast<float2*>(to) = make_float2(acc[m][n][0], acc[m][n][2]);
-        *reinterpret_cast<float2*>(to + kRedStride) = make_float2(acc[m][n][1], acc[m][n][3]);
+        float* to = red + (n * 8 + 2 * (lane & 3)) * kRedStride + 16 * m + 2 * (lane >> 2);
+        *reinterpret_cast<float2*>(to) = make_float2(acc.v[m][n][0], acc.v[m][n][2]);
+        *reinterpret_cast<float2*>(to + kRedStride) = make_float2(acc.v[m][n][1], acc.v[m][n][3]);
       }
     }
-    if (lane == 0) s.red[warp] = at;
     return red;
-  }
-  __device__ __forceinline__ void store(int64_t row, int col, float v) const {
-    if (p.out_f32)
-      static_cast<float*>(p.out)[row * p.ld_out + col] = v;
-    else
-      static_cast<uint16_t*>(p.out)[row * p.ld_out + col] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-  }
-
-  // ---------------------------------------------- each pair a row of its own
-  __device__ __forceinline__ void rows() {
-    ks = p.ks;
-    const int mine = warp % ks, first_warp = warp - mine;
-    const int from = blockIdx.x * (kWarps / ks) + warp / ks;
-    end = s.n_parts * tiles;
-    step = gridDim.x * (kWarps / ks);
-    start_row(in, from);
-    for (int i = 0; i < p.depth - 1; ++i) issue();
-    auto meet = [&]() {  // the warps that share a tile
-      if (ks > 1)
-        named_bar_sync(1 + warp / ks, ks * 32);
-      else
-        __syncwarp();
-    };
-    for (int sub = from; sub < end; sub += step) {
-      const int part = sub / tiles, tile = sub - part * tiles;
-      const int count = s.count[part], first = s.first[part];
-      float acc[2][NT][4];
-      clear(acc);
-      for (int st = mine; st < nst; st += ks) take(st, count, acc);
-      put_sums(acc, count);
-      meet();
-      for (int i = mine; i < count; i += ks) {
-        float v = 0.f;
-        for (int w = 0; w < ks; ++w)
-          v += reinterpret_cast<const float*>(dynamic + s.red[first_warp + w])[i * kRedStride + lane];
-        const int64_t row = s.pair[first + i];
-        if (p.swiglu) {
-          const float up = __shfl_down_sync(0xffffffffu, v, kRows / 2);
-          const int col = tile * (kRows / 2) + lane;
-          if (lane < kRows / 2) store(row, col, v / (1.f + expf(-v)) * up);
-        } else {
-          const int col = tile * kRows + lane;
-          if (col < p.n) store(row, col, v);
-        }
-      }
-      meet();
-    }
-    cp_async_wait_all();
-    // rows whose expert does not exist
-    const int cols = p.swiglu ? p.n / 2 : p.n;
-    for (int i = 0; i < p.pairs; ++i)
-      if (s.bad[i / 32] >> (i % 32) & 1u)
-        for (int c = blockIdx.x * F::kThreads + threadIdx.x; c < cols; c += gridDim.x * F::kThreads)
-          store(i, c, __int_as_float(0x7FC00000));
-  }
-
-  // ------------------------------------------- the weighted sum of a row's pairs
-  // The warps take a tile's parts in turn, or `ks` of them a part's stages:
-  // whichever leaves the busiest with the least (a part's end costs about a
-  // stage).
-  __device__ __forceinline__ void weighted() {
-    const int tokens = p.pairs / p.top;
-    float* all = reinterpret_cast<float*>(dynamic + kWarps * p.depth * bytes);  // [warp][row of x][weight row]
-    float* sums = all + warp * tokens * kRows;
-    int least = INT_MAX;
-    for (int k = 1; k <= kWarps && k <= nst; k *= 2) {
-      const int each = kWarps / k, load = (s.n_parts + each - 1) / each * ((nst + k - 1) / k + 1);
-      if (load < least) {
-        least = load;
-        ks = k;
-      }
-    }
-    end = tiles;
-    step = gridDim.x;
-    start_sum(in, blockIdx.x);
-    for (int i = 0; i < p.depth - 1; ++i) issue();
-    for (int sub = blockIdx.x; sub < end; sub += step) {
-      for (int t = 0; t < tokens; ++t) sums[t * kRows + lane] = 0.f;
-      for (int part = warp / ks; part < s.n_parts; part += kWarps / ks) {
-        const int count = s.count[part], first = s.first[part];
-        float acc[2][NT][4];
-        clear(acc);
-        for (int st = warp % ks; st < nst; st += ks) take(st, count, acc);
-        const float* red = put_sums(acc, count);
-        __syncwarp();
-        for (int i = 0; i < count; ++i) {
-          const int pair = s.pair[first + i];
-          float& v = sums[pair / p.top * kRows + lane];
-          v = fmaf(__ldg(p.w + pair), red[i * kRedStride + lane], v);
-        }
-        __syncwarp();
-      }
-      __syncthreads();
-      const int col = sub * kRows + lane;
-      for (int t = warp; t < tokens; t += kWarps) {
-        float v = 0.f;
-        for (int w = 0; w < kWarps; ++w) v += all[(w * tokens + t) * kRows + lane];
-        for (int i = t * p.top; i < (t + 1) * p.top; ++i)
-          if (s.bad[i / 32] >> (i % 32) & 1u) v = __int_as_float(0x7FC00000);
-        if (col < p.n) store(t, col, v);
-      }
-      __syncthreads();
-    }
-    cp_async_wait_all();
   }
 };
 
+__device__ __forceinline__ void store(const Int4Args& p, int64_t row, int col, float v) {
+  if (p.out_f32)
+    static_cast<float*>(p.out)[row * p.ld_out + col] = v;
+  else
+    static_cast<uint16_t*>(p.out)[row * p.ld_out + col] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+__device__ __forceinline__ bool is_bad(const Shared& s, int pair) { return s.bad[pair / 32] >> (pair % 32) & 1u; }
+
 // The parts: each expert's pairs in order, at most nx to a part.  masks:
 // scratch of kMaxExperts x kMaxPairs bits.
-template <class F>
-__device__ __forceinline__ void find_parts(const Int4Args& p, Shared<F::kWarps>& s, uint32_t* masks) {
+__device__ __forceinline__ void find_parts(const Int4Args& p, Shared& s, uint32_t* masks) {
   constexpr int kWordsOf = kMaxPairs / 32;
-  const int most = p.nx;
-  const int e = threadIdx.x, lane = e % 32, warp = e / 32;
+  const int e = threadIdx.x, lane = e % 32, warp = e / 32, most = p.nx;
   if (p.ids == nullptr) {
     if (e < p.pairs) s.pair[e] = s.row[e] = static_cast<uint8_t>(e);
     if (e < kWordsOf) s.bad[e] = 0u;
@@ -579,7 +393,7 @@ __device__ __forceinline__ void find_parts(const Int4Args& p, Shared<F::kWarps>&
     __syncthreads();
     return;
   }
-  for (int i = e; i < kMaxExperts * kWordsOf; i += F::kThreads) masks[i] = 0u;
+  for (int i = e; i < kMaxExperts * kWordsOf; i += kThreads) masks[i] = 0u;
   if (e < kWordsOf) s.bad[e] = 0u;
   __syncthreads();
   if (e < p.pairs) {
@@ -628,69 +442,473 @@ __device__ __forceinline__ void find_parts(const Int4Args& p, Shared<F::kWarps>&
   __syncthreads();
 }
 
-template <class F>
-__global__ void __launch_bounds__(F::kThreads, kWarpsOfSm / F::kWarps) int4_few_kernel(const Int4Args p) {
-  static_assert(F::kThreads >= kMaxExperts && F::kThreads >= kMaxPairs, "a thread per expert and per pair");
+// ------------------------------------------------ each pair a row of its own
+// Dynamic shared memory: the rings (and first the masks), the sums of a batch
+// of tiles where a cluster splits k, x, its scales.
+template <int GROUP, int NT, bool F8>
+struct RowsWorker {
+  static constexpr int kWords = GROUP / 32;
+  const Int4Args& p;
+  Shared& s;
+  uint8_t* const block;   // the dynamic array
+  Ring<GROUP> ring;
+  uint8_t* const x;       // [stage][word of a lane][row of x][quad's lane] x 16 bytes
+  float* const x_scales;  // [stage][row of x]
+  float* const sums;      // [tile of the batch][row of x][weight row]
+  const int lane, group, mine, groups;  // groups of ks warps; this warp's place in its own
+  const int tiles;        // of a matrix
+  int lo, hi;             // this block's (or cluster's) tiles of all parts
+  int s0, s1;             // its stages
+
+  // A walk over the group's tiles.  Segments end where the part or the batch does.
+  struct Place {
+    int sub, seg_end, st;
+    typename Ring<GROUP>::Tile tile;
+  };
+  Place in;
+
+  __device__ __forceinline__ RowsWorker(const Int4Args& p_, Shared& s_, uint8_t* smem)
+      : p(p_),
+        s(s_),
+        block(smem),
+        ring(p_, smem + threadIdx.x / 32 * p_.depth * kStage<GROUP>, kStage<GROUP>),
+        x(smem + kWarps * p_.depth * kStage<GROUP> + p_.batch * p_.nx * kRows * 4),
+        x_scales(reinterpret_cast<float*>(x + p_.slice * p_.nx * kXBytes)),
+        sums(reinterpret_cast<float*>(smem + kWarps * p_.depth * kStage<GROUP>)),
+        lane(threadIdx.x % 32),
+        group(threadIdx.x / 32 / p_.ks),
+        mine(threadIdx.x / 32 % p_.ks),
+        groups(kWarps / p_.ks),
+        tiles(((p_.swiglu ? p_.n / 2 : p_.n) + out_cols(p_) - 1) / out_cols(p_)) {
+    const int nst = (p.k + kStageK - 1) / kStageK;
+    const int rank = p.cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    s0 = min(nst, rank * p.slice);
+    s1 = min(nst, s0 + p.slice);
+    const int64_t total = static_cast<int64_t>(s.n_parts) * tiles;
+    const int at = blockIdx.x / p.cluster, of = gridDim.x / p.cluster;
+    lo = static_cast<int>(total * at / of);
+    hi = static_cast<int>(total * (at + 1) / of);
+  }
+  __device__ __forceinline__ static int out_cols(const Int4Args& p) { return p.swiglu ? kRows / 2 : kRows; }
+
+  __device__ __forceinline__ int segment_end(int from) const {
+    int end = min(hi, (from / tiles + 1) * tiles);
+    if (p.cluster > 1) end = min(end, lo + ((from - lo) / p.batch + 1) * p.batch);
+    return end;
+  }
+  __device__ __forceinline__ void settle(Place& a) const {  // onto a tile of this group, or to the end
+    while (a.sub >= a.seg_end && a.seg_end < hi) {
+      a.sub = a.seg_end + group;
+      a.seg_end = segment_end(a.seg_end);
+    }
+    if (a.sub >= a.seg_end || s0 + mine >= s1) {
+      a.sub = hi;
+      return;
+    }
+    a.st = s0 + mine;
+    const int part = a.sub / tiles;
+    a.tile = ring.tile(s.act[part], a.sub - part * tiles);
+  }
+  __device__ __forceinline__ void issue() {
+    if (in.sub < hi) {
+      ring.load(in.tile, in.st);
+      in.st += p.ks;
+      if (in.st >= s1) {
+        in.sub += groups;
+        settle(in);
+      }
+    }
+    ring.commit();
+  }
+
+  // The rows of x of a part, as operands.
+  __device__ __forceinline__ void load_x(int part) {
+    const int count = s.count[part], first = s.first[part];
+    const int units = min((s1 - s0) * (kStageK / 8), (p.k - s0 * kStageK) / 8);  // of 8 elements
+    for (int i = threadIdx.x; i < units * count; i += kThreads) {
+      const int t = i / units, u = i - t * units;
+      const int64_t from = s.row[first + t] * p.ld_x + s0 * kStageK + u * 8;
+      uint32_t b[4];
+      if constexpr (F8)
+        x_e4m3(__ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.x) + from)), b);
+      else
+        x_bf16(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + from)), b);
+      const int st = u / 16, r = u % 16 % (GROUP / 8), word = u % 16 / (GROUP / 8) * kWords + r % kWords, quad = r / kWords;
+      *reinterpret_cast<uint4*>(x + (((st * 4 + word) * p.nx + t) * 4 + quad) * 16) = make_uint4(b[0], b[1], b[2], b[3]);
+    }
+    if constexpr (F8)
+      for (int i = threadIdx.x; i < (s1 - s0) * count; i += kThreads) {
+        const int st = i / count, t = i - st * count;
+        x_scales[st * p.nx + t] = __ldg(p.x_scales + static_cast<int64_t>(s.row[first + t]) * ((p.k + 127) / 128) + s0 + st);
+      }
+  }
+
+  // A tile's result for one row of x, from the lanes' sums over k.
+  __device__ __forceinline__ void finish(int tile, int pair, float v) const {
+    if (p.swiglu) {
+      const float up = __shfl_down_sync(0xffffffffu, v, kRows / 2);
+      if (lane < kRows / 2) store(p, pair, tile * (kRows / 2) + lane, v / (1.f + expf(-v)) * up);
+    } else if (tile * kRows + lane < p.n) {
+      store(p, pair, tile * kRows + lane, v);
+    }
+  }
+
+  __device__ __forceinline__ void take(int st, int count, Sums<NT>& acc) {
+    const uint8_t* src = ring.wait();
+    issue();
+    const int g = lane >> 2, q = lane & 3;
+    const uint8_t* xs = x + (st - s0) * p.nx * kXBytes + q * 16;
+    const uint8_t* at[NT];
+    float scale[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      at[n] = xs + min(n * 8 + g, count - 1) * 64;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        scale[n][i] = F8 ? x_scales[(st - s0) * p.nx + min(n * 8 + 2 * q + i, count - 1)] : 1.f;
+    }
+    const int word = p.nx * 64;
+    add_stage<GROUP, NT, F8>(
+        src, (p.k - st * kStageK) / GROUP, p.zeros != nullptr, count > 8,
+        [&](int n, int i, uint32_t(&b)[4]) {
+          const uint4 e = *reinterpret_cast<const uint4*>(at[n] + i * word);
+          b[0] = e.x, b[1] = e.y, b[2] = e.z, b[3] = e.w;
+        },
+        scale, acc);
+  }
+
+  // The sums of a batch of tiles over the cluster's blocks; a tile's is finished by one of them.
+  __device__ __forceinline__ void join(int from, int to) {
+    cluster_sync();
+    const int rank = static_cast<int>(cluster_ctarank()), warp = threadIdx.x / 32;
+    const int count = s.count[0];  // (one part: its rows are all the matrix meets at once)
+    for (int i = warp; i < (to - from) * count; i += kWarps) {
+      const int b = i / count, t = i - b * count;
+      if (b % p.cluster != rank) continue;
+      const uint32_t at = smem_u32(sums + (b * p.nx + t) * kRows + lane);
+      float v = 0.f;
+      for (int r = 0; r < p.cluster; ++r) {
+        float w;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(w) : "r"(mapa_shared(at, r)) : "memory");
+        v += w;
+      }
+      const int part = (from + b) / tiles;
+      if (t < s.count[part]) finish(from + b - part * tiles, s.pair[s.first[part] + t], v);
+    }
+    cluster_sync();
+  }
+
+  __device__ __forceinline__ void run() {
+    in.sub = lo + group;
+    in.seg_end = segment_end(lo);
+    if (lo >= hi) in.seg_end = lo;
+    settle(in);
+    for (int i = 0; i < p.depth - 1; ++i) issue();
+    auto meet = [&]() {  // the warps that share a tile
+      if (p.ks > 1)
+        named_bar_sync(1 + group, p.ks * 32);
+      else
+        __syncwarp();
+    };
+    const int first_warp = group * p.ks;
+    for (int from = lo; from < hi;) {
+      const int part = from / tiles, to = segment_end(from);
+      const int count = s.count[part], first = s.first[part];
+      if (from == lo || from == part * tiles) load_x(part);
+      __syncthreads();
+      for (int sub = from + group; sub < to; sub += groups) {
+        Sums<NT> acc;
+        acc.clear();
+        for (int st = s0 + mine; st < s1; st += p.ks) take(st, count, acc);
+        const float* red = ring.put(acc, count > 8);
+        if (lane == 0) s.red[threadIdx.x / 32] = static_cast<int>(reinterpret_cast<const uint8_t*>(red) - block);
+        meet();
+        for (int t = mine; t < count; t += p.ks) {
+          float v = 0.f;
+          for (int w = 0; w < p.ks; ++w)
+            v += reinterpret_cast<const float*>(block + s.red[first_warp + w])[t * kRedStride + lane];
+          if (p.cluster > 1)
+            sums[((sub - lo) % p.batch * p.nx + t) * kRows + lane] = v;
+          else
+            finish(sub - part * tiles, s.pair[first + t], v);
+        }
+        meet();
+      }
+      __syncthreads();  // x may be replaced
+      if (p.cluster > 1 && (to == hi || (to - lo) % p.batch == 0)) join(lo + (to - 1 - lo) / p.batch * p.batch, to);
+      from = to;
+    }
+    cp_async_wait_all();
+    // rows whose expert does not exist
+    const int cols = p.swiglu ? p.n / 2 : p.n;
+    if (p.ids != nullptr)
+      for (int i = 0; i < p.pairs; ++i)
+        if (is_bad(s, i))
+          for (int c = blockIdx.x * kThreads + threadIdx.x; c < cols; c += gridDim.x * kThreads)
+            store(p, i, c, __int_as_float(0x7FC00000));
+  }
+};
+
+template <int GROUP, int NT, bool F8>
+__global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Int4Args p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Shared<F::kWarps> s;
-  // the warps' rings, and before they are filled the masks; behind them the weighted sums
-  find_parts<F>(p, s, reinterpret_cast<uint32_t*>(smem));
-  Worker<F> w(p, s, smem);
-  if constexpr (F::kWarps == 8)
-    w.rows();
-  else
-    w.weighted();
+  __shared__ Shared s;
+  find_parts(p, s, reinterpret_cast<uint32_t*>(smem));
+  RowsWorker<GROUP, NT, F8> w(p, s, smem);
+  w.run();
 }
 
-constexpr int kSmemOfSm = 228 * 1024, kSmemOfBlock = 227 * 1024;
-constexpr int kMaskBytes = kMaxExperts * kMaxPairs / 8;
+// --------------------------------------------- the weighted sum of a row's pairs
+// Dynamic shared memory: the rings (and first the masks), the warps' sums.
+template <int GROUP, bool F8>
+struct SumWorker {
+  static constexpr int kWords = GROUP / 32;
+  const Int4Args& p;
+  Shared& s;
+  Ring<GROUP> ring;
+  float* const all;       // [warp][row of out][weight row]
+  const int lane, warp, tokens, nst;
+  int ks = 1;             // warps that share a part
+  int tiles;
 
-template <class F>
-cudaError_t launch(Int4Args a, int num_sms, cudaStream_t st) {
-  auto kernel = int4_few_kernel<F>;
-  constexpr int kBlocks = kWarpsOfSm / F::kWarps;  // of an SM
-  const int stage = F::kWarps * F::stage(a.nx), fixed = static_cast<int>(sizeof(Shared<F::kWarps>)) + 1024;
-  const int sums = F::kWarps == 8 ? 0 : F::kWarps * (a.pairs / a.top) * kRows * 4;
-  const int most = std::min(kSmemOfSm / kBlocks - fixed, kSmemOfBlock - fixed + 1024);
-  a.depth = std::max(2, std::min(kMaxDepth, (most - sums) / stage));
-  const int smem = std::max(a.depth * stage + sums, kMaskBytes);
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  const int tile_out = a.swiglu ? kRows / 2 : kRows, cols = a.swiglu ? a.n / 2 : a.n;
-  const int64_t tiles = (cols + tile_out - 1) / tile_out;
-  const int64_t slots = static_cast<int64_t>(kBlocks) * num_sms;
-  a.ks = 1;
-  int64_t blocks = tiles;
-  if (F::kWarps == 8) {
-    const int stages = (a.k + F::SK - 1) / F::SK;
-    const int64_t parts = a.ids != nullptr ? std::min(a.pairs, a.n_experts) : 1;  // about
-    while (a.ks < F::kWarps && 2 * a.ks <= stages && parts * tiles * a.ks < slots * F::kWarps) a.ks *= 2;
-    const int64_t at_most = (a.ids != nullptr ? a.pairs : 1) * tiles;
-    blocks = (at_most * a.ks + F::kWarps - 1) / F::kWarps;
+  struct Place {
+    int tile, part, st;
+    typename Ring<GROUP>::Tile at;
+  };
+  Place in;
+
+  __host__ __device__ static constexpr int stage(int nx) {
+    return (kStage<GROUP> + nx * (kRingX<F8> + (F8 ? 4 : 0)) + 127) / 128 * 128;
   }
-  const int grid = static_cast<int>(blocks < slots ? blocks : slots);
-  return launch_kernel(kernel, dim3(grid), dim3(F::kThreads), static_cast<size_t>(smem), st, a);
+  __device__ __forceinline__ SumWorker(const Int4Args& p_, Shared& s_, uint8_t* smem)
+      : p(p_),
+        s(s_),
+        ring(p_, smem + threadIdx.x / 32 * p_.depth * stage(p_.nx), stage(p_.nx)),
+        all(reinterpret_cast<float*>(smem + kWarps * p_.depth * stage(p_.nx))),
+        lane(threadIdx.x % 32),
+        warp(threadIdx.x / 32),
+        tokens(p_.pairs / p_.top),
+        nst((p_.k + kStageK - 1) / kStageK),
+        tiles((p_.n + kRows - 1) / kRows) {
+    // The warps take a tile's parts in turn, or `ks` of them a part's stages:
+    // whichever leaves the busiest with the least (a part's end costs about a stage).
+    int least = INT_MAX;
+    for (int k = 1; k <= kWarps && k <= nst; k *= 2) {
+      const int each = kWarps / k, load = (s.n_parts + each - 1) / each * ((nst + k - 1) / k + 1);
+      if (load < least) {
+        least = load;
+        ks = k;
+      }
+    }
+  }
+  __device__ __forceinline__ void start(Place& a, int tile) const {
+    a.tile = tile;
+    a.part = warp / ks;
+    a.st = warp % ks;
+    if (a.part >= s.n_parts) a.tile = tiles;  // (in every tile)
+    if (a.tile < tiles) a.at = ring.tile(s.act[a.part], tile);
+  }
+  __device__ __forceinline__ void issue() {
+    if (in.tile < tiles) {
+      uint8_t* x = ring.load(in.at, in.st) + kStage<GROUP>;
+      // x: 8 elements to a lane, in the order in which the quads read them
+      const int count = s.count[in.part], first = s.first[in.part], k0 = in.st * kStageK;
+      const int u = lane % 16, r = u % (GROUP / 8);
+      const int at = u / (GROUP / 8) * (GROUP / 8) + r % kWords * 4 + r / kWords;
+      if (u * 8 < p.k - k0)
+        for (int t = lane / 16; t < count; t += 2) {
+          const int64_t from = s.row[first + t] * p.ld_x + k0 + u * 8;
+          if constexpr (F8)
+            cp_async_8(x + t * kRingX<F8> + at * 8, static_cast<const uint8_t*>(p.x) + from);
+          else
+            cp_async_16(x + t * kRingX<F8> + ((at ^ (t & 1) << 2) << 4), static_cast<const uint16_t*>(p.x) + from);
+        }
+      if constexpr (F8)
+        if (lane < count)
+          cp_async_4(x + p.nx * kRingX<F8> + lane * 4,
+                     p.x_scales + static_cast<int64_t>(s.row[first + lane]) * ((p.k + 127) / 128) + in.st);
+      in.st += ks;
+      if (in.st >= nst) {
+        in.st = warp % ks;
+        in.part += kWarps / ks;
+        if (in.part >= s.n_parts)
+          start(in, in.tile + gridDim.x);
+        else
+          in.at = ring.tile(s.act[in.part], in.tile);
+      }
+    }
+    ring.commit();
+  }
+  __device__ __forceinline__ void take(int st, int count, Sums<1>& acc) {
+    const uint8_t* src = ring.wait();
+    issue();
+    const int q = lane & 3, t = min(lane >> 2, count - 1);
+    const uint8_t* x = src + kStage<GROUP> + t * kRingX<F8>;
+    // 16-bit rows: where the units of even and of odd 64 bytes are
+    const uint8_t* at[2] = {x + q * (F8 ? 8 : 16) + (F8 ? 0 : (t & 1) << 6), x + q * (F8 ? 8 : 16) - (F8 ? 0 : (t & 1) << 6)};
+    float scale[1][2] = {{1.f, 1.f}};
+    if constexpr (F8) {
+      const float* xs = reinterpret_cast<const float*>(src + kStage<GROUP> + p.nx * kRingX<F8>);
+      scale[0][0] = xs[min(2 * q, count - 1)];
+      scale[0][1] = xs[min(2 * q + 1, count - 1)];
+    }
+    add_stage<GROUP, 1, F8>(
+        src, (p.k - st * kStageK) / GROUP, p.zeros != nullptr, false,
+        [&](int, int i, uint32_t(&b)[4]) {
+          if constexpr (F8)
+            x_e4m3(*reinterpret_cast<const uint2*>(at[0] + i * 32), b);
+          else
+            x_bf16(*reinterpret_cast<const uint4*>(at[i & 1] + i * 64), b);
+        },
+        scale, acc);
+  }
+  __device__ __forceinline__ void run() {
+    float* sums = all + warp * tokens * kRows;
+    start(in, blockIdx.x);
+    for (int i = 0; i < p.depth - 1; ++i) issue();
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+      for (int t = 0; t < tokens; ++t) sums[t * kRows + lane] = 0.f;
+      for (int part = warp / ks; part < s.n_parts; part += kWarps / ks) {
+        const int count = s.count[part], first = s.first[part];
+        Sums<1> acc;
+        acc.clear();
+        for (int st = warp % ks; st < nst; st += ks) take(st, count, acc);
+        const float* red = ring.put(acc, false);
+        __syncwarp();
+        for (int i = 0; i < count; ++i) {
+          const int pair = s.pair[first + i];
+          float& v = sums[pair / p.top * kRows + lane];
+          v = fmaf(__ldg(p.w + pair), red[i * kRedStride + lane], v);
+        }
+        __syncwarp();
+      }
+      __syncthreads();
+      const int col = tile * kRows + lane;
+      for (int t = warp; t < tokens; t += kWarps) {
+        float v = 0.f;
+        for (int w = 0; w < kWarps; ++w) v += all[(w * tokens + t) * kRows + lane];
+        for (int i = t * p.top; i < (t + 1) * p.top; ++i)
+          if (is_bad(s, i)) v = __int_as_float(0x7FC00000);
+        if (col < p.n) store(p, t, col, v);
+      }
+      __syncthreads();
+    }
+    cp_async_wait_all();
+  }
+};
+
+template <int GROUP, bool F8>
+__global__ void __launch_bounds__(kThreads, 1) sum_kernel(const Int4Args p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Shared s;
+  find_parts(p, s, reinterpret_cast<uint32_t*>(smem));
+  SumWorker<GROUP, F8> w(p, s, smem);
+  w.run();
+}
+
+// ------------------------------------------------------------------ launches
+constexpr int kSmem = 227 * 1024 - static_cast<int>(sizeof(Shared)) - 128;  // dynamic, of a block
+
+// Allows a kernel its shared memory, once per device (bits of `done`).
+template <typename K>
+cudaError_t allow_shared(K kernel, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+constexpr int kXRoom = 104 * 1024;  // of shared memory for x, at most: three stages a warp beside it
+
+template <int GROUP, int NT, bool F8>
+cudaError_t launch_rows(Int4Args a, int num_sms, cudaStream_t st) {
+  auto kernel = rows_kernel<GROUP, NT, F8>;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_shared(kernel, done);
+  if (e != cudaSuccess) return e;
+  const int out_cols = a.swiglu ? kRows / 2 : kRows, cols = a.swiglu ? a.n / 2 : a.n;
+  const int64_t tiles = (cols + out_cols - 1) / out_cols;
+  const int nst = (a.k + kStageK - 1) / kStageK;
+  const int stage_x = kXBytes + (F8 ? 4 : 0);  // of a row of x
+  const int64_t clusters = std::max(1, num_sms / a.cluster);
+  const int64_t at_most = (a.ids != nullptr ? a.pairs : (a.pairs + a.nx - 1) / a.nx) * tiles;
+  const int64_t about = (a.ids != nullptr ? std::min(a.pairs, a.n_experts) : (a.pairs + a.nx - 1) / a.nx) * tiles;
+  const int64_t of = std::min(at_most, clusters);
+  a.slice = (nst + a.cluster - 1) / a.cluster;
+  // Sixteen warps on one tile, or groups of them on several: what leaves the
+  // busiest with the least (a tile's end costs about two stages), with 256
+  // bytes of each row read together if there are that many.
+  const int64_t share = (about + of - 1) / of;
+  int64_t least = INT64_MAX;
+  int fewest = 1;
+  while (fewest < 4 && 2 * fewest <= a.slice) fewest *= 2;
+  for (int ks = fewest; ks == fewest || (ks <= kWarps && ks <= a.slice); ks *= 2) {
+    const int64_t load = (share + kWarps / ks - 1) / (kWarps / ks) * ((a.slice + ks - 1) / ks + 2);
+    if (load < least) {
+      least = load;
+      a.ks = ks;
+    }
+  }
+  const int x_bytes = a.slice * a.nx * stage_x;
+  a.batch = a.cluster > 1 ? static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(share, 24 * 1024 / (a.nx * kRows * 4)))) : 0;
+  const int rest = kSmem - x_bytes - a.batch * a.nx * kRows * 4;
+  a.depth = std::min(kMaxDepth, rest / (kWarps * kStage<GROUP>));
+  if (a.depth < 2) return cudaErrorInvalidValue;
+  const int smem = std::max(kSmem - rest + a.depth * kWarps * kStage<GROUP>, kMaskBytes);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(of * a.cluster), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = a.cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <int GROUP, bool F8>
+cudaError_t launch_sum(Int4Args a, int num_sms, cudaStream_t st) {
+  auto kernel = sum_kernel<GROUP, F8>;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_shared(kernel, done);
+  if (e != cudaSuccess) return e;
+  const int stage = kWarps * SumWorker<GROUP, F8>::stage(a.nx), sums = kWarps * (a.pairs / a.top) * kRows * 4;
+  a.depth = std::min(kMaxDepth, (kSmem - sums) / stage);
+  if (a.depth < 2) return cudaErrorInvalidValue;
+  const int tiles = (a.n + kRows - 1) / kRows;
+  return launch_kernel(kernel, dim3(std::min(tiles, num_sms)), dim3(kThreads),
+                       static_cast<size_t>(std::max(a.depth * stage + sums, kMaskBytes)), st, a);
 }
 
 template <int GROUP, bool F8>
 cudaError_t launch_form(Int4Args a, int num_sms, cudaStream_t s) {
   const int rows = a.pairs / a.top;  // of an expert, unless a row names it twice
-  // Parts of up to 16 rows where experts have more than 4 on average; else the few with more than 8 are taken twice.
-  // (The weighted sum's blocks have no room for 16 beside their sums.)
-  if (a.w == nullptr && rows > 8 && (a.ids == nullptr || a.pairs > 4 * a.n_experts)) {
-    a.nx = std::min(rows, 16);
-    return launch<Form<GROUP, 2, 128, F8, 8>>(a, num_sms, s);
-  }
+  a.cluster = 1;
   a.nx = std::min(rows, 8);
-  // twice as long stages while few rows of x stand beside the codes
-  if (a.w == nullptr) return a.nx <= 3 ? launch<Form<GROUP, 1, 256, F8, 8>>(a, num_sms, s) : launch<Form<GROUP, 1, 128, F8, 8>>(a, num_sms, s);
-  return a.nx <= 3 ? launch<Form<GROUP, 1, 256, F8, 16>>(a, num_sms, s) : launch<Form<GROUP, 1, 128, F8, 16>>(a, num_sms, s);
+  if (a.w != nullptr) return launch_sum<GROUP, F8>(a, num_sms, s);
+  // Parts of up to 16 rows where experts have more than 4 on average; else the few with more than 8 are taken twice.
+  if (rows > 8 && (a.ids == nullptr || a.pairs > 4 * a.n_experts)) a.nx = rows;
+  // x has to fit: one matrix splits k over a cluster (its blocks walk the same
+  // tiles, whatever is in memory), experts take fewer rows at a time
+  const int nst = (a.k + kStageK - 1) / kStageK, stage_x = kXBytes + (F8 ? 4 : 0);
+  auto fits = [&]() { return static_cast<int64_t>((nst + a.cluster - 1) / a.cluster) * a.nx * stage_x <= kXRoom; };
+  while (!fits() && a.ids == nullptr && a.cluster < kMaxCluster) a.cluster *= 2;
+  while (!fits() && a.nx > 1) a.nx = (a.nx + 1) / 2;
+  if (!fits()) return cudaErrorInvalidValue;
+  return a.nx > 8 ? launch_rows<GROUP, 2, F8>(a, num_sms, s) : launch_rows<GROUP, 1, F8>(a, num_sms, s);
 }
 
 template <int GROUP>
 cudaError_t launch_group(const Int4Args& a, int num_sms, cudaStream_t s) {
-  const bool f8 = a.x_scales != nullptr;
-  return f8 ? launch_form<GROUP, true>(a, num_sms, s) : launch_form<GROUP, false>(a, num_sms, s);
+  return a.x_scales != nullptr ? launch_form<GROUP, true>(a, num_sms, s) : launch_form<GROUP, false>(a, num_sms, s);
 }
 
 }  // namespace

@@ -428,9 +428,13 @@ struct Int4Args {
   int64_t ld_out;
   int32_t out_f32;
   int32_t* status;
-  int32_t nx;          // set by the launch: rows of x that a stage has room for,
-  int32_t ks;          //   warps that share a tile, stages of a warp's ring
-  int32_t depth;
+  // set by the launch:
+  int32_t nx;          // rows of x in a part, at most
+  int32_t ks;          // warps that share a tile
+  int32_t depth;       // stages of a warp's ring
+  int32_t cluster;     // blocks that split k,
+  int32_t slice;       //   stages of each,
+  int32_t batch;       //   tiles whose sums they join at once
 };
 cudaError_t launch_int4_few(int group, const Int4Args& a, int num_sms, cudaStream_t s);
 

@@ -50,8 +50,8 @@ def test_header_declares_what_the_library_exports(lib):
     raw = ctypes.CDLL(cb.LIB_PATH)
     assert all(hasattr(raw, name) for name in declared)
     enums = dict(re.findall(r"\b(CB_(?:SCORE|GROUP)_\w+)\s*=\s*(\d+)", header()))
-    enums.update(re.findall(r"#define (CB_(?:NORM|FP8|ROUTE)_\w+)\s+(\d+)", header()))
-    assert len(enums) == 7 and all(getattr(cb, n) == int(v) for n, v in enums.items()), enums
+    enums.update(re.findall(r"#define (CB_(?:NORM|FP8|ROUTE|INT4)_\w+)\s+(\d+)", header()))
+    assert len(enums) == 8 and all(getattr(cb, n) == int(v) for n, v in enums.items()), enums
     assert cb.CB_INT4_MAX_ROWS == cb.CB_MOE_MAX_FEW
 
 
@@ -133,7 +133,7 @@ def test_int4_refuses_bad_arguments_before_cuda(lib):
                dict(ids=0x500002, n_experts=8), dict(out=0x400001), dict(ld_x=260), dict(status=0x700002)):
         assert cb.cb_int4_matmul_few(int4_args(**kw)) == cb.CB_ERR_ALIGNMENT, kw
     for kw in (dict(n_tokens=17), dict(by, n_experts=257), dict(by, top_k=17), dict(n=(1 << 24) + 16, ld_out=1 << 25),
-               dict(k=1 << 25, ld_x=1 << 25), dict(ld_out=1 << 50)):
+               dict(k=1 << 25, ld_x=1 << 25), dict(k=393216 + 64, ld_x=1 << 20), dict(by, k=49152 + 64, ld_x=1 << 16), dict(ld_out=1 << 50)):
         assert cb.cb_int4_matmul_few(int4_args(**kw)) == cb.CB_ERR_UNSUPPORTED, kw
     assert cb.cb_int4_matmul_few(int4_args(n_tokens=0, x=None, codes=None, scales=None, out=None)) == cb.CB_OK
 
@@ -608,6 +608,49 @@ def test_int4_by_expert(group, kind, experts, top, n, k):
         check_int4(x, m, ids=ids, weights=w, dtype=F32)
         check_int4(slots, m, ids=ids, weights=w)
         check_int4(slots, m, ids=ids, dtype=F32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,k,group,kind,rows", [(80, 16384, 128, "bf16", (16, 9, 3)), (4128, 14336, 64, "fp8", (16, 8)),
+                                                 (48, 65536, 64, "fp8", (5, 16)), (32, 53248, 32, "bf16", (16, 1)), (16, 393216, 128, "bf16", (2,))])
+def test_int4_long_rows(n, k, group, kind, rows):
+    """Rows of x that several blocks share."""
+    g = gen(n)
+    m = int4_weights(g, n, k, group)
+    for r in rows:
+        x = randn(g, r, k, dtype=BF16) if kind == "bf16" else fp8_rows(g, r, k)
+        check_int4(x, m, dtype=F32)
+        if n % 32 == 0:
+            check_int4(x, m, swiglu=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("experts,k,group", [(3, 16384, 128), (2, 49152, 32)])
+def test_int4_long_rows_by_expert(experts, k, group):
+    g = gen(experts)
+    m = int4_weights(g, 64, k, group, experts)
+    for rows, top in ((16, 2), (3, 1)):
+        ids = torch.randint(0, experts, (rows, top), generator=g, device="cuda", dtype=torch.int32)
+        x = randn(g, rows, k, dtype=BF16)
+        check_int4(x, m, ids=ids)
+        check_int4(x, m, ids=ids, swiglu=True)
+        check_int4(x, m, ids=ids, weights=randn(g, rows, top), dtype=F32)
+
+
+@pytest.mark.gpu
+def test_int4_sizes_of_x():
+    """Large and small elements, up to the documented limits."""
+    g = gen(14)
+    m = int4_weights(g, 64, 512, 64)
+    for power in (-30, -10, 0, 20, 50):
+        check_int4((randn(g, 5, 512) * 2.0 ** power).to(BF16), m, dtype=F32)
+    x = randn(g, 3, 512, dtype=BF16)
+    x[1] = x[1] * 2.0 ** -100          # far below what can be told from 0
+    got = cb.int4_matmul_few(x, m, dtype=F32)
+    assert (got[1].abs() <= 512 * 15 * 0.02 * 2.0 ** -56).all()
+    x[1, 7] = 2.0 ** 100
+    got = cb.int4_matmul_few(x, m, dtype=F32)
+    assert not got[1].isfinite().any() and got[[0, 2]].isfinite().all()
 
 
 @pytest.mark.gpu
