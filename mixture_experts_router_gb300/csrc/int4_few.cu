@@ -55,6 +55,7 @@
 #include <algorithm>
 #include <atomic>
 #include <climits>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -71,7 +72,7 @@ constexpr int kRowBytes = kStageK / 2;
 constexpr int kMaxPairs = 256;       // (row of x, slot)
 constexpr int kMaxExperts = 256;
 constexpr int kRedStride = 36;       // floats: the fragments' stores meet no bank twice
-constexpr int kMaxDepth = 6;
+constexpr int kMaxDepth = 5;
 constexpr int kMaxCluster = 8;
 constexpr int kXBytes = 2 * kStageK; // of a row of x in a stage, as MMA operands
 constexpr int kMaskBytes = kMaxExperts * kMaxPairs / 8;
@@ -91,12 +92,14 @@ constexpr int kRingX = F8 ? kStageK + 32 : 2 * kStageK;
 
 struct Shared {
   uint8_t pair[kMaxPairs];      // pairs by expert, then in order,
-  uint8_t row[kMaxPairs];       //   and their rows of x
+  uint8_t row[kMaxPairs];       //   their rows of x,
+  uint8_t token[kMaxPairs];     //   rows of ids
+  float w[kMaxPairs];           //   and weights
   int16_t act[kMaxPairs];       // parts: their expert,
   int16_t first[kMaxPairs];     //   first entry of `pair`
   uint8_t count[kMaxPairs];     //   and number of them
   uint32_t bad[kMaxPairs / 32]; // pairs whose expert does not exist
-  int red[kWarps];              // where a warp has its sums of a tile, in the dynamic array
+  int red[kWarps];              // where a warp has its sums of a tile, floats of the dynamic array
   int warp_parts[kMaxExperts / 32];
   int n_parts;
 };
@@ -110,13 +113,14 @@ __device__ __forceinline__ void cp_async_8(void* dst, const void* src) {
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All but the n newest groups have landed.
 __device__ __forceinline__ void cp_async_wait_pending(int n) {
-  switch (n) {
-    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-  }
+  if (n == 1)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else if (n == 0)
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (n == 2)
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
 
 template <bool F8>
@@ -200,7 +204,7 @@ struct Sums {  // m16n8 fragments: [fragment][n-tile]
 // operands for this lane's i-th word of codes.  wide: the second n-tile too.
 // x_scale: of the lane's two columns of each n-tile.
 template <int GROUP, int NT, bool F8, typename Fetch>
-__device__ __forceinline__ void add_stage(const uint8_t* stage, int groups, bool has_zeros, bool wide, Fetch&& fetch,
+__device__ __forceinline__ void add_stage(const uint8_t* stage, int groups, bool wide, Fetch&& fetch,
                                           const float (&x_scale)[NT][2], Sums<NT>& acc) {
   constexpr int kWords = GROUP / 32;  // of a thread, row and group
   const int g = threadIdx.x % 32 >> 2, q = threadIdx.x & 3;
@@ -258,8 +262,7 @@ __device__ __forceinline__ void add_stage(const uint8_t* stage, int groups, bool
       float2 sc = *reinterpret_cast<const float2*>(stage + kScales + (gi * kRows + m * 16 + 2 * g) * 4);
       sc.x *= kUnit<F8>;
       sc.y *= kUnit<F8>;
-      uint32_t z = 0x0808u;
-      if (has_zeros) z = *reinterpret_cast<const uint16_t*>(stage + kZeros<GROUP> + gi * kRows + m * 16 + 2 * g);
+      const uint32_t z = *reinterpret_cast<const uint16_t*>(stage + kZeros<GROUP> + gi * kRows + m * 16 + 2 * g);
       // 2^23 + z as a float's bits, less 2^23
       const float z0 = __uint_as_float(__byte_perm(z, 0x4B000000u, 0x7650)) - 8388608.f;
       const float z1 = __uint_as_float(__byte_perm(z, 0x4B000000u, 0x7651)) - 8388608.f;
@@ -284,87 +287,79 @@ __device__ __forceinline__ void add_stage(const uint8_t* stage, int groups, bool
   }
 }
 
-// What both kernels' warps have: their ring and a tile's codes in it.
+// What both kernels' warps have: their ring and the tile whose codes go into it.
 template <int GROUP>
 struct Ring {
   const Int4Args& p;
-  uint8_t* const base;    // of this warp
+  uint8_t *const base, *const end;  // of this warp
   const int bytes;        // of a stage
   const int lane;
-  const int row_bytes;
-  int slot_in = 0, slot_out = 0;
+  uint8_t *in, *out;      // the slots to be filled and to be read next
 
   __device__ __forceinline__ Ring(const Int4Args& p_, uint8_t* base_, int bytes_)
-      : p(p_), base(base_), bytes(bytes_), lane(threadIdx.x % 32), row_bytes(p_.k / 2) {}
+      : p(p_), base(base_), end(base_ + p_.depth * bytes_), bytes(bytes_), lane(threadIdx.x % 32), in(base_), out(base_) {
+    if (p.zeros == nullptr)  // 8 everywhere, and nothing loaded over it
+      for (uint8_t* slot = base; slot < end; slot += bytes)
+        for (int i = lane; i < kGroups<GROUP> * kRows / 4; i += 32)
+          *reinterpret_cast<uint32_t*>(slot + kZeros<GROUP> + i * 4) = 0x08080808u;
+  }
 
-  // This lane's codes, scales and zero points of a tile.
+  // This lane's codes, scales and zero points of a tile's next stage.
   struct Tile {
-    const uint8_t *lo, *hi;     // codes of the tile's rows of the first and the second fragment
-    int64_t scales, zeros;      // elements
+    const uint8_t* codes[4];
+    const float* scales;
+    const uint8_t* zeros;
   };
-  __device__ __forceinline__ Tile tile(int expert, int index) const {
+  __device__ __forceinline__ Tile tile(int expert, int index, int st) const {
     const int r0 = p.swiglu ? index * (kRows / 2) : index * kRows, second = p.swiglu ? p.n / 2 : kRows / 2;
-    const bool both = p.swiglu || r0 + kRows / 2 < p.n;  // else the second fragment is the first again
+    const int up = p.swiglu || r0 + kRows / 2 < p.n ? second : 0;  // without a second fragment: the first again
+    const int row_bytes = p.k / 2;
     Tile t;
-    t.lo = p.codes + (static_cast<int64_t>(expert) * p.n + r0 + 2 * (lane / 4)) * row_bytes + lane % 4 * 16;
-    t.hi = both ? t.lo + static_cast<int64_t>(second) * row_bytes : t.lo;
-    const int64_t meta = static_cast<int64_t>(expert) * (p.k / GROUP) * p.n + r0;
-    const int up = both ? second : 0;
-    t.scales = meta + (lane % 8 >= 4 ? up : 0) + lane % 4 * 4 + static_cast<int64_t>(lane / 8) * p.n;
-    t.zeros = meta + (lane % 4 >= 2 ? up : 0) + lane % 2 * 8 + static_cast<int64_t>(lane / 4) * p.n;
+    t.codes[0] = p.codes + (static_cast<int64_t>(expert) * p.n + r0 + 2 * (lane / 4)) * row_bytes + lane % 4 * 16 + st * kRowBytes;
+    t.codes[1] = t.codes[0] + row_bytes;
+    t.codes[2] = t.codes[0] + static_cast<int64_t>(up) * row_bytes;
+    t.codes[3] = t.codes[2] + row_bytes;
+    const int64_t meta = (static_cast<int64_t>(expert) * (p.k / GROUP) + st * kGroups<GROUP>) * p.n + r0;
+    t.scales = p.scales + meta + (lane % 8 >= 4 ? up : 0) + lane % 4 * 4 + static_cast<int64_t>(lane / 8) * p.n;
+    t.zeros = p.zeros + meta + (lane % 4 >= 2 ? up : 0) + lane % 2 * 8 + static_cast<int64_t>(lane / 4) * p.n;
     return t;
   }
-  // Stage st of a tile into the next slot, whose address is returned.
-  __device__ __forceinline__ uint8_t* load(const Tile& t, int st) {
-    uint8_t* dst = base + slot_in * bytes;
-    const int k0 = st * kStageK, left = p.k - k0;
+  // A tile's stage into the next slot: `left` elements of a row from it on; t goes on by `step` stages.
+  __device__ __forceinline__ void load(Tile& t, int left, int step) {
+    // row j of lane group h stands at row 8 j + h: rows 2 h and 2 h + 1 of each fragment
+    const int h = lane / 4;
+    uint8_t* to = in + h * kRowBytes + ((lane % 4 ^ unit_key(h)) << 4);
     if (lane % 4 * 32 < left) {
-      // row j of lane group h stands at row 8 j + h: rows 2 h and 2 h + 1 of each fragment
-      const int h = lane / 4;
-      uint8_t* to = dst + h * kRowBytes + ((lane % 4 ^ unit_key(h)) << 4);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        cp_async_16(to + j * 8 * kRowBytes, (j < 2 ? t.lo : t.hi) + (k0 / 2 + (j & 1) * row_bytes));
+      for (int j = 0; j < 4; ++j) cp_async_16(to + j * 8 * kRowBytes, t.codes[j]);
     }
     // scales: 4 rows to a lane; zero points: 8
-    const int64_t before = static_cast<int64_t>(st * kGroups<GROUP>) * p.n;
-    if (lane / 8 < kGroups<GROUP> && lane / 8 * GROUP < left)
-      cp_async_16(dst + kScales + lane * 16, p.scales + t.scales + before);
-    if (p.zeros != nullptr && lane / 4 < kGroups<GROUP> && lane / 4 * GROUP < left)
-      cp_async_8(dst + kZeros<GROUP> + lane * 8, p.zeros + t.zeros + before);
-    return dst;
+    if (lane < kGroups<GROUP> * 8 && lane / 8 * GROUP < left) cp_async_16(in + kScales + lane * 16, t.scales);
+    if (p.zeros != nullptr && lane < kGroups<GROUP> * 4 && lane / 4 * GROUP < left)
+      cp_async_8(in + kZeros<GROUP> + lane * 8, t.zeros);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) t.codes[j] += step * kRowBytes;
+    const int64_t meta = static_cast<int64_t>(step * kGroups<GROUP>) * p.n;
+    t.scales += meta;
+    t.zeros += meta;
   }
   // Ends the loads into a slot (there may be none).
   __device__ __forceinline__ void commit() {
     cp_async_commit();
-    slot_in = slot_in + 1 == p.depth ? 0 : slot_in + 1;
+    in += bytes;
+    if (in == end) in = base;
   }
   // The oldest slot, landed for the whole warp, which has also read the one before it.
   __device__ __forceinline__ const uint8_t* wait() {
     cp_async_wait_pending(p.depth - 2);
     __syncwarp();
-    const uint8_t* src = base + slot_out * bytes;
-    slot_out = slot_out + 1 == p.depth ? 0 : slot_out + 1;
+    const uint8_t* src = out;
+    out += bytes;
+    if (out == end) out = base;
     return src;
   }
-  // A tile's sums, [row of x][weight row], into the slot that was read last:
-  // nothing is loaded there before the next wait.
-  template <int NT>
-  __device__ __forceinline__ float* put(const Sums<NT>& acc, bool wide) {
-    float* red = reinterpret_cast<float*>(base + (slot_out == 0 ? p.depth - 1 : slot_out - 1) * bytes);
-    __syncwarp();  // all lanes have read it
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if (n > 0 && !wide) break;
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        float* to = red + (n * 8 + 2 * (lane & 3)) * kRedStride + 16 * m + 2 * (lane >> 2);
-        *reinterpret_cast<float2*>(to) = make_float2(acc.v[m][n][0], acc.v[m][n][2]);
-        *reinterpret_cast<float2*>(to + kRedStride) = make_float2(acc.v[m][n][1], acc.v[m][n][3]);
-      }
-    }
-    return red;
-  }
+  // The slot that was read last: nothing is loaded there before the next wait.
+  __device__ __forceinline__ float* used() const { return reinterpret_cast<float*>((out == base ? end : out) - bytes); }
 };
 
 __device__ __forceinline__ void store(const Int4Args& p, int64_t row, int col, float v) {
@@ -434,17 +429,41 @@ __device__ __forceinline__ void find_parts(const Int4Args& p, Shared& s, uint32_
     for (int i = 0; i < kWordsOf; ++i)
       for (uint32_t m = mine[i]; m != 0u; m &= m - 1u) {
         const int pair = i * 32 + __ffs(m) - 1;
+        const int token = pair / p.top;
         s.pair[at] = static_cast<uint8_t>(pair);
-        s.row[at++] = static_cast<uint8_t>(p.x_per_slot ? pair : pair / p.top);
+        s.token[at] = static_cast<uint8_t>(token);
+        s.row[at] = static_cast<uint8_t>(p.x_per_slot ? pair : token);
+        if (p.w != nullptr) s.w[at] = __ldg(p.w + pair);
+        ++at;
       }
     if (e == kMaxExperts - 1) s.n_parts = base + parts;
   }
   __syncthreads();
 }
 
+// A tile's sums, [row of x][weight row].
+template <int NT>
+__device__ __forceinline__ void put_sums(const Sums<NT>& acc, int count, float* red) {
+  const int g = threadIdx.x % 32 >> 2, q = threadIdx.x & 3;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = n * 8 + 2 * q + i;
+      if (t >= count) continue;
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        *reinterpret_cast<float2*>(red + t * kRedStride + 16 * m + 2 * g) = make_float2(acc.v[m][n][i], acc.v[m][n][2 + i]);
+    }
+}
+
 // ------------------------------------------------ each pair a row of its own
-// Dynamic shared memory: the rings (and first the masks), the sums of a batch
-// of tiles where a cluster splits k, x, its scales.
+// Dynamic shared memory: the rings (and first the masks), the warps' sums of
+// two tiles, those of a batch of tiles where a cluster splits k, x, its scales.
+template <int NT>
+constexpr int kRedRows = NT == 1 ? 2 * kWarps * kRedStride : 0;  // floats of the warps' sums, for a row of x
+constexpr int kBatchBytes = 8 * 1024;                            // of a batch's sums, about
+
 template <int GROUP, int NT, bool F8>
 struct RowsWorker {
   static constexpr int kWords = GROUP / 32;
@@ -455,6 +474,7 @@ struct RowsWorker {
   uint8_t* const x;       // [stage][word of a lane][row of x][quad's lane] x 16 bytes
   float* const x_scales;  // [stage][row of x]
   float* const sums;      // [tile of the batch][row of x][weight row]
+  float* const reds;      // [turn][warp][row of x][weight row]
   const int lane, group, mine, groups;  // groups of ks warps; this warp's place in its own
   const int tiles;        // of a matrix
   int lo, hi;             // this block's (or cluster's) tiles of all parts
@@ -472,9 +492,10 @@ struct RowsWorker {
         s(s_),
         block(smem),
         ring(p_, smem + threadIdx.x / 32 * p_.depth * kStage<GROUP>, kStage<GROUP>),
-        x(smem + kWarps * p_.depth * kStage<GROUP> + p_.batch * p_.nx * kRows * 4),
+        x(smem + kWarps * p_.depth * kStage<GROUP> + (p_.batch * kRows + kRedRows<NT>) * p_.nx * 4),
         x_scales(reinterpret_cast<float*>(x + p_.slice * p_.nx * kXBytes)),
         sums(reinterpret_cast<float*>(smem + kWarps * p_.depth * kStage<GROUP>)),
+        reds(sums + p_.batch * p_.nx * kRows),
         lane(threadIdx.x % 32),
         group(threadIdx.x / 32 / p_.ks),
         mine(threadIdx.x / 32 % p_.ks),
@@ -507,11 +528,11 @@ struct RowsWorker {
     }
     a.st = s0 + mine;
     const int part = a.sub / tiles;
-    a.tile = ring.tile(s.act[part], a.sub - part * tiles);
+    a.tile = ring.tile(s.act[part], a.sub - part * tiles, a.st);
   }
   __device__ __forceinline__ void issue() {
     if (in.sub < hi) {
-      ring.load(in.tile, in.st);
+      ring.load(in.tile, p.k - in.st * kStageK, p.ks);
       in.st += p.ks;
       if (in.st >= s1) {
         in.sub += groups;
@@ -525,16 +546,30 @@ struct RowsWorker {
   __device__ __forceinline__ void load_x(int part) {
     const int count = s.count[part], first = s.first[part];
     const int units = min((s1 - s0) * (kStageK / 8), (p.k - s0 * kStageK) / 8);  // of 8 elements
-    for (int i = threadIdx.x; i < units * count; i += kThreads) {
-      const int t = i / units, u = i - t * units;
-      const int64_t from = s.row[first + t] * p.ld_x + s0 * kStageK + u * 8;
-      uint32_t b[4];
-      if constexpr (F8)
-        x_e4m3(__ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.x) + from)), b);
-      else
-        x_bf16(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + from)), b);
-      const int st = u / 16, r = u % 16 % (GROUP / 8), word = u % 16 / (GROUP / 8) * kWords + r % kWords, quad = r / kWords;
-      *reinterpret_cast<uint4*>(x + (((st * 4 + word) * p.nx + t) * 4 + quad) * 16) = make_uint4(b[0], b[1], b[2], b[3]);
+    // a warp takes kBatch x 32 units of a row at a time, their loads together
+    constexpr int kBatch = 8;
+    using Unit = std::conditional_t<F8, uint2, uint4>;
+    const int blocks = (units + kBatch * 32 - 1) / (kBatch * 32);
+    for (int i = threadIdx.x / 32; i < blocks * count; i += kWarps) {
+      const int t = i / blocks, u0 = (i - t * blocks) * kBatch * 32 + lane;
+      const Unit* from = reinterpret_cast<const Unit*>(static_cast<const uint8_t*>(p.x) +
+                                                       (s.row[first + t] * p.ld_x + s0 * kStageK) * (F8 ? 1 : 2));
+      Unit e[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (u0 + j * 32 < units) e[j] = __ldg(from + u0 + j * 32);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int u = u0 + j * 32;
+        if (u >= units) break;
+        uint32_t b[4];
+        if constexpr (F8)
+          x_e4m3(e[j], b);
+        else
+          x_bf16(e[j], b);
+        const int st = u / 16, r = u % 16 % (GROUP / 8), word = u % 16 / (GROUP / 8) * kWords + r % kWords, quad = r / kWords;
+        *reinterpret_cast<uint4*>(x + (((st * 4 + word) * p.nx + t) * 4 + quad) * 16) = make_uint4(b[0], b[1], b[2], b[3]);
+      }
     }
     if constexpr (F8)
       for (int i = threadIdx.x; i < (s1 - s0) * count; i += kThreads) {
@@ -569,7 +604,7 @@ struct RowsWorker {
     }
     const int word = p.nx * 64;
     add_stage<GROUP, NT, F8>(
-        src, (p.k - st * kStageK) / GROUP, p.zeros != nullptr, count > 8,
+        src, (p.k - st * kStageK) / GROUP, count > 8,
         [&](int n, int i, uint32_t(&b)[4]) {
           const uint4 e = *reinterpret_cast<const uint4*>(at[n] + i * word);
           b[0] = e.x, b[1] = e.y, b[2] = e.z, b[3] = e.w;
@@ -611,6 +646,7 @@ struct RowsWorker {
         __syncwarp();
     };
     const int first_warp = group * p.ks;
+    int turn = 0;
     for (int from = lo; from < hi;) {
       const int part = from / tiles, to = segment_end(from);
       const int count = s.count[part], first = s.first[part];
@@ -620,19 +656,29 @@ struct RowsWorker {
         Sums<NT> acc;
         acc.clear();
         for (int st = s0 + mine; st < s1; st += p.ks) take(st, count, acc);
-        const float* red = ring.put(acc, count > 8);
-        if (lane == 0) s.red[threadIdx.x / 32] = static_cast<int>(reinterpret_cast<const uint8_t*>(red) - block);
+        // the warps' sums: two sets in turn, so that a tile's are read while the next one's are written
+        // (with more than 8 rows in the slot just read, which no one loads into meanwhile)
+        float* red = reds + (turn * kWarps + threadIdx.x / 32) * p.nx * kRedStride;
+        turn ^= 1;
+        if constexpr (NT > 1) {
+          red = ring.used();
+          __syncwarp();  // all lanes have read it
+        }
+        put_sums(acc, count, red);
+        if (lane == 0) s.red[threadIdx.x / 32] = static_cast<int>(red - reinterpret_cast<float*>(block));
         meet();
-        for (int t = mine; t < count; t += p.ks) {
+        // another warp each time, where there are fewer rows than warps
+        for (int t = (mine - (sub - from) / groups) & (p.ks - 1); t < count; t += p.ks) {
           float v = 0.f;
-          for (int w = 0; w < p.ks; ++w)
-            v += reinterpret_cast<const float*>(block + s.red[first_warp + w])[t * kRedStride + lane];
+          const float* all = reinterpret_cast<const float*>(block) + t * kRedStride + lane;
+#pragma unroll 4
+          for (int w = 0; w < p.ks; ++w) v += all[s.red[first_warp + w]];
           if (p.cluster > 1)
             sums[((sub - lo) % p.batch * p.nx + t) * kRows + lane] = v;
           else
             finish(sub - part * tiles, s.pair[first + t], v);
         }
-        meet();
+        if constexpr (NT > 1) meet();
       }
       __syncthreads();  // x may be replaced
       if (p.cluster > 1 && (to == hi || (to - lo) % p.batch == 0)) join(lo + (to - 1 - lo) / p.batch * p.batch, to);
@@ -668,11 +714,12 @@ struct SumWorker {
   Ring<GROUP> ring;
   float* const all;       // [warp][row of out][weight row]
   const int lane, warp, tokens, nst;
-  int ks = 1;             // warps that share a part
-  int tiles;
+  const int tiles;
+  int lo, hi;             // of the stages of all parts, one after the other: this warp's
 
   struct Place {
     int tile, part, st;
+    int64_t x;
     typename Ring<GROUP>::Tile at;
   };
   Place in;
@@ -690,34 +737,35 @@ struct SumWorker {
         tokens(p_.pairs / p_.top),
         nst((p_.k + kStageK - 1) / kStageK),
         tiles((p_.n + kRows - 1) / kRows) {
-    // The warps take a tile's parts in turn, or `ks` of them a part's stages:
-    // whichever leaves the busiest with the least (a part's end costs about a stage).
-    int least = INT_MAX;
-    for (int k = 1; k <= kWarps && k <= nst; k *= 2) {
-      const int each = kWarps / k, load = (s.n_parts + each - 1) / each * ((nst + k - 1) / k + 1);
-      if (load < least) {
-        least = load;
-        ks = k;
-      }
-    }
+    const int64_t total = static_cast<int64_t>(s.n_parts) * nst;
+    lo = static_cast<int>(total * warp / kWarps);
+    hi = static_cast<int>(total * (warp + 1) / kWarps);
   }
   __device__ __forceinline__ void start(Place& a, int tile) const {
-    a.tile = tile;
-    a.part = warp / ks;
-    a.st = warp % ks;
-    if (a.part >= s.n_parts) a.tile = tiles;  // (in every tile)
-    if (a.tile < tiles) a.at = ring.tile(s.act[a.part], tile);
+    a.tile = lo < hi ? tile : tiles;
+    a.part = lo / nst;
+    a.st = lo - a.part * nst;
+    if (a.tile < tiles) at_part(a);
+  }
+  __device__ __forceinline__ void at_part(Place& a) const {
+    a.at = ring.tile(s.act[a.part], a.tile, a.st);
+    a.x = x_of(a.part, lane / 16) + a.st * kStageK;
+  }
+  // this lane's elements of the first stage of a part's row t, as an index into x
+  __device__ __forceinline__ int64_t x_of(int part, int t) const {
+    return s.row[s.first[part] + min(t, s.count[part] - 1)] * p.ld_x + lane % 16 * 8;
   }
   __device__ __forceinline__ void issue() {
     if (in.tile < tiles) {
-      uint8_t* x = ring.load(in.at, in.st) + kStage<GROUP>;
       // x: 8 elements to a lane, in the order in which the quads read them
-      const int count = s.count[in.part], first = s.first[in.part], k0 = in.st * kStageK;
+      uint8_t* x = ring.in + kStage<GROUP>;
+      const int count = s.count[in.part], left = p.k - in.st * kStageK;
       const int u = lane % 16, r = u % (GROUP / 8);
       const int at = u / (GROUP / 8) * (GROUP / 8) + r % kWords * 4 + r / kWords;
-      if (u * 8 < p.k - k0)
+      int64_t from = in.x;
+      if (u * 8 < left)
         for (int t = lane / 16; t < count; t += 2) {
-          const int64_t from = s.row[first + t] * p.ld_x + k0 + u * 8;
+          if (t >= 2) from = x_of(in.part, t) + in.st * kStageK;
           if constexpr (F8)
             cp_async_8(x + t * kRingX<F8> + at * 8, static_cast<const uint8_t*>(p.x) + from);
           else
@@ -726,15 +774,16 @@ struct SumWorker {
       if constexpr (F8)
         if (lane < count)
           cp_async_4(x + p.nx * kRingX<F8> + lane * 4,
-                     p.x_scales + static_cast<int64_t>(s.row[first + lane]) * ((p.k + 127) / 128) + in.st);
-      in.st += ks;
-      if (in.st >= nst) {
-        in.st = warp % ks;
-        in.part += kWarps / ks;
-        if (in.part >= s.n_parts)
-          start(in, in.tile + gridDim.x);
-        else
-          in.at = ring.tile(s.act[in.part], in.tile);
+                     p.x_scales + static_cast<int64_t>(s.row[s.first[in.part] + lane]) * ((p.k + 127) / 128) + in.st);
+      ring.load(in.at, left, 1);
+      in.x += kStageK;
+      ++in.st;
+      if (in.part * nst + in.st == hi) {
+        start(in, in.tile + gridDim.x);
+      } else if (in.st == nst) {
+        in.st = 0;
+        ++in.part;
+        at_part(in);
       }
     }
     ring.commit();
@@ -753,7 +802,7 @@ struct SumWorker {
       scale[0][1] = xs[min(2 * q + 1, count - 1)];
     }
     add_stage<GROUP, 1, F8>(
-        src, (p.k - st * kStageK) / GROUP, p.zeros != nullptr, false,
+        src, (p.k - st * kStageK) / GROUP, false,
         [&](int, int i, uint32_t(&b)[4]) {
           if constexpr (F8)
             x_e4m3(*reinterpret_cast<const uint2*>(at[0] + i * 32), b);
@@ -768,17 +817,19 @@ struct SumWorker {
     for (int i = 0; i < p.depth - 1; ++i) issue();
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
       for (int t = 0; t < tokens; ++t) sums[t * kRows + lane] = 0.f;
-      for (int part = warp / ks; part < s.n_parts; part += kWarps / ks) {
+      for (int at = lo; at < hi;) {
+        const int part = at / nst, end = min(hi, (part + 1) * nst);
         const int count = s.count[part], first = s.first[part];
         Sums<1> acc;
         acc.clear();
-        for (int st = warp % ks; st < nst; st += ks) take(st, count, acc);
-        const float* red = ring.put(acc, false);
+        for (; at < end; ++at) take(at - part * nst, count, acc);
+        float* red = ring.used();
+        __syncwarp();  // all lanes have read it
+        put_sums(acc, count, red);
         __syncwarp();
         for (int i = 0; i < count; ++i) {
-          const int pair = s.pair[first + i];
-          float& v = sums[pair / p.top * kRows + lane];
-          v = fmaf(__ldg(p.w + pair), red[i * kRedStride + lane], v);
+          float& v = sums[s.token[first + i] * kRows + lane];
+          v = fmaf(s.w[first + i], red[i * kRedStride + lane], v);
         }
         __syncwarp();
       }
@@ -822,7 +873,35 @@ cudaError_t allow_shared(K kernel, std::atomic<uint64_t>& done) {
   return e;
 }
 
-constexpr int kXRoom = 104 * 1024;  // of shared memory for x, at most: three stages a warp beside it
+
+// Clusters of `size` blocks that are resident at once (a cluster stays within
+// a part of the GPU: 36 of 4, 15 of 8), asked for once per device.
+template <typename K>
+int64_t resident_clusters(K kernel, int size, int num_sms, std::atomic<int> (&known)[64]) {
+  if (size <= 1) return num_sms;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 1;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_sms / size * size, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      return 1;
+    }
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
 
 template <int GROUP, int NT, bool F8>
 cudaError_t launch_rows(Int4Args a, int num_sms, cudaStream_t st) {
@@ -834,28 +913,29 @@ cudaError_t launch_rows(Int4Args a, int num_sms, cudaStream_t st) {
   const int64_t tiles = (cols + out_cols - 1) / out_cols;
   const int nst = (a.k + kStageK - 1) / kStageK;
   const int stage_x = kXBytes + (F8 ? 4 : 0);  // of a row of x
-  const int64_t clusters = std::max(1, num_sms / a.cluster);
+  static std::atomic<int> known[4][64];  // by the logarithm of the size
+  const int64_t clusters = resident_clusters(kernel, a.cluster, num_sms, known[a.cluster >= 8 ? 3 : a.cluster >= 4 ? 2 : a.cluster - 1]);
   const int64_t at_most = (a.ids != nullptr ? a.pairs : (a.pairs + a.nx - 1) / a.nx) * tiles;
   const int64_t about = (a.ids != nullptr ? std::min(a.pairs, a.n_experts) : (a.pairs + a.nx - 1) / a.nx) * tiles;
   const int64_t of = std::min(at_most, clusters);
   a.slice = (nst + a.cluster - 1) / a.cluster;
   // Sixteen warps on one tile, or groups of them on several: what leaves the
-  // busiest with the least (a tile's end costs about two stages), with 256
+  // busiest with the least (a tile's end costs about a stage), with 256
   // bytes of each row read together if there are that many.
   const int64_t share = (about + of - 1) / of;
   int64_t least = INT64_MAX;
   int fewest = 1;
   while (fewest < 4 && 2 * fewest <= a.slice) fewest *= 2;
   for (int ks = fewest; ks == fewest || (ks <= kWarps && ks <= a.slice); ks *= 2) {
-    const int64_t load = (share + kWarps / ks - 1) / (kWarps / ks) * ((a.slice + ks - 1) / ks + 2);
+    const int64_t load = (share + kWarps / ks - 1) / (kWarps / ks) * ((a.slice + ks - 1) / ks + 1);
     if (load < least) {
       least = load;
       a.ks = ks;
     }
   }
   const int x_bytes = a.slice * a.nx * stage_x;
-  a.batch = a.cluster > 1 ? static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(share, 24 * 1024 / (a.nx * kRows * 4)))) : 0;
-  const int rest = kSmem - x_bytes - a.batch * a.nx * kRows * 4;
+  a.batch = a.cluster > 1 ? static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(share, kBatchBytes / (a.nx * kRows * 4)))) : 0;
+  const int rest = kSmem - x_bytes - (a.batch * kRows + kRedRows<NT>) * a.nx * 4;
   a.depth = std::min(kMaxDepth, rest / (kWarps * kStage<GROUP>));
   if (a.depth < 2) return cudaErrorInvalidValue;
   const int smem = std::max(kSmem - rest + a.depth * kWarps * kStage<GROUP>, kMaskBytes);
@@ -899,7 +979,10 @@ cudaError_t launch_form(Int4Args a, int num_sms, cudaStream_t s) {
   // x has to fit: one matrix splits k over a cluster (its blocks walk the same
   // tiles, whatever is in memory), experts take fewer rows at a time
   const int nst = (a.k + kStageK - 1) / kStageK, stage_x = kXBytes + (F8 ? 4 : 0);
-  auto fits = [&]() { return static_cast<int64_t>((nst + a.cluster - 1) / a.cluster) * a.nx * stage_x <= kXRoom; };
+  auto fits = [&]() {
+    const int64_t of_row = static_cast<int64_t>((nst + a.cluster - 1) / a.cluster) * stage_x + 4 * (a.nx > 8 ? kRedRows<2> : kRedRows<1>);
+    return of_row * a.nx <= kSmem - 2 * kWarps * kStage<GROUP> - kBatchBytes;  // two stages a warp at least
+  };
   while (!fits() && a.ids == nullptr && a.cluster < kMaxCluster) a.cluster *= 2;
   while (!fits() && a.nx > 1) a.nx = (a.nx + 1) / 2;
   if (!fits()) return cudaErrorInvalidValue;
