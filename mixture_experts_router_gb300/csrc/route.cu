@@ -15,19 +15,23 @@
 // and a maximum, and a round one warp maximum and one vote.
 //
 // The order is that of the real numbers.  Without a bias it is the logits'
-// own (both scores grow with them), which needs no score; bf16 logits have
-// nothing in the four bits.  Otherwise c is off by at most 2^-21 (sigmoid) or
-// 2^-17 (softmax: the rounded argument of exp and the sum) of the largest
-// score, half a step of its own and the four bits: where two neighbours in the
-// order, or the last group kept and the first dropped, are nearer than twice
-// that and not of equal logits and biases, the warp makes the token's choice
-// again in 64 bits (exact_choice).  Weights are computed from the chosen
-// logits, relative to the largest of them, so that they neither vanish nor
-// overflow.
+// own (both scores grow with them), and needs no score but of the groups' two
+// best; bf16 logits have nothing in the four bits.  Otherwise c is off by at
+// most 2^-21 (sigmoid) or 2^-20 of the largest score (softmax), half a step of
+// its own and the four bits.  Where two neighbours in the order are nearer than
+// twice that and not of equal logits and biases, those experts are put in order
+// in 64 bits (exact_order); where the last group kept and the first dropped
+// are, the groups near them get their values in 64 bits.  Weights are computed
+// from the chosen logits, relative to the largest of them, so that they neither
+// vanish nor overflow.
+//
+// (The rounded product in exp(-l) = 2^(-l log2 e) moves a sigmoid by at most
+// s (1 - s) |l| 2^-24 < 2^-26, a softmax score by e^-x x 2^-24 of the largest.)
 #include <cuda_bf16.h>
 
 #include <algorithm>
 #include <cfloat>
+#include <type_traits>
 
 #include "internal.h"
 #include "router_common.cuh"
@@ -232,6 +236,40 @@ __device__ __noinline__ int exact_choice(const RouteArgs& a, int64_t t, double* 
   return mine;
 }
 
+// The experts of lanes 0 .. n - 1 in the order of their c in 64 bits: lane s
+// gets the s-th.  m: the largest logit, for the softmax.
+template <bool F32>
+__device__ __noinline__ int exact_order(const RouteArgs& a, int64_t t, int id, int n, float m, double* smem) {
+  const int lane = threadIdx.x % 32;
+  double c = 0.0, z = 1.0;
+  if (a.softmax && a.bias != nullptr) {
+    z = 0.0;
+    for (int e = lane; e < a.n_experts; e += 32) {
+      const float l = logit_at<F32>(a, t, e);
+      if (l > -INFINITY) z += exp(static_cast<double>(l) - static_cast<double>(m));
+    }
+    z = warp_sum(z);
+  }
+  if (lane < n) {
+    c = logit_at<F32>(a, t, id);
+    if (a.bias != nullptr)
+      c = (a.softmax ? exp(c - static_cast<double>(m)) / z : 1.0 / (1.0 + exp(-c))) + static_cast<double>(__ldg(a.bias + id));
+  }
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const double o = __shfl_sync(kAll, c, j);
+    const int e = __shfl_sync(kAll, id, j);
+    rank += o > c || (o == c && e < id) ? 1 : 0;
+  }
+  int* order = reinterpret_cast<int*>(smem);
+  __syncwarp();
+  if (lane < n) order[rank] = id;
+  __syncwarp();
+  const int mine = lane < n ? order[lane] : -1;
+  __syncwarp();
+  return mine;
+}
+
 // The lane's keys in descending order, by a network of minima and maxima
 // (Batcher's odd-even merge sort).
 template <int N>
@@ -252,20 +290,86 @@ __device__ __forceinline__ void sort_keys(uint32_t (&key)[N]) {
 }
 
 // lanes: those of a group (32 without groups: the experts are all one group's).
-template <int PER, bool F32>
-__global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__ RouteArgs a, const int lanes, const int vec) {
+enum Mode { kByLogit = 0, kSigmoid = 1, kSoftmax = 2 };  // what c is: the logit, or a score and its bias
+
+// The groups kept, the values of those in `who` taken again in 64 bits: of their
+// experts with keys not below `low` (a lane's own group's).  v: lane g's group's.
+template <int PER, bool F32, int MODE>
+__device__ __noinline__ uint32_t exact_groups(const RouteArgs& a, int64_t t, const uint32_t (&key)[PER], uint32_t who,
+                                              uint32_t kept, float v, float low, int first, int lanes, float m, bool one) {
+  const int lane = threadIdx.x % 32, group = lane / lanes;
+  double z = 1.0;
+  if constexpr (MODE == kSoftmax) {
+    z = 0.0;
+    for (int e = lane; e < a.n_experts; e += 32) {
+      const float l = logit_at<F32>(a, t, e);
+      if (l > -INFINITY) z += exp(static_cast<double>(l) - static_cast<double>(m));
+    }
+    z = warp_sum(z);
+  }
+  double best = 0.0, second = 0.0;
+  int n = 0;
+  auto add = [&](double c) {
+    if (n == 0 || c > best) {
+      second = best;
+      best = c;
+    } else if (n == 1 || c > second) {
+      second = c;
+    }
+    n = min(n + 1, 2);
+  };
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    const bool go = group < 32 && (who >> group & 1u) && key[p] > (kOutKey | kPlace) && !(key_number(key[p] & ~kPlace) < low);
+    if (!__any_sync(kAll, go)) break;
+    if (!go) continue;
+    const int e = first + static_cast<int>(kPlace - (key[p] & kPlace));
+    double c = logit_at<F32>(a, t, e);
+    if (MODE != kByLogit || !one) {
+      c = a.softmax ? exp(c - static_cast<double>(m)) / z : 1.0 / (1.0 + exp(-c));
+      if (MODE != kByLogit) c += static_cast<double>(__ldg(a.bias + e));
+    }
+    add(c);
+  }
+  for (int j = 1; j < lanes; j *= 2) {
+    const double ob = __shfl_down_sync(kAll, best, j), os = __shfl_down_sync(kAll, second, j);
+    const int on = __shfl_down_sync(kAll, n, j);
+    if (lane % lanes + j < lanes) {
+      if (on > 0) add(ob);
+      if (on > 1) add(os);
+    }
+  }
+  const double value = one || n == 1 ? best : best + second;
+  const double exact = __shfl_sync(kAll, value, min(lane * lanes, 31));
+  int rank;
+  return best_groups(who >> lane & 1u ? exact : static_cast<double>(v), a.n_groups, a.top_groups, &rank);
+}
+
+__device__ __forceinline__ float exp_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.4426950408889634f));
+  return r;
+}
+
+// lanes: those of a group (32 without groups: the experts are all one group's).
+template <int PER, bool F32, int MODE>
+__global__ void __launch_bounds__(kThreads, PER > 8 ? 2 : 4)
+    route_kernel(const __grid_constant__ RouteArgs a, const int lanes, const int vec) {
   __shared__ double c_smem[kWarps][kMaxExperts];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int size = a.n_experts / a.n_groups, group = lane / lanes, first = group * size + lane % lanes * PER;
   // this lane's experts: first .. first + mine - 1
   const int mine = group < a.n_groups ? min(max(size - lane % lanes * PER, 0), PER) : 0;
-  const bool by_logit = a.bias == nullptr;           // the logits' own order is the experts',
-  const bool groups_by_logit = by_logit && (a.group_max || size == 1);  // and the groups' too
-  const bool scores = !by_logit || (a.n_groups > 1 && !groups_by_logit);
-  const bool exact_keys = by_logit && !F32;
-  float bias[PER];
+  constexpr bool kExactKeys = MODE == kByLogit && !F32;
+  constexpr float kCut = 3.814697265625e-06f;  // 2^-18: the four bits, twice
+  const bool one = a.group_max || size == 1;   // a group's value is its best c
+  float bias[PER], far = 1.f;                  // far: no |c| is larger
 #pragma unroll
-  for (int p = 0; p < PER; ++p) bias[p] = !by_logit && p < mine ? __ldg(a.bias + first + p) : 0.f;
+  for (int p = 0; p < PER; ++p) {
+    bias[p] = MODE != kByLogit && p < mine ? __ldg(a.bias + first + p) : 0.f;
+    far = fmaxf(far, 1.f + fabsf(bias[p]));
+  }
+  if (MODE != kByLogit) far = warp_max(far);
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < a.n_tokens;
        t += static_cast<int64_t>(gridDim.x) * kWarps) {
     float l[PER];
@@ -275,45 +379,54 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
 #pragma unroll
       for (int p = 0; p < PER; ++p) l[p] = p < mine ? logit_at<F32>(a, t, first + p) : -INFINITY;
     }
-    float m = -INFINITY, z = 1.f, top_score = 1.f;
-    if (a.softmax && (scores || !a.renormalise)) {
+    float m = -INFINITY, top_score = 1.f;
+    if (a.softmax) {
 #pragma unroll
       for (int p = 0; p < PER; ++p) m = fmaxf(m, l[p]);  // (NaN is skipped)
       m = warp_max(m);
-      z = 0.f;
+      if (MODE == kSoftmax || !a.renormalise) {
+        float z = 0.f;
 #pragma unroll
-      for (int p = 0; p < PER; ++p)
-        if (l[p] > -INFINITY) z += expf(l[p] - m);
-      z = warp_sum(z);
-      top_score = 1.f / z;
+        for (int p = 0; p < PER; ++p)
+          if (l[p] > -INFINITY) z += expf(l[p] - m);
+        top_score = 1.f / warp_sum(z);
+      }
     }
-    uint32_t key[PER];     // what is chosen by
-    float second = -INFINITY, best = -INFINITY;  // the lane's two best c, which the keys have cut short
-    int numbers = 0;
-    float far = 0.f;       // the largest |c|
+    // the keys; classes beside numbers only where one of the lanes has any
+    float c[PER];
+    float odd = 0.f;
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
-      float c = l[p];
-      if (scores) {
-        c = (a.softmax ? expf(l[p] - m) * top_score : __fdividef(1.f, 1.f + expf(-l[p]))) + bias[p];
-        far = fmaxf(far, fabsf(c));
-      }
-      if (l[p] > -INFINITY && !isnan(c)) {
-        second = fmaxf(second, fminf(best, c));
-        best = fmaxf(best, c);
-        ++numbers;
-      }
-      const float by = by_logit ? l[p] : c;
-      uint32_t k = number_key(by);
-      if (l[p] == -INFINITY) k = kOutKey;
-      if (isnan(l[p]) || isnan(by)) k = kNaNKey;
-      key[p] = p < mine ? (k & ~kPlace) | (kPlace - p) : 0u;
+      c[p] = MODE == kByLogit   ? l[p] + 0.f  // (the two zeros tie)
+             : MODE == kSigmoid ? __fdividef(1.f, 1.f + exp_fast(-l[p])) + bias[p]
+                                : exp_fast(l[p] - m) * top_score + bias[p];
+      odd = fmaf(MODE == kByLogit ? c[p] : c[p] + l[p], 0.f, odd);  // NaN after a NaN or an infinity
     }
+    uint32_t key[PER];
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+      const uint32_t u = __float_as_uint(c[p]);
+      key[p] = ((u ^ ((static_cast<int32_t>(u) >> 31) | 0x80000000u)) & ~kPlace) | (kPlace - p);
+    }
+    if (__any_sync(kAll, isnan(odd) && mine > 0)) {
+#pragma unroll
+      for (int p = 0; p < PER; ++p) {
+        uint32_t k = number_key(c[p]);
+        if (l[p] == -INFINITY) k = kOutKey;
+        if (isnan(l[p]) || isnan(bias[p])) k = kNaNKey;
+        key[p] = (k & ~kPlace) | (kPlace - p);
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+      if (p >= mine) key[p] = 0u;
     sort_keys(key);
-    bool sure = true;
-    const float near = scores ? top_score * (a.softmax ? 1.52587890625e-05f : 9.5367431640625e-07f) : 0.f;
+    const float near = MODE == kByLogit ? 0.f : top_score * (MODE == kSigmoid ? 9.5367431640625e-07f : 1.9073486328125e-06f);
     if (a.n_groups > 1) {
       // a group's two best, over its lanes
+      const uint32_t k0 = key[0] & ~kPlace, k1 = PER > 1 ? key[PER > 1 ? 1 : 0] & ~kPlace : 0u;
+      float best = k0 > kOutKey ? key_number(k0) : -INFINITY, second = k1 > kOutKey ? key_number(k1) : -INFINITY;
+      int numbers = (k0 > kOutKey) + (k1 > kOutKey);
       for (int j = 1; j < lanes; j *= 2) {
         const float ob = __shfl_down_sync(kAll, best, j), os = __shfl_down_sync(kAll, second, j);
         const int on = __shfl_down_sync(kAll, numbers, j);
@@ -323,65 +436,102 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
           best = fmaxf(best, ob);
         }
       }
-      float v = numbers == 0 ? NAN : a.group_max || numbers == 1 ? best : best + second;
-      v = __shfl_sync(kAll, v, min(lane * lanes, 31));  // group `lane`'s
-      int rank;
-      const uint32_t kept = best_groups(v, a.n_groups, a.top_groups, &rank);
-      if (!groups_by_logit && a.top_groups < a.n_groups) {
-        const uint32_t in = __ballot_sync(kAll, lane < a.n_groups && rank == a.top_groups - 1);
-        const uint32_t out = __ballot_sync(kAll, lane < a.n_groups && rank == a.top_groups);
-        const float vi = __shfl_sync(kAll, v, __ffs(in) - 1), vo = __shfl_sync(kAll, v, __ffs(out) - 1);
-        far = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(far)));
-        sure = isnan(vo) || vi - vo > 2.f * (near + far * 2.384185791015625e-07f);
+      // to lane g group g's value; of its two best scores without a bias (softmax: in units of the largest)
+      const int from = min(lane * lanes, 31);
+      const float gb = __shfl_sync(kAll, best, from), gs = __shfl_sync(kAll, second, from);
+      const int gn = __shfl_sync(kAll, numbers, from);
+      auto score = [&](float x) { return a.softmax ? exp_fast(x - m) : __fdividef(1.f, 1.f + exp_fast(-x)); };
+      float v = NAN;
+      if (gn > 0) v = one || gn == 1 ? gb : MODE == kByLogit ? score(gb) + score(gs) : gb + gs;
+      if (MODE == kByLogit && !one && gn == 1) v = score(gb);
+      uint32_t kept = 0u, left = lane < a.n_groups && !isnan(v) ? number_key(v) : 0u, last = 0u;
+      uint32_t in_play = lane < a.n_groups ? 1u : 0u;
+      for (int s = 0; s < a.top_groups; ++s) {
+        last = __reduce_max_sync(kAll, left);
+        const uint32_t who = __ballot_sync(kAll, left == last && in_play != 0u);
+        const uint32_t lowest = who & (0u - who);
+        kept |= lowest;
+        if (lowest >> lane & 1u) left = in_play = 0u;
+      }
+      const uint32_t next = __reduce_max_sync(kAll, left);
+      // near the cut?
+      float slack = 0.f;
+      if (MODE != kByLogit)
+        slack = 2.f * (near + far * kCut);
+      else if (!one)
+        slack = a.softmax ? 4.f * kCut * (1.f + fabsf(m)) : 4.f * kCut;
+      else if (F32)
+        slack = kCut * fmaxf(fabsf(key_number(last)), fabsf(key_number(next)));
+      if (next != 0u && !(kExactKeys && one) && !(key_number(last) - key_number(next) > slack)) {
+        // all groups that may lie on either side of it, their experts that may be among the two best
+        const bool play = !isnan(v) && v <= key_number(last) + slack && v >= key_number(next) - slack;
+        const uint32_t who = __ballot_sync(kAll, lane < a.n_groups && play);
+        const float low = __shfl_sync(kAll, one || gn < 2 ? gb : gs, min(group, 31));
+        kept = exact_groups<PER, F32, MODE>(a, t, key, who, kept, v, low - (near + fabsf(low) * kCut), first, lanes, m, one);
       }
       if (group >= a.n_groups || !(kept >> group & 1u)) {
 #pragma unroll
         for (int p = 0; p < PER; ++p) key[p] = 0u;
       }
     }
-    int id = -1;
-    uint32_t mine_key = 0u;
-    const int rounds = a.top_k + (exact_keys ? 0 : 1);  // one more, to be sure of the last
-    for (int s = 0; s < rounds; ++s) {
+    uint2* picks = reinterpret_cast<uint2*>(c_smem[warp]);  // the chosen ones' keys and indexes, in order
+    auto pick = [&](int s) {
       const uint32_t head = key[0] & ~kPlace;
       const uint32_t top = __reduce_max_sync(kAll, head);
-      const int owner = __ffs(__ballot_sync(kAll, head == top)) - 1;
-      const int e = __shfl_sync(kAll, first + static_cast<int>(kPlace - (key[0] & kPlace)), owner);
-      if (lane == owner) {
+      const uint32_t who = __ballot_sync(kAll, head == top);
+      if (head == top && (who & ((1u << lane) - 1u)) == 0u) {
+        picks[s] = make_uint2(top, first + static_cast<int>(kPlace - (key[0] & kPlace)));
 #pragma unroll
         for (int p = 0; p + 1 < PER; ++p) key[p] = key[p + 1];
         key[PER - 1] = 0u;
       }
-      if (lane == s) {
-        id = e;
-        mine_key = top;
+    };
+    __syncwarp();
+    for (int s = 0; s < a.top_k + (kExactKeys ? 0 : 1); ++s) pick(s);  // one more, to be sure of the last
+    __syncwarp();
+    uint2 own = lane <= a.top_k ? picks[lane] : make_uint2(0u, 0u);
+    int id = static_cast<int>(own.y);
+    const bool on = lane < a.top_k;
+    float x = on ? logit_at<F32>(a, t, id) : -INFINITY;
+    if constexpr (!kExactKeys) {  // each of the k beside the one that follows it
+      auto apart = [&](uint32_t k, uint32_t following) {
+        const float u = key_number(k), v = key_number(following);
+        return following <= kOutKey || u - v > near + fmaxf(fabsf(u), fabsf(v)) * kCut;
+      };
+      const uint32_t next_key = __shfl_down_sync(kAll, own.x, 1);
+      const int next = __shfl_down_sync(kAll, id, 1);
+      bool fine = !on || apart(own.x, next_key);
+      if (!fine) fine = x == logit_at<F32>(a, t, next) && (MODE == kByLogit || __ldg(a.bias + id) == __ldg(a.bias + next));
+      if (!__all_sync(kAll, fine)) {
+        // all that may belong before the k-th, and one that does not; then these in 64 bits
+        int n = a.top_k;
+        while (n < 31 && !apart(picks[n - 1].x, picks[n].x)) {
+          __syncwarp();
+          pick(++n);
+          __syncwarp();
+        }
+        if (lane <= n) id = static_cast<int>(picks[lane].y);
+        __syncwarp();
+        id = n < 31 ? exact_order<F32>(a, t, id, n, m, c_smem[warp]) : exact_choice<F32>(a, t, c_smem[warp]);
+        x = on ? logit_at<F32>(a, t, id) : -INFINITY;
       }
     }
-    if (!exact_keys) {  // each of the k beside the one that follows it
-      const uint32_t next_key = __shfl_down_sync(kAll, mine_key, 1);
-      const int next = __shfl_down_sync(kAll, id, 1);
-      const float c = key_number(mine_key), d = key_number(next_key);
-      // 2^-18: four bits of each
-      bool fine = lane >= a.top_k || next_key <= kOutKey || c - d > near + fmaxf(fabsf(c), fabsf(d)) * 3.814697265625e-06f;
-      if (!fine)
-        fine = logit_at<F32>(a, t, id) == logit_at<F32>(a, t, next) &&
-               (by_logit || __ldg(a.bias + id) == __ldg(a.bias + next));
-      sure = __all_sync(kAll, fine) && sure;
-    }
-    if (!sure) id = exact_choice<F32>(a, t, c_smem[warp]);
     // the weights
-    const bool on = lane < a.top_k;
-    const float x = on ? logit_at<F32>(a, t, id) : -INFINITY;
-    float w;
+    float w = x == -INFINITY ? 0.f : a.softmax ? expf(x - m) : 1.f / (1.f + expf(-x));
     if (a.renormalise) {
-      const float lm = warp_max(isnan(x) ? -INFINITY : x);
-      // far below 0 the sigmoid is the exponential
-      const bool exponential = a.softmax || lm < -60.f;
-      w = x == -INFINITY ? 0.f : exponential ? expf(x - lm) : 1.f / (1.f + expf(-x));
-      const float sum = warp_sum(w);
+      if (a.softmax || __all_sync(kAll, !(x >= -60.f))) {
+        // relative to the largest of them: far below 0 the sigmoid is the exponential
+        float lm = isnan(x) ? -INFINITY : x;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) lm = fmaxf(lm, __shfl_xor_sync(kAll, lm, o));
+        w = x == -INFINITY ? 0.f : expf(x - lm);
+      }
+      float sum = w;  // of the first 16 lanes
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
       w = sum == 0.f ? 0.f : w / sum;
-    } else {
-      w = x == -INFINITY ? 0.f : a.softmax ? expf(x - m) * top_score : 1.f / (1.f + expf(-x));
+    } else if (a.softmax) {
+      w = x == -INFINITY ? 0.f : w * top_score;
     }
     if (on) {
       a.ids[t * a.top_k + lane] = id;
@@ -405,11 +555,18 @@ cudaError_t launch(const RouteArgs& a, int num_sms, cudaStream_t s) {
                ? 1
                : 0;
   };
-  if (fits(1)) return launch_kernel(route_kernel<1, F32>, grid, block, 0, s, a, lanes(1), vec(1));
-  if (fits(2)) return launch_kernel(route_kernel<2, F32>, grid, block, 0, s, a, lanes(2), vec(2));
-  if (fits(4)) return launch_kernel(route_kernel<4, F32>, grid, block, 0, s, a, lanes(4), vec(4));
-  if (fits(8)) return launch_kernel(route_kernel<8, F32>, grid, block, 0, s, a, lanes(8), vec(8));
-  return launch_kernel(route_kernel<16, F32>, grid, block, 0, s, a, lanes(16), vec(16));
+  auto run = [&](auto per) {
+    constexpr int PER = decltype(per)::value;
+    auto go = [&](auto kernel) { return launch_kernel(kernel, grid, block, 0, s, a, lanes(PER), vec(PER)); };
+    return a.bias == nullptr ? go(route_kernel<PER, F32, kByLogit>)
+           : a.softmax       ? go(route_kernel<PER, F32, kSoftmax>)
+                             : go(route_kernel<PER, F32, kSigmoid>);
+  };
+  if (fits(1)) return run(std::integral_constant<int, 1>{});
+  if (fits(2)) return run(std::integral_constant<int, 2>{});
+  if (fits(4)) return run(std::integral_constant<int, 4>{});
+  if (fits(8)) return run(std::integral_constant<int, 8>{});
+  return run(std::integral_constant<int, 16>{});
 }
 
 }  // namespace
