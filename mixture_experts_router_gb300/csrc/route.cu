@@ -43,6 +43,9 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxExperts = 256;
 constexpr uint32_t kAll = 0xffffffffu;
+constexpr int kScratch = 320;                 // 8-byte words of a warp's shared memory,
+constexpr int kPicks = kScratch - 32;         //   of which the last are for the chosen ones
+static_assert(kPicks * 2 >= 18 * 32 && kScratch >= kMaxExperts, "room for 16 keys of each lane, and all c");
 
 // Classes of experts, in the order of their keys: none (not to be chosen),
 // NaN, out (logit -inf), numbers.
@@ -289,14 +292,14 @@ __device__ __forceinline__ void sort_keys(uint32_t (&key)[N]) {
           }
 }
 
-// lanes: those of a group (32 without groups: the experts are all one group's).
 enum Mode { kByLogit = 0, kSigmoid = 1, kSoftmax = 2 };  // what c is: the logit, or a score and its bias
 
 // The groups kept, the values of those in `who` taken again in 64 bits: of their
-// experts with keys not below `low` (a lane's own group's).  v: lane g's group's.
+// experts with keys not below `low` (a lane's own group's).  v: lane g's group's;
+// keys: the lanes' sorted ones, [place][lane].
 template <int PER, bool F32, int MODE>
-__device__ __noinline__ uint32_t exact_groups(const RouteArgs& a, int64_t t, const uint32_t (&key)[PER], uint32_t who,
-                                              uint32_t kept, float v, float low, int first, int lanes, float m, bool one) {
+__device__ __noinline__ uint32_t exact_groups(const RouteArgs& a, int64_t t, const uint32_t* keys, uint32_t who, float v,
+                                              float low, int first, int lanes, float m, bool one) {
   const int lane = threadIdx.x % 32, group = lane / lanes;
   double z = 1.0;
   if constexpr (MODE == kSoftmax) {
@@ -318,12 +321,12 @@ __device__ __noinline__ uint32_t exact_groups(const RouteArgs& a, int64_t t, con
     }
     n = min(n + 1, 2);
   };
-#pragma unroll
   for (int p = 0; p < PER; ++p) {
-    const bool go = group < 32 && (who >> group & 1u) && key[p] > (kOutKey | kPlace) && !(key_number(key[p] & ~kPlace) < low);
+    const uint32_t key = keys[p * 32 + lane];
+    const bool go = (who >> group & 1u) && key > (kOutKey | kPlace) && !(key_number(key & ~kPlace) < low);
     if (!__any_sync(kAll, go)) break;
     if (!go) continue;
-    const int e = first + static_cast<int>(kPlace - (key[p] & kPlace));
+    const int e = first + static_cast<int>(kPlace - (key & kPlace));
     double c = logit_at<F32>(a, t, e);
     if (MODE != kByLogit || !one) {
       c = a.softmax ? exp(c - static_cast<double>(m)) / z : 1.0 / (1.0 + exp(-c));
@@ -351,11 +354,18 @@ __device__ __forceinline__ float exp_fast(float v) {
   return r;
 }
 
+__device__ __forceinline__ float sigmoid_fast(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp_fast(-v)));
+  return r;
+}
+
 // lanes: those of a group (32 without groups: the experts are all one group's).
 template <int PER, bool F32, int MODE>
 __global__ void __launch_bounds__(kThreads, PER > 8 ? 2 : 4)
     route_kernel(const __grid_constant__ RouteArgs a, const int lanes, const int vec) {
-  __shared__ double c_smem[kWarps][kMaxExperts];
+  // a warp's sorted keys ([place][lane], and one 0 behind them) and picks; or c in 64 bits
+  __shared__ double c_smem[kWarps][kScratch];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int size = a.n_experts / a.n_groups, group = lane / lanes, first = group * size + lane % lanes * PER;
   // this lane's experts: first .. first + mine - 1
@@ -398,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, PER > 8 ? 2 : 4)
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
       c[p] = MODE == kByLogit   ? l[p] + 0.f  // (the two zeros tie)
-             : MODE == kSigmoid ? __fdividef(1.f, 1.f + exp_fast(-l[p])) + bias[p]
+             : MODE == kSigmoid ? sigmoid_fast(l[p]) + bias[p]
                                 : exp_fast(l[p] - m) * top_score + bias[p];
       odd = fmaf(MODE == kByLogit ? c[p] : c[p] + l[p], 0.f, odd);  // NaN after a NaN or an infinity
     }
@@ -417,10 +427,18 @@ __global__ void __launch_bounds__(kThreads, PER > 8 ? 2 : 4)
         key[p] = (k & ~kPlace) | (kPlace - p);
       }
     }
+    if (mine < PER) {
 #pragma unroll
-    for (int p = 0; p < PER; ++p)
-      if (p >= mine) key[p] = 0u;
+      for (int p = 0; p < PER; ++p)
+        if (p >= mine) key[p] = 0u;
+    }
     sort_keys(key);
+    uint32_t* keys = reinterpret_cast<uint32_t*>(c_smem[warp]) + lane;
+    __syncwarp();
+#pragma unroll
+    for (int p = 0; p < PER; ++p) keys[p * 32] = key[p];
+    keys[PER * 32] = 0u;
+    uint32_t head = key[0];
     const float near = MODE == kByLogit ? 0.f : top_score * (MODE == kSigmoid ? 9.5367431640625e-07f : 1.9073486328125e-06f);
     if (a.n_groups > 1) {
       // a group's two best, over its lanes
@@ -440,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, PER > 8 ? 2 : 4)
       const int from = min(lane * lanes, 31);
       const float gb = __shfl_sync(kAll, best, from), gs = __shfl_sync(kAll, second, from);
       const int gn = __shfl_sync(kAll, numbers, from);
-      auto score = [&](float x) { return a.softmax ? exp_fast(x - m) : __fdividef(1.f, 1.f + exp_fast(-x)); };
+      auto score = [&](float x) { return a.softmax ? exp_fast(x - m) : sigmoid_fast(x); };
       float v = NAN;
       if (gn > 0) v = one || gn == 1 ? gb : MODE == kByLogit ? score(gb) + score(gs) : gb + gs;
       if (MODE == kByLogit && !one && gn == 1) v = score(gb);
@@ -467,23 +485,21 @@ __global__ void __launch_bounds__(kThreads, PER > 8 ? 2 : 4)
         const bool play = !isnan(v) && v <= key_number(last) + slack && v >= key_number(next) - slack;
         const uint32_t who = __ballot_sync(kAll, lane < a.n_groups && play);
         const float low = __shfl_sync(kAll, one || gn < 2 ? gb : gs, min(group, 31));
-        kept = exact_groups<PER, F32, MODE>(a, t, key, who, kept, v, low - (near + fabsf(low) * kCut), first, lanes, m, one);
+        kept = exact_groups<PER, F32, MODE>(a, t, keys - lane, who, v, low - (near + fabsf(low) * kCut), first, lanes, m, one);
       }
-      if (group >= a.n_groups || !(kept >> group & 1u)) {
-#pragma unroll
-        for (int p = 0; p < PER; ++p) key[p] = 0u;
-      }
+      if (group >= a.n_groups || !(kept >> group & 1u)) head = 0u;
     }
-    uint2* picks = reinterpret_cast<uint2*>(c_smem[warp]);  // the chosen ones' keys and indexes, in order
+    uint2* picks = reinterpret_cast<uint2*>(c_smem[warp] + kPicks);  // the chosen ones' keys and indexes, in order
+    const uint32_t below = (1u << lane) - 1u;
+    const uint32_t* at = keys;
     auto pick = [&](int s) {
-      const uint32_t head = key[0] & ~kPlace;
-      const uint32_t top = __reduce_max_sync(kAll, head);
-      const uint32_t who = __ballot_sync(kAll, head == top);
-      if (head == top && (who & ((1u << lane) - 1u)) == 0u) {
-        picks[s] = make_uint2(top, first + static_cast<int>(kPlace - (key[0] & kPlace)));
-#pragma unroll
-        for (int p = 0; p + 1 < PER; ++p) key[p] = key[p + 1];
-        key[PER - 1] = 0u;
+      const uint32_t top = __reduce_max_sync(kAll, head & ~kPlace);
+      const bool mine_too = (head & ~kPlace) == top;
+      const uint32_t who = __ballot_sync(kAll, mine_too);
+      if (mine_too && (who & below) == 0u) {
+        picks[s] = make_uint2(top, first + static_cast<int>(kPlace - (head & kPlace)));
+        at += 32;
+        head = *at;
       }
     };
     __syncwarp();
