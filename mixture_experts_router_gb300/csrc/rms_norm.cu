@@ -19,7 +19,7 @@ namespace cbmoe {
 namespace {
 
 constexpr int kMaxThreads = 1024;
-constexpr int kBlock = 256;  // threads of a block that holds several rows
+constexpr int kBlock = 256;  // threads of a block with rows of at most as many
 
 __device__ __forceinline__ float bf16_to_f32(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
 __device__ __forceinline__ uint16_t f32_to_bf16(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
@@ -109,8 +109,8 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
-template <int STEPS, bool F32, bool VEC>
-__global__ void __launch_bounds__(kMaxThreads, 1) rms_norm_kernel(const NormArgs a, const int per_row) {
+template <int STEPS, bool F32, bool VEC, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS > kBlock ? 1 : STEPS > 2 ? 3 : 6) rms_norm_kernel(const NormArgs a, const int per_row) {
   __shared__ float partial[32];
   const int rows_here = blockDim.x / per_row, tid = threadIdx.x % per_row, lane = threadIdx.x % 32;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * rows_here + threadIdx.x / per_row;
@@ -206,15 +206,21 @@ __global__ void __launch_bounds__(kMaxThreads, 1) rms_norm_kernel(const NormArgs
 template <int STEPS, bool F32, bool VEC>
 cudaError_t launch(const NormArgs& a, int per_row, cudaStream_t s) {
   const int threads = per_row < kBlock ? kBlock : per_row, rows_here = threads / per_row;
-  const unsigned grid = static_cast<unsigned>((a.rows + rows_here - 1) / rows_here);
-  return launch_kernel(rms_norm_kernel<STEPS, F32, VEC>, dim3(grid), dim3(threads), 0, s, a, per_row);
+  const dim3 grid(static_cast<unsigned>((a.rows + rows_here - 1) / rows_here));
+  if (threads > kBlock) return launch_kernel(rms_norm_kernel<STEPS, F32, VEC, kMaxThreads>, grid, dim3(threads), 0, s, a, per_row);
+  return launch_kernel(rms_norm_kernel<STEPS, F32, VEC, kBlock>, grid, dim3(threads), 0, s, a, per_row);
 }
 template <bool F32, bool VEC>
-cudaError_t launch_steps(const NormArgs& a, cudaStream_t s) {
+cudaError_t launch_steps(const NormArgs& a, int num_sms, cudaStream_t s) {
   const int chunks = (a.cols + 255) / 256 * 32;  // of 8 columns; unaligned rows take them by warps
+  // Few rows: as many threads as there are chunks, the shortest way through a
+  // row.  Many: blocks of 256 threads while 4 steps suffice, more rows in
+  // flight (16384 x 4096, residual and both results: 146 us with 512 threads
+  // a row, 126 with 128, 110 with 256).
   int per_row = 32;
-  while (per_row < kMaxThreads && per_row < chunks) per_row *= 2;
-  // two steps of 8 per thread where that still fills a block
+  while (per_row < kMaxThreads && per_row < chunks &&
+         (per_row < kBlock || a.rows <= 2 * num_sms || 4 * per_row < chunks))
+    per_row *= 2;
   const int steps = (chunks + per_row - 1) / per_row;
   if (steps <= 1) return launch<1, F32, VEC>(a, per_row, s);
   if (steps <= 2) return launch<2, F32, VEC>(a, per_row, s);
@@ -227,13 +233,13 @@ bool on16(const void* p, int64_t ld, int size) {
 
 }  // namespace
 
-cudaError_t launch_rms_norm(const NormArgs& a, int, cudaStream_t s) {
+cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t s) {
   const int size = a.f32 ? 4 : 2;
   const bool vec = a.cols % 8 == 0 && on16(a.x, a.ld_x, size) && on16(a.residual, a.ld_residual, size) &&
                    on16(a.sum, a.ld_sum, size) && on16(a.weight, 0, 1) && on16(a.out, a.ld_out, a.out_f32 ? 4 : 2) &&
                    (reinterpret_cast<uintptr_t>(a.codes) & 7u) == 0;
-  if (a.f32) return vec ? launch_steps<true, true>(a, s) : launch_steps<true, false>(a, s);
-  return vec ? launch_steps<false, true>(a, s) : launch_steps<false, false>(a, s);
+  if (a.f32) return vec ? launch_steps<true, true>(a, num_sms, s) : launch_steps<true, false>(a, num_sms, s);
+  return vec ? launch_steps<false, true>(a, num_sms, s) : launch_steps<false, false>(a, num_sms, s);
 }
 
 }  // namespace cbmoe
