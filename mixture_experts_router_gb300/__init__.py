@@ -759,45 +759,63 @@ def rms_norm(x, weight, eps=1e-6, residual=None, want="out", dtype=None, out=Non
     `dtype`, or into `out`), "fp8" (y as Fp8Rows) or "both".  With a residual h is returned too, in x's
     type (into `sum`, which may be x or residual itself).  `out` may be x itself."""
     torch = _torch or _load_torch()
-    kind, wkind = _FP4_TYPES.get(x.dtype), _FP4_TYPES.get(weight.dtype)
+    xtype, shape, device = x.dtype, x.shape, x.get_device()
+    kind = _FP4_TYPES.get(xtype)
+    wkind = kind if weight.dtype is xtype else _FP4_TYPES.get(weight.dtype)
     if kind is None or wkind is None:
-        raise ValueError(f"rms_norm: x {x.dtype}, weight {weight.dtype}: bfloat16 or float32 are needed")
-    if want not in ("out", "fp8", "both"):
-        raise ValueError(f"rms_norm: want {want!r} is none of 'out', 'fp8', 'both'")
-    ld, (rows, cols), device = _row_stride(x), x.shape, x.get_device()
+        raise ValueError(f"rms_norm: x {xtype}, weight {weight.dtype}: bfloat16 or float32 are needed")
+    ld = _row_stride(x)
+    rows, cols = shape
     if weight.dim() != 1 or weight.shape[0] != cols or not weight.is_contiguous():
         raise ValueError(f"rms_norm: a weight of {tuple(weight.shape)} for {cols} columns")
-    if out is not None and (want == "fp8" or out.shape != x.shape or (dtype is not None and out.dtype != dtype)):
-        raise ValueError(f"rms_norm: out {tuple(out.shape)} {out.dtype} for rows of {tuple(x.shape)}, want {want!r}")
-    okind = _FP4_TYPES.get((dtype or x.dtype) if out is None else out.dtype)
+    if weight.get_device() != device:
+        _check_device(device, weight)
+    want_out, want_fp8 = want != "fp8", want != "out"
+    if want_out and want_fp8 and want != "both":
+        raise ValueError(f"rms_norm: want {want!r} is none of 'out', 'fp8', 'both'")
+    otype = dtype or xtype
+    ld_out = ld_sum = cols
+    if out is not None:
+        if not want_out or out.shape != shape or (dtype is not None and out.dtype != dtype):
+            raise ValueError(f"rms_norm: out {tuple(out.shape)} {out.dtype} for rows of {tuple(shape)}, want {want!r}")
+        otype, ld_out = out.dtype, _row_stride(out)
+        _check_device(device, out)
+    okind = kind if otype is xtype else _FP4_TYPES.get(otype)
     if okind is None:
         raise ValueError("rms_norm: a result in bfloat16 or float32")
-    if residual is None and sum is not None:
-        raise ValueError("rms_norm: a sum without a residual")
-    for t in (residual, sum):
-        if t is not None and (t.dtype != x.dtype or t.shape != x.shape):
-            raise ValueError(f"rms_norm: residual or sum {tuple(t.shape)} {t.dtype} beside x {tuple(x.shape)} {x.dtype}")
-    _check_device(device, weight, residual, out, sum)
+    if residual is None:
+        if sum is not None:
+            raise ValueError("rms_norm: a sum without a residual")
+        r_ptr = ld_r = 0
+    else:
+        if residual.dtype is not xtype or residual.shape != shape:
+            raise ValueError(f"rms_norm: a residual of {tuple(residual.shape)} {residual.dtype} beside x {tuple(shape)} {xtype}")
+        if sum is not None:
+            if sum.dtype is not xtype or sum.shape != shape:
+                raise ValueError(f"rms_norm: a sum of {tuple(sum.shape)} {sum.dtype} beside x {tuple(shape)} {xtype}")
+            ld_sum = _row_stride(sum)
+            _check_device(device, sum)
+        if residual.get_device() != device:
+            _check_device(device, residual)
+        r_ptr, ld_r = residual.data_ptr(), _row_stride(residual)
     s = _stream_here(device, stream)
     if s is None:
         with _On(device, stream):
             return rms_norm(x, weight, eps, residual, want, dtype, out, sum)
-    where, fp8 = x.device, None
-    if want != "fp8" and out is None:
-        out = torch.empty((rows, cols), dtype=dtype or x.dtype, device=where)
+    where, fp8, codes, scales = x.device, None, 0, 0
+    if want_out and out is None:
+        out = torch.empty(shape, dtype=otype, device=where)
     if residual is not None and sum is None:
-        sum = torch.empty((rows, cols), dtype=x.dtype, device=where)
-    if want != "out":
+        sum = torch.empty(shape, dtype=xtype, device=where)
+    if want_fp8:
         fp8 = Fp8Rows.__new__(Fp8Rows)
         fp8.rows, fp8.cols = rows, cols
-        fp8.codes = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=where)
-        fp8.scales = torch.empty((rows, -(-cols // CB_FP8_COLS)), dtype=torch.float32, device=where)
+        fp8.codes = c = torch.empty(shape, dtype=torch.float8_e4m3fn, device=where)
+        fp8.scales = f = torch.empty((rows, (cols + 127) // 128), dtype=torch.float32, device=where)
+        codes, scales = c.data_ptr(), f.data_ptr()
     st = (_lib or load_library()).cb_rms_norm(_RMS_NORM.pack(
-        rows, cols, x.data_ptr(), ld,
-        *((0, 0) if residual is None else (residual.data_ptr(), _row_stride(residual))), weight.data_ptr(),
-        *((0, 0) if sum is None else (sum.data_ptr(), _row_stride(sum))),
-        *((0, 0) if out is None else (out.data_ptr(), _row_stride(out))),
-        *((0, 0) if fp8 is None else (fp8.codes.data_ptr(), fp8.scales.data_ptr())), eps, kind, wkind, okind), s)
+        rows, cols, x.data_ptr(), ld, r_ptr, ld_r, weight.data_ptr(), 0 if sum is None else sum.data_ptr(), ld_sum,
+        out.data_ptr() if want_out else 0, ld_out, codes, scales, eps, kind, wkind, okind), s)
     if st != CB_OK:
         raise CbMoeError(st, "cb_rms_norm")
     return RmsNormed(out, fp8, sum)
@@ -814,23 +832,27 @@ def route(logits, top_k, score="sigmoid", bias=None, groups=1, top_groups=None, 
     if kind is None or how is None or by is None:
         raise ValueError(f"route: logits {logits.dtype} (bfloat16 or float32), score {score!r} (one of {sorted(SCORES)}), "
                          f"group_score {group_score!r} (one of {sorted(GROUP_SCORES)})")
-    ld, (tokens, experts), device = _row_stride(logits), logits.shape, logits.get_device()
+    ld, device = _row_stride(logits), logits.get_device()
+    tokens, experts = logits.shape
+    b_ptr = 0
     if bias is not None:
         if bias.dtype is not torch.float32 or bias.numel() != experts or not bias.is_contiguous():
             raise ValueError(f"route: a contiguous fp32 bias of {experts} is needed")
-        _check_device(device, bias)
+        if bias.get_device() != device:
+            _check_device(device, bias)
+        b_ptr = bias.data_ptr()
     s = _stream_here(device, stream)
     if s is None:
         with _On(device, stream):
             return route(logits, top_k, score, bias, groups, top_groups, group_score, renormalise, scale)
     if top_k < 1:
         raise CbMoeError(CB_ERR_INVALID_ARG, f"route: top_k = {top_k}")
-    where = logits.device
-    ids = torch.empty((tokens, top_k), dtype=torch.int32, device=where)
-    w = torch.empty((tokens, top_k), dtype=torch.float32, device=where)
+    shape, where = (tokens, top_k), logits.device
+    ids = torch.empty(shape, dtype=torch.int32, device=where)
+    w = torch.empty(shape, dtype=torch.float32, device=where)
     st = (_lib or load_library()).cb_route(_ROUTE.pack(
-        tokens, logits.data_ptr(), ld, 0 if bias is None else bias.data_ptr(), ids.data_ptr(), w.data_ptr(), scale, kind,
-        experts, top_k, how, groups, groups if top_groups is None else top_groups, by, 1 if renormalise else 0), s)
+        tokens, logits.data_ptr(), ld, b_ptr, ids.data_ptr(), w.data_ptr(), scale, kind, experts, top_k, how, groups,
+        groups if top_groups is None else top_groups, by, 1 if renormalise else 0), s)
     if st != CB_OK:
         raise CbMoeError(st, "cb_route")
     return ids, w
@@ -848,20 +870,22 @@ class Int4Matrix:
     def __init__(self, codes, scales, zeros=None):
         torch = _torch or _load_torch()
         self.codes, self.scales, self.zeros = codes, scales, zeros
-        shape, meta = codes.shape, scales.shape
+        shape, meta, device = codes.shape, scales.shape, codes.get_device()
         dims = len(shape)
-        self.experts = shape[0] if dims == 3 else None
         if dims not in (2, 3) or len(meta) != dims or codes.dtype is not torch.uint8 or scales.dtype is not torch.float32 or \
                 (dims == 3 and meta[0] != shape[0]) or meta[-1] != shape[-2] or meta[-2] == 0 or \
-                (zeros is not None and (zeros.dtype is not torch.uint8 or zeros.shape != meta or not zeros.is_contiguous())) \
-                or not (codes.is_contiguous() and scales.is_contiguous()):
+                not (codes.is_contiguous() and scales.is_contiguous()):
             raise ValueError(f"codes {tuple(shape)} {codes.dtype}, scales {tuple(meta)} {scales.dtype}: not contiguous "
-                             f"4-bit weights [..][rows][cols / 2] with scales (and zeros alike) [..][cols / group][rows]")
-        self.rows, self.cols = shape[-2], 2 * shape[-1]
-        self.group = self.cols // meta[-2]
-        if self.group not in (32, 64, 128) or self.group * meta[-2] != self.cols:
-            raise ValueError(f"{meta[-2]} groups in {self.cols} columns: groups of 32, 64 or 128 are needed")
-        _check_device(codes.get_device(), scales, zeros)
+                             f"4-bit weights [..][rows][cols / 2] with scales [..][cols / group][rows]")
+        if zeros is not None and (zeros.dtype is not torch.uint8 or zeros.shape != meta or not zeros.is_contiguous()):
+            raise ValueError(f"zeros {tuple(zeros.shape)} {zeros.dtype}: contiguous uint8 of {tuple(meta)}, as the scales, are needed")
+        self.experts = shape[0] if dims == 3 else None
+        self.rows, self.cols = rows, cols = shape[-2], 2 * shape[-1]
+        self.group = group = cols // meta[-2]
+        if group not in (32, 64, 128) or group * meta[-2] != cols:
+            raise ValueError(f"{meta[-2]} groups in {cols} columns: groups of 32, 64 or 128 are needed")
+        if scales.get_device() != device or (zeros is not None and zeros.get_device() != device):
+            _check_device(device, scales, zeros)
 
 
 def int4_matmul_few(x, m: Int4Matrix, ids=None, weights=None, swiglu=False, dtype=None, out=None, status=None,
@@ -873,64 +897,72 @@ def int4_matmul_few(x, m: Int4Matrix, ids=None, weights=None, swiglu=False, dtyp
     open: half as many columns.  `status`: an int32 CUDA tensor that receives CB_ERR_DEVICE where an id is no expert
     (that row is NaN)."""
     torch = _torch or _load_torch()
-    if isinstance(x, Fp8Rows):
-        data, scales, ld = x.codes, x.scales, x.cols
-        x_rows, cols, per_slot = x.rows, x.cols, False
-        if ids is not None and x_rows != ids.shape[0]:
-            per_slot = True
+    experts, per_slot, tokens, top, i_ptr, w_ptr, x_scales = m.experts, 0, 0, 1, 0, 0, 0
+    if ids is None:
+        if experts is not None or weights is not None:
+            raise ValueError("int4_matmul_few: ids come with a matrix per expert, and weights with ids")
     else:
-        data, scales, per_slot = x, None, x.dim() == 3
-        if x.dtype is not torch.bfloat16 or x.dim() not in (2, 3):
-            raise ValueError(f"int4_matmul_few: x {tuple(x.shape)} {x.dtype}: rows of bfloat16, or Fp8Rows, are needed")
-        if per_slot:
-            if ids is None or not x.is_contiguous():
-                raise ValueError("int4_matmul_few: a contiguous x of [T][k][cols] comes with ids")
-            x_rows, cols = x.shape[0] * x.shape[1], x.shape[2]
-            ld = cols
-        else:
-            (x_rows, cols), ld = x.shape, _row_stride(x)
-    if cols != m.cols:
-        raise ValueError(f"int4_matmul_few: rows of {cols} by a matrix of {m.cols} columns")
-    if (ids is not None) != (m.experts is not None):
-        raise ValueError("int4_matmul_few: ids and a matrix per expert come together")
-    device = data.get_device()
-    tokens, top = x_rows, 1
-    if ids is not None:
+        if experts is None:
+            raise ValueError("int4_matmul_few: ids need a matrix per expert")
         if ids.dim() != 2 or ids.dtype is not torch.int32 or not ids.is_contiguous():
             raise ValueError("int4_matmul_few: ids: a contiguous int32 CUDA tensor [T][k] is needed")
         tokens, top = ids.shape
-        if x_rows != (tokens * top if per_slot else tokens) or (per_slot and scales is None and x.shape[0] != tokens):
-            raise ValueError(f"int4_matmul_few: {x_rows} rows of x for ids of {tuple(ids.shape)}")
-        if weights is not None and (weights.dtype is not torch.float32 or weights.shape != ids.shape or
-                                    not weights.is_contiguous()):
-            raise ValueError(f"int4_matmul_few: weights: a contiguous fp32 tensor of {tuple(ids.shape)} is needed")
-    if weights is not None and (ids is None or swiglu):
-        raise ValueError("int4_matmul_few: weights come with ids and without swiglu")
+        i_ptr = ids.data_ptr()
+        if weights is not None:
+            if swiglu or weights.dtype is not torch.float32 or weights.shape != ids.shape or not weights.is_contiguous():
+                raise ValueError(f"int4_matmul_few: weights: a contiguous fp32 tensor of {tuple(ids.shape)} is needed, "
+                                 f"without swiglu")
+            w_ptr = weights.data_ptr()
+    if isinstance(x, Fp8Rows):
+        data, x_scales, cols = x.codes, x.scales.data_ptr(), x.cols
+        x_rows, ld = x.rows, cols
+        if ids is not None and x_rows != tokens:
+            per_slot = 1
+    else:
+        data, shape = x, x.shape
+        if x.dtype is not torch.bfloat16:
+            raise ValueError(f"int4_matmul_few: x {x.dtype}: rows of bfloat16, or Fp8Rows, are needed")
+        if len(shape) == 3:
+            if ids is None or not x.is_contiguous() or shape[:2] != ids.shape:
+                raise ValueError(f"int4_matmul_few: x {tuple(shape)}: a contiguous x of [T][k][cols] comes with ids [T][k]")
+            x_rows, cols, per_slot = tokens * top, shape[2], 1
+            ld = cols
+        else:
+            ld = _row_stride(x)
+            x_rows, cols = shape
+    if cols != m.cols:
+        raise ValueError(f"int4_matmul_few: rows of {cols} by a matrix of {m.cols} columns")
+    if ids is None:
+        tokens = x_rows
+    elif x_rows != (tokens * top if per_slot else tokens):
+        raise ValueError(f"int4_matmul_few: {x_rows} rows of x for ids of {tuple(ids.shape)}")
     width = m.rows // 2 if swiglu else m.rows
     shape = (tokens, width) if ids is None or weights is not None else (tokens, top, width)
-    if out is not None and (tuple(out.shape) != shape or (dtype is not None and out.dtype != dtype) or
-                            (len(shape) == 3 and not out.is_contiguous())):
-        raise ValueError(f"int4_matmul_few: out {tuple(out.shape)} {out.dtype} for a result of {shape}")
-    kind = _FP4_TYPES.get((dtype or torch.bfloat16) if out is None else out.dtype)
+    otype, ld_out, device = dtype or torch.bfloat16, width, data.get_device()
+    if out is not None:
+        if tuple(out.shape) != shape or (dtype is not None and out.dtype != dtype) or (len(shape) == 3 and not out.is_contiguous()):
+            raise ValueError(f"int4_matmul_few: out {tuple(out.shape)} {out.dtype} for a result of {shape}")
+        otype = out.dtype
+        if len(shape) == 2:
+            ld_out = _row_stride(out)
+    kind = _FP4_TYPES.get(otype)
     if kind is None:
         raise ValueError("int4_matmul_few: a result in bfloat16 or float32")
     if status is not None:
         _check_int32(status, 1, "status")
-    _check_device(device, m.codes, ids, weights, out, status)
+    if m.codes.get_device() != device or ids is not None or out is not None or status is not None:
+        _check_device(device, m.codes, ids, weights, out, status)
     s = _stream_here(device, stream)
     if s is None:
         with _On(device, stream):
             return int4_matmul_few(x, m, ids, weights, swiglu, dtype, out, status)
     if out is None:
-        out, ld_out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=data.device), width
-    else:
-        ld_out = width if len(shape) == 3 else _row_stride(out)
+        out = torch.empty(shape, dtype=otype, device=data.device)
+    zeros = m.zeros
     st = (_lib or load_library()).cb_int4_matmul_few(_INT4.pack(
-        data.data_ptr(), 0 if scales is None else scales.data_ptr(), m.codes.data_ptr(), m.scales.data_ptr(),
-        0 if m.zeros is None else m.zeros.data_ptr(), 0 if ids is None else ids.data_ptr(),
-        0 if weights is None else weights.data_ptr(), out.data_ptr(), 0 if status is None else status.data_ptr(),
-        ld, ld_out, m.rows, m.cols, tokens, top, m.experts or 1, m.group, 1 if per_slot else 0, 1 if swiglu else 0,
-        kind), s)
+        data.data_ptr(), x_scales, m.codes.data_ptr(), m.scales.data_ptr(), 0 if zeros is None else zeros.data_ptr(), i_ptr,
+        w_ptr, out.data_ptr(), 0 if status is None else status.data_ptr(), ld, ld_out, m.rows, cols, tokens, top,
+        experts or 1, m.group, per_slot, 1 if swiglu else 0, kind), s)
     if st != CB_OK:
         raise CbMoeError(st, "cb_int4_matmul_few")
     return out
