@@ -5,7 +5,10 @@ them a dense expert that every token takes, its weights kept in 4-bit floating p
   dense expert by `fp4_quantize` and `fp4_matmul`, all in one CUDA graph;
 * prompt: the handle's ordinary forward, and the same dense expert with more rows;
 * routed experts in 4 bits: `fp4_matmul` over the handle's own dispatch (the 128-row tiles of
-  its routing), one matrix per expert.
+  its routing), one matrix per expert;
+* a whole block with the residual's addition and the norm (`rms_norm`), routing in groups with a
+  balance bias (`route`), prompts on the handle with that routing, decode steps on 4-bit integer
+  weights in groups (`int4_matmul_few`), again in one CUDA graph.
 
     python examples/serving_block.py        # runs both on a GB300 and prints their times
 """
@@ -128,6 +131,77 @@ class Fp4Experts:
         return (y[at] * grab["w"][:, None]).view(T, k, -1).sum(1)
 
 
+def int4_groups(w, group=128):
+    """w [..][rows][cols] as an Int4Matrix: per group of a row the 16 steps from its least to its largest value."""
+    v = w.float().unflatten(-1, (-1, group))
+    low, high = v.amin(-1).clamp_max(0), v.amax(-1).clamp_min(0)
+    scale = ((high - low) / 15).clamp_min(1e-12)
+    zero = (-low / scale).round().clamp(0, 15)
+    q = ((v / scale[..., None]).round() + zero[..., None]).clamp(0, 15).to(torch.uint8).flatten(-2)
+    codes = q[..., 0::2] | (q[..., 1::2] << 4)
+    return cb.Int4Matrix(codes.contiguous(), scale.transpose(-1, -2).contiguous(),
+                         zero.to(torch.uint8).transpose(-1, -2).contiguous())
+
+
+class RoutedBlock:
+    """x + residual, norm, routing, routed experts.  Prompts of exactly `prompt_tokens` (shorter ones
+    padded) run on a handle with 16-bit weights, decode steps of up to 16 tokens on 4-bit ones."""
+
+    def __init__(self, prompt_tokens, norm, w_router, balance, w_gate, w_up, w_down, top_k, groups, top_groups, scale, group=128):
+        E, f, d = w_gate.shape
+        self.layer = cb.MoELayer(prompt_tokens, d, f, E, top_k, w_router, w_gate, w_up, w_down)
+        self.up, self.down = int4_groups(torch.cat([w_gate, w_up], 1), group), int4_groups(w_down, group)
+        self.norm, self.router_t, self.balance = norm, w_router.t().contiguous(), balance
+        self.how = dict(top_k=top_k, score="sigmoid", bias=balance, groups=groups, top_groups=top_groups, scale=scale)
+        self.graphs = {}
+
+    def prompt(self, x, residual):
+        """(the experts' sum, the new residual), both bf16."""
+        n, T = x.shape[0], self.layer.cfg.n_tokens
+        if n > T:
+            raise ValueError(f"a prompt of {n} tokens for a handle of {T}")
+        r = cb.rms_norm(x, self.norm, residual=residual)
+        rows = r.out if n == T else torch.cat([r.out, r.out.new_zeros((T - n, x.shape[1]))])
+        out = torch.empty_like(rows)
+        self.layer.forward(rows, out, stream=torch.cuda.current_stream(), routing=cb.route(rows @ self.router_t, **self.how))
+        return out[:n], r.sum
+
+    def _decode(self, x, residual):
+        r = cb.rms_norm(x, self.norm, residual=residual, want="both")
+        ids, w = cb.route(r.out @ self.router_t, **self.how)
+        h = cb.int4_matmul_few(r.fp8, self.up, ids=ids, swiglu=True)     # a row per (token, expert)
+        return cb.int4_matmul_few(h, self.down, ids=ids, weights=w), r.sum
+
+    def decode(self, x, residual):
+        """One step, replayed from a graph per token count."""
+        n = x.shape[0]
+        if n not in self.graphs:
+            held = x.clone(), residual.clone()
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                self._decode(*held)                      # warm-up outside the capture
+            torch.cuda.current_stream().wait_stream(side)
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                out = self._decode(*held)
+            self.graphs[n] = (g, held, out)
+        g, held, out = self.graphs[n]
+        held[0].copy_(x), held[1].copy_(residual)
+        g.replay()
+        return tuple(t.clone() for t in out)
+
+
+def random_routed_block(d=2048, f=768, E=64, top_k=6, groups=8, top_groups=4, prompt_tokens=256, group=128, seed=0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    w = lambda *s: torch.empty(s, device="cuda").normal_(0, 0.02, generator=g).bfloat16()  # noqa: E731
+    norm = (1 + torch.empty(d, device="cuda").normal_(0, 0.1, generator=g)).bfloat16()
+    balance = torch.empty(E, device="cuda").normal_(0, 0.05, generator=g)
+    weights = w(E, d), w(E, f, d), w(E, f, d), w(E, d, f)
+    return RoutedBlock(prompt_tokens, norm, weights[0], balance, *weights[1:], top_k, groups, top_groups, 2.5, group), weights
+
+
 def random_block(d=2048, f=768, E=16, top_k=4, dense_f=1536, prompt_tokens=256, format="mx", seed=0):
     g = torch.Generator(device="cuda")
     g.manual_seed(seed)
@@ -155,6 +229,11 @@ def main():
     print(f"prompt of 2048 tokens: {time(lambda: block.prompt(x)):.0f} us")
     for n in (1, 4, 16):
         print(f"decode, {n} tokens: {time(lambda: block.decode(x[:n])):.0f} us")
+    quant, _ = random_routed_block(4096, 1536, 64, 6, prompt_tokens=2048)
+    res = torch.randn(2048, 4096, device="cuda").bfloat16()
+    print(f"norm, routing and experts, prompt of 2048 tokens: {time(lambda: quant.prompt(x, res)):.0f} us")
+    for n in (1, 4, 16):
+        print(f"norm, routing and 4-bit experts, decode, {n} tokens: {time(lambda: quant.decode(x[:n], res[:n])):.0f} us")
     experts = Fp4Experts(*routed[1:])
     print(f"routed experts in 4 bits, 2048 tokens: {time(lambda: experts(x, block.layer)):.0f} us")
 
