@@ -148,3 +148,28 @@ def test_routings_that_are_none():
         buf = torch.empty(T * d, dtype=torch.float32, device="cuda")
         layer.forward(x, buf.view(T, d), f32out=True, routing=(ids, buf[:T * k].view(T, k)))
     layer.close()
+
+
+@pytest.mark.gpu
+def test_captured_with_another_routing():
+    """A captured forward reads the routing that is there when the graph runs."""
+    T, d, f, E, k = 90, 256, 256, 12, 2
+    g, (wr, wg, wu, wd) = weights(E, d, f, 7)
+    layer = cb.MoELayer(T, d, f, E, k, wr, wg, wu, wd)
+    x = torch.randn(T, d, generator=g, device="cuda").bfloat16()
+    new = lambda: (torch.rand(T, E, generator=g, device="cuda").argsort(-1)[:, :k].to(torch.int32).contiguous(),  # noqa: E731
+                   torch.rand(T, k, generator=g, device="cuda"))
+    ids, w = new()
+    out, want = torch.empty(T, d, dtype=torch.bfloat16, device="cuda"), torch.empty(T, d, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer.forward(x, out, stream=torch.cuda.current_stream(), routing=(ids, w))
+    for _ in range(3):
+        for t, v in zip((ids, w), new()):
+            t.copy_(v)
+        graph.replay()
+        layer.forward(x, want, stream=torch.cuda.current_stream(), routing=(ids, w))
+        assert torch.equal(out, want)
+    assert layer.last_error() == cb.CB_OK
+    layer.close()

@@ -433,8 +433,17 @@ def test_route_ties_and_near_ties(score):
     steps = torch.randint(0, 5, (40, 256), generator=g, device="cuda", dtype=torch.int32)
     near = (base.view(torch.int32) + steps).view(F32)
     for bias in (None, torch.full((256,), 0.25, device="cuda")):
-        for groups, top_groups in ((1, 1), (8, 4)):
+        for groups, top_groups in ((1, 1), (8, 4), (32, 7), (4, 1)):
             check_route(near, 8, bias, score, groups, top_groups, "max")
+            check_route(near, 8, bias, score, groups, top_groups, "top2")
+    # groups whose values meet, and values of one expert each that do
+    twin = randn(g, 30, 64)
+    twin[:, 16:32] = twin[:, :16]
+    for bias in (None, torch.zeros(64, device="cuda")):
+        for groups, top_groups in ((4, 1), (4, 2), (8, 3)):
+            check_route(twin, 4, bias, score, groups, top_groups, "max")
+            check_route(twin, 4, bias, score, groups, top_groups, "top2")
+            check_route(twin.to(BF16), 4, bias, score, groups, top_groups, "top2")
     # biases that nearly undo the scores' differences
     s = 1 / (1 + torch.exp(-l.double()))
     if score == "softmax":
@@ -741,6 +750,54 @@ def test_int4_streams_graphs_and_two_at_once():
     ids.copy_(torch.randint(0, 8, (6, 2), generator=g, device="cuda", dtype=torch.int32))
     graph.replay()
     assert torch.equal(out, cb.int4_matmul_few(x, m, ids=ids, swiglu=True))
+
+
+@pytest.mark.gpu
+def test_int4_first_call_of_a_form_in_a_capture():
+    """Nothing that a first launch asks the driver for is refused while a stream is captured."""
+    g = gen(15)
+    m = int4_weights(g, 64, 16384, 32)
+    x = fp8_rows(g, 16, 16384)        # clusters; no other test takes this form
+    out = torch.empty(16, 64, dtype=F32, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cb.int4_matmul_few(x, m, out=out)
+    graph.replay()
+    want, err = int4_64(x, m)
+    assert ((out.double() - want).abs() <= err + EPS[F32] * want.abs() + TINY).all()
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """The last rows of arrays of more than 2^32 bytes."""
+    g = gen(16)
+    E, n, k = 256, 8192, 4352
+    codes = torch.empty(E, n, k // 2, dtype=torch.uint8, device="cuda")     # 4.6 GB, of which two experts are used
+    scales, zeros = torch.empty(E, k // 128, n, device="cuda"), torch.empty(E, k // 128, n, dtype=torch.uint8, device="cuda")
+    for e in (0, E - 1):
+        one = int4_weights(g, n, k, 128)
+        codes[e], scales[e], zeros[e] = one.codes, one.scales, one.zeros
+    m = cb.Int4Matrix(codes, scales, zeros)
+    ids = torch.tensor([[0, E - 1], [E - 1, 0], [E - 1, E - 1]], dtype=torch.int32, device="cuda")
+    x = randn(g, 3, k, dtype=BF16)
+    check_int4(x, m, ids=ids, swiglu=True)
+    check_int4(x, m, ids=ids, weights=randn(g, 3, 2))
+    del m, codes, scales, zeros
+    rows, cols = 540000, 4096                                               # 4.4 GB each
+    x = torch.empty(rows, cols, dtype=BF16, device="cuda").normal_(generator=g)
+    weight = torch.ones(cols, dtype=BF16, device="cuda")
+    r = cb.rms_norm(x, weight, residual=x, want="both", sum=x)
+    assert torch.isfinite(r.fp8.scales).all()
+    last = cb.rms_norm(x[-3:].clone(), weight, want="both", eps=1e-6)
+    assert torch.equal(r.out[-3:], last.out) or (r.out[-3:].float() - last.out.float()).abs().max() <= 0.02   # x is rounded in between
+    assert torch.equal(r.fp8.scales[-3:] > 0, last.fp8.scales > 0)
+    del r
+    l = x.view(-1, 256)                                                     # 8.6 M tokens
+    ids, w = cb.route(l, 6, groups=8, top_groups=3)
+    for at in (slice(0, 50), slice(-50, None)):
+        want, _ = choose64(l[at].double().cpu().numpy(), 6, "sigmoid", None, 8, 3, "top2")
+        assert np.array_equal(ids[at].cpu().numpy(), want)
 
 
 @pytest.mark.gpu
