@@ -464,7 +464,8 @@ template <int NT>
 constexpr int kRedRows = NT == 1 ? 2 * kWarps * kRedStride : 0;  // floats of the warps' sums, for a row of x
 constexpr int kBatchBytes = 8 * 1024;                            // of a batch's sums, about
 
-template <int GROUP, int NT, bool F8>
+// SPLIT: k is split over the blocks of a cluster.
+template <int GROUP, int NT, bool F8, bool SPLIT>
 struct RowsWorker {
   static constexpr int kWords = GROUP / 32;
   const Int4Args& p;
@@ -502,11 +503,11 @@ struct RowsWorker {
         groups(kWarps / p_.ks),
         tiles(((p_.swiglu ? p_.n / 2 : p_.n) + out_cols(p_) - 1) / out_cols(p_)) {
     const int nst = (p.k + kStageK - 1) / kStageK;
-    const int rank = p.cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
     s0 = min(nst, rank * p.slice);
     s1 = min(nst, s0 + p.slice);
     const int64_t total = static_cast<int64_t>(s.n_parts) * tiles;
-    const int at = blockIdx.x / p.cluster, of = gridDim.x / p.cluster;
+    const int at = SPLIT ? blockIdx.x / p.cluster : blockIdx.x, of = SPLIT ? gridDim.x / p.cluster : gridDim.x;
     lo = static_cast<int>(total * at / of);
     hi = static_cast<int>(total * (at + 1) / of);
   }
@@ -514,7 +515,7 @@ struct RowsWorker {
 
   __device__ __forceinline__ int segment_end(int from) const {
     int end = min(hi, (from / tiles + 1) * tiles);
-    if (p.cluster > 1) end = min(end, lo + ((from - lo) / p.batch + 1) * p.batch);
+    if (SPLIT) end = min(end, lo + ((from - lo) / p.batch + 1) * p.batch);
     return end;
   }
   __device__ __forceinline__ void settle(Place& a) const {  // onto a tile of this group, or to the end
@@ -673,7 +674,7 @@ struct RowsWorker {
           const float* all = reinterpret_cast<const float*>(block) + t * kRedStride + lane;
 #pragma unroll 4
           for (int w = 0; w < p.ks; ++w) v += all[s.red[first_warp + w]];
-          if (p.cluster > 1)
+          if constexpr (SPLIT)
             sums[((sub - lo) % p.batch * p.nx + t) * kRows + lane] = v;
           else
             finish(sub - part * tiles, s.pair[first + t], v);
@@ -681,7 +682,8 @@ struct RowsWorker {
         if constexpr (NT > 1) meet();
       }
       __syncthreads();  // x may be replaced
-      if (p.cluster > 1 && (to == hi || (to - lo) % p.batch == 0)) join(lo + (to - 1 - lo) / p.batch * p.batch, to);
+      if constexpr (SPLIT)
+        if (to == hi || (to - lo) % p.batch == 0) join(lo + (to - 1 - lo) / p.batch * p.batch, to);
       from = to;
     }
     cp_async_wait_all();
@@ -695,12 +697,12 @@ struct RowsWorker {
   }
 };
 
-template <int GROUP, int NT, bool F8>
-__global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Int4Args p) {
+template <int GROUP, int NT, bool F8, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant__ Int4Args p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Shared s;
   find_parts(p, s, reinterpret_cast<uint32_t*>(smem));
-  RowsWorker<GROUP, NT, F8> w(p, s, smem);
+  RowsWorker<GROUP, NT, F8, SPLIT> w(p, s, smem);
   w.run();
 }
 
@@ -849,7 +851,7 @@ struct SumWorker {
 };
 
 template <int GROUP, bool F8>
-__global__ void __launch_bounds__(kThreads, 1) sum_kernel(const Int4Args p) {
+__global__ void __launch_bounds__(kThreads, 1) sum_kernel(const __grid_constant__ Int4Args p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Shared s;
   find_parts(p, s, reinterpret_cast<uint32_t*>(smem));
@@ -903,9 +905,9 @@ int64_t resident_clusters(K kernel, int size, int num_sms, std::atomic<int> (&kn
   return n;
 }
 
-template <int GROUP, int NT, bool F8>
+template <int GROUP, int NT, bool F8, bool SPLIT>
 cudaError_t launch_rows(Int4Args a, int num_sms, cudaStream_t st) {
-  auto kernel = rows_kernel<GROUP, NT, F8>;
+  auto kernel = rows_kernel<GROUP, NT, F8, SPLIT>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_shared(kernel, done);
   if (e != cudaSuccess) return e;
@@ -986,7 +988,9 @@ cudaError_t launch_form(Int4Args a, int num_sms, cudaStream_t s) {
   while (!fits() && a.ids == nullptr && a.cluster < kMaxCluster) a.cluster *= 2;
   while (!fits() && a.nx > 1) a.nx = (a.nx + 1) / 2;
   if (!fits()) return cudaErrorInvalidValue;
-  return a.nx > 8 ? launch_rows<GROUP, 2, F8>(a, num_sms, s) : launch_rows<GROUP, 1, F8>(a, num_sms, s);
+  if (a.cluster > 1)
+    return a.nx > 8 ? launch_rows<GROUP, 2, F8, true>(a, num_sms, s) : launch_rows<GROUP, 1, F8, true>(a, num_sms, s);
+  return a.nx > 8 ? launch_rows<GROUP, 2, F8, false>(a, num_sms, s) : launch_rows<GROUP, 1, F8, false>(a, num_sms, s);
 }
 
 template <int GROUP>
