@@ -240,6 +240,26 @@ def test_norm_against_64_bits(rows, cols, dtype, want):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", [(2432, 1032), (5000, 2048), (2500, 2056), (4871, 4096), (2600, 4104), (2433, 8192), (2500, 96),
+                                       (2500, 1024), (2500, 1031), (3000, 8200)])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_norm_many_rows(rows, cols, dtype):
+    g = gen(rows + cols)
+    wide = randn(g, rows, cols + 8, dtype=dtype)
+    x, res, weight = wide[:, :cols], randn(g, rows, cols, std=2.0, dtype=dtype), 1 + randn(g, cols, std=0.3, dtype=dtype)
+    r = cb.rms_norm(x, weight, residual=res, want="both", dtype=F32)
+    check_norm(x, weight, res, r, 1e-6, "both", F32)
+    bare = cb.rms_norm(x, weight)
+    check_norm(x, weight, None, bare, 1e-6, "out")
+    x2, res2 = x.clone(), res.clone()
+    again = cb.rms_norm(x2, weight, residual=res2, sum=res2, out=x2, want="both")
+    check_norm(x, weight, res, again, 1e-6, "both")
+    assert torch.equal(res2, r.sum) and torch.equal(x2, again.out)
+    # a few of the rows alone: another way through the kernels, the same definition
+    check_norm(x[-5:], weight, None, cb.rms_norm(x[-5:], weight), 1e-6, "out")
+
+
+@pytest.mark.gpu
 def test_norm_types_strides_and_places():
     g = gen(5)
     wide = randn(g, 9, 700, dtype=BF16)
