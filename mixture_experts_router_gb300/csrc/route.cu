@@ -7,7 +7,9 @@
 //   index.
 //
 // What bounds it: for many tokens the instructions of the scores and the
-// rounds, not the bytes of the logits; for few, the launch.
+// rounds (16384 x 256 sigmoid, 4 of 8 groups, 8 chosen: 18.9 us with some 760
+// instructions a token and warp; 8192 x 128 softmax, 4 chosen: 5.4), not the
+// bytes of the logits; for few, the launch (3.4 us for one).
 //
 // Keys.  The order of a lane's experts is that of unsigned words: c's bits in
 // an order-preserving form, the last four replaced by the expert's place in the
@@ -292,6 +294,12 @@ __device__ __forceinline__ void sort_keys(uint32_t (&key)[N]) {
           }
 }
 
+// Blocks of an SM, all of them resident: registers are worth more than warps
+// (16384 x 256 in groups: 20.5 us with 4 blocks, 18.9 with 3; 65536 x 128 in
+// groups: 52.7 with 5, 50.3 with 4).
+template <int PER>
+constexpr int kBlocks = PER > 8 ? 2 : PER == 8 ? 3 : 4;
+
 enum Mode { kByLogit = 0, kSigmoid = 1, kSoftmax = 2 };  // what c is: the logit, or a score and its bias
 
 // The groups kept, the values of those in `who` taken again in 64 bits: of their
@@ -362,14 +370,14 @@ __device__ __forceinline__ float sigmoid_fast(float v) {
 
 // lanes: those of a group (32 without groups: the experts are all one group's).
 template <int PER, bool F32, int MODE>
-__global__ void __launch_bounds__(kThreads, PER > 8 ? 2 : 4)
+__global__ void __launch_bounds__(kThreads, kBlocks<PER>)
     route_kernel(const __grid_constant__ RouteArgs a, const int lanes, const int vec) {
   // a warp's sorted keys ([place][lane], and one 0 behind them) and picks; or c in 64 bits
   __shared__ double c_smem[kWarps][kScratch];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int size = a.n_experts / a.n_groups, group = lane / lanes, first = group * size + lane % lanes * PER;
+  const int size = a.n_experts / a.n_groups, group = lane / lanes, place = lane % lanes, first = group * size + place * PER;
   // this lane's experts: first .. first + mine - 1
-  const int mine = group < a.n_groups ? min(max(size - lane % lanes * PER, 0), PER) : 0;
+  const int mine = group < a.n_groups ? min(max(size - place * PER, 0), PER) : 0;
   constexpr bool kExactKeys = MODE == kByLogit && !F32;
   constexpr float kCut = 3.814697265625e-06f;  // 2^-18: the four bits, twice
   const bool one = a.group_max || size == 1;   // a group's value is its best c
@@ -448,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, PER > 8 ? 2 : 4)
       for (int j = 1; j < lanes; j *= 2) {
         const float ob = __shfl_down_sync(kAll, best, j), os = __shfl_down_sync(kAll, second, j);
         const int on = __shfl_down_sync(kAll, numbers, j);
-        if (lane % lanes + j < lanes) {
+        if (place + j < lanes) {
           numbers += on;
           second = fmaxf(fmaxf(second, os), fminf(best, ob));
           best = fmaxf(best, ob);
@@ -558,8 +566,7 @@ __global__ void __launch_bounds__(kThreads, PER > 8 ? 2 : 4)
 
 template <bool F32>
 cudaError_t launch(const RouteArgs& a, int num_sms, cudaStream_t s) {
-  const int64_t need = (static_cast<int64_t>(a.n_tokens) + kWarps - 1) / kWarps, most = static_cast<int64_t>(num_sms) * 8;
-  const dim3 grid(static_cast<unsigned>(need < most ? need : most)), block(kThreads);
+  const int need = (a.n_tokens - 1) / kWarps + 1;
   // the fewest experts to a lane that leave every group lanes of its own
   const int size = a.n_experts / a.n_groups;
   auto lanes = [&](int per) { return a.n_groups > 1 ? (size + per - 1) / per : 32; };
@@ -573,7 +580,8 @@ cudaError_t launch(const RouteArgs& a, int num_sms, cudaStream_t s) {
   };
   auto run = [&](auto per) {
     constexpr int PER = decltype(per)::value;
-    auto go = [&](auto kernel) { return launch_kernel(kernel, grid, block, 0, s, a, lanes(PER), vec(PER)); };
+    const dim3 grid(std::min(need, num_sms * kBlocks<PER>));
+    auto go = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kThreads), 0, s, a, lanes(PER), vec(PER)); };
     return a.bias == nullptr ? go(route_kernel<PER, F32, kByLogit>)
            : a.softmax       ? go(route_kernel<PER, F32, kSoftmax>)
                              : go(route_kernel<PER, F32, kSigmoid>);
