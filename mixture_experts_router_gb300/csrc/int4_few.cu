@@ -70,12 +70,11 @@ constexpr int kRows = 32;            // weight rows of a tile: two m16 fragments
 constexpr int kStageK = 128;         // elements of a row in a stage
 constexpr int kRowBytes = kStageK / 2;
 constexpr int kMaxPairs = 256;       // (row of x, slot)
-constexpr int kMaxExperts = 256;
 constexpr int kRedStride = 36;       // floats: the fragments' stores meet no bank twice
 constexpr int kMaxDepth = 5;
 constexpr int kMaxCluster = 8;
 constexpr int kXBytes = 2 * kStageK; // of a row of x in a stage, as MMA operands
-constexpr int kMaskBytes = kMaxExperts * kMaxPairs / 8;
+constexpr int kKeyBytes = kMaxPairs * 4;
 
 // A stage: codes, scales, zero points (and in sum_kernel rows of x).
 constexpr int kScales = kRows * kRowBytes;
@@ -100,8 +99,9 @@ struct Shared {
   uint8_t count[kMaxPairs];     //   and number of them
   uint32_t bad[kMaxPairs / 32]; // pairs whose expert does not exist
   int red[kWarps];              // where a warp has its sums of a tile, floats of the dynamic array
-  int warp_parts[kMaxExperts / 32];
-  int n_parts;
+  uint32_t starts[kMaxPairs / 32];  // entries of `pair` that begin a part
+  uint32_t n_parts;
+  int n_good;                   // pairs whose expert exists
 };
 
 __device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
@@ -370,73 +370,87 @@ __device__ __forceinline__ void store(const Int4Args& p, int64_t row, int col, f
 }
 __device__ __forceinline__ bool is_bad(const Shared& s, int pair) { return s.bad[pair / 32] >> (pair % 32) & 1u; }
 
-// The parts: each expert's pairs in order, at most nx to a part.  masks:
-// scratch of kMaxExperts x kMaxPairs bits.
-__device__ __forceinline__ void find_parts(const Int4Args& p, Shared& s, uint32_t* masks) {
+// The parts: each expert's pairs in order, at most nx to a part.  A pair's
+// place is the number of smaller keys (expert, pair), compared one by one: 256
+// of them take 2 us, 32 the time of a barrier.  keys: scratch of kMaxPairs words.
+__device__ __forceinline__ void find_parts(const Int4Args& p, Shared& s, int32_t* keys) {
   constexpr int kWordsOf = kMaxPairs / 32;
+  static_assert(kMaxPairs <= kThreads, "a thread per pair");
   const int e = threadIdx.x, lane = e % 32, warp = e / 32, most = p.nx;
   if (p.ids == nullptr) {
     if (e < p.pairs) s.pair[e] = s.row[e] = static_cast<uint8_t>(e);
-    if (e < kWordsOf) s.bad[e] = 0u;
     const int parts = (p.pairs + most - 1) / most;
     if (e < parts) {
       s.act[e] = 0;
       s.first[e] = static_cast<int16_t>(e * most);
       s.count[e] = static_cast<uint8_t>(min(most, p.pairs - e * most));
     }
-    if (e == 0) s.n_parts = parts;
+    if (e == 0) {
+      s.n_parts = parts;
+      s.n_good = p.pairs;
+    }
     __syncthreads();
     return;
   }
-  for (int i = e; i < kMaxExperts * kWordsOf; i += kThreads) masks[i] = 0u;
-  if (e < kWordsOf) s.bad[e] = 0u;
-  __syncthreads();
-  if (e < p.pairs) {
-    const int id = __ldg(p.ids + e);
-    const bool ok = id >= 0 && id < p.n_experts;
-    atomicOr(ok ? &masks[id * kWordsOf + warp] : &s.bad[warp], 1u << lane);
-    if (!ok && blockIdx.x == 0) set_error(p.status, kErrDevice);
-  }
-  __syncthreads();
-  uint32_t mine[kWordsOf];
-  int count = 0;
-#pragma unroll
-  for (int i = 0; i < kWordsOf; ++i) {
-    mine[i] = e < kMaxExperts ? masks[e * kWordsOf + i] : 0u;
-    count += __popc(mine[i]);
-  }
-  const int parts = (count + most - 1) / most;
-  const int both = parts | count << 16;  // scanned together
-  int sum = both;
-#pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const int below = __shfl_up_sync(0xffffffffu, sum, o);
-    if (lane >= o) sum += below;
-  }
-  if (e < kMaxExperts && lane == 31) s.warp_parts[warp] = sum;
-  __syncthreads();
-  if (e < kMaxExperts) {
-    int before = sum - both;
-    for (int i = 0; i < warp; ++i) before += s.warp_parts[i];
-    const int base = before & 0xFFFF;
-    int at = before >> 16;
-    for (int a = 0; a < parts; ++a) {
-      s.act[base + a] = static_cast<int16_t>(e);
-      s.first[base + a] = static_cast<int16_t>(at + a * most);
-      s.count[base + a] = static_cast<uint8_t>(min(most, count - a * most));
+  int32_t key = INT_MAX;  // of the pairs whose expert exists: expert x kMaxPairs + pair
+  float w = 0.f;
+  if (e < kMaxPairs) {
+    const int id = e < p.pairs ? __ldg(p.ids + e) : -1;
+    if (p.w != nullptr && e < p.pairs) w = __ldg(p.w + e);
+    if (id >= 0 && id < p.n_experts)
+      key = id * kMaxPairs + e;
+    else if (e < p.pairs && blockIdx.x == 0)
+      set_error(p.status, kErrDevice);
+    keys[e] = key;
+    const uint32_t bad = __ballot_sync(0xffffffffu, e < p.pairs && key == INT_MAX);
+    if (lane == 0) {
+      s.bad[warp] = bad;
+      s.starts[warp] = 0u;
     }
+  }
+  __syncthreads();
+  const bool good = key != INT_MAX;
+  bool start = false;
+  int at = 0;
+  if (good) {
+    const int own = key & ~(kMaxPairs - 1);
+    int less = 0;
+    for (int i = 0; i < p.pairs; i += 4) {
+      const int4 k = *reinterpret_cast<const int4*>(keys + i);
+      at += (k.x < key) + (k.y < key) + (k.z < key) + (k.w < key);
+      less += (k.x < own) + (k.y < own) + (k.z < own) + (k.w < own);
+    }
+    const int token = e / p.top;
+    s.pair[at] = static_cast<uint8_t>(e);
+    s.token[at] = static_cast<uint8_t>(token);
+    s.row[at] = static_cast<uint8_t>(p.x_per_slot ? e : token);
+    s.w[at] = w;
+    start = (at - less) % most == 0;
+    if (start) atomicOr(&s.starts[at / 32], 1u << at % 32);
+  }
+  __syncthreads();
+  if (e < kMaxPairs) {
+    int part = 0, parts = 0, good_ones = p.pairs, next = kMaxPairs;
 #pragma unroll
-    for (int i = 0; i < kWordsOf; ++i)
-      for (uint32_t m = mine[i]; m != 0u; m &= m - 1u) {
-        const int pair = i * 32 + __ffs(m) - 1;
-        const int token = pair / p.top;
-        s.pair[at] = static_cast<uint8_t>(pair);
-        s.token[at] = static_cast<uint8_t>(token);
-        s.row[at] = static_cast<uint8_t>(p.x_per_slot ? pair : token);
-        if (p.w != nullptr) s.w[at] = __ldg(p.w + pair);
-        ++at;
-      }
-    if (e == kMaxExperts - 1) s.n_parts = base + parts;
+    for (int i = 0; i < kWordsOf; ++i) {
+      const uint32_t word = s.starts[i];
+      const int d = at - i * 32;  // bits below, and above, this one
+      const uint32_t below = d >= 32 ? word : d > 0 ? word & ((1u << d) - 1u) : 0u;
+      const uint32_t above = d < 0 ? word : d < 31 ? word >> (d + 1) << (d + 1) : 0u;
+      part += __popc(below);
+      parts += __popc(word);
+      if (above != 0u) next = min(next, i * 32 + __ffs(above) - 1);
+      good_ones -= __popc(s.bad[i]);
+    }
+    if (start) {
+      s.act[part] = static_cast<int16_t>(key / kMaxPairs);
+      s.first[part] = static_cast<int16_t>(at);
+      s.count[part] = static_cast<uint8_t>(min(next, good_ones) - at);
+    }
+    if (e == 0) {
+      s.n_parts = parts;
+      s.n_good = good_ones;
+    }
   }
   __syncthreads();
 }
@@ -458,7 +472,7 @@ __device__ __forceinline__ void put_sums(const Sums<NT>& acc, int count, float* 
 }
 
 // ------------------------------------------------ each pair a row of its own
-// Dynamic shared memory: the rings (and first the masks), the warps' sums of
+// Dynamic shared memory: the rings (and first the keys), the warps' sums of
 // two tiles, those of a batch of tiles where a cluster splits k, x, its scales.
 template <int NT>
 constexpr int kRedRows = NT == 1 ? 2 * kWarps * kRedStride : 0;  // floats of the warps' sums, for a row of x
@@ -498,18 +512,31 @@ struct RowsWorker {
         sums(reinterpret_cast<float*>(smem + kWarps * p_.depth * kStage<GROUP>)),
         reds(sums + p_.batch * p_.nx * kRows),
         lane(threadIdx.x % 32),
-        group(threadIdx.x / 32 / p_.ks),
-        mine(threadIdx.x / 32 % p_.ks),
-        groups(kWarps / p_.ks),
+        group(threadIdx.x / 32 >> p_.ks_bits),
+        mine(threadIdx.x / 32 & (p_.ks - 1)),
+        groups(kWarps >> p_.ks_bits),
         tiles(((p_.swiglu ? p_.n / 2 : p_.n) + out_cols(p_) - 1) / out_cols(p_)) {
     const int nst = (p.k + kStageK - 1) / kStageK;
     const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
     s0 = min(nst, rank * p.slice);
     s1 = min(nst, s0 + p.slice);
-    const int64_t total = static_cast<int64_t>(s.n_parts) * tiles;
-    const int at = SPLIT ? blockIdx.x / p.cluster : blockIdx.x, of = SPLIT ? gridDim.x / p.cluster : gridDim.x;
-    lo = static_cast<int>(total * at / of);
-    hi = static_cast<int>(total * (at + 1) / of);
+    const uint32_t total = s.n_parts * tiles;  // n is at most 2^24: 2^28
+    const uint32_t at = SPLIT ? blockIdx.x / p.cluster : blockIdx.x, of = SPLIT ? gridDim.x / p.cluster : gridDim.x;
+    uint32_t each = total / of, more = total - each * of, first = 0, place = at;
+    if (!SPLIT && s.n_parts > 1 && of >= s.n_parts) {
+      // Blocks of their own for each part, where none has more tiles for it:
+      // no block changes its x (one row by 8 of 256 experts of 4096 x 2048: 17 -> 15 us).
+      const uint32_t blocks = of / s.n_parts, own = tiles / blocks, rest = tiles - own * blocks;
+      if (own + (rest > 0) <= each + (more > 0)) {
+        const uint32_t part = at / blocks;
+        first = part * tiles;
+        place = at - part * blocks;
+        each = part < s.n_parts ? own : 0;
+        more = part < s.n_parts ? rest : 0;
+      }
+    }
+    lo = static_cast<int>(first + each * place + min(place, more));
+    hi = lo + static_cast<int>(each + (place < more));
   }
   __device__ __forceinline__ static int out_cols(const Int4Args& p) { return p.swiglu ? kRows / 2 : kRows; }
 
@@ -669,7 +696,7 @@ struct RowsWorker {
         if (lane == 0) s.red[threadIdx.x / 32] = static_cast<int>(red - reinterpret_cast<float*>(block));
         meet();
         // another warp each time, where there are fewer rows than warps
-        for (int t = (mine - (sub - from) / groups) & (p.ks - 1); t < count; t += p.ks) {
+        for (int t = (mine - ((sub - from) >> (4 - p.ks_bits))) & (p.ks - 1); t < count; t += p.ks) {
           float v = 0.f;
           const float* all = reinterpret_cast<const float*>(block) + t * kRedStride + lane;
 #pragma unroll 4
@@ -689,7 +716,7 @@ struct RowsWorker {
     cp_async_wait_all();
     // rows whose expert does not exist
     const int cols = p.swiglu ? p.n / 2 : p.n;
-    if (p.ids != nullptr)
+    if (s.n_good < p.pairs)
       for (int i = 0; i < p.pairs; ++i)
         if (is_bad(s, i))
           for (int c = blockIdx.x * kThreads + threadIdx.x; c < cols; c += gridDim.x * kThreads)
@@ -701,13 +728,13 @@ template <int GROUP, int NT, bool F8, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant__ Int4Args p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Shared s;
-  find_parts(p, s, reinterpret_cast<uint32_t*>(smem));
+  find_parts(p, s, reinterpret_cast<int32_t*>(smem));
   RowsWorker<GROUP, NT, F8, SPLIT> w(p, s, smem);
   w.run();
 }
 
 // --------------------------------------------- the weighted sum of a row's pairs
-// Dynamic shared memory: the rings (and first the masks), the warps' sums.
+// Dynamic shared memory: the rings (and first the keys), the warps' sums.
 template <int GROUP, bool F8>
 struct SumWorker {
   static constexpr int kWords = GROUP / 32;
@@ -739,9 +766,9 @@ struct SumWorker {
         tokens(p_.pairs / p_.top),
         nst((p_.k + kStageK - 1) / kStageK),
         tiles((p_.n + kRows - 1) / kRows) {
-    const int64_t total = static_cast<int64_t>(s.n_parts) * nst;
-    lo = static_cast<int>(total * warp / kWarps);
-    hi = static_cast<int>(total * (warp + 1) / kWarps);
+    const int total = s.n_parts * nst;  // k is at most 49152: 2^17
+    lo = total * warp / kWarps;
+    hi = total * (warp + 1) / kWarps;
   }
   __device__ __forceinline__ void start(Place& a, int tile) const {
     a.tile = lo < hi ? tile : tiles;
@@ -840,8 +867,9 @@ struct SumWorker {
       for (int t = warp; t < tokens; t += kWarps) {
         float v = 0.f;
         for (int w = 0; w < kWarps; ++w) v += all[(w * tokens + t) * kRows + lane];
-        for (int i = t * p.top; i < (t + 1) * p.top; ++i)
-          if (is_bad(s, i)) v = __int_as_float(0x7FC00000);
+        if (s.n_good < p.pairs)
+          for (int i = t * p.top; i < (t + 1) * p.top; ++i)
+            if (is_bad(s, i)) v = __int_as_float(0x7FC00000);
         if (col < p.n) store(p, t, col, v);
       }
       __syncthreads();
@@ -854,7 +882,7 @@ template <int GROUP, bool F8>
 __global__ void __launch_bounds__(kThreads, 1) sum_kernel(const __grid_constant__ Int4Args p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Shared s;
-  find_parts(p, s, reinterpret_cast<uint32_t*>(smem));
+  find_parts(p, s, reinterpret_cast<int32_t*>(smem));
   SumWorker<GROUP, F8> w(p, s, smem);
   w.run();
 }
@@ -874,7 +902,6 @@ cudaError_t allow_shared(K kernel, std::atomic<uint64_t>& done) {
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }
-
 
 // Clusters of `size` blocks that are resident at once (a cluster stays within
 // a part of the GPU: 36 of 4, 15 of 8), asked for once per device.
@@ -935,12 +962,13 @@ cudaError_t launch_rows(Int4Args a, int num_sms, cudaStream_t st) {
       a.ks = ks;
     }
   }
+  for (a.ks_bits = 0; 1 << a.ks_bits < a.ks;) ++a.ks_bits;
   const int x_bytes = a.slice * a.nx * stage_x;
   a.batch = a.cluster > 1 ? static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(share, kBatchBytes / (a.nx * kRows * 4)))) : 0;
   const int rest = kSmem - x_bytes - (a.batch * kRows + kRedRows<NT>) * a.nx * 4;
   a.depth = std::min(kMaxDepth, rest / (kWarps * kStage<GROUP>));
   if (a.depth < 2) return cudaErrorInvalidValue;
-  const int smem = std::max(kSmem - rest + a.depth * kWarps * kStage<GROUP>, kMaskBytes);
+  const int smem = std::max(kSmem - rest + a.depth * kWarps * kStage<GROUP>, kKeyBytes);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(of * a.cluster), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -967,7 +995,7 @@ cudaError_t launch_sum(Int4Args a, int num_sms, cudaStream_t st) {
   if (a.depth < 2) return cudaErrorInvalidValue;
   const int tiles = (a.n + kRows - 1) / kRows;
   return launch_kernel(kernel, dim3(std::min(tiles, num_sms)), dim3(kThreads),
-                       static_cast<size_t>(std::max(a.depth * stage + sums, kMaskBytes)), st, a);
+                       static_cast<size_t>(std::max(a.depth * stage + sums, kKeyBytes)), st, a);
 }
 
 template <int GROUP, bool F8>
