@@ -46,7 +46,9 @@
 // keeps its stretch of x and the sums of a batch of tiles, which are joined
 // over distributed shared memory.
 //   sum_kernel has one tile per block at a time and all its experts' parts; each
-// pair has its own row of x there, which comes through the ring.
+// pair has its own row of x there, which comes through the ring.  Where that
+// leaves SMs without a tile, a cluster shares one: its parts' stages, then the
+// joining of the sums over distributed shared memory.
 //
 // All sums are in a fixed order.
 #include <cuda_bf16.h>
@@ -742,6 +744,7 @@ struct SumWorker {
   Shared& s;
   Ring<GROUP> ring;
   float* const all;       // [warp][row of out][weight row]
+  float* const joined;    // [turn][row of out][weight row], where a cluster shares a tile
   const int lane, warp, tokens, nst;
   const int tiles;
   int lo, hi;             // of the stages of all parts, one after the other: this warp's
@@ -761,14 +764,16 @@ struct SumWorker {
         s(s_),
         ring(p_, smem + threadIdx.x / 32 * p_.depth * stage(p_.nx), stage(p_.nx)),
         all(reinterpret_cast<float*>(smem + kWarps * p_.depth * stage(p_.nx))),
+        joined(all + kWarps * (p_.pairs / p_.top) * kRows),
         lane(threadIdx.x % 32),
         warp(threadIdx.x / 32),
         tokens(p_.pairs / p_.top),
         nst((p_.k + kStageK - 1) / kStageK),
         tiles((p_.n + kRows - 1) / kRows) {
     const int total = s.n_parts * nst;  // k is at most 49152: 2^17
-    lo = total * warp / kWarps;
-    hi = total * (warp + 1) / kWarps;
+    const int place = cluster_ctarank() * kWarps + warp, of = p.cluster * kWarps;
+    lo = total * place / of;
+    hi = total * (place + 1) / of;
   }
   __device__ __forceinline__ void start(Place& a, int tile) const {
     a.tile = lo < hi ? tile : tiles;
@@ -808,7 +813,7 @@ struct SumWorker {
       in.x += kStageK;
       ++in.st;
       if (in.part * nst + in.st == hi) {
-        start(in, in.tile + gridDim.x);
+        start(in, in.tile + gridDim.x / p.cluster);
       } else if (in.st == nst) {
         in.st = 0;
         ++in.part;
@@ -840,11 +845,19 @@ struct SumWorker {
         },
         scale, acc);
   }
+  __device__ __forceinline__ void finish(int tile, int t, float v) const {
+    if (s.n_good < p.pairs)
+      for (int i = t * p.top; i < (t + 1) * p.top; ++i)
+        if (is_bad(s, i)) v = __int_as_float(0x7FC00000);
+    if (tile * kRows + lane < p.n) store(p, t, tile * kRows + lane, v);
+  }
   __device__ __forceinline__ void run() {
     float* sums = all + warp * tokens * kRows;
-    start(in, blockIdx.x);
+    const int step = gridDim.x / p.cluster, rank = cluster_ctarank();
+    start(in, blockIdx.x / p.cluster);
     for (int i = 0; i < p.depth - 1; ++i) issue();
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    int turn = 0;
+    for (int tile = blockIdx.x / p.cluster; tile < tiles; tile += step) {
       for (int t = 0; t < tokens; ++t) sums[t * kRows + lane] = 0.f;
       for (int at = lo; at < hi;) {
         const int part = at / nst, end = min(hi, (part + 1) * nst);
@@ -863,17 +876,33 @@ struct SumWorker {
         __syncwarp();
       }
       __syncthreads();
-      const int col = tile * kRows + lane;
       for (int t = warp; t < tokens; t += kWarps) {
         float v = 0.f;
         for (int w = 0; w < kWarps; ++w) v += all[(w * tokens + t) * kRows + lane];
-        if (s.n_good < p.pairs)
-          for (int i = t * p.top; i < (t + 1) * p.top; ++i)
-            if (is_bad(s, i)) v = __int_as_float(0x7FC00000);
-        if (col < p.n) store(p, t, col, v);
+        if (p.cluster == 1)
+          finish(tile, t, v);
+        else
+          joined[(turn * tokens + t) * kRows + lane] = v;
       }
-      __syncthreads();
+      if (p.cluster == 1) {
+        __syncthreads();
+        continue;
+      }
+      // the blocks' sums; those of the next tile go elsewhere, and the one after that waits for all blocks
+      cluster_sync();
+      for (int t = warp * p.cluster + rank; t < tokens; t += kWarps * p.cluster) {
+        const uint32_t at = smem_u32(joined + (turn * tokens + t) * kRows + lane);
+        float v = 0.f;
+        for (int r = 0; r < p.cluster; ++r) {
+          float w;
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(w) : "r"(mapa_shared(at, r)) : "memory");
+          v += w;
+        }
+        finish(tile, t, v);
+      }
+      turn ^= 1;
     }
+    if (p.cluster > 1) cluster_sync();  // a block's shared memory is read until here
     cp_async_wait_all();
   }
 };
@@ -932,6 +961,23 @@ int64_t resident_clusters(K kernel, int size, int num_sms, std::atomic<int> (&kn
   return n;
 }
 
+template <typename K>
+cudaError_t launch_clusters(K kernel, int64_t clusters, const Int4Args& a, int smem, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * a.cluster), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = a.cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 template <int GROUP, int NT, bool F8, bool SPLIT>
 cudaError_t launch_rows(Int4Args a, int num_sms, cudaStream_t st) {
   auto kernel = rows_kernel<GROUP, NT, F8, SPLIT>;
@@ -969,19 +1015,7 @@ cudaError_t launch_rows(Int4Args a, int num_sms, cudaStream_t st) {
   a.depth = std::min(kMaxDepth, rest / (kWarps * kStage<GROUP>));
   if (a.depth < 2) return cudaErrorInvalidValue;
   const int smem = std::max(kSmem - rest + a.depth * kWarps * kStage<GROUP>, kKeyBytes);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(of * a.cluster), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = a.cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = a.cluster > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return launch_clusters(kernel, of, a, smem, st);
 }
 
 template <int GROUP, bool F8>
@@ -990,12 +1024,28 @@ cudaError_t launch_sum(Int4Args a, int num_sms, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_shared(kernel, done);
   if (e != cudaSuccess) return e;
-  const int stage = kWarps * SumWorker<GROUP, F8>::stage(a.nx), sums = kWarps * (a.pairs / a.top) * kRows * 4;
+  const int tokens = a.pairs / a.top, tiles = (a.n + kRows - 1) / kRows, nst = (a.k + kStageK - 1) / kStageK;
+  static std::atomic<int> known[4][64];  // by the logarithm of the size
+  int64_t clusters[4];
+  int best = 0;
+  // A tile to a block, or to a cluster: what leaves the busiest with the fewest
+  // stages, a tile's end counting as 2 and a cluster's as 3 (16 rows by 6 of 64
+  // experts of 2048 x 1408, 64 tiles: 34 us by blocks, 23 by pairs; 4096 x 1536: 43 and 48).
+  int64_t least = INT64_MAX;
+  for (int i = 0; i < 4; ++i) {
+    clusters[i] = resident_clusters(kernel, 1 << i, num_sms, known[i]);
+    const int64_t stages = (static_cast<int64_t>(std::min(a.pairs, a.n_experts)) * nst + (kWarps << i) - 1) / (kWarps << i);
+    const int64_t load = (tiles + clusters[i] - 1) / clusters[i] * (stages + (i == 0 ? 2 : 3));
+    if (load < least) {
+      least = load;
+      best = i;
+    }
+  }
+  a.cluster = 1 << best;
+  const int stage = kWarps * SumWorker<GROUP, F8>::stage(a.nx), sums = (kWarps + 2) * tokens * kRows * 4;
   a.depth = std::min(kMaxDepth, (kSmem - sums) / stage);
   if (a.depth < 2) return cudaErrorInvalidValue;
-  const int tiles = (a.n + kRows - 1) / kRows;
-  return launch_kernel(kernel, dim3(std::min(tiles, num_sms)), dim3(kThreads),
-                       static_cast<size_t>(std::max(a.depth * stage + sums, kKeyBytes)), st, a);
+  return launch_clusters(kernel, std::min<int64_t>(tiles, clusters[best]), a, std::max(a.depth * stage + sums, kKeyBytes), st);
 }
 
 template <int GROUP, bool F8>

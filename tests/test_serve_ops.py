@@ -667,6 +667,26 @@ def test_int4_long_rows_by_expert(experts, k, group):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,n,k,group,experts,top", [
+    (12, 96, 2304, 32, 4, 2), (7, 736, 6656, 128, 4, 1), (16, 2048, 1408, 128, 64, 6), (16, 6400, 512, 64, 64, 8), (3, 16, 8192, 64, 2, 2)])
+def test_int4_weighted_sum_by_clusters(rows, n, k, group, experts, top):
+    """Few tiles of columns, whose experts and k several blocks share; and many, in rounds."""
+    g = gen(rows * n)
+    m = int4_weights(g, n, k, group, experts)
+    ids = torch.randint(0, experts, (rows, top), generator=g, device="cuda", dtype=torch.int32)
+    w, x = randn(g, rows, top), randn(g, rows, k, dtype=BF16)
+    check_int4(x, m, ids=ids, weights=w, dtype=F32)
+    check_int4(fp8_rows(g, rows * top, k), m, ids=ids, weights=w)
+    got = cb.int4_matmul_few(x, m, ids=ids, weights=w)
+    assert torch.equal(got, cb.int4_matmul_few(x, m, ids=ids, weights=w))
+    ids[rows // 2, 0] = experts
+    bad = cb.int4_matmul_few(x, m, ids=ids, weights=w)
+    keep = torch.arange(rows, device="cuda") != rows // 2
+    assert bad[rows // 2].isnan().all() and torch.isfinite(bad[keep].float()).all()
+    check_int4(x, m, ids=ids, weights=w, dtype=F32)
+
+
+@pytest.mark.gpu
 def test_int4_sizes_of_x():
     """Large and small elements, up to the documented limits."""
     g = gen(14)
