@@ -25,9 +25,11 @@
 // normal range.  8-bit x goes the same way in fp16, whose spacing is 2^-24 and
 // which holds every e4m3 number and its sixteenth.  The tensor core takes
 // subnormal operands exactly (measured: 256 byte values, both types).
-//   The zero points' sum over x comes from one more MMA per 16 elements, whose
-// weights are all 1.  A group's sums are taken from zero and join the tile's
-// with their scale, in fp32: no weight is rounded.
+//   The zero points meet a group's sum of x: in rows_kernel it is made with the
+// operands (8 rows by two of 8 experts of 28672 x 4096: 75 -> 68 us), in
+// sum_kernel it comes from one more MMA per 16 elements, whose weights are all
+// 1.  A group's sums are taken from zero and join the tile's with their scale,
+// in fp32: no weight is rounded.
 //
 // Layouts.  A dot product does not depend on the order of its terms: within a
 // group thread q of a quad owns a quarter of the group's consecutive elements,
@@ -187,6 +189,24 @@ __device__ __forceinline__ void x_e4m3(const uint2& e, uint32_t (&b)[4]) {
   }
 }
 
+// The sum of eight elements that are operands.
+template <bool F8>
+__device__ __forceinline__ float operand_sum(const uint32_t (&b)[4]) {
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (F8) {
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&b[i]));
+      sum = fmaf(v.x + v.y, i % 2 == 0 ? 1.f : 16.f, sum);
+    } else {
+      const float one = i % 2 == 0 ? 0x1p-64f : 0x1p-60f;
+      sum = fmaf(__uint_as_float(b[i] << 16), one, sum);
+      sum = fmaf(__uint_as_float(b[i] & 0xFFFF0000u), one, sum);
+    }
+  }
+  return sum;
+}
+
 // The lane group's place among the 16-byte units of its rows: what differs
 // between neighbours is first the widest reads' own bit.
 __device__ __forceinline__ int unit_key(int g) { return (g & 2) | g >> 2; }
@@ -204,10 +224,12 @@ struct Sums {  // m16n8 fragments: [fragment][n-tile]
 
 // acc += the first `groups` groups of a stage.  fetch(n, i, b): n-tile n's
 // operands for this lane's i-th word of codes.  wide: the second n-tile too.
-// x_scale: of the lane's two columns of each n-tile.
-template <int GROUP, int NT, bool F8, typename Fetch>
-__device__ __forceinline__ void add_stage(const uint8_t* stage, int groups, bool wide, Fetch&& fetch,
+// x_scale: of the lane's two columns of each n-tile.  x_sums(n, i): the sums
+// of x over group i in these columns, or null: by MMAs of their own.
+template <int GROUP, int NT, bool F8, typename Fetch, typename XSums>
+__device__ __forceinline__ void add_stage(const uint8_t* stage, int groups, bool wide, Fetch&& fetch, XSums&& x_sums,
                                           const float (&x_scale)[NT][2], Sums<NT>& acc) {
+  constexpr bool kGiven = !std::is_same_v<std::decay_t<XSums>, std::nullptr_t>;
   constexpr int kWords = GROUP / 32;  // of a thread, row and group
   const int g = threadIdx.x % 32 >> 2, q = threadIdx.x & 3;
   const uint8_t* codes = stage + g * kRowBytes;
@@ -237,11 +259,13 @@ __device__ __forceinline__ void add_stage(const uint8_t* stage, int groups, bool
       for (int n = 0; n < NT; ++n) {
         if (n > 0 && !wide) break;
         fetch(n, gi * kWords + w, b[n]);
-        if (w == 0)
-          mma_first<F8>(all[n], kOnes, kOnes, kSixteens, kSixteens, b[n][0], b[n][1]);
-        else
-          mma<F8>(all[n], kOnes, kOnes, kSixteens, kSixteens, b[n][0], b[n][1]);
-        mma<F8>(all[n], kOnes, kOnes, kSixteens, kSixteens, b[n][2], b[n][3]);
+        if constexpr (!kGiven) {
+          if (w == 0)
+            mma_first<F8>(all[n], kOnes, kOnes, kSixteens, kSixteens, b[n][0], b[n][1]);
+          else
+            mma<F8>(all[n], kOnes, kOnes, kSixteens, kSixteens, b[n][0], b[n][1]);
+          mma<F8>(all[n], kOnes, kOnes, kSixteens, kSixteens, b[n][2], b[n][3]);
+        }
       }
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
@@ -257,6 +281,15 @@ __device__ __forceinline__ void add_stage(const uint8_t* stage, int groups, bool
             mma<F8>(sum[m][n], a0[0], a1[0], a0[1], a1[1], b[n][0], b[n][1]);
           mma<F8>(sum[m][n], a0[2], a1[2], a0[3], a1[3], b[n][2], b[n][3]);
         }
+      }
+    }
+    if constexpr (kGiven) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (n > 0 && !wide) break;
+        const float2 v = x_sums(n, gi);
+        all[n][0] = v.x;
+        all[n][1] = v.y;
       }
     }
 #pragma unroll
@@ -489,6 +522,7 @@ struct RowsWorker {
   uint8_t* const block;   // the dynamic array
   Ring<GROUP> ring;
   uint8_t* const x;       // [stage][word of a lane][row of x][quad's lane] x 16 bytes
+  float* const x_sums;    // [group][row of x], an even number of them: in the operands' units
   float* const x_scales;  // [stage][row of x]
   float* const sums;      // [tile of the batch][row of x][weight row]
   float* const reds;      // [turn][warp][row of x][weight row]
@@ -510,7 +544,8 @@ struct RowsWorker {
         block(smem),
         ring(p_, smem + threadIdx.x / 32 * p_.depth * kStage<GROUP>, kStage<GROUP>),
         x(smem + kWarps * p_.depth * kStage<GROUP> + (p_.batch * kRows + kRedRows<NT>) * p_.nx * 4),
-        x_scales(reinterpret_cast<float*>(x + p_.slice * p_.nx * kXBytes)),
+        x_sums(reinterpret_cast<float*>(x + p_.slice * p_.nx * kXBytes)),
+        x_scales(x_sums + p_.slice * kGroups<GROUP> * ((p_.nx + 1) & ~1)),
         sums(reinterpret_cast<float*>(smem + kWarps * p_.depth * kStage<GROUP>)),
         reds(sums + p_.batch * p_.nx * kRows),
         lane(threadIdx.x % 32),
@@ -591,12 +626,19 @@ struct RowsWorker {
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         const int u = u0 + j * 32;
+        if (u - lane >= units) break;
+        uint32_t b[4] = {};
+        if (u < units) {
+          if constexpr (F8)
+            x_e4m3(e[j], b);
+          else
+            x_bf16(e[j], b);
+        }
+        float sum = operand_sum<F8>(b);
+#pragma unroll
+        for (int o = GROUP / 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (u >= units) break;
-        uint32_t b[4];
-        if constexpr (F8)
-          x_e4m3(e[j], b);
-        else
-          x_bf16(e[j], b);
+        if (u % (GROUP / 8) == 0) x_sums[u / (GROUP / 8) * ((p.nx + 1) & ~1) + t] = sum / kUnit<F8>;
         const int st = u / 16, r = u % 16 % (GROUP / 8), word = u % 16 / (GROUP / 8) * kWords + r % kWords, quad = r / kWords;
         *reinterpret_cast<uint4*>(x + (((st * 4 + word) * p.nx + t) * 4 + quad) * 16) = make_uint4(b[0], b[1], b[2], b[3]);
       }
@@ -638,6 +680,9 @@ struct RowsWorker {
         [&](int n, int i, uint32_t(&b)[4]) {
           const uint4 e = *reinterpret_cast<const uint4*>(at[n] + i * word);
           b[0] = e.x, b[1] = e.y, b[2] = e.z, b[3] = e.w;
+        },
+        [&](int n, int i) {
+          return *reinterpret_cast<const float2*>(x_sums + ((st - s0) * kGroups<GROUP> + i) * ((p.nx + 1) & ~1) + min(n * 8 + 2 * q, (count - 1) & ~1));
         },
         scale, acc);
   }
@@ -843,7 +888,7 @@ struct SumWorker {
           else
             x_bf16(*reinterpret_cast<const uint4*>(at[i & 1] + i * 64), b);
         },
-        scale, acc);
+        nullptr, scale, acc);
   }
   __device__ __forceinline__ void finish(int tile, int t, float v) const {
     if (s.n_good < p.pairs)
@@ -961,6 +1006,12 @@ int64_t resident_clusters(K kernel, int size, int num_sms, std::atomic<int> (&kn
   return n;
 }
 
+// Of x in rows_kernel: operands, sums, scales.
+template <int GROUP, bool F8>
+int rows_x_bytes(int stages, int rows) {
+  return stages * (rows * kXBytes + kGroups<GROUP> * ((rows + 1) & ~1) * 4 + (F8 ? rows * 4 : 0));
+}
+
 template <typename K>
 cudaError_t launch_clusters(K kernel, int64_t clusters, const Int4Args& a, int smem, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
@@ -987,7 +1038,6 @@ cudaError_t launch_rows(Int4Args a, int num_sms, cudaStream_t st) {
   const int out_cols = a.swiglu ? kRows / 2 : kRows, cols = a.swiglu ? a.n / 2 : a.n;
   const int64_t tiles = (cols + out_cols - 1) / out_cols;
   const int nst = (a.k + kStageK - 1) / kStageK;
-  const int stage_x = kXBytes + (F8 ? 4 : 0);  // of a row of x
   static std::atomic<int> known[4][64];  // by the logarithm of the size
   const int64_t clusters = resident_clusters(kernel, a.cluster, num_sms, known[a.cluster >= 8 ? 3 : a.cluster >= 4 ? 2 : a.cluster - 1]);
   const int64_t at_most = (a.ids != nullptr ? a.pairs : (a.pairs + a.nx - 1) / a.nx) * tiles;
@@ -1009,7 +1059,7 @@ cudaError_t launch_rows(Int4Args a, int num_sms, cudaStream_t st) {
     }
   }
   for (a.ks_bits = 0; 1 << a.ks_bits < a.ks;) ++a.ks_bits;
-  const int x_bytes = a.slice * a.nx * stage_x;
+  const int x_bytes = rows_x_bytes<GROUP, F8>(a.slice, a.nx);
   a.batch = a.cluster > 1 ? static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(share, kBatchBytes / (a.nx * kRows * 4)))) : 0;
   const int rest = kSmem - x_bytes - (a.batch * kRows + kRedRows<NT>) * a.nx * 4;
   a.depth = std::min(kMaxDepth, rest / (kWarps * kStage<GROUP>));
@@ -1058,10 +1108,10 @@ cudaError_t launch_form(Int4Args a, int num_sms, cudaStream_t s) {
   if (rows > 8 && (a.ids == nullptr || a.pairs > 4 * a.n_experts)) a.nx = rows;
   // x has to fit: one matrix splits k over a cluster (its blocks walk the same
   // tiles, whatever is in memory), experts take fewer rows at a time
-  const int nst = (a.k + kStageK - 1) / kStageK, stage_x = kXBytes + (F8 ? 4 : 0);
+  const int nst = (a.k + kStageK - 1) / kStageK;
   auto fits = [&]() {
-    const int64_t of_row = static_cast<int64_t>((nst + a.cluster - 1) / a.cluster) * stage_x + 4 * (a.nx > 8 ? kRedRows<2> : kRedRows<1>);
-    return of_row * a.nx <= kSmem - 2 * kWarps * kStage<GROUP> - kBatchBytes;  // two stages a warp at least
+    const int x = rows_x_bytes<GROUP, F8>((nst + a.cluster - 1) / a.cluster, a.nx) + 4 * (a.nx > 8 ? kRedRows<2> : kRedRows<1>) * a.nx;
+    return x <= kSmem - 2 * kWarps * kStage<GROUP> - kBatchBytes;  // two stages a warp at least
   };
   while (!fits() && a.ids == nullptr && a.cluster < kMaxCluster) a.cluster *= 2;
   while (!fits() && a.nx > 1) a.nx = (a.nx + 1) / 2;
