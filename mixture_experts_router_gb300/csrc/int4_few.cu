@@ -533,7 +533,7 @@ struct RowsWorker {
 
   // A walk over the group's tiles.  Segments end where the part or the batch does.
   struct Place {
-    int sub, seg_end, st;
+    int sub, seg_end, st, part;
     typename Ring<GROUP>::Tile tile;
   };
   Place in;
@@ -552,7 +552,7 @@ struct RowsWorker {
         group(threadIdx.x / 32 >> p_.ks_bits),
         mine(threadIdx.x / 32 & (p_.ks - 1)),
         groups(kWarps >> p_.ks_bits),
-        tiles(((p_.swiglu ? p_.n / 2 : p_.n) + out_cols(p_) - 1) / out_cols(p_)) {
+        tiles(p_.tiles) {
     const int nst = (p.k + kStageK - 1) / kStageK;
     const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
     s0 = min(nst, rank * p.slice);
@@ -575,25 +575,23 @@ struct RowsWorker {
     lo = static_cast<int>(first + each * place + min(place, more));
     hi = lo + static_cast<int>(each + (place < more));
   }
-  __device__ __forceinline__ static int out_cols(const Int4Args& p) { return p.swiglu ? kRows / 2 : kRows; }
-
-  __device__ __forceinline__ int segment_end(int from) const {
-    int end = min(hi, (from / tiles + 1) * tiles);
+  __device__ __forceinline__ int segment_end(int from, int part) const {
+    int end = min(hi, (part + 1) * tiles);
     if (SPLIT) end = min(end, lo + ((from - lo) / p.batch + 1) * p.batch);
     return end;
   }
   __device__ __forceinline__ void settle(Place& a) const {  // onto a tile of this group, or to the end
     while (a.sub >= a.seg_end && a.seg_end < hi) {
       a.sub = a.seg_end + group;
-      a.seg_end = segment_end(a.seg_end);
+      if (a.seg_end == (a.part + 1) * tiles) ++a.part;
+      a.seg_end = segment_end(a.seg_end, a.part);
     }
     if (a.sub >= a.seg_end || s0 + mine >= s1) {
       a.sub = hi;
       return;
     }
     a.st = s0 + mine;
-    const int part = a.sub / tiles;
-    a.tile = ring.tile(s.act[part], a.sub - part * tiles, a.st);
+    a.tile = ring.tile(s.act[a.part], a.sub - a.part * tiles, a.st);
   }
   __device__ __forceinline__ void issue() {
     if (in.sub < hi) {
@@ -709,9 +707,10 @@ struct RowsWorker {
   }
 
   __device__ __forceinline__ void run() {
+    int part = s.n_parts > 1 ? lo / tiles : 0;
     in.sub = lo + group;
-    in.seg_end = segment_end(lo);
-    if (lo >= hi) in.seg_end = lo;
+    in.part = part;
+    in.seg_end = lo < hi ? segment_end(lo, part) : lo;
     settle(in);
     for (int i = 0; i < p.depth - 1; ++i) issue();
     auto meet = [&]() {  // the warps that share a tile
@@ -723,7 +722,7 @@ struct RowsWorker {
     const int first_warp = group * p.ks;
     int turn = 0;
     for (int from = lo; from < hi;) {
-      const int part = from / tiles, to = segment_end(from);
+      const int to = segment_end(from, part);
       const int count = s.count[part], first = s.first[part];
       if (from == lo || from == part * tiles) load_x(part);
       __syncthreads();
@@ -759,6 +758,7 @@ struct RowsWorker {
       if constexpr (SPLIT)
         if (to == hi || (to - lo) % p.batch == 0) join(lo + (to - 1 - lo) / p.batch * p.batch, to);
       from = to;
+      if (to == (part + 1) * tiles) ++part;
     }
     cp_async_wait_all();
     // rows whose expert does not exist
@@ -1036,7 +1036,7 @@ cudaError_t launch_rows(Int4Args a, int num_sms, cudaStream_t st) {
   const cudaError_t e = allow_shared(kernel, done);
   if (e != cudaSuccess) return e;
   const int out_cols = a.swiglu ? kRows / 2 : kRows, cols = a.swiglu ? a.n / 2 : a.n;
-  const int64_t tiles = (cols + out_cols - 1) / out_cols;
+  const int64_t tiles = a.tiles = (cols + out_cols - 1) / out_cols;
   const int nst = (a.k + kStageK - 1) / kStageK;
   static std::atomic<int> known[4][64];  // by the logarithm of the size
   const int64_t clusters = resident_clusters(kernel, a.cluster, num_sms, known[a.cluster >= 8 ? 3 : a.cluster >= 4 ? 2 : a.cluster - 1]);

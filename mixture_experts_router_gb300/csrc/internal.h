@@ -431,6 +431,7 @@ struct Int4Args {
   // set by the launch:
   int32_t nx;          // rows of x in a part, at most
   int32_t ks, ks_bits; // warps that share a tile, and its logarithm
+  int32_t tiles;       // of a matrix (rows_kernel)
   int32_t depth;       // stages of a warp's ring
   int32_t cluster;     // blocks that split k,
   int32_t slice;       //   stages of each,
