@@ -161,7 +161,7 @@ typedef struct {
 /* Errors: CB_ERR_INVALID_ARG (NULL, negative sizes, an unknown type or group,
  * n or k not such multiples, row strides below the columns, weights without
  * ids or with swiglu, x_per_slot without ids, out overlapping an input),
- * CB_ERR_ALIGNMENT (x, codes, scales, zeros: 16 bytes; x's rows: 16 bytes (8 in 8 bits);
+ * CB_ERR_ALIGNMENT (x, codes, scales, zeros: 16 bytes; several rows of x: 16 bytes each (8 in 8 bits);
  * out: its element; the others: 4), CB_ERR_UNSUPPORTED (more than
  * CB_INT4_MAX_ROWS tokens, 16 slots or 256 experts, n above 2^24, k above
  * CB_INT4_MAX_K, a wrong GPU), CB_ERR_CUDA. */

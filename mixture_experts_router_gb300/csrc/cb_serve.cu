@@ -165,10 +165,11 @@ cb_status_t cb_int4_matmul_few(const cb_int4_matmul_t* p, void* stream) {
   if (p->n_tokens == 0) return CB_OK;
   if (p->x == nullptr || p->codes == nullptr || p->scales == nullptr || p->out == nullptr) return CB_ERR_INVALID_ARG;
   const int x_size = p->x_scales != nullptr ? 1 : 2;
-  if (!on(p->x, 16) || !on(p->codes, 16) || !on(p->scales, 16) || !on(p->zeros, 16) || !on(p->x_scales, 4) ||
-      !on(p->ids, 4) || !on(p->w, 4) || !on(p->status, 4) || !on(p->out, size_of(p->out_type)) || p->ld_x % 8 != 0)
-    return CB_ERR_ALIGNMENT;
   const int64_t pairs = static_cast<int64_t>(p->n_tokens) * p->top_k, x_rows = p->x_per_slot ? pairs : p->n_tokens;
+  if (!on(p->x, 16) || !on(p->codes, 16) || !on(p->scales, 16) || !on(p->zeros, 16) || !on(p->x_scales, 4) ||
+      !on(p->ids, 4) || !on(p->w, 4) || !on(p->status, 4) || !on(p->out, size_of(p->out_type)) ||
+      (p->ld_x % 8 != 0 && x_rows > 1))
+    return CB_ERR_ALIGNMENT;
   const int64_t out_rows = p->w != nullptr ? p->n_tokens : pairs, blocks = (p->k + CB_FP8_COLS - 1) / CB_FP8_COLS;
   const uint64_t meta = static_cast<uint64_t>(p->n_experts) * (p->k / p->group) * p->n;
   const Span out = rows_of(p->out, out_rows, cols, p->ld_out, size_of(p->out_type));

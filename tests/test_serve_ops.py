@@ -260,6 +260,18 @@ def test_norm_many_rows(rows, cols, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", [(607, 4096), (608, 4096), (609, 1032), (456, 8192), (1217, 520), (1500, 2048), (700, 6258), (650, 770)])
+def test_norm_rows_about_the_number_of_blocks(rows, cols):
+    """As many rows as blocks that stay, one more, one less; and pairs of columns."""
+    g = gen(rows + cols)
+    for dtype in (BF16, F32):
+        x, r = randn(g, rows, cols, dtype=dtype), randn(g, rows, cols, dtype=dtype)
+        w = (1 + randn(g, cols, std=0.2)).to(dtype)
+        check_norm(x, w, r, cb.rms_norm(x, w, residual=r, want="both"), 1e-6, "both")
+        check_norm(x, w, None, cb.rms_norm(x, w, want="fp8"), 1e-6, "fp8")
+
+
+@pytest.mark.gpu
 def test_norm_types_strides_and_places():
     g = gen(5)
     wide = randn(g, 9, 700, dtype=BF16)
@@ -746,6 +758,17 @@ def test_int4_strides_and_rows_left_alone():
     with pytest.raises(cb.CbMoeError):
         cb.int4_matmul_few(randn(g, 17, 256, dtype=BF16), m)
     assert cb.int4_matmul_few(x[:0], m).shape == (0, 80)
+
+
+@pytest.mark.gpu
+def test_int4_one_row_has_no_stride():
+    """A single row of a matrix whose rows do not start on 16 bytes is a row on 16 bytes like any other."""
+    g = gen(77)
+    m, by = int4_weights(g, 80, 256, 32), int4_weights(g, 48, 256, 32, 3)
+    x = randn(g, 3, 261, dtype=BF16)[:1, :256]
+    assert x.stride(0) == 261
+    check_int4(x, m, dtype=F32)
+    check_int4(x, by, ids=torch.tensor([[2, 0]], dtype=torch.int32, device="cuda"))
 
 
 @pytest.mark.gpu
