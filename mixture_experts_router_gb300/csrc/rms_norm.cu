@@ -4,13 +4,19 @@
 //   h = x + r,  y = h / sqrt(mean h^2 + eps) * g,  s = max|y| / 448,  code = e4m3(y / s).
 //
 // Bound by memory: every element is read and written once, a row staying in
-// registers between its sum of squares and its results.  R threads share a row
+// registers between its sum of squares and its results (16384 x 4096 bf16 with
+// the residual and both results: 96 us, 6.3 TB/s; one row of 4096: 2.4 us, the
+// launch and two round trips).  R threads share a row
 // (a power of two from 32), each holding up to 4 times 8 elements.  Rows that
 // start on 16 bytes: a thread's elements are 8 in a row (16 bytes of bf16),
-// 16 lanes a scale's 128 columns.  Others: an element of every 32 (a warp's
-// loads are whole lines), a warp's first 4 and last 4 steps a scale's columns.
+// 16 lanes a scale's 128 columns.  Others: 2 of every 64, or an element of every
+// 32 where rows are odd (a warp's loads are whole lines), a warp's first half
+// and last half of steps a scale's columns (2915 rows of bf16, both results, 91
+// MB: 59 us for 6259 columns, 49 for 6258 in pairs, 59 one by one).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
+
+#include <algorithm>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -24,11 +30,11 @@ constexpr int kBlock = 256;  // threads of a block with rows of at most as many
 __device__ __forceinline__ float bf16_to_f32(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
 __device__ __forceinline__ uint16_t f32_to_bf16(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
-// Eight elements of one thread: consecutive from p (VEC: on 16 bytes), or
-// every 32nd from p of which those below `left` exist.
-template <bool F32, bool VEC>
+// Eight elements of one thread: consecutive from p (VEC 8: on 16 bytes), or
+// VEC of every 32 VEC from p, of which those below `left` exist.
+template <bool F32, int VEC>
 __device__ __forceinline__ void load8(const void* base, int64_t at, int left, float (&v)[8]) {
-  if constexpr (VEC) {
+  if constexpr (VEC == 8) {
     if constexpr (F32) {
       const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
       const float4 a = q[0], b = q[1];
@@ -40,6 +46,20 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, int left, fl
       for (int i = 0; i < 4; ++i) {
         v[2 * i] = __uint_as_float(u[i] << 16);
         v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+      }
+    }
+  } else if constexpr (VEC == 2) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      v[i] = v[i + 1] = 0.f;
+      if (i * 32 < left) {
+        if constexpr (F32) {
+          const float2 a = *reinterpret_cast<const float2*>(static_cast<const float*>(base) + at + i * 32);
+          v[i] = a.x, v[i + 1] = a.y;
+        } else {
+          const uint32_t u = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(base) + at + i * 32);
+          v[i] = __uint_as_float(u << 16), v[i + 1] = __uint_as_float(u & 0xFFFF0000u);
+        }
       }
     }
   } else {
@@ -55,9 +75,9 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, int left, fl
     }
   }
 }
-template <bool F32, bool VEC>
+template <bool F32, int VEC>
 __device__ __forceinline__ void store8(void* base, int64_t at, int left, const float (&v)[8]) {
-  if constexpr (VEC) {
+  if constexpr (VEC == 8) {
     if constexpr (F32) {
       float4* q = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
       q[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -68,6 +88,16 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int left, const f
       for (int i = 0; i < 4; ++i) u[i] = f32_to_bf16(v[2 * i]) | static_cast<uint32_t>(f32_to_bf16(v[2 * i + 1])) << 16;
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = make_uint4(u[0], u[1], u[2], u[3]);
     }
+  } else if constexpr (VEC == 2) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+      if (i * 32 < left) {
+        if constexpr (F32)
+          *reinterpret_cast<float2*>(static_cast<float*>(base) + at + i * 32) = make_float2(v[i], v[i + 1]);
+        else
+          *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(base) + at + i * 32) =
+              f32_to_bf16(v[i]) | static_cast<uint32_t>(f32_to_bf16(v[i + 1])) << 16;
+      }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -79,7 +109,7 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int left, const f
       }
   }
 }
-template <bool VEC>
+template <int VEC>
 __device__ __forceinline__ void load8(bool f32, const void* base, int64_t at, int left, float (&v)[8]) {
   if (f32)
     load8<true, VEC>(base, at, left, v);
@@ -109,8 +139,8 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
-template <int STEPS, bool F32, bool VEC, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS > kBlock ? 1 : STEPS > 2 ? 3 : 6) rms_norm_kernel(const NormArgs a, const int per_row) {
+template <int STEPS, bool F32, int VEC, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS > kBlock ? 1 : STEPS > 2 ? 3 : STEPS == 2 ? 4 : 6) rms_norm_kernel(const NormArgs a, const int per_row) {
   __shared__ float partial[32];
   const int rows_here = blockDim.x / per_row, tid = threadIdx.x % per_row, lane = threadIdx.x % 32;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * rows_here + threadIdx.x / per_row;
@@ -122,7 +152,7 @@ __global__ void __launch_bounds__(THREADS, THREADS > kBlock ? 1 : STEPS > 2 ? 3 
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
     const int chunk = i * per_row + tid;  // of 8 columns
-    col[i] = VEC ? chunk * 8 : chunk / 32 * 256 + lane;
+    col[i] = VEC == 8 ? chunk * 8 : chunk / 32 * 256 + lane * VEC;
     const int left = a.cols - col[i];
 #pragma unroll
     for (int j = 0; j < 8; ++j) h[i][j] = 0.f;
@@ -166,13 +196,13 @@ __global__ void __launch_bounds__(THREADS, THREADS > kBlock ? 1 : STEPS > 2 ? 3 
     }
     if (a.codes != nullptr) {  // (the same for all threads)
       const int groups = (a.cols + 127) / 128;
-      uint32_t top[VEC ? 1 : 2] = {};
+      uint32_t top[VEC == 8 ? 1 : 2] = {};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        uint32_t& t = top[VEC ? 0 : j / 4];
+        uint32_t& t = top[VEC == 8 ? 0 : j / 4];
         t = max(t, __float_as_uint(y[j]) & 0x7FFFFFFFu);
       }
-      if constexpr (VEC) {
+      if constexpr (VEC == 8) {
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) top[0] = max(top[0], __shfl_xor_sync(0xffffffffu, top[0], o));
         if (left > 0) {
@@ -192,10 +222,15 @@ __global__ void __launch_bounds__(THREADS, THREADS > kBlock ? 1 : STEPS > 2 ? 3 
           if (b * 128 < left) {
             if (lane == 0) a.scales[row * groups + col[i] / 128 + b] = s.scale;
 #pragma unroll
-            for (int j = 4 * b; j < 4 * b + 4; ++j)
-              if (j * 32 < left)
-                a.codes[row * a.cols + col[i] + j * 32] =
-                    s.finite ? static_cast<uint8_t>(e4m3x2(scaled(y[j], s), 0.f)) : uint8_t{0};
+            for (int j = 4 * b; j < 4 * b + 4; j += VEC)
+              if (j * 32 < left) {
+                uint8_t* const to = a.codes + row * a.cols + col[i] + j * 32;
+                const uint32_t u = s.finite ? e4m3x2(scaled(y[j], s), VEC == 2 ? scaled(y[j + 1], s) : 0.f) : 0u;
+                if constexpr (VEC == 2)
+                  *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(u);
+                else
+                  *to = static_cast<uint8_t>(u);
+              }
           }
         }
       }
@@ -222,8 +257,9 @@ struct Raw {
 
 // Many rows of 513 to 8192 columns that start on 16 bytes: blocks that stay,
 // a row at a time, whose next row is on its way while this one is written
-// (16384 x 4096, residual and both results: 110 us a block per row, 105 with
-// 4 blocks an SM, 96.5 with 3: 6.3 TB/s).
+// (residual and both results, 16384 x 4096: 110 us a block per row, 105 with
+// 4 blocks an SM, 96.5 with 3: 6.3 TB/s; 2048 x 4096: 21 a block per row, 16;
+// 512 x 4096: 6.5, 7.3).
 template <int THREADS, int STEPS>
 constexpr int kRowBlocks = THREADS == kBlock ? (STEPS == 2 ? 3 : 2) : STEPS == 1 ? 8 : 6;  // of an SM
 
@@ -281,15 +317,15 @@ __global__ void __launch_bounds__(THREADS, kRowBlocks<THREADS, STEPS>) rms_norm_
       const int col = (i * THREADS + tid) * 8;
       float y[8] = {};
       if (col < a.cols) {
-        if (a.sum != nullptr) store8<F32, true>(a.sum, row * a.ld_sum + col, 8, h[i]);
-        load8<true>(a.weight_f32 != 0, a.weight, col, 8, y);
+        if (a.sum != nullptr) store8<F32, 8>(a.sum, row * a.ld_sum + col, 8, h[i]);
+        load8<8>(a.weight_f32 != 0, a.weight, col, 8, y);
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] *= h[i][j] * factor;
         if (a.out != nullptr) {
           if (a.out_f32)
-            store8<true, true>(a.out, row * a.ld_out + col, 8, y);
+            store8<true, 8>(a.out, row * a.ld_out + col, 8, y);
           else
-            store8<false, true>(a.out, row * a.ld_out + col, 8, y);
+            store8<false, 8>(a.out, row * a.ld_out + col, 8, y);
         }
       }
       if (a.codes != nullptr) {
@@ -313,14 +349,14 @@ __global__ void __launch_bounds__(THREADS, kRowBlocks<THREADS, STEPS>) rms_norm_
   }
 }
 
-template <int STEPS, bool F32, bool VEC>
+template <int STEPS, bool F32, int VEC>
 cudaError_t launch(const NormArgs& a, int per_row, cudaStream_t s) {
   const int threads = per_row < kBlock ? kBlock : per_row, rows_here = threads / per_row;
   const dim3 grid(static_cast<unsigned>((a.rows + rows_here - 1) / rows_here));
   if (threads > kBlock) return launch_kernel(rms_norm_kernel<STEPS, F32, VEC, kMaxThreads>, grid, dim3(threads), 0, s, a, per_row);
   return launch_kernel(rms_norm_kernel<STEPS, F32, VEC, kBlock>, grid, dim3(threads), 0, s, a, per_row);
 }
-template <bool F32, bool VEC>
+template <bool F32, int VEC>
 cudaError_t launch_steps(const NormArgs& a, int num_sms, cudaStream_t s) {
   const int chunks = (a.cols + 255) / 256 * 32;  // of 8 columns; unaligned rows take them by warps
   // Few rows: as many threads as there are chunks, the shortest way through a
@@ -331,10 +367,11 @@ cudaError_t launch_steps(const NormArgs& a, int num_sms, cudaStream_t s) {
   while (per_row < kMaxThreads && per_row < chunks &&
          (per_row < kBlock || a.rows <= 2 * num_sms || 4 * per_row < chunks))
     per_row *= 2;
-  if constexpr (VEC) {
-    if (a.rows >= 16 * num_sms && chunks > 64 && chunks <= 1024) {
+  if constexpr (VEC == 8) {
+    if (a.rows >= (chunks > 512 ? 3 : 4) * num_sms && chunks > 64 && chunks <= 1024) {
       auto rows = [&](auto kernel, int threads, int blocks) {
-        return launch_kernel(kernel, dim3(num_sms * blocks), dim3(threads), 0, s, a);
+        // (a block has a row at least: its first is fetched unasked)
+        return launch_kernel(kernel, dim3(static_cast<unsigned>(std::min<int64_t>(a.rows, num_sms * blocks))), dim3(threads), 0, s, a);
       };
       if (chunks <= 128) return rows(rms_norm_rows_kernel<128, 1, F32>, 128, kRowBlocks<128, 1>);
       if (chunks <= 256) return rows(rms_norm_rows_kernel<128, 2, F32>, 128, kRowBlocks<128, 2>);
@@ -348,19 +385,29 @@ cudaError_t launch_steps(const NormArgs& a, int num_sms, cudaStream_t s) {
   return launch<4, F32, VEC>(a, per_row, s);
 }
 
-bool on16(const void* p, int64_t ld, int size) {
-  return p == nullptr || ((reinterpret_cast<uintptr_t>(p) | static_cast<uint64_t>(ld) * size) & 15u) == 0;
+// Rows that all start on `bytes` bytes.
+bool on(const void* p, int64_t ld, int size, unsigned bytes) {
+  return p == nullptr || ((reinterpret_cast<uintptr_t>(p) | static_cast<uint64_t>(ld) * size) & (bytes - 1)) == 0;
+}
+// Whether the columns, and all rows, are whole pieces of n (8: of 16 bytes at least).
+bool in_pieces(const NormArgs& a, int n) {
+  const int size = a.f32 ? 4 : 2, out_size = a.out_f32 ? 4 : 2, weight_size = a.weight_f32 ? 4 : 2;
+  auto bytes = [&](int of) { return static_cast<unsigned>(n == 8 ? 16 : n * of); };
+  return a.cols % n == 0 && on(a.x, a.ld_x, size, bytes(size)) && on(a.residual, a.ld_residual, size, bytes(size)) &&
+         on(a.sum, a.ld_sum, size, bytes(size)) && on(a.weight, 0, 1, bytes(weight_size)) &&
+         on(a.out, a.ld_out, out_size, bytes(out_size)) && on(a.codes, 0, 1, static_cast<unsigned>(n));
+}
+
+template <bool F32>
+cudaError_t launch_type(const NormArgs& a, int num_sms, cudaStream_t s) {
+  if (in_pieces(a, 8)) return launch_steps<F32, 8>(a, num_sms, s);
+  return in_pieces(a, 2) ? launch_steps<F32, 2>(a, num_sms, s) : launch_steps<F32, 1>(a, num_sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t s) {
-  const int size = a.f32 ? 4 : 2;
-  const bool vec = a.cols % 8 == 0 && on16(a.x, a.ld_x, size) && on16(a.residual, a.ld_residual, size) &&
-                   on16(a.sum, a.ld_sum, size) && on16(a.weight, 0, 1) && on16(a.out, a.ld_out, a.out_f32 ? 4 : 2) &&
-                   (reinterpret_cast<uintptr_t>(a.codes) & 7u) == 0;
-  if (a.f32) return vec ? launch_steps<true, true>(a, num_sms, s) : launch_steps<true, false>(a, num_sms, s);
-  return vec ? launch_steps<false, true>(a, num_sms, s) : launch_steps<false, false>(a, num_sms, s);
+  return a.f32 ? launch_type<true>(a, num_sms, s) : launch_type<false>(a, num_sms, s);
 }
 
 }  // namespace cbmoe
