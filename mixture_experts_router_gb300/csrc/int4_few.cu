@@ -13,8 +13,8 @@
 // by two of 8 experts of 28672 x 4096: 67 us, 5.4 TB/s of what is read; 16 rows
 // by 6 of 64 of 4096 x 1536 in groups of 32, summed: 43 us, 3.4 TB/s).  Few
 // tiles are bound by latency (one row by 14336 x 4096: 10 us, 2.5 of them
-// before the first weights arrive); more than 8 rows of one matrix by the MMAs
-// and operands of two column tiles (16 rows by 4096 x 14336: 21 us).
+// before the first weights arrive); more than 8 rows of one matrix by the
+// instructions of two column tiles (16 rows by 4096 x 14336: 21 us).
 // Both kernels take tiles of 32 weight rows (SwiGLU: 16 features' gate and up
 // rows) in stages of 128 elements, 64 bytes of a row: codes, scales and zero
 // points come by cp.async into a ring in shared memory that belongs to one
@@ -229,12 +229,12 @@ struct Sums {  // m16n8 fragments: [fragment][n-tile]
 };
 
 // acc += the first `groups` groups of a stage.  fetch(n, i, b): n-tile n's
-// operands for this lane's i-th word of codes.  wide: the second n-tile too.
+// operands for this lane's i-th word of codes, of the first NT n-tiles.
 // x_scale: of the lane's two columns of each n-tile.  x_sums(n, i): the sums
 // of x over group i in these columns, or null: by MMAs of their own.
-template <int GROUP, int NT, bool F8, typename Fetch, typename XSums>
-__device__ __forceinline__ void add_stage(const uint8_t* stage, int groups, bool wide, Fetch&& fetch, XSums&& x_sums,
-                                          const float (&x_scale)[NT][2], Sums<NT>& acc) {
+template <int GROUP, int NT, bool F8, int TILES, typename Fetch, typename XSums>
+__device__ __forceinline__ void add_stage(const uint8_t* stage, int groups, Fetch&& fetch, XSums&& x_sums,
+                                          const float (&x_scale)[TILES][2], Sums<TILES>& acc) {
   constexpr bool kGiven = !std::is_same_v<std::decay_t<XSums>, std::nullptr_t>;
   constexpr int kWords = GROUP / 32;  // of a thread, row and group
   const int g = threadIdx.x % 32 >> 2, q = threadIdx.x & 3;
@@ -263,7 +263,6 @@ __device__ __forceinline__ void add_stage(const uint8_t* stage, int groups, bool
       uint32_t b[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        if (n > 0 && !wide) break;
         fetch(n, gi * kWords + w, b[n]);
         if constexpr (!kGiven) {
           if (w == 0)
@@ -280,7 +279,6 @@ __device__ __forceinline__ void add_stage(const uint8_t* stage, int groups, bool
         widen(v[2 * m + 1][w], a1);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          if (n > 0 && !wide) break;
           if (w == 0)
             mma_first<F8>(sum[m][n], a0[0], a1[0], a0[1], a1[1], b[n][0], b[n][1]);
           else
@@ -292,7 +290,6 @@ __device__ __forceinline__ void add_stage(const uint8_t* stage, int groups, bool
     if constexpr (kGiven) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        if (n > 0 && !wide) break;
         const float2 v = x_sums(n, gi);
         all[n][0] = v.x;
         all[n][1] = v.y;
@@ -309,7 +306,6 @@ __device__ __forceinline__ void add_stage(const uint8_t* stage, int groups, bool
       const float z1 = __uint_as_float(__byte_perm(z, 0x4B000000u, 0x7651)) - 8388608.f;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        if (n > 0 && !wide) break;
         float* c = acc.v[m][n];
         float t[4] = {fmaf(-z0, all[n][0], sum[m][n][0]), fmaf(-z0, all[n][1], sum[m][n][1]),
                       fmaf(-z1, all[n][0], sum[m][n][2]), fmaf(-z1, all[n][1], sum[m][n][3])};
@@ -678,17 +674,19 @@ struct RowsWorker {
       for (int i = 0; i < 2; ++i)
         scale[n][i] = F8 ? x_scales[(st - s0) * p.nx + min(n * 8 + 2 * q + i, count - 1)] : 1.f;
     }
-    const int word = p.nx * 64;
-    add_stage<GROUP, NT, F8>(
-        src, (p.k - st * kStageK) / GROUP, count > 8,
-        [&](int n, int i, uint32_t(&b)[4]) {
-          const uint4 e = *reinterpret_cast<const uint4*>(at[n] + i * word);
-          b[0] = e.x, b[1] = e.y, b[2] = e.z, b[3] = e.w;
-        },
-        [&](int n, int i) {
-          return *reinterpret_cast<const float2*>(x_sums + ((st - s0) * kGroups<GROUP> + i) * ((p.nx + 1) & ~1) + min(n * 8 + 2 * q, (count - 1) & ~1));
-        },
-        scale, acc);
+    const int word = p.nx * 64, left = (p.k - st * kStageK) / GROUP;
+    auto fetch = [&](int n, int i, uint32_t(&b)[4]) {
+      const uint4 e = *reinterpret_cast<const uint4*>(at[n] + i * word);
+      b[0] = e.x, b[1] = e.y, b[2] = e.z, b[3] = e.w;
+    };
+    auto sums_of = [&](int n, int i) {
+      return *reinterpret_cast<const float2*>(x_sums + ((st - s0) * kGroups<GROUP> + i) * ((p.nx + 1) & ~1) +
+                                              min(n * 8 + 2 * q, (count - 1) & ~1));
+    };
+    if (NT > 1 && count <= 8)
+      add_stage<GROUP, 1, F8>(src, left, fetch, sums_of, scale, acc);
+    else
+      add_stage<GROUP, NT, F8>(src, left, fetch, sums_of, scale, acc);
   }
 
   // The sums of a batch of tiles over the cluster's blocks; a tile's is finished by one of them.
@@ -887,7 +885,7 @@ struct SumWorker {
       scale[0][1] = xs[min(2 * q + 1, count - 1)];
     }
     add_stage<GROUP, 1, F8>(
-        src, (p.k - st * kStageK) / GROUP, false,
+        src, (p.k - st * kStageK) / GROUP,
         [&](int, int i, uint32_t(&b)[4]) {
           if constexpr (F8)
             x_e4m3(*reinterpret_cast<const uint2*>(at[0] + i * 32), b);
