@@ -816,6 +816,33 @@ def test_int4_streams_graphs_and_two_at_once():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_int4_clusters_on_streams_and_in_graphs(kind):
+    """Sums that blocks exchange, and a last stage of one group, several calls at once and replayed."""
+    g = gen(12)
+    k = 14368
+    by, one = int4_weights(g, 160, k, 32, 4), int4_weights(g, 48, k, 32)
+    x = randn(g, 12, k, dtype=BF16) if kind == "bf16" else fp8_rows(g, 12, k)
+    ids = torch.randint(0, 4, (12, 2), generator=g, device="cuda", dtype=torch.int32)
+    w = randn(g, 12, 2)
+    want = [check_int4(x, by, ids=ids, weights=w), check_int4(x, one)]
+    sides = [torch.cuda.Stream() for _ in range(4)]
+    for s in sides:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [(cb.int4_matmul_few(x, by, ids=ids, weights=w, stream=s), cb.int4_matmul_few(x, one, stream=s)) for s in sides for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, want[0]) and torch.equal(b, want[1]) for a, b in got)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a, b = cb.int4_matmul_few(x, by, ids=ids, weights=w), cb.int4_matmul_few(x, one)
+    ids.copy_(ids.flip(0))
+    w.copy_(w.flip(0) * 2)
+    for _ in range(2):
+        graph.replay()
+    assert torch.equal(a, cb.int4_matmul_few(x, by, ids=ids, weights=w)) and torch.equal(b, want[1])
+
+
+@pytest.mark.gpu
 def test_int4_first_call_of_a_form_in_a_capture():
     """Nothing that a first launch asks the driver for is refused while a stream is captured."""
     g = gen(15)
