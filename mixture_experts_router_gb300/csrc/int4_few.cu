@@ -108,7 +108,7 @@ struct Shared {
   int16_t first[kMaxPairs];     //   first entry of `pair`
   uint8_t count[kMaxPairs];     //   and number of them
   uint32_t bad[kMaxPairs / 32]; // pairs whose expert does not exist
-  int red[kWarps];              // where a warp has its sums of a tile, floats of the dynamic array
+  int red[kWarps];              // where a warp has its sums of more than 8 rows, floats of the dynamic array
   uint32_t starts[kMaxPairs / 32];  // entries of `pair` that begin a part
   uint32_t n_parts;
   int n_good;                   // pairs whose expert exists
@@ -408,8 +408,8 @@ __device__ __forceinline__ void store(const Int4Args& p, int64_t row, int col, f
 __device__ __forceinline__ bool is_bad(const Shared& s, int pair) { return s.bad[pair / 32] >> (pair % 32) & 1u; }
 
 // The parts: each expert's pairs in order, at most nx to a part.  A pair's
-// place is the number of smaller keys (expert, pair), compared one by one: 256
-// of them take 2 us, 32 the time of a barrier.  keys: scratch of kMaxPairs words.
+// place is the number of smaller keys (expert, pair), compared one by one.
+// keys: scratch of kMaxPairs words.
 __device__ __forceinline__ void find_parts(const Int4Args& p, Shared& s, int32_t* keys) {
   constexpr int kWordsOf = kMaxPairs / 32;
   static_assert(kMaxPairs <= kThreads, "a thread per pair");
@@ -735,22 +735,25 @@ struct RowsWorker {
         acc.clear();
         for (int st = s0 + mine; st < s1; st += p.ks) take(st, count, acc);
         // the warps' sums: two sets in turn, so that a tile's are read while the next one's are written
-        // (with more than 8 rows in the slot just read, which no one loads into meanwhile)
-        float* red = reds + (turn * kWarps + threadIdx.x / 32) * p.nx * kRedStride;
+        // (with more than 8 rows in the slot just read, which no one loads into before all have read it)
+        float* const set = reds + (turn * kWarps + first_warp) * p.nx * kRedStride;
         turn ^= 1;
         if constexpr (NT > 1) {
-          red = ring.used();
+          float* red = ring.used();
           __syncwarp();  // all lanes have read it
+          put_sums(acc, count, red);
+          if (lane == 0) s.red[threadIdx.x / 32] = static_cast<int>(red - reinterpret_cast<float*>(block));
+        } else {
+          put_sums(acc, count, set + mine * p.nx * kRedStride);
         }
-        put_sums(acc, count, red);
-        if (lane == 0) s.red[threadIdx.x / 32] = static_cast<int>(red - reinterpret_cast<float*>(block));
         meet();
         // another warp each time, where there are fewer rows than warps
         for (int t = (mine - ((sub - from) >> (4 - p.ks_bits))) & (p.ks - 1); t < count; t += p.ks) {
           float v = 0.f;
-          const float* all = reinterpret_cast<const float*>(block) + t * kRedStride + lane;
+          const int at = t * kRedStride + lane;
 #pragma unroll 4
-          for (int w = 0; w < p.ks; ++w) v += all[s.red[first_warp + w]];
+          for (int w = 0; w < p.ks; ++w)
+            v += NT > 1 ? reinterpret_cast<const float*>(block)[s.red[first_warp + w] + at] : set[w * p.nx * kRedStride + at];
           if constexpr (SPLIT)
             sums[((sub - lo) % p.batch * p.nx + t) * kRows + lane] = v;
           else

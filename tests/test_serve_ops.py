@@ -816,6 +816,18 @@ def test_int4_streams_graphs_and_two_at_once():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("k", [256, 512, 640])
+@pytest.mark.parametrize("rows", [1, 3, 16])
+def test_int4_many_short_tiles_repeat(k, rows):
+    """Warps that share a tile of a stage each, and are done with the next while one still adds this one's sums up."""
+    g = gen(k + rows)
+    m = int4_weights(g, 65536, k, 128)
+    x = randn(g, rows, k, dtype=BF16)
+    want = check_int4(x, m)
+    assert all(torch.equal(cb.int4_matmul_few(x, m), want) for _ in range(40))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["bf16", "fp8"])
 def test_int4_clusters_on_streams_and_in_graphs(kind):
     """Sums that blocks exchange, and a last stage of one group, several calls at once and replayed."""
