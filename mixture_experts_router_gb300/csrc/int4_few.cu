@@ -80,7 +80,6 @@ constexpr int kRows = 32;            // weight rows of a tile: two m16 fragments
 constexpr int kStageK = 128;         // elements of a row in a stage
 constexpr int kRowBytes = kStageK / 2;
 constexpr int kMaxPairs = 256;       // (row of x, slot)
-constexpr int kRedStride = 36;       // floats: the fragments' stores meet no bank twice
 constexpr int kMaxDepth = 5;
 constexpr int kMaxCluster = 8;
 constexpr int kXBytes = 2 * kStageK; // of a row of x in a stage, as MMA operands
@@ -94,6 +93,12 @@ template <int GROUP>
 constexpr int kZeros = kScales + kGroups<GROUP> * kRows * 4;
 template <int GROUP>
 constexpr int kStage = (kZeros<GROUP> + kGroups<GROUP> * kRows + 127) / 128 * 128;
+// Floats of a row of a warp's sums: with 36 the fragments' stores meet no bank
+// twice.  The sums of two column tiles stand in a stage that has been read, where
+// the zero points may be the constant ones that no load brings back: with 34
+// (some banks twice) all 16 rows end before them.
+template <int NT>
+constexpr int kRedStride = NT == 1 ? 36 : 34;
 // a row of x in sum_kernel's ring; for neighbours' reads to meet no bank twice
 // 8-bit rows are padded, and of 16-bit ones every other has its 64-byte halves swapped
 template <bool F8>
@@ -504,7 +509,7 @@ __device__ __forceinline__ void put_sums(const Sums<NT>& acc, int count, float* 
       if (t >= count) continue;
 #pragma unroll
       for (int m = 0; m < 2; ++m)
-        *reinterpret_cast<float2*>(red + t * kRedStride + 16 * m + 2 * g) = make_float2(acc.v[m][n][i], acc.v[m][n][2 + i]);
+        *reinterpret_cast<float2*>(red + t * kRedStride<NT> + 16 * m + 2 * g) = make_float2(acc.v[m][n][i], acc.v[m][n][2 + i]);
     }
 }
 
@@ -512,13 +517,14 @@ __device__ __forceinline__ void put_sums(const Sums<NT>& acc, int count, float* 
 // Dynamic shared memory: the rings (and first the keys), the warps' sums of
 // two tiles, those of a batch of tiles where a cluster splits k, x, its scales.
 template <int NT>
-constexpr int kRedRows = NT == 1 ? 2 * kWarps * kRedStride : 0;  // floats of the warps' sums, for a row of x
+constexpr int kRedRows = NT == 1 ? 2 * kWarps * kRedStride<NT> : 0;  // floats of the warps' sums, for a row of x
 constexpr int kBatchBytes = 8 * 1024;                            // of a batch's sums, about
 
 // SPLIT: k is split over the blocks of a cluster.
 template <int GROUP, int NT, bool F8, bool SPLIT>
 struct RowsWorker {
   static constexpr int kWords = GROUP / 32;
+  static_assert(NT == 1 || NT * 8 * kRedStride<NT> * 4 <= kZeros<GROUP>, "sums over the zero points");
   const Int4Args& p;
   Shared& s;
   uint8_t* const block;   // the dynamic array
@@ -736,7 +742,7 @@ struct RowsWorker {
         for (int st = s0 + mine; st < s1; st += p.ks) take(st, count, acc);
         // the warps' sums: two sets in turn, so that a tile's are read while the next one's are written
         // (with more than 8 rows in the slot just read, which no one loads into before all have read it)
-        float* const set = reds + (turn * kWarps + first_warp) * p.nx * kRedStride;
+        float* const set = reds + (turn * kWarps + first_warp) * p.nx * kRedStride<NT>;
         turn ^= 1;
         if constexpr (NT > 1) {
           float* red = ring.used();
@@ -744,16 +750,16 @@ struct RowsWorker {
           put_sums(acc, count, red);
           if (lane == 0) s.red[threadIdx.x / 32] = static_cast<int>(red - reinterpret_cast<float*>(block));
         } else {
-          put_sums(acc, count, set + mine * p.nx * kRedStride);
+          put_sums(acc, count, set + mine * p.nx * kRedStride<NT>);
         }
         meet();
         // another warp each time, where there are fewer rows than warps
         for (int t = (mine - ((sub - from) >> (4 - p.ks_bits))) & (p.ks - 1); t < count; t += p.ks) {
           float v = 0.f;
-          const int at = t * kRedStride + lane;
+          const int at = t * kRedStride<NT> + lane;
 #pragma unroll 4
           for (int w = 0; w < p.ks; ++w)
-            v += NT > 1 ? reinterpret_cast<const float*>(block)[s.red[first_warp + w] + at] : set[w * p.nx * kRedStride + at];
+            v += NT > 1 ? reinterpret_cast<const float*>(block)[s.red[first_warp + w] + at] : set[w * p.nx * kRedStride<NT> + at];
           if constexpr (SPLIT)
             sums[((sub - lo) % p.batch * p.nx + t) * kRows + lane] = v;
           else
@@ -792,6 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
 template <int GROUP, bool F8>
 struct SumWorker {
   static constexpr int kWords = GROUP / 32;
+  static_assert(8 * kRedStride<1> * 4 <= kZeros<GROUP>, "sums over the zero points");
   const Int4Args& p;
   Shared& s;
   Ring<GROUP> ring;
@@ -923,7 +930,7 @@ struct SumWorker {
         __syncwarp();
         for (int i = 0; i < count; ++i) {
           float& v = sums[s.token[first + i] * kRows + lane];
-          v = fmaf(s.w[first + i], red[i * kRedStride + lane], v);
+          v = fmaf(s.w[first + i], red[i * kRedStride<1> + lane], v);
         }
         __syncwarp();
       }

@@ -944,3 +944,35 @@ def test_norm_routing_and_experts_together():
     x.copy_(randn(g, T, d, dtype=BF16))
     graph.replay()
     assert all(torch.equal(a, b) for a, b in zip(held[1:], step()[1:]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("n,k", [(28672, 4096), (65536, 640), (8192, 14336)], ids=["wide", "short", "clusters"])
+def test_int4_without_zero_points_over_many_tiles(group, kind, n, k):
+    """Each warp takes several tiles, so that stages which have held sums are read again: the 8s have to be there."""
+    g = gen(n + group)
+    m = int4_weights(g, n, k, group, zeros=False)
+    for rows in (1, 8, 9, 15, 16):
+        x = randn(g, rows, k, dtype=BF16) if kind == "bf16" else fp8_rows(g, rows, k)
+        check_int4(x, m, dtype=F32)
+        if rows > 8:
+            check_int4(x, m, swiglu=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_int4_without_zero_points_by_expert(group, kind):
+    """Parts of 16 rows and fewer, several of them, by rows, SwiGLU and the weighted sum."""
+    g = gen(group)
+    n, k, experts = 28672, 768, 3
+    m = int4_weights(g, n, k, group, experts, zeros=False)
+    for rows, top in ((16, 1), (15, 2), (16, 3), (8, 2), (1, 2)):
+        x = randn(g, rows, k, dtype=BF16) if kind == "bf16" else fp8_rows(g, rows, k)
+        for ids in (torch.full((rows, top), 1, dtype=torch.int32, device="cuda"),
+                    torch.randint(0, experts, (rows, top), generator=g, device="cuda", dtype=torch.int32)):
+            check_int4(x, m, ids=ids, dtype=F32)
+            check_int4(x, m, ids=ids, swiglu=True)
+            check_int4(x, m, ids=ids, weights=randn(g, rows, top), dtype=F32)
