@@ -241,8 +241,9 @@ __device__ __noinline__ int exact_choice(const RouteArgs& a, int64_t t, double* 
   return mine;
 }
 
-// The experts of lanes 0 .. n - 1 in the order of their c in 64 bits: lane s
-// gets the s-th.  m: the largest logit, for the softmax.
+// The experts of lanes 0 .. n - 1, whose c are numbers, in the order of these
+// in 64 bits: lane s gets the s-th, the lanes from n on keep theirs.  m: the
+// largest logit, for the softmax.
 template <bool F32>
 __device__ __noinline__ int exact_order(const RouteArgs& a, int64_t t, int id, int n, float m, double* smem) {
   const int lane = threadIdx.x % 32;
@@ -270,7 +271,7 @@ __device__ __noinline__ int exact_order(const RouteArgs& a, int64_t t, int id, i
   __syncwarp();
   if (lane < n) order[rank] = id;
   __syncwarp();
-  const int mine = lane < n ? order[lane] : -1;
+  const int mine = lane < n ? order[lane] : id;
   __syncwarp();
   return mine;
 }
@@ -535,8 +536,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks<PER>)
           __syncwarp();
         }
         if (lane <= n) id = static_cast<int>(picks[lane].y);
+        // numbers come first; what is none stands in its place already, and compares with nothing
+        const int numbers = __popc(__ballot_sync(kAll, lane < n && picks[lane].x > kOutKey));
         __syncwarp();
-        id = n < 31 ? exact_order<F32>(a, t, id, n, m, c_smem[warp]) : exact_choice<F32>(a, t, c_smem[warp]);
+        id = n < 31 ? exact_order<F32>(a, t, id, numbers, m, c_smem[warp]) : exact_choice<F32>(a, t, c_smem[warp]);
         x = on ? logit_at<F32>(a, t, id) : -INFINITY;
       }
     }

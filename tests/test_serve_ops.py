@@ -976,3 +976,29 @@ def test_int4_without_zero_points_by_expert(group, kind):
             check_int4(x, m, ids=ids, dtype=F32)
             check_int4(x, m, ids=ids, swiglu=True)
             check_int4(x, m, ids=ids, weights=randn(g, rows, top), dtype=F32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("experts,groups,top_groups,top", [
+    (8, 1, 1, 8), (32, 1, 1, 16), (64, 8, 3, 8), (64, 8, 8, 16), (256, 1, 1, 12), (256, 8, 4, 16), (256, 32, 5, 9)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_route_near_ties_beside_what_is_no_number(experts, groups, top_groups, top, score, dtype):
+    """A few numbers a step apart (bf16: with scores far below the bias) among NaN and -inf, fewer than are chosen."""
+    g = gen(experts + top)
+    T, nan, inf = 60, float("nan"), float("inf")
+    rand = lambda *s: torch.rand(s, generator=g, device="cuda")  # noqa: E731
+    l = torch.where(rand(T, experts) < 0.5, nan, -inf)
+    l[:20], l[20:40] = nan, -inf
+    near = torch.full((T, experts), 0.5 if dtype is F32 else -12.0, dtype=dtype, device="cuda")
+    bits = torch.int32 if dtype is F32 else torch.int16
+    near = (near.view(bits) + torch.randint(0, 2, near.shape, generator=g, device="cuda").to(bits)).view(dtype)
+    count = torch.randint(2, 7, (T, 1), generator=g, device="cuda")
+    l = torch.where(rand(T, experts).argsort(-1).argsort(-1) < count, near.float(), l)
+    if dtype is BF16:
+        l[:, 0] = 0.0
+    l = l.to(dtype)
+    for bias in (None, torch.full((experts,), 0.9, device="cuda"), torch.full((experts,), -0.25, device="cuda")):
+        for group_score in ("top2", "max")[:2 if groups > 1 else 1]:
+            check_route(l, top, bias, score, groups, top_groups, group_score)
+            check_route(l, top, bias, score, groups, top_groups, group_score, renormalise=False)
