@@ -21,9 +21,10 @@
 // best; bf16 logits have nothing in the four bits.  Otherwise c is off by at
 // most 2^-21 (sigmoid) or 2^-20 of the largest score (softmax), half a step of
 // its own and the four bits.  Where two neighbours in the order are nearer than
-// twice that and not of equal logits and biases, those experts are put in order
-// in 64 bits (exact_order); where the last group kept and the first dropped
-// are, the groups near them get their values in 64 bits.  Weights are computed
+// twice that and not of equal logits and biases, or the last one chosen and any
+// that is left, those experts are put in order in 64 bits (exact_order); where
+// the last group kept and the first dropped are near, the groups near them get
+// their values in 64 bits.  Weights are computed
 // from the chosen logits, relative to the largest of them, so that they neither
 // vanish nor overflow.
 //
@@ -523,24 +524,37 @@ __global__ void __launch_bounds__(kThreads, kBlocks<PER>)
         const float u = key_number(k), v = key_number(following);
         return following <= kOutKey || u - v > near + fmaxf(fabsf(u), fabsf(v)) * kCut;
       };
+      auto same = [&](float of, int e, int other) {  // equal logits and biases: a tie, which the index decides
+        return of == logit_at<F32>(a, t, other) && (MODE == kByLogit || __ldg(a.bias + e) == __ldg(a.bias + other));
+      };
       const uint32_t next_key = __shfl_down_sync(kAll, own.x, 1);
       const int next = __shfl_down_sync(kAll, id, 1);
       bool fine = !on || apart(own.x, next_key);
-      if (!fine) fine = x == logit_at<F32>(a, t, next) && (MODE == kByLogit || __ldg(a.bias + id) == __ldg(a.bias + next));
       if (!__all_sync(kAll, fine)) {
-        // all that may belong before the k-th, and one that does not; then these in 64 bits
-        int n = a.top_k;
-        while (n < 31 && !apart(picks[n - 1].x, picks[n].x)) {
-          __syncwarp();
-          pick(++n);
-          __syncwarp();
+        if (!fine) fine = same(x, id, next);
+        // the last one beside all that are left, each lane's
+        const uint2 last = picks[a.top_k - 1];
+        const int last_id = static_cast<int>(last.y);
+        if (!apart(last.x, picks[a.top_k].x) && head != 0u) {
+          const float lx = logit_at<F32>(a, t, last_id);
+          for (const uint32_t* q = at; fine && !apart(last.x, *q & ~kPlace); q += 32)
+            fine = same(lx, last_id, first + static_cast<int>(kPlace - (*q & kPlace)));
         }
-        if (lane <= n) id = static_cast<int>(picks[lane].y);
-        // numbers come first; what is none stands in its place already, and compares with nothing
-        const int numbers = __popc(__ballot_sync(kAll, lane < n && picks[lane].x > kOutKey));
-        __syncwarp();
-        id = n < 31 ? exact_order<F32>(a, t, id, numbers, m, c_smem[warp]) : exact_choice<F32>(a, t, c_smem[warp]);
-        x = on ? logit_at<F32>(a, t, id) : -INFINITY;
+        if (!__all_sync(kAll, fine)) {
+          // all that may belong before the k-th, and one that does not; then these in 64 bits
+          int n = a.top_k;
+          while (n < 31 && !apart(picks[n - 1].x, picks[n].x)) {
+            __syncwarp();
+            pick(++n);
+            __syncwarp();
+          }
+          if (lane <= n) id = static_cast<int>(picks[lane].y);
+          // numbers come first; what is none stands in its place already, and compares with nothing
+          const int numbers = __popc(__ballot_sync(kAll, lane < n && picks[lane].x > kOutKey));
+          __syncwarp();
+          id = n < 31 ? exact_order<F32>(a, t, id, numbers, m, c_smem[warp]) : exact_choice<F32>(a, t, c_smem[warp]);
+          x = on ? logit_at<F32>(a, t, id) : -INFINITY;
+        }
       }
     }
     // the weights

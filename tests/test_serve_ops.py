@@ -1002,3 +1002,48 @@ def test_route_near_ties_beside_what_is_no_number(experts, groups, top_groups, t
         for group_score in ("top2", "max")[:2 if groups > 1 else 1]:
             check_route(l, top, bias, score, groups, top_groups, group_score)
             check_route(l, top, bias, score, groups, top_groups, group_score, renormalise=False)
+
+
+def nearly_level(g, T, experts, dtype, base):
+    """Rows of one value, a few elements of which are a step away from it."""
+    bits = torch.int32 if dtype is F32 else torch.int16
+    l = torch.full((T, experts), base, dtype=dtype, device="cuda").view(bits)
+    share = torch.tensor([0.0, 0.02, 0.1, 0.4], device="cuda")[torch.arange(T, device="cuda") % 4]
+    return (l + (torch.rand((T, experts), generator=g, device="cuda") < share[:, None]).to(bits)).view(dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("experts,groups,top_groups", [(8, 1, 1), (37, 1, 1), (64, 8, 2), (256, 1, 1), (256, 8, 4), (256, 32, 7)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_the_last_choice_among_equals_and_near_ones(experts, groups, top_groups, score):
+    """Equal values at the last choice, and behind them one that is a step larger: it belongs before them."""
+    g = gen(experts * 3 + groups)
+    l = nearly_level(g, 120, experts, F32, 1.0)
+    l[0, :3] = torch.tensor([1.0, 1.0, 1.0 + 2.0 ** -23], device="cuda")
+    l[1] = 1.0
+    l[1, experts - 1] = 1.0 + 2.0 ** -23
+    low = nearly_level(g, 120, experts, F32, -12.0)                      # scores far below the bias
+    low16 = nearly_level(g, 120, experts, BF16, -12.0)
+    low[:, experts // 2], low16[:, experts // 2] = 0.0, 0.0
+    steps = torch.full((experts,), 0.25, device="cuda")
+    steps[experts // 3] += 2.0 ** -20
+    for top in (1, 2, 3, 5):
+        for group_score in ("top2", "max")[:2 if groups > 1 else 1]:
+            for bias in (None, torch.full((experts,), 0.25, device="cuda"), steps):
+                check_route(l, top, bias, score, groups, top_groups, group_score)
+                check_route(low, top, bias, score, groups, top_groups, group_score)
+                check_route(low16, top, bias, score, groups, top_groups, group_score)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("experts,top", [(8, 1), (8, 4), (256, 2), (256, 5)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_the_last_choice_beside_what_is_no_number(experts, top, score):
+    g = gen(experts + top)
+    l = nearly_level(g, 90, experts, F32, 0.5)
+    rand = torch.rand(l.shape, generator=g, device="cuda")
+    l[30:60] = torch.where(rand[30:60] < 0.7, float("nan"), l[30:60])
+    l[60:] = torch.where(rand[60:] < 0.4, float("nan"), torch.where(rand[60:] < 0.8, -float("inf"), l[60:]))
+    for bias in (None, torch.full((experts,), 0.9, device="cuda")):
+        check_route(l, top, bias, score)
+        check_route(l, top, bias, score, 4, 2)
