@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<PER>)
     if (__any_sync(kAll, isnan(odd) && mine > 0)) {
 #pragma unroll
       for (int p = 0; p < PER; ++p) {
-        uint32_t k = number_key(c[p]);
+        uint32_t k = number_key(fmaxf(c[p], -FLT_MAX));  // (of -inf the four bits would leave a NaN)
         if (l[p] == -INFINITY) k = kOutKey;
         if (isnan(l[p]) || isnan(bias[p])) k = kNaNKey;
         key[p] = (k & ~kPlace) | (kPlace - p);

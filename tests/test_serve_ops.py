@@ -1047,3 +1047,24 @@ def test_route_the_last_choice_beside_what_is_no_number(experts, top, score):
     for bias in (None, torch.full((experts,), 0.9, device="cuda")):
         check_route(l, top, bias, score)
         check_route(l, top, bias, score, 4, 2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("experts,groups", [(16, 4), (64, 32), (256, 32), (256, 8), (12, 3)])
+@pytest.mark.parametrize("group_score", ["top2", "max"])
+def test_route_experts_masked_by_their_bias(experts, groups, group_score):
+    """A bias of -inf makes a choice the last of the numbers: behind it come experts and groups that are out."""
+    g = gen(experts + groups)
+    size = experts // groups
+    l = randn(g, 40, experts)
+    l[:, :size] = -float("inf")                           # the first group is out
+    l[20:, size:2 * size] = float("nan")
+    for masked in (size, size - 1):                       # of the last two groups all, or all but one
+        bias = randn(g, experts, std=0.1)
+        for last in (1, 2):
+            at = experts - last * size
+            bias[at:at + masked] = -float("inf")
+        for top_groups in sorted({1, groups // 2, groups - 1, groups}):
+            for top in sorted({1, min(size * top_groups, 4), min(size * top_groups, 16)}):
+                for score in ("sigmoid", "softmax"):
+                    check_route(l, top, bias, score, groups, top_groups, group_score)
