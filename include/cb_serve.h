@@ -27,8 +27,8 @@ extern "C" {
  *   out = y                     (rounded once, if asked for)
  *   codes, scales               (if asked for): per row and 128 columns (the
  *     last ones of a row may be fewer) a scale s = max|y| / 448 and the e4m3
- *     code nearest y / s, ties to the even one.  Y = s v(code).  A group of
- *     zeros has the scale 0 and zero codes; one that holds a NaN or an infinity
+ *     code nearest the quotient y / s (y, s and the quotient in fp32), ties to
+ *     the even one.  Y = s v(code).  A group of zeros has the scale 0 and zero codes; one that holds a NaN or an infinity
  *     a NaN scale and zero codes.
  * The norm is taken of the unrounded h; the sum of squares is fp32 (h up to
  * about 1e18).  In place: sum may be x or residual itself and out may be x

@@ -5,7 +5,7 @@
 //
 // Bound by memory: every element is read and written once, a row staying in
 // registers between its sum of squares and its results (16384 x 4096 bf16 with
-// the residual and both results: 96 us, 6.3 TB/s; one row of 4096: 2.4 us, the
+// the residual and both results: 95 us, 6.4 TB/s; one row of 4096: 2.5 us, the
 // launch and two round trips).  R threads share a row
 // (a power of two from 32), each holding up to 4 times 8 elements.  Rows that
 // start on 16 bytes: a thread's elements are 8 in a row (16 bytes of bf16),
@@ -117,26 +117,48 @@ __device__ __forceinline__ void load8(bool f32, const void* base, int64_t at, in
     load8<false, VEC>(base, at, left, v);
 }
 
-// The scale of a group whose largest magnitude has the bits `top`, and what
-// its elements are multiplied by (0: divide by the scale, which is too small
-// for a reciprocal).
+// The scale of a group whose largest magnitude has the bits `top`.
 struct GroupScale {
-  float scale, inverse;
+  float scale;
   bool finite;
 };
 __device__ __forceinline__ GroupScale group_scale(uint32_t top) {
   GroupScale r;
   r.finite = top < 0x7F800000u;
   r.scale = r.finite ? __uint_as_float(top) / 448.f : __int_as_float(0x7FC00000);
-  r.inverse = r.scale > 1e-30f ? 1.f / r.scale : 0.f;
   return r;
-}
-__device__ __forceinline__ float scaled(float y, const GroupScale& s) {
-  if (s.inverse > 0.f) return y * s.inverse;
-  return s.scale > 0.f ? y / s.scale : 0.f;  // (a NaN scale: zero)
 }
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+// What a code of a finite group is nearest to.
+__device__ __forceinline__ float quotient(float y, float scale) { return scale > 0.f ? y / scale : 0.f; }
+// The codes of eight elements.  A product with the reciprocal may lie on the
+// other side of a border between two codes; but where products with a little
+// less and with a little more than it (2^-21 of it: it, the factors, the
+// products and the quotient are rounded, 2^-24 each) give the same codes, so do
+// the quotients in between.  Else, in one of some 400 warps, they are divided
+// (16384 x 4096 bf16, residual and both results: 95.6 us, with divisions alone
+// 110.6).  fp32 rows have the time to divide (8192 x 4096, residual, codes: 70.5
+// us, by products 73.5).
+template <bool DIVIDE>
+__device__ __forceinline__ uint2 codes8(const float (&y)[8], float scale) {
+  uint32_t u[2] = {}, v[2] = {};
+  if constexpr (!DIVIDE) {
+    const bool fine = scale > 1e-30f && scale < 1e30f;  // the reciprocal and the products are normal numbers
+    const float inverse = 1.f / scale, less = fine ? inverse * (1.f - 0x1p-21f) : 0.f,
+                more = fine ? inverse * (1.f + 0x1p-21f) : INFINITY;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      u[j / 2] |= e4m3x2(y[2 * j] * less, y[2 * j + 1] * less) << (j % 2 * 16);
+      v[j / 2] |= e4m3x2(y[2 * j] * more, y[2 * j + 1] * more) << (j % 2 * 16);
+    }
+    if (u[0] == v[0] && u[1] == v[1]) return make_uint2(u[0], u[1]);
+    u[0] = u[1] = 0u;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) u[j / 2] |= e4m3x2(quotient(y[2 * j], scale), quotient(y[2 * j + 1], scale)) << (j % 2 * 16);
+  return make_uint2(u[0], u[1]);
 }
 
 template <int STEPS, bool F32, int VEC, int THREADS>
@@ -207,12 +229,7 @@ __global__ void __launch_bounds__(THREADS, THREADS > kBlock ? 1 : STEPS > 2 ? 3 
         for (int o = 8; o > 0; o >>= 1) top[0] = max(top[0], __shfl_xor_sync(0xffffffffu, top[0], o));
         if (left > 0) {
           const GroupScale s = group_scale(top[0]);
-          uint32_t u[2] = {};
-          if (s.finite) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) u[j / 2] |= e4m3x2(scaled(y[2 * j], s), scaled(y[2 * j + 1], s)) << (j % 2 * 16);
-          }
-          *reinterpret_cast<uint2*>(a.codes + row * a.cols + col[i]) = make_uint2(u[0], u[1]);
+          *reinterpret_cast<uint2*>(a.codes + row * a.cols + col[i]) = s.finite ? codes8<F32>(y, s.scale) : make_uint2(0u, 0u);
           if (lane % 16 == 0) a.scales[row * groups + col[i] / 128] = s.scale;
         }
       } else {
@@ -225,7 +242,7 @@ __global__ void __launch_bounds__(THREADS, THREADS > kBlock ? 1 : STEPS > 2 ? 3 
             for (int j = 4 * b; j < 4 * b + 4; j += VEC)
               if (j * 32 < left) {
                 uint8_t* const to = a.codes + row * a.cols + col[i] + j * 32;
-                const uint32_t u = s.finite ? e4m3x2(scaled(y[j], s), VEC == 2 ? scaled(y[j + 1], s) : 0.f) : 0u;
+                const uint32_t u = s.finite ? e4m3x2(quotient(y[j], s.scale), VEC == 2 ? quotient(y[j + 1], s.scale) : 0.f) : 0u;
                 if constexpr (VEC == 2)
                   *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(u);
                 else
@@ -336,12 +353,7 @@ __global__ void __launch_bounds__(THREADS, kRowBlocks<THREADS, STEPS>) rms_norm_
         for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         if (col < a.cols) {
           const GroupScale s = group_scale(top);
-          uint32_t u[2] = {};
-          if (s.finite) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) u[j / 2] |= e4m3x2(scaled(y[2 * j], s), scaled(y[2 * j + 1], s)) << (j % 2 * 16);
-          }
-          *reinterpret_cast<uint2*>(a.codes + row * a.cols + col) = make_uint2(u[0], u[1]);
+          *reinterpret_cast<uint2*>(a.codes + row * a.cols + col) = s.finite ? codes8<F32>(y, s.scale) : make_uint2(0u, 0u);
           if (lane % 16 == 0) a.scales[row * ((a.cols + 127) / 128) + col / 128] = s.scale;
         }
       }

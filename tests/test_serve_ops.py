@@ -1068,3 +1068,31 @@ def test_route_experts_masked_by_their_bias(experts, groups, group_score):
             for top in sorted({1, min(size * top_groups, 4), min(size * top_groups, 16)}):
                 for score in ("sigmoid", "softmax"):
                     check_route(l, top, bias, score, groups, top_groups, group_score)
+
+
+def check_codes(r):
+    """Codes of an fp32 result and its scales: the e4m3 nearest the fp32 quotient (a double quotient of two
+    floats, rounded to fp32, is the rounded quotient), bit for bit."""
+    rows, cols = r.out.shape
+    s = r.fp8.scales.double().repeat_interleave(128, -1)[:, :cols]
+    q = torch.where(s > 0, (r.out.double() / s.clamp_min(1e-300)).float().double(), 0.0)
+    assert torch.equal(r.fp8.codes.view(torch.float8_e4m3fn).double(), e4m3_64(q))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", [(1, 128), (40, 500), (3000, 1025), (700, 4096), (5000, 2048), (3000, 8192), (9, 16384)])
+def test_norm_codes_are_the_nearest_of_the_quotient(rows, cols):
+    """Quotients at and beside the borders between two codes: weights that are such borders, times what a row gives."""
+    g = gen(rows + cols)
+    step = torch.arange(8, 16, device="cuda", dtype=F32)
+    border = torch.cat([(step[None] + 0.5) * torch.exp2(torch.arange(-9.0, 6.0, device="cuda"))[:, None],
+                        (torch.arange(0, 8, device="cuda")[None] + 0.5) * 2.0 ** -9]).flatten()
+    border = border[border < 448]
+    weight = border[torch.randint(0, border.numel(), (cols,), generator=g, device="cuda")]
+    weight[::128] = 448.0                             # the largest of each group
+    x = randn(g, rows, 1) * (randn(g, rows, cols) > 0).float().mul(2).sub(1)      # a row's elements differ in sign alone
+    for w in (weight, weight * 0.7, 1 + randn(g, cols, std=0.3)):
+        check_codes(cb.rms_norm(x, w, want="both", eps=1e-12))
+    check_codes(cb.rms_norm(x.to(BF16), weight, want="both", dtype=F32))
+    check_codes(cb.rms_norm(randn(g, rows, cols), weight, residual=x, want="both"))
+    check_codes(cb.rms_norm(x, weight * 1e-40, want="both"))                       # scales that are no normal numbers
