@@ -28,8 +28,8 @@ extern "C" {
  *   codes, scales               (if asked for): per row and 128 columns (the
  *     last ones of a row may be fewer) a scale s = max|y| / 448 and the e4m3
  *     code nearest the quotient y / s (y, s and the quotient in fp32), ties to
- *     the even one.  Y = s v(code).  A group of zeros has the scale 0 and zero codes; one that holds a NaN or an infinity
- *     a NaN scale and zero codes.
+ *     the even one.  Y = s v(code).  A group of zeros has the scale 0 and zero
+ *     codes; one that holds a NaN or an infinity a NaN scale and zero codes.
  * The norm is taken of the unrounded h; the sum of squares is fp32 (h up to
  * about 1e18).  In place: sum may be x or residual itself and out may be x
  * itself (the same pointer, stride and type); otherwise nothing that is
@@ -120,8 +120,10 @@ CB_API cb_status_t cb_route(const cb_route_t *args, void *stream);
  *   y[r][j] = sum_i x[r][i] W[j][i],
  * x in bf16, or e4m3 codes with a scale per row and 128 columns (cb_rms_norm's).
  * The integers code - zero are exact operands and every group's sum meets its
- * scale in fp32: nothing is rounded before the result.  (Elements of bf16 x
- * from 2^62 on count as infinite, and what is below 2^-57 may be lost.)
+ * scale in fp32: nothing is rounded before the result.  An infinite element of x
+ * makes its row of out NaN, whatever its weights: it meets the zero points too.
+ * (Elements of bf16 x from 2^64 on may count as infinite, and what is below
+ * 2^-57 may be lost.  Scales of W are below 2^58 in magnitude.)
  *
  * One matrix (n_experts = 1, ids NULL): out [n_tokens][n].  With ids
  * [n_tokens][top_k] (device, in [0, n_experts)) one matrix per expert, and

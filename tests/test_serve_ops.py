@@ -1096,3 +1096,27 @@ def test_norm_codes_are_the_nearest_of_the_quotient(rows, cols):
     check_codes(cb.rms_norm(x.to(BF16), weight, want="both", dtype=F32))
     check_codes(cb.rms_norm(randn(g, rows, cols), weight, residual=x, want="both"))
     check_codes(cb.rms_norm(x, weight * 1e-40, want="both"))                       # scales that are no normal numbers
+
+
+@pytest.mark.gpu
+def test_int4_ranges_of_x_and_of_the_scales():
+    """What the header promises: x up to 2^64, scales up to 2^58, and NaN rows for infinite elements."""
+    g = gen(23)
+    for rows in (3, 16):
+        m = int4_weights(g, 96, 512, 64)
+        big = randn(g, rows, 512).clamp(-1.9, 1.9).to(BF16) * 2.0 ** 63
+        check_int4(big, m, dtype=F32)
+        for scale in (2.0 ** 57, 2.0 ** -100):
+            for zeros in (True, False):
+                check_int4((randn(g, rows, 512) * 2.0 ** -20).to(BF16), int4_weights(g, 96, 512, 64, zeros=zeros, scale=scale), dtype=F32)
+        check_int4(fp8_rows(g, rows, 512), int4_weights(g, 96, 512, 64, scale=2.0 ** 57), dtype=F32)
+        by = int4_weights(g, 96, 512, 64, 4)
+        ids = torch.randint(0, 4, (rows, 2), generator=g, device="cuda", dtype=torch.int32)
+        w = torch.ones(rows, 2, device="cuda")
+        x = randn(g, rows, 512, dtype=BF16)
+        clean = cb.int4_matmul_few(x, m), cb.int4_matmul_few(x, by, ids=ids), cb.int4_matmul_few(x, by, ids=ids, weights=w)
+        x[1, 77], x[2, 5], x[2, 6] = -float("inf"), float("inf"), float("inf")
+        got = cb.int4_matmul_few(x, m), cb.int4_matmul_few(x, by, ids=ids), cb.int4_matmul_few(x, by, ids=ids, weights=w)
+        rest = [t for t in range(rows) if t not in (1, 2)]
+        for a, b in zip(got, clean):
+            assert a[[1, 2]].isnan().all() and torch.equal(a[rest], b[rest])
