@@ -1059,8 +1059,9 @@ cudaError_t launch_rows(Int4Args a, int num_sms, cudaStream_t st) {
   const int64_t of = std::min(at_most, clusters);
   a.slice = (nst + a.cluster - 1) / a.cluster;
   // Sixteen warps on one tile, or groups of them on several: what leaves the
-  // busiest with the least (a tile's end costs about a stage), with 256
-  // bytes of each row read together if there are that many.
+  // busiest with the least, with 256 bytes of each row read together if there
+  // are that many.  A tile's end counts as a stage (one row by 14336 x 4096: 10.4 us,
+  // 11.7 where it counts as none; as two or three: the same, here and at 11 other shapes).
   const int64_t share = (about + of - 1) / of;
   int64_t least = INT64_MAX;
   int fewest = 1;
@@ -1118,8 +1119,10 @@ cudaError_t launch_form(Int4Args a, int num_sms, cudaStream_t s) {
   a.cluster = 1;
   a.nx = std::min(rows, 8);
   if (a.w != nullptr) return launch_sum<GROUP, F8>(a, num_sms, s);
-  // Parts of up to 16 rows where experts have more than 4 on average; else the few with more than 8 are taken twice.
-  if (rows > 8 && (a.ids == nullptr || a.pairs > 4 * a.n_experts)) a.nx = rows;
+  // Parts of up to 16 rows where experts have more than 8 on average; else the few with more than 8 are taken twice
+  // (28672 x 4096, SwiGLU, 16 rows by top of E experts, parts of 16 and of 8: 8 of 8 143 and 184 us, 3 of 4 77 and 89;
+  // 4 of 8 136 and 137, 2 of 4 75 and 72, 3 of 8 136 and 114, 2 of 8 127 and 96).
+  if (rows > 8 && (a.ids == nullptr || a.pairs > 8 * a.n_experts)) a.nx = rows;
   // x has to fit: one matrix splits k over a cluster (its blocks walk the same
   // tiles, whatever is in memory), experts take fewer rows at a time
   const int nst = (a.k + kStageK - 1) / kStageK;
