@@ -560,12 +560,17 @@ __global__ void __launch_bounds__(kThreads, kBlocks<PER>)
     // the weights
     float w = x == -INFINITY ? 0.f : a.softmax ? expf(x - m) : 1.f / (1.f + expf(-x));
     if (a.renormalise) {
-      if (a.softmax || __all_sync(kAll, !(x >= -60.f))) {
-        // relative to the largest of them: far below 0 the sigmoid is the exponential
+      if (a.softmax || __any_sync(kAll, on && x < -60.f)) {  // relative to the largest of them
         float lm = isnan(x) ? -INFINITY : x;
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) lm = fmaxf(lm, __shfl_xor_sync(kAll, lm, o));
-        w = x == -INFINITY ? 0.f : expf(x - lm);
+        if (a.softmax) {
+          w = x == -INFINITY ? 0.f : expf(x - lm);
+        } else if (x > -INFINITY) {
+          // s(x) = e^min(x, 0) / (1 + e^-|x|); the difference with what its rounding leaves, exactly: |from| >= |to|
+          const float from = fminf(x, 0.f), to = fminf(lm, 0.f), d = from - to, e = expf(d);
+          w = fmaf(e, (from - d) - to, e) / (1.f + expf(-fabsf(x)));
+        }
       }
       float sum = w;  // of the first 16 lanes
 #pragma unroll

@@ -1120,3 +1120,19 @@ def test_int4_ranges_of_x_and_of_the_scales():
         rest = [t for t in range(rows) if t not in (1, 2)]
         for a, b in zip(got, clean):
             assert a[[1, 2]].isnan().all() and torch.equal(a[rest], b[rest])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_route_weights_of_scores_far_below_the_largest(dtype):
+    """Sigmoid scores that vanish in 32 bits beside larger ones that are small too: what remains after the division
+    by their sum does not."""
+    g = gen(31)
+    l = randn(g, 120, 16, std=40.0) - torch.linspace(0, 100, 120, device="cuda")[:, None]
+    l[0, :4] = torch.tensor([-20.0, -95.0, -59.5, -100.25], device="cuda")
+    l[0, 4:] = -float("inf")
+    l[1], l[2, 1:] = -90.0, -float("inf")
+    for bias in (None, randn(g, 16) * 2):
+        for top in (1, 2, 5, 16):
+            check_route(l.to(dtype), top, bias, "sigmoid")
+            check_route(l.to(dtype), top, bias, "sigmoid", scale=2.5)
