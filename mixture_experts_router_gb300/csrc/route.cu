@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<PER>)
     if (__any_sync(kAll, isnan(odd) && mine > 0)) {
 #pragma unroll
       for (int p = 0; p < PER; ++p) {
-        uint32_t k = number_key(fmaxf(c[p], -FLT_MAX));  // (of -inf the four bits would leave a NaN)
+        uint32_t k = number_key(fminf(fmaxf(c[p], -FLT_MAX), FLT_MAX));  // (of -inf the four bits would leave a NaN)
         if (l[p] == -INFINITY) k = kOutKey;
         if (isnan(l[p]) || isnan(bias[p])) k = kNaNKey;
         key[p] = (k & ~kPlace) | (kPlace - p);
@@ -470,7 +470,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks<PER>)
       const int gn = __shfl_sync(kAll, numbers, from);
       auto score = [&](float x) { return a.softmax ? exp_fast(x - m) : sigmoid_fast(x); };
       float v = NAN;
-      if (gn > 0) v = one || gn == 1 ? gb : MODE == kByLogit ? score(gb) + score(gs) : gb + gs;
+      // (finite, so that what is near the cut can be told: infinite biases are looked at again in 64 bits)
+      if (gn > 0) v = one || gn == 1 ? gb : MODE == kByLogit ? score(gb) + score(gs) : fminf(fmaxf(gb + gs, -FLT_MAX), FLT_MAX);
       if (MODE == kByLogit && !one && gn == 1) v = score(gb);
       uint32_t kept = 0u, left = lane < a.n_groups && !isnan(v) ? number_key(v) : 0u, last = 0u;
       uint32_t in_play = lane < a.n_groups ? 1u : 0u;

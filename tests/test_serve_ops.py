@@ -1136,3 +1136,21 @@ def test_route_weights_of_scores_far_below_the_largest(dtype):
         for top in (1, 2, 5, 16):
             check_route(l.to(dtype), top, bias, "sigmoid")
             check_route(l.to(dtype), top, bias, "sigmoid", scale=2.5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("experts,groups", [(64, 16), (128, 32), (256, 16), (40, 8)])
+@pytest.mark.parametrize("infinity", [-float("inf"), float("inf")], ids=["masked", "forced"])
+def test_route_groups_of_infinite_values(experts, groups, infinity):
+    """Groups whose values are infinite tie, whether one of their two best is or both; behind -inf come those that are out."""
+    g = gen(experts + 7)
+    l = randn(g, 30, experts)
+    rand = torch.rand(l.shape, generator=g, device="cuda")
+    l[10:20] = torch.where(rand[10:20] < 0.4, -float("inf"), l[10:20])
+    l[20:] = torch.where(rand[20:] < 0.5, float("nan"), torch.where(rand[20:] < 0.7, -float("inf"), l[20:]))
+    for share in (0.1, 0.3, 0.7):
+        bias = torch.where(torch.rand((experts,), generator=g, device="cuda") < share, infinity, randn(g, experts, std=0.1))
+        for top_groups in (1, groups // 2, groups - 3, groups):
+            for score in ("sigmoid", "softmax"):
+                for group_score in ("top2", "max"):
+                    check_route(l, min(8, top_groups * experts // groups), bias, score, groups, top_groups, group_score)
