@@ -30,8 +30,8 @@ extern "C" {
  *     code nearest the quotient y / s (y, s and the quotient in fp32), ties to
  *     the even one.  Y = s v(code).  A group of zeros has the scale 0 and zero
  *     codes; one that holds a NaN or an infinity a NaN scale and zero codes.
- * The norm is taken of the unrounded h; the sum of squares is fp32 (h up to
- * about 1e18).  In place: sum may be x or residual itself and out may be x
+ * The norm is taken of the unrounded h; the sum of squares is fp32 (|h| up to
+ * about 1e18; what is below 1e-18 may vanish beside eps = 0).  In place: sum may be x or residual itself and out may be x
  * itself (the same pointer, stride and type); otherwise nothing that is
  * written may overlap what is read or written beside it.
  */

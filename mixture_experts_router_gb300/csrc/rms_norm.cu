@@ -5,14 +5,14 @@
 //
 // Bound by memory: every element is read and written once, a row staying in
 // registers between its sum of squares and its results (16384 x 4096 bf16 with
-// the residual and both results: 95 us, 6.4 TB/s; one row of 4096: 2.5 us, the
+// the residual and both results: 95.6 us, 6.3 TB/s; one row of 4096: 2.5 us, the
 // launch and two round trips).  R threads share a row
 // (a power of two from 32), each holding up to 4 times 8 elements.  Rows that
 // start on 16 bytes: a thread's elements are 8 in a row (16 bytes of bf16),
 // 16 lanes a scale's 128 columns.  Others: 2 of every 64, or an element of every
 // 32 where rows are odd (a warp's loads are whole lines), a warp's first half
 // and last half of steps a scale's columns (2915 rows of bf16, both results, 91
-// MB: 59 us for 6259 columns, 49 for 6258 in pairs, 59 one by one).
+// MB: 58 us for 6259 columns one by one, 48 for 6258 in pairs).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -274,9 +274,9 @@ struct Raw {
 
 // Many rows of 513 to 8192 columns that start on 16 bytes: blocks that stay,
 // a row at a time, whose next row is on its way while this one is written
-// (residual and both results, 16384 x 4096: 110 us a block per row, 105 with
-// 4 blocks an SM, 96.5 with 3: 6.3 TB/s; 2048 x 4096: 21 a block per row, 16;
-// 512 x 4096: 6.5, 7.3).
+// (residual and both results, 16384 x 4096: 124 us a block per row, 108 with
+// 4 blocks an SM, 95.6 with 3: 6.3 TB/s; 2048 x 4096: 18.6 a block per row, 14.4;
+// 512 x 4096: 5.2, 5.8; 512 x 7168: 11.4, 8.6; 304 x 7168: 5.6, 7.3).
 template <int THREADS, int STEPS>
 constexpr int kRowBlocks = THREADS == kBlock ? (STEPS == 2 ? 3 : 2) : STEPS == 1 ? 8 : 6;  // of an SM
 
@@ -373,8 +373,8 @@ cudaError_t launch_steps(const NormArgs& a, int num_sms, cudaStream_t s) {
   const int chunks = (a.cols + 255) / 256 * 32;  // of 8 columns; unaligned rows take them by warps
   // Few rows: as many threads as there are chunks, the shortest way through a
   // row.  Many: blocks of 256 threads while 4 steps suffice, more rows in
-  // flight (16384 x 4096 that way: 146 us with 512 threads a row, 126 with 128,
-  // 110 with 256).
+  // flight (16384 x 4096 that way, with codes by the reciprocal: 146 us with 512
+  // threads a row, 126 with 128, 110 with 256).
   int per_row = 32;
   while (per_row < kMaxThreads && per_row < chunks &&
          (per_row < kBlock || a.rows <= 2 * num_sms || 4 * per_row < chunks))

@@ -7,9 +7,9 @@
 //   index.
 //
 // What bounds it: for many tokens the instructions of the scores and the
-// rounds (16384 x 256 sigmoid, 4 of 8 groups, 8 chosen: 18.9 us with some 760
-// instructions a token and warp; 8192 x 128 softmax, 4 chosen: 5.4), not the
-// bytes of the logits; for few, the launch (3.4 us for one).
+// rounds (16384 x 256 sigmoid, 4 of 8 groups, 8 chosen: 18.6 us with some 770
+// instructions a token and warp; 8192 x 128 softmax, 4 chosen: 5.5), not the
+// bytes of the logits; for few, the launch (3.5 us for one).
 //
 // Keys.  The order of a lane's experts is that of unsigned words: c's bits in
 // an order-preserving form, the last four replaced by the expert's place in the
